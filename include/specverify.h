@@ -62,7 +62,9 @@
 extern "C" {
 #endif
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* SPEC_E4M3 (8-bit floating point, 4 exponent and 3 mantissa bits, no
+ * infinity, largest value 448) is a type of cache pages only. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_E4M3 = 2 } spec_dtype;
 
 typedef enum {
     SPEC_OK = 0,
@@ -413,6 +415,177 @@ int spec_tree_verify(const void *logits, int dtype, const int32_t *parent, const
                      const int32_t *n_nodes, int R, int M, int V, int max_depth,
                      int32_t *out_accepted, int32_t *out_path, int32_t *out_tokens,
                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The paged key/value cache around verification
+ *
+ * The target pass that spec_tree_verify and spec_verify_batch take their
+ * logits from runs over the drafted tokens (a tree of n_nodes[r] nodes, or the
+ * chain anchor, x_1 .. x_gamma) behind ctx_len[r] committed tokens.  The
+ * entry points below do its work on the cache:
+ *   once a step    spec_tree_mask        positions and ancestor bits
+ *   every layer    spec_qkv_write        norms, rotation, cache write
+ *                  spec_tree_attention   every node over context + ancestors
+ *   after the step spec_kv_commit        the accepted path's rows move behind
+ *                                        the context
+ * and spec_kv_read reads stretches back.
+ *
+ * The cache of one layer:
+ *   k_cache, v_cache  [num_pages][Hkv][page_size][D]  SPEC_BF16 or SPEC_E4M3
+ *   k_scale, v_scale  [num_pages][Hkv][page_size]     fp32, SPEC_E4M3 only
+ *                                                     (NULL for SPEC_BF16)
+ *   page_table        [R][max_pages]                  int32 page numbers
+ * Token t of request r lies in page page_table[r][t / page_size] at offset
+ * t % page_size; node v of the request's tree is token ctx_len[r] + v.  A
+ * SPEC_E4M3 row x of one token and head is stored as round(x / s), to
+ * nearest even, with s = max(max|x| / 448, 2^-126) in its scale; it stands
+ * for code * s.  A row with a NaN or infinity gets the scale NaN and codes 0.
+ *
+ * Common rules:
+ *  - page_size is a power of two, 16 .. 1024; D is 64, 128 or 256; Hkv >= 1 and
+ *    Hq is a multiple of Hkv (query head h reads key head h / (Hq / Hkv)).
+ *  - Pointers to activations, pages and out_q / out_k / out_v / out are
+ *    16-byte aligned (SPEC_EINVAL otherwise).
+ *  - n_nodes[r] may be 0 (an idle slot of a padded batch).  Rows v >=
+ *    n_nodes[r] are neither read nor written, in inputs, outputs or cache.
+ *  - Data faults (each sets SPEC_DEV_BAD_REQUEST): n_nodes outside [0, M],
+ *    ctx_len < 0 or ctx_len + n_nodes past the page table mark the whole
+ *    request; a page number outside [0, num_pages) marks the tokens in it.
+ *    Nothing outside the given arrays is read or written for them.
+ *  - Two requests may share pages that only hold context (a common prefix);
+ *    a page that one call writes must belong to one request.
+ */
+
+/* Workspace bytes of spec_tree_mask, spec_qkv_write, spec_kv_read and
+ * spec_kv_commit (the device status word). */
+size_t spec_cache_workspace_bytes(void);
+
+/*
+ * Positions and visibility of drafted trees, once per step for all layers.
+ *   parent   [R][M]  int32 as in spec_tree_verify (root ignored)
+ *   n_nodes  [R]     int32 in [0, M]
+ *   ctx_len  [R]     int32 >= 0
+ *   out_positions [R][M]     int32: ctx_len + depth of the node
+ *   out_mask      [R][M][W]  uint32, W = (M + 31) / 32: bit u % 32 of word
+ *                            u / 32 is set iff u is node v itself or one of
+ *                            its ancestors and, when window > 0, less than
+ *                            `window` levels above it
+ * Rows v >= n_nodes get position -1 and an empty mask.  A request with
+ * n_nodes outside [0, M], a negative ctx_len, ctx_len + M past 2^31 - 1 or a
+ * parent outside [0, v) gets that in all its rows and sets
+ * SPEC_DEV_BAD_REQUEST.
+ * Sizes: R >= 0, 1 <= M <= SPEC_TREE_MAX_NODES, window >= 0 (0: no window).
+ */
+int spec_tree_mask(const int32_t *parent, const int32_t *n_nodes, const int32_t *ctx_len, int R,
+                   int M, int window, int32_t *out_positions, uint32_t *out_mask, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * Norms of queries and keys, the position rotation and the cache write of the
+ * drafted (or prompt) tokens in one pass over the projections' output.
+ * For every token (r, v < n_nodes[r]) and head row x of D values (fp32
+ * arithmetic, rounded once where it is stored):
+ *   y = x * rsqrt(mean(x^2) + eps) * weight      (q with q_weight, k with
+ *                                                 k_weight; NULL: y = x)
+ *   for i < rot_dim / 2, with (c, s) = rope[position][i]:
+ *   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s), (a, b) = (i, i + rot_dim/2),
+ *                                  or (2 i, 2 i + 1) when `interleaved`
+ * q rows go to out_q, k rows to the k cache, v rows unchanged to the v cache.
+ *   q         [R][M][Hq][D]   dtype, nullable (with out_q: cache write only)
+ *   k, v      [R][M][Hkv][D]  dtype (SPEC_F32 or SPEC_BF16)
+ *   ld_q, ld_k, ld_v          elements from one token to the next (at least
+ *                             the heads' H * D, a multiple of 16 bytes): q, k
+ *                             and v may be parts of one projection's output
+ *   q_weight, k_weight [D]    dtype, nullable
+ *   rope      [max_pos][rot_dim / 2][2]  fp32 (cos, sin), NULL iff rot_dim == 0
+ *   positions [R][M]          int32, nullable (ctx_len + v)
+ *   out_q     [R][M][Hq][D]   bf16
+ * rot_dim is a multiple of 16, at most D.  A position outside [0, max_pos) is
+ * a data fault (with rot_dim > 0): the token's out_q rows and its k rows
+ * become NaN.  A faulty request's out_q rows become NaN and its tokens are
+ * not written.  Sizes: R, M >= 0.
+ */
+int spec_qkv_write(const void *q, const void *k, const void *v, int dtype, int64_t ld_q,
+                   int64_t ld_k, int64_t ld_v, const void *q_weight, const void *k_weight,
+                   float eps, const float *rope, int max_pos, int rot_dim, int interleaved,
+                   const int32_t *positions, const int32_t *ctx_len, const int32_t *n_nodes,
+                   const int32_t *page_table, int max_pages, int R, int M, int Hq, int Hkv, int D,
+                   void *k_cache, void *v_cache, int cache_dtype, float *k_scale, float *v_scale,
+                   int num_pages, int page_size, void *out_q, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * Reads tokens start[r] .. start[r] + len[r] - 1 of every request back.
+ *   out_k, out_v  [R][max_len][Hkv][D]  out_dtype (SPEC_BF16 or SPEC_F32;
+ *                 code * scale rounded once); rows past len[r] are left alone
+ * A request with start < 0, len outside [0, max_len] or start + len past the
+ * page table gets NaN in all max_len rows, a token in a bad page NaN in its
+ * row.  Sizes: R, max_len >= 0.
+ */
+int spec_kv_read(const void *k_cache, const void *v_cache, int cache_dtype, const float *k_scale,
+                 const float *v_scale, int num_pages, int page_size, const int32_t *page_table,
+                 int max_pages, const int32_t *start, const int32_t *len, int R, int max_len,
+                 int Hkv, int D, void *out_k, void *out_v, int out_dtype, void *workspace,
+                 size_t workspace_bytes, void *stream);
+
+/*
+ * Moves the accepted path's cache rows behind the context after
+ * spec_tree_verify: for i < accepted[r], the rows of node path[r][i] (token
+ * ctx_len + path[i]) become token ctx_len + 1 + i, codes and scales alike
+ * (the root is token ctx_len already).
+ *   accepted  [R]     int32 as spec_tree_verify's out_accepted
+ *   path      [R][M]  int32 as its out_path: accepted nodes, increasing
+ *   out_ctx_len [R]   int32, nullable: ctx_len + 1 + accepted (may not be
+ *                     ctx_len itself: other layers still read that)
+ * accepted[r] = -1 (an invalid tree) moves nothing and keeps ctx_len.  An
+ * accepted outside [-1, M - 1], a path that is not increasing inside
+ * [1, M), tokens past the page table or a bad page are data faults: nothing
+ * of the request moves and out_ctx_len is -1.  A chain's accepted prefix lies
+ * where it belongs already (path[i] = i + 1): no call is needed.
+ * Sizes: R >= 0, 1 <= M <= SPEC_TREE_MAX_NODES.
+ */
+int spec_kv_commit(void *k_cache, void *v_cache, int cache_dtype, float *k_scale, float *v_scale,
+                   int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                   const int32_t *ctx_len, const int32_t *accepted, const int32_t *path, int R,
+                   int M, int Hkv, int D, int32_t *out_ctx_len, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* Workspace bytes for spec_tree_attention (0 for sizes it does not accept). */
+size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D);
+
+/*
+ * Attention of the drafted tokens over the paged cache: for every node (r, v)
+ * and query head h, with key head g = h / (Hq / Hkv),
+ *   o = sum_j softmax_j(scale * q . k_j) v_j
+ * over the tokens j the node sees:
+ *   context  j < ctx_len[r], with window > 0 only j > position - window;
+ *   tree     token ctx_len[r] + u, u < n_nodes[r], iff bit u of the node's mask
+ *            row is set; without a mask iff u <= v (a chain; one node is a
+ *            single-token step, a prompt chunk is a long chain) and, with
+ *            window > 0, v - u < window.
+ * A token that a node does not see has no part in its row, whatever its
+ * cache rows hold.  A row that sees nothing gets 0 and log-sum-exp -inf.
+ * Scores, softmax sums and products are held in fp32.
+ *   q         [R][M][Hq][D]  SPEC_BF16
+ *   mask      [R][M][W]      uint32 as spec_tree_mask writes it, nullable
+ *   positions [R][M]         int32, nullable (ctx_len + v); read when a window
+ *                            or a mask is given.  A negative one is a data fault.
+ *   out       [R][M][Hq][D]  bf16
+ *   out_lse   [R][M][Hq]     fp32, nullable: natural log of the softmax sum
+ * A faulty request's or node's rows become NaN, and so do the rows that see a
+ * token in a bad page.  The tokens of the tree must be in the cache
+ * (spec_qkv_write).  Results do not depend on what else is in the batch's
+ * padding; the order of sums depends on the lengths in the batch.
+ * Sizes: R >= 0, 1 <= M <= SPEC_TREE_MAX_NODES, Hq / Hkv <= 64, window >= 0.
+ */
+int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const void *v_cache,
+                        int cache_dtype, const float *k_scale, const float *v_scale,
+                        int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                        const int32_t *ctx_len, const int32_t *n_nodes, const uint32_t *mask,
+                        const int32_t *positions, float scale, int window, int R, int M, int Hq,
+                        int Hkv, int D, void *out, float *out_lse, void *workspace,
+                        size_t workspace_bytes, void *stream);
 
 /* Synchronises `stream`, copies the workspace's device status word (the OR
  * of SPEC_DEV_* bits raised since the last clear) to *host_bits, and clears

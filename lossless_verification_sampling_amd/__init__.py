@@ -22,7 +22,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libspecverify.so")
 
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_E4M3 = 0, 1, 2
 SPEC_OK = 0
 SPEC_ETOOLARGE = -6
 SPEC_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -58,6 +58,13 @@ EXPORTED = (
     "spec_tree_workspace_bytes",
     "spec_tree_verify",
     "spec_markov_draft_sample",
+    "spec_cache_workspace_bytes",
+    "spec_tree_mask",
+    "spec_qkv_write",
+    "spec_kv_read",
+    "spec_kv_commit",
+    "spec_tree_attention_workspace_bytes",
+    "spec_tree_attention",
     "spec_get_device_status",
     "spec_time_stats_launch",
 )
@@ -117,6 +124,23 @@ def _load() -> ctypes.CDLL:
     lib.spec_tree_workspace_bytes.argtypes = [i, i, i]
     lib.spec_tree_verify.restype = i
     lib.spec_tree_verify.argtypes = [p, i, p, p, p, i, i, i, i, p, p, p, p, sz, p]
+    f, l = ctypes.c_float, ctypes.c_int64
+    lib.spec_cache_workspace_bytes.restype = sz
+    lib.spec_cache_workspace_bytes.argtypes = []
+    lib.spec_tree_mask.restype = i
+    lib.spec_tree_mask.argtypes = [p, p, p, i, i, i, p, p, p, sz, p]
+    lib.spec_qkv_write.restype = i
+    lib.spec_qkv_write.argtypes = [p, p, p, i, l, l, l, p, p, f, p, i, i, i, p, p, p, p, i, i, i,
+                                   i, i, i, p, p, i, p, p, i, i, p, p, sz, p]
+    lib.spec_kv_read.restype = i
+    lib.spec_kv_read.argtypes = [p, p, i, p, p, i, i, p, i, p, p, i, i, i, i, p, p, i, p, sz, p]
+    lib.spec_kv_commit.restype = i
+    lib.spec_kv_commit.argtypes = [p, p, i, p, p, i, i, p, i, p, p, p, i, i, i, i, p, p, sz, p]
+    lib.spec_tree_attention_workspace_bytes.restype = sz
+    lib.spec_tree_attention_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.spec_tree_attention.restype = i
+    lib.spec_tree_attention.argtypes = [p, i, p, p, i, p, p, i, i, p, i, p, p, p, p, f, i, i, i, i,
+                                        i, i, p, p, p, sz, p]
     lib.spec_get_device_status.restype = i
     lib.spec_get_device_status.argtypes = [p, ctypes.POINTER(ctypes.c_uint32), i, p]
     return lib
@@ -177,6 +201,14 @@ def spec_sts_workspace_bytes(N: int, gamma: int, G: int, bins: int) -> int:
 
 def spec_tree_workspace_bytes(R: int, M: int, V: int) -> int:
     return int(_lib.spec_tree_workspace_bytes(R, M, V))
+
+
+def spec_cache_workspace_bytes() -> int:
+    return int(_lib.spec_cache_workspace_bytes())
+
+
+def spec_tree_attention_workspace_bytes(R: int, M: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(_lib.spec_tree_attention_workspace_bytes(R, M, Hq, Hkv, D))
 
 
 # ---------------------------------------------------------------------------
@@ -586,3 +618,242 @@ def spec_markov_draft_sample(U: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor
                                        _stream_ptr(stream, dev))
     _raise(st, "spec_markov_draft_sample")
     return tok, lg
+
+
+# ---------------------------------------------------------------------------
+# the paged key/value cache and attention over it
+# ---------------------------------------------------------------------------
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev):
+    """Checks a layer's pages and returns (dtype code, P, Hkv, page size, D,
+    page table width)."""
+    _need(k_cache.dim() == 4, "k_cache must be [pages, heads, page size, D]")
+    P, Hkv, size, D = shape = tuple(k_cache.shape)
+    code = SPEC_BF16 if k_cache.dtype == torch.bfloat16 else SPEC_E4M3
+    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"cache pages must be bfloat16 or float8_e4m3fn, got {k_cache.dtype}")
+    _check(k_cache, "k_cache", None, None, dev)
+    _check(v_cache, "v_cache", k_cache.dtype, shape, dev)
+    if code == SPEC_E4M3:
+        _need(k_scale is not None and v_scale is not None, "e4m3 pages need k_scale and v_scale")
+        _check(k_scale, "k_scale", torch.float32, shape[:3], dev)
+        _check(v_scale, "v_scale", torch.float32, shape[:3], dev)
+    else:
+        _need(k_scale is None and v_scale is None, "bfloat16 pages have no scales")
+    _need(page_table.dim() == 2, "page_table must be [R, max_pages]")
+    wide = page_table.shape[1]
+    _check(page_table, "page_table", torch.int32, (R, wide), dev)
+    return code, P, Hkv, size, D, wide
+
+
+def _raw(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _ordered_heads(t: torch.Tensor, name: str, dev) -> int:
+    """Elements from one token's heads to the next of [R, M, H, D] whose
+    tokens are evenly spaced and whose heads are dense."""
+    _need(t.is_cuda and t.device == dev, f"{name} must be on {dev}")
+    R, M, H, D = t.shape
+    s = t.stride()
+    ld = s[1] if M > 1 else s[0] if R > 1 else H * D
+    _need((D == 1 or s[3] == 1) and (H == 1 or s[2] == D) and ld >= H * D and
+          (R == 1 or M == 1 or s[0] == M * ld),
+          f"{name} must hold dense heads at evenly spaced tokens")
+    return ld
+
+
+def _cache_buf(workspace, dev, need, stream):
+    ws = workspace or default_workspace(dev)
+    buf = ws.buf
+    return buf if buf is not None and buf.numel() >= need else ws.ensure(need, stream)
+
+
+def spec_tree_mask(parent: torch.Tensor, n_nodes: torch.Tensor, ctx_len: torch.Tensor, *,
+                   window: int = 0, out_positions: Optional[torch.Tensor] = None,
+                   out_mask: Optional[torch.Tensor] = None,
+                   workspace: Optional[Workspace] = None, stream=None):
+    """Positions and ancestor bits of drafted trees, once a step for all
+    layers.  parent [R, M], n_nodes [R], ctx_len [R] int32.  Returns
+    (positions [R, M] int32, mask [R, M, (M + 31) // 32] int32 bit words)."""
+    R, M = parent.shape
+    dev = parent.device
+    W = (M + 31) // 32
+    _check(parent, "parent", torch.int32, None, dev)
+    _check(n_nodes, "n_nodes", torch.int32, (R,), dev)
+    _check(ctx_len, "ctx_len", torch.int32, (R,), dev)
+    pos = out_positions if out_positions is not None else torch.empty((R, M), dtype=torch.int32,
+                                                                      device=dev)
+    mask = out_mask if out_mask is not None else torch.empty((R, M, W), dtype=torch.int32,
+                                                             device=dev)
+    _check(pos, "out_positions", torch.int32, (R, M), dev)
+    _check(mask, "out_mask", torch.int32, (R, M, W), dev)
+    buf = _cache_buf(workspace, dev, 256, stream)
+    st = _lib.spec_tree_mask(parent.data_ptr(), n_nodes.data_ptr(), ctx_len.data_ptr(), R, M,
+                             int(window), pos.data_ptr(), mask.data_ptr(), buf.data_ptr(),
+                             buf.numel(), _stream_ptr(stream, dev))
+    _raise(st, "spec_tree_mask")
+    return pos, mask
+
+
+def spec_qkv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   page_table: torch.Tensor, ctx_len: torch.Tensor, n_nodes: torch.Tensor, *,
+                   q: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                   k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   rope: Optional[torch.Tensor] = None, interleaved: bool = False,
+                   positions: Optional[torch.Tensor] = None,
+                   k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None, out_q: Optional[torch.Tensor] = None,
+                   workspace: Optional[Workspace] = None, stream=None) -> Optional[torch.Tensor]:
+    """Norms of queries and keys, the position rotation and the cache write in
+    one pass.  k, v [R, M, Hkv, D] and q [R, M, Hq, D] float32 or bfloat16
+    (parts of one projection's output: tokens evenly spaced, heads dense),
+    weights [D] of that type, rope [max_pos, rot / 2, 2] float32 (cos, sin),
+    positions [R, M] int32 (ctx_len + index without).  Token v < n_nodes[r] of
+    request r goes to cache token ctx_len[r] + v.  Returns the queries
+    [R, M, Hq, D] bfloat16 (out_q), or None without q."""
+    _need(k.dim() == 4 and v.dim() == 4, "k and v must be [R, M, heads, D]")
+    R, M, Hkv, D = shape = tuple(k.shape)
+    dev = k.device
+    code, P, H, size, Dc, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev)
+    _need(H == Hkv and Dc == D and tuple(v.shape) == shape, "k, v and the cache differ in heads or D")
+    dt = _dtype(k)
+    _need(v.dtype == k.dtype and (q is None or q.dtype == k.dtype), "q, k and v differ in type")
+    ld_k, ld_v = _ordered_heads(k, "k", dev), _ordered_heads(v, "v", dev)
+    Hq = ld_q = 0
+    if q is not None:
+        _need(q.dim() == 4 and q.shape[0] == R and q.shape[1] == M and q.shape[3] == D,
+              "q must be [R, M, Hq, D]")
+        Hq, ld_q = q.shape[2], _ordered_heads(q, "q", dev)
+        if out_q is None:
+            out_q = torch.empty((R, M, Hq, D), dtype=torch.bfloat16, device=dev)
+        _check(out_q, "out_q", torch.bfloat16, (R, M, Hq, D), dev)
+    else:
+        _need(q_weight is None and out_q is None, "q_weight and out_q belong to q")
+    _check(q_weight, "q_weight", k.dtype, (D,), dev)
+    _check(k_weight, "k_weight", k.dtype, (D,), dev)
+    max_pos = rot = 0
+    if rope is not None:
+        _need(rope.dim() == 3 and rope.shape[2] == 2, "rope must be [max_pos, rot / 2, 2]")
+        _check(rope, "rope", torch.float32, None, dev)
+        max_pos, rot = rope.shape[0], 2 * rope.shape[1]
+    _check(positions, "positions", torch.int32, (R, M), dev)
+    _check(ctx_len, "ctx_len", torch.int32, (R,), dev)
+    _check(n_nodes, "n_nodes", torch.int32, (R,), dev)
+    buf = _cache_buf(workspace, dev, 256, stream)
+    st = _lib.spec_qkv_write(_raw(q), k.data_ptr(), v.data_ptr(), dt, ld_q, ld_k, ld_v,
+                             _raw(q_weight), _raw(k_weight), eps, _raw(rope), max_pos, rot,
+                             int(interleaved), _raw(positions), ctx_len.data_ptr(),
+                             n_nodes.data_ptr(), page_table.data_ptr(), wide, R, M, Hq, Hkv, D,
+                             k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
+                             _raw(v_scale), P, size, _raw(out_q), buf.data_ptr(), buf.numel(),
+                             _stream_ptr(stream, dev))
+    _raise(st, "spec_qkv_write")
+    return out_q
+
+
+def spec_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                 start: torch.Tensor, length: torch.Tensor, max_len: int, *,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                 dtype: torch.dtype = torch.bfloat16, out_k: Optional[torch.Tensor] = None,
+                 out_v: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None,
+                 stream=None):
+    """Reads tokens start[r] .. start[r] + length[r] - 1 of every request.
+    Returns (k, v) [R, max_len, Hkv, D] in `dtype` (bfloat16 or float32, or
+    that of the given outputs); rows past length[r] are left as they were."""
+    R, dev = page_table.shape[0], k_cache.device
+    code, P, Hkv, size, D, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev)
+    _check(start, "start", torch.int32, (R,), dev)
+    _check(length, "length", torch.int32, (R,), dev)
+    if out_k is not None:
+        dtype = out_k.dtype
+    shape = (R, int(max_len), Hkv, D)
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=dtype, device=dev)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=dtype, device=dev)
+    _check(out_k, "out_k", dtype, shape, dev)
+    _check(out_v, "out_v", dtype, shape, dev)
+    buf = _cache_buf(workspace, dev, 256, stream)
+    st = _lib.spec_kv_read(k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
+                           _raw(v_scale), P, size, page_table.data_ptr(), wide, start.data_ptr(),
+                           length.data_ptr(), R, int(max_len), Hkv, D, out_k.data_ptr(),
+                           out_v.data_ptr(), _dtype(out_k), buf.data_ptr(), buf.numel(),
+                           _stream_ptr(stream, dev))
+    _raise(st, "spec_kv_read")
+    return out_k, out_v
+
+
+def spec_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                   ctx_len: torch.Tensor, accepted: torch.Tensor, path: torch.Tensor, *,
+                   k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                   out_ctx_len: Optional[torch.Tensor] = None,
+                   workspace: Optional[Workspace] = None, stream=None) -> torch.Tensor:
+    """Moves the accepted path's rows (spec_tree_verify's accepted [R] and path
+    [R, M]) behind the context, in place.  Returns the new context lengths."""
+    R, M = path.shape
+    dev = k_cache.device
+    code, P, Hkv, size, D, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev)
+    _check(ctx_len, "ctx_len", torch.int32, (R,), dev)
+    _check(accepted, "accepted", torch.int32, (R,), dev)
+    _check(path, "path", torch.int32, (R, M), dev)
+    if out_ctx_len is None:
+        out_ctx_len = torch.empty((R,), dtype=torch.int32, device=dev)
+    _check(out_ctx_len, "out_ctx_len", torch.int32, (R,), dev)
+    buf = _cache_buf(workspace, dev, 256, stream)
+    st = _lib.spec_kv_commit(k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
+                             _raw(v_scale), P, size, page_table.data_ptr(), wide,
+                             ctx_len.data_ptr(), accepted.data_ptr(), path.data_ptr(), R, M, Hkv,
+                             D, out_ctx_len.data_ptr(), buf.data_ptr(), buf.numel(),
+                             _stream_ptr(stream, dev))
+    _raise(st, "spec_kv_commit")
+    return out_ctx_len
+
+
+def spec_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        page_table: torch.Tensor, ctx_len: torch.Tensor, n_nodes: torch.Tensor, *,
+                        mask: Optional[torch.Tensor] = None,
+                        positions: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                        window: int = 0, k_scale: Optional[torch.Tensor] = None,
+                        v_scale: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None, want_lse: bool = False,
+                        out_lse: Optional[torch.Tensor] = None,
+                        workspace: Optional[Workspace] = None, stream=None):
+    """Attention of the drafted tokens q [R, M, Hq, D] bfloat16 over the paged
+    cache: the context and, by `mask` (spec_tree_mask), their ancestors; without
+    a mask the tokens are a chain.  scale defaults to D ** -0.5.  Returns
+    (out [R, M, Hq, D] bfloat16, log-sum-exp [R, M, Hq] float32 or None)."""
+    _need(q.dim() == 4, "q must be [R, M, Hq, D]")
+    R, M, Hq, D = shape = tuple(q.shape)
+    dev = q.device
+    code, P, Hkv, size, Dc, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev)
+    _need(Dc == D, "q and the cache differ in D")
+    _check(q, "q", torch.bfloat16, None, dev)
+    _check(ctx_len, "ctx_len", torch.int32, (R,), dev)
+    _check(n_nodes, "n_nodes", torch.int32, (R,), dev)
+    _check(mask, "mask", torch.int32, (R, M, (M + 31) // 32), dev)
+    _check(positions, "positions", torch.int32, (R, M), dev)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _check(out, "out", torch.bfloat16, shape, dev)
+    if out_lse is None and want_lse:
+        out_lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
+    _check(out_lse, "out_lse", torch.float32, shape[:3], dev)
+    need = _lib.spec_tree_attention_workspace_bytes(R, M, Hq, Hkv, D)
+    if need == 0:
+        raise SpecError(-5, "spec_tree_attention_workspace_bytes")
+    buf = _cache_buf(workspace, dev, need, stream)
+    st = _lib.spec_tree_attention(q.data_ptr(), SPEC_BF16, k_cache.data_ptr(), v_cache.data_ptr(),
+                                  code, _raw(k_scale), _raw(v_scale), P, size,
+                                  page_table.data_ptr(), wide, ctx_len.data_ptr(),
+                                  n_nodes.data_ptr(), _raw(mask), _raw(positions),
+                                  D ** -0.5 if scale is None else scale, int(window), R, M, Hq,
+                                  Hkv, D, out.data_ptr(), _raw(out_lse), buf.data_ptr(),
+                                  buf.numel(), _stream_ptr(stream, dev))
+    _raise(st, "spec_tree_attention")
+    return out, out_lse

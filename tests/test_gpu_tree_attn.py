@@ -1,0 +1,213 @@
+"""Attention of drafted tokens over the paged cache against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from cache_util import Cache, bf16, random_trees, reference_attention
+from oracle import cache as oc
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    import lossless_verification_sampling_amd as m
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return m
+
+
+@pytest.fixture(scope="module")
+def dev(sv):
+    return torch.device("cuda:0")
+
+
+def D(x, dev):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(dev)
+
+
+class Case:
+    def __init__(self, seed, R, M, Hq, Hkv, Dh, page, kind, ctx, tree, window=0, n=None, qs=2.0):
+        g = np.random.default_rng(seed)
+        self.window, self.tree, self.dims = window, tree, (R, M, Hq, Dh)
+        self.ctx = np.asarray(ctx, np.int32)
+        self.n = np.array([M] * R if n is None else n, np.int32)
+        self.c = Cache(g, R, int((self.ctx + self.n).max()), Hkv, Dh, page, kind)
+        self.q = bf16(g.standard_normal((R, M, Hq, Dh)) * qs)
+        self.parent = random_trees(g, R, M, self.n)
+        self.pos, self.see = oc.tree_mask(self.parent, self.n, self.ctx, window)
+        if not tree:
+            self.pos = self.ctx[:, None] + np.arange(M)[None, :]
+        self.scale = float(np.float32(Dh ** -0.5))
+
+    def run(self, sv, dev, **kw):
+        self.c.to(dev)
+        out = torch.full(self.dims, 7.0, dtype=torch.bfloat16, device=dev)
+        lse = torch.full(self.dims[:3], 7.0, dtype=torch.float32, device=dev)
+        m = dict(mask=D(oc.pack_bits(self.see), dev), positions=D(self.pos, dev)) if self.tree else {}
+        m.update(kw)
+        sv.spec_tree_attention(self.q.to(dev), *self.c.args(), D(self.ctx, dev), D(self.n, dev),
+                               scale=self.scale, window=self.window, out=out, out_lse=lse,
+                               **self.c.kw(), **m)
+        torch.cuda.synchronize()
+        return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+    def check(self, got, rows=None):
+        out, lse = got
+        q = self.q.double().numpy()
+        ro, rl, to, tl = reference_attention(self.c, q, self.ctx, self.n, self.see, self.pos,
+                                             self.scale, self.window, not self.tree)
+        M = self.dims[1]
+        for r in range(self.dims[0]):
+            m = int(self.n[r])
+            assert (out[r, m:] == 7.0).all() and (lse[r, m:] == 7.0).all()
+            for v in range(m):
+                a, b = out[r, v], ro[r, v]
+                assert np.array_equal(np.isnan(a), np.isnan(b)), (r, v)
+                f = np.isfinite(b)
+                assert (np.abs(a - b) <= to[r, v])[f].all(), (r, v, float(
+                    (np.abs(a - b) / to[r, v])[f].max()))
+                a, b = lse[r, v], rl[r, v]
+                f = np.isfinite(b)
+                assert np.array_equal(a[~f], b[~f], equal_nan=True), (r, v)
+                assert (np.abs(a - b) <= tl[r, v])[f].all(), (r, v, a, b)
+
+
+SHAPES = [  # R, M, Hq, Hkv, D, page, ctx, tree, window, n
+    (1, 1, 1, 1, 64, 16, [0], False, 0, None),                 # itself alone
+    (1, 1, 4, 1, 128, 16, [1], False, 0, None),
+    (1, 1, 32, 8, 128, 64, [1023], False, 0, None),
+    (1, 9, 32, 8, 128, 64, [700], True, 0, None),
+    (3, 8, 8, 2, 128, 32, [31, 0, 300], False, 0, [8, 3, 0]),  # an idle slot
+    (2, 48, 8, 2, 128, 32, [129, 47], True, 0, [48, 31]),
+    (2, 33, 7, 1, 64, 16, [65, 200], True, 0, None),           # seven heads a key head
+    (2, 70, 2, 2, 256, 64, [90, 15], True, 0, [70, 1]),
+    (1, 200, 5, 1, 128, 128, [77], True, 0, None),
+    (2, 100, 3, 3, 64, 16, [16, 513], False, 0, None),
+    (1, 300, 1, 1, 64, 32, [0], False, 0, None),               # a prompt
+    (2, 20, 4, 2, 128, 16, [500, 3], False, 17, None),         # a window inside the chain
+    (2, 40, 4, 2, 64, 32, [400, 90], True, 3, None),
+    (2, 5, 16, 1, 256, 16, [260, 33], True, 100, None),
+    (1, 1, 8, 8, 64, 1024, [5000], False, 1, None),            # a window of one
+    (5, 3, 64, 1, 128, 16, [5, 17, 1000, 64, 0], False, 0, None),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_against_fp64(sv, dev, shape, kind):
+    R, M, Hq, Hkv, Dh, page, ctx, tree, window, n = shape
+    print(f"[attn] {shape} {kind}", flush=True)
+    c = Case(sum(ctx) + M, R, M, Hq, Hkv, Dh, page, kind, ctx, tree, window, n)
+    c.check(c.run(sv, dev))
+
+
+def test_largest_tree(sv, dev):
+    c = Case(11, 1, 1024, 2, 1, 64, 64, "bf16", [130], True)
+    c.check(c.run(sv, dev))
+
+
+def test_long_contexts_beside_short_ones(sv, dev):
+    c = Case(12, 6, 2, 4, 2, 64, 64, "e4m3", [9001, 1, 0, 33, 4097, 2], False, 0, [2, 2, 1, 2, 0, 2])
+    c.check(c.run(sv, dev))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_rows_that_see_nothing(sv, dev, kind):
+    c = Case(13, 2, 6, 4, 2, 128, 16, kind, [0, 40], True)
+    c.see[0, 3] = False                       # no context, no node
+    c.see[1, 2] = False                       # context alone
+    c.see[0, 5] = False
+    c.see[0, 5, 1] = True                     # not even itself
+    got = c.run(sv, dev)
+    assert not got[0][0, 3].any() and (got[1][0, 3] == -np.inf).all()
+    c.check(got)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf, float(np.finfo(np.float32).max)])
+def test_unseen_tokens_have_no_part(sv, dev, tree, value):
+    """A node's K and V rows hold NaN, infinities or the type's largest value:
+    rows that do not see the node are as if it were not there."""
+    M = 20
+    c = Case(14, 1, M, 4, 2, 64, 16, "bf16", [37], tree)
+    if tree:
+        c.see[0, :, 7] = False                # nobody sees node 7
+        c.see[0, 9] = False
+        c.see[0, 9, :7] = True
+    clean = Case(14, 1, M, 4, 2, 64, 16, "bf16", [37], tree)
+    clean.see = c.see
+    t = 37 + (7 if tree else M - 1)           # the chain's last token
+    pg, off = int(c.c.table[0, t // 16]), t % 16
+    for x in c.c.dev:
+        x[pg, :, off] = value
+    a, b = c.run(sv, dev), clean.run(sv, dev)
+    seen = M if tree else M - 1
+    np.testing.assert_array_equal(a[0][:, :seen], b[0][:, :seen])
+    np.testing.assert_array_equal(a[1][:, :seen], b[1][:, :seen])
+    assert np.isfinite(a[0][:, :seen]).all()
+
+
+def test_seen_infinities_follow_the_formula(sv, dev):
+    c = Case(15, 1, 8, 2, 1, 64, 16, "bf16", [50], True)
+    k, v = c.c.dev
+    at = lambda t: (int(c.c.table[0, t // 16]), 0, t % 16)  # noqa: E731
+    v[at(50 + 3)][5] = np.inf                 # its descendants' d = 5 becomes inf
+    v[at(20)][9] = np.nan                     # everybody's d = 9
+    out, lse = c.run(sv, dev)
+    below = c.see[0, :, 3]
+    assert (out[0, below, :, 5] == np.inf).all() and np.isfinite(out[0, ~below][..., 5]).all()
+    assert np.isnan(out[0, ..., 9]).all()
+    rest = np.delete(out[0], [5, 9], -1)
+    assert np.isfinite(rest).all() and np.isfinite(lse).all()
+
+
+def test_garbage_behind_the_last_token(sv, dev):
+    c = Case(16, 2, 5, 4, 1, 128, 32, "bf16", [40, 3], False)
+    c.run(sv, dev)
+    for r, L in ((0, 45), (1, 8)):
+        pg = int(c.c.table[r, L // 32])
+        for x in c.c.dev:
+            x[pg, :, L % 32:] = float("nan")
+    c.check(c.run(sv, dev))
+
+
+def test_far_scores(sv, dev):
+    """Scores in the thousands: one token takes all the weight."""
+    c = Case(17, 1, 4, 4, 1, 128, 16, "bf16", [300], False, qs=300.0)
+    c.check(c.run(sv, dev))
+
+
+@pytest.mark.parametrize("fault", ["n_high", "n_negative", "ctx", "past", "page", "position"])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_faults(sv, dev, fault, kind):
+    c = Case(18, 3, 6, 4, 2, 64, 16, kind, [30, 40, 9], True)
+    good = c.run(sv, dev)
+    if fault == "n_high":
+        c.n[1] = 7
+    elif fault == "n_negative":
+        c.n[1] = -1
+    elif fault == "ctx":
+        c.ctx[1] = -1
+    elif fault == "past":
+        c.ctx[1] = 43
+    elif fault == "page":
+        c.c.table[1, 2] = c.c.P               # tokens 32 .. 47
+    else:
+        c.pos[1, 4] = -1
+    ws = sv.Workspace(dev, sv.spec_tree_attention_workspace_bytes(3, 6, 4, 2, 64))
+    out, lse = c.run(sv, dev, workspace=ws)
+    assert sv.spec_get_device_status(ws) == sv.SPEC_DEV_BAD_REQUEST
+    rows = [4] if fault == "position" else list(range(6))
+    assert np.isnan(out[1, rows]).all() and np.isnan(lse[1, rows]).all()
+    rest = [i for i in range(6) if i not in rows]
+    for a, b in ((out, good[0]), (lse, good[1])):
+        np.testing.assert_allclose(a[[0, 2]], b[[0, 2]], rtol=2.0 ** -7, atol=1e-6)
+        np.testing.assert_allclose(a[1, rest], b[1, rest], rtol=2.0 ** -7, atol=1e-6)
+    assert sv.spec_get_device_status(ws) == 0
+
+
+def test_same_call_same_bits(sv, dev):
+    c = Case(19, 4, 12, 8, 2, 128, 16, "e4m3", [1000, 20, 300, 5], True)
+    a, b = c.run(sv, dev), c.run(sv, dev)
+    np.testing.assert_array_equal(a[0], b[0])
+    np.testing.assert_array_equal(a[1], b[1])
