@@ -565,12 +565,13 @@ size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D)
  *            single-token step, a prompt chunk is a long chain) and, with
  *            window > 0, v - u < window.
  * A token that a node does not see has no part in its row, whatever its
- * cache rows hold.  A row that sees nothing gets 0 and log-sum-exp -inf.
+ * cache rows hold.  A row that sees nothing (or whose scores are all -inf) gets
+ * 0 and log-sum-exp -inf.
  * Scores, softmax sums and products are held in fp32.
  *   q         [R][M][Hq][D]  SPEC_BF16
  *   mask      [R][M][W]      uint32 as spec_tree_mask writes it, nullable
  *   positions [R][M]         int32, nullable (ctx_len + v); read when a window
- *                            or a mask is given.  A negative one is a data fault.
+ * XX
  *   out       [R][M][Hq][D]  bf16
  *   out_lse   [R][M][Hq]     fp32, nullable: natural log of the softmax sum
  * A faulty request's or node's rows become NaN, and so do the rows that see a
