@@ -32,6 +32,8 @@
 
 namespace sv {
 
+struct Cut;
+
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
@@ -52,6 +54,8 @@ struct AttnArgs {
     float *lse;
     Control *ctl;
     float *part;                 // [2 groups][part_stride]
+    Cut *cuts;                   // [groups]
+    int *n_cuts;                 // cuts that the launch wrote
     int groups, part_stride;
 };
 
@@ -94,81 +98,70 @@ __device__ __forceinline__ int tile_units(const AttnArgs &a, const Req &q, int t
 }
 // Units of one key head.
 template <int TR>
-__device__ __forceinline__ int64_t head_units(const AttnArgs &a, const Req &q) {
+__device__ __forceinline__ int head_units(const AttnArgs &a, const Req &q) {
     if (q.tiles == 0) return 0;
-    if (a.mask || !q.ok) return (int64_t)q.tiles * tile_units<TR>(a, q, 0);
-    int64_t s = 0;
+    if (a.mask || !q.ok) return q.tiles * tile_units<TR>(a, q, 0);
+    int s = 0;
     for (int t = 0; t < q.tiles; ++t) s += tile_units<TR>(a, q, t);
     return s;
 }
 
+// Ranges of the batch's `total` units (below 2^31, checked on the host): the
+// first `extra` of `parts` ranges have `each` + 1 of them.
 struct Place {
-    int r;                       // request
-    int64_t off;                 // units into it
-    int64_t total;               // units of the whole batch
-    int parts;                   // ranges with work: min(groups, total)
+    int r;                       // the request of the range's first unit
+    int off;                     // units into it
+    int total, parts, each, extra;
 };
 
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
-    return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-
 // The first unit of range `num` of `parts`.
-__device__ __forceinline__ int64_t border(const Place &p, int num) {
-    return p.total * num / p.parts;
+__device__ __forceinline__ int border(const Place &p, int num) {
+    return p.each * num + min(num, p.extra);
 }
 
-// The request that the first unit of a range falls into: of range `num`, or,
-// with XCD, of the range of workgroup `num` when neighbouring ranges, which
-// often share a key head's pages, go to one XCD (num becomes the range; -1:
-// none).  Every thread of the workgroup gets the same answer.
-template <int TR, bool XCD>
+// The request that the first unit of this workgroup's range falls into.
+// Neighbouring ranges, which often share a key head's pages, go to one XCD
+// (workgroups are dealt to the eight in turn); num becomes the range, or -1.
+// Every thread of the workgroup gets the same answer.
+template <int TR>
 __device__ __forceinline__ Place find_unit(const AttnArgs &a, int &num) {
-    __shared__ int64_t sum_s[kWaves];
-    __shared__ int r_s;
-    __shared__ int64_t off_s;
+    __shared__ int sum_s[kWaves];
+    __shared__ int r_s, off_s;
     const int tid = threadIdx.x;
     const int chunk = (a.R + kBlock - 1) / kBlock;
     const int r0 = min(tid * chunk, a.R), r1 = min(r0 + chunk, a.R);
-    int64_t mine = 0;
+    int mine = 0;
     for (int r = r0; r < r1; ++r) mine += head_units<TR>(a, request_of<TR>(a, r)) * a.c.heads;
     // scan inside the wave, then over the four waves
-    int64_t inc = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int64_t up = __shfl_up(inc, o, 64);
-        if ((tid & 63) >= o) inc += up;
-    }
+    const int inc = (int)wave_incl_scan_dpp((uint32_t)mine);
     if ((tid & 63) == 63) sum_s[tid >> 6] = inc;
     __syncthreads();
-    int64_t base = 0;
+    int base = 0;
     Place p;
     p.total = 0;
     for (int w = 0; w < kWaves; ++w) {
         if (w < (tid >> 6)) base += sum_s[w];
         p.total += sum_s[w];
     }
-    p.total = uniform(p.total);
-    p.parts = (int)min((int64_t)a.groups, p.total);
+    p.total = __builtin_amdgcn_readfirstlane(p.total);
+    p.parts = min(a.groups, p.total);
+    p.each = p.parts ? p.total / p.parts : 0;
+    p.extra = p.total - p.each * p.parts;
     p.r = a.R;
     p.off = 0;
-    if (XCD) {
-        const int per = (p.parts + 7) >> 3, in = num >> 3;
-        num = in < per ? (num & 7) * per + in : a.groups;
-    }
+    const int per = (p.parts + 7) >> 3, in = num >> 3;
+    num = in < per ? (num & 7) * per + in : a.groups;
     if (num >= p.parts) {
         num = -1;
         return p;
     }
-    const int64_t at = border(p, num);
-    const int64_t first = base + inc - mine;
+    const int at = border(p, num);
+    const int first = base + inc - mine;
     if (at >= first && at < first + mine) {
-        int64_t left = at - first;
+        int left = at - first;
         int r = r0;
         for (; r < r1; ++r) {
-            const int64_t u = head_units<TR>(a, request_of<TR>(a, r)) * a.c.heads;
+            const int u = head_units<TR>(a, request_of<TR>(a, r)) * a.c.heads;
             if (left < u) break;
             left -= u;
         }
@@ -177,33 +170,47 @@ __device__ __forceinline__ Place find_unit(const AttnArgs &a, int &num) {
     }
     __syncthreads();
     p.r = __builtin_amdgcn_readfirstlane(r_s);
-    p.off = uniform(off_s);
+    p.off = __builtin_amdgcn_readfirstlane(off_s);
     return p;
 }
 
 struct Item {
     int h, t, u;                 // key head, row tile, unit in the item
-    int units;
 };
 template <int TR>
-__device__ __forceinline__ Item item_of(const AttnArgs &a, const Req &rq, int64_t off) {
-    const int64_t hu = head_units<TR>(a, rq);
+__device__ __forceinline__ Item item_of(const AttnArgs &a, const Req &rq, int off) {
+    const int hu = head_units<TR>(a, rq);
     Item i;
-    i.h = (int)(off / hu);
+    i.h = off / hu;
     i.t = 0;
-    int64_t rem = off - i.h * hu;
+    i.u = off - i.h * hu;
     if (a.mask || !rq.ok) {
-        i.units = tile_units<TR>(a, rq, 0);
-        i.t = (int)(rem / i.units);
-        rem -= (int64_t)i.t * i.units;
+        const int units = tile_units<TR>(a, rq, 0);
+        i.t = i.u / units;
+        i.u -= i.t * units;
     } else {
-        while (rem >= (i.units = tile_units<TR>(a, rq, i.t))) {
-            rem -= i.units;
-            ++i.t;
-        }
+        for (int units; i.u >= (units = tile_units<TR>(a, rq, i.t)); ++i.t) i.u -= units;
     }
-    i.u = (int)rem;
     return i;
+}
+
+// What a range left of the item it began and did not finish, for the join.
+struct Cut {
+    int node0, h, row0;          // first node of the request, key head, first row
+    int rows;                    // rows of the item; 0: none
+    int parts;                   // ranges that hold its units, from this one on
+    int pad[3];
+};
+
+// Range `grp`'s entry; `rest` units of the item are behind the range.
+template <int TR>
+__device__ __forceinline__ void write_cut(const AttnArgs &a, const Place &p, int grp, bool cuts,
+                                          int r, const Req &rq, int h, int t, int rest) {
+    Cut cut{r * a.M, h, t * TR, cuts ? min(TR, rq.rows - t * TR) : 0, 1, {0, 0, 0}};
+    const int last = border(p, grp + 1) + rest;
+    while (grp + cut.parts < p.parts && border(p, grp + cut.parts) < last) ++cut.parts;
+    a.cuts[grp] = cut;
+    if (grp == 0) *a.n_cuts = p.parts - 1;  // the last range cuts nothing
 }
 
 // ---------------------------------------------------------------------------
@@ -248,13 +255,27 @@ struct Half {
     int bad;                     // bit h: half h lies in a bad page
 };
 
-__device__ __forceinline__ Half halves_of(const AttnArgs &a, int r, int h, int t, int L) {
+// The page numbers of a step's halves, one load ahead of their use: a wave
+// that waited for them before it could ask for the rows stood still for a
+// memory round trip each step.
+struct Numbers {
+    int page[2];
+};
+__device__ __forceinline__ Numbers numbers_of(const AttnArgs &a, int r, int t, int L) {
+    Numbers x;
+    const int32_t *row = a.c.table + (int64_t)r * a.c.max_pages;
+    t = min(t, L - 1);                                  // a step behind the end is not used
+    x.page[0] = row[t >> a.c.shift];
+    x.page[1] = row[min(t + 16, L - 1) >> a.c.shift];
+    return x;
+}
+__device__ __forceinline__ Half halves_of(const AttnArgs &a, const Numbers &num, int h, int t, int L) {
     Half x;
     x.bad = 0;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const int tt = t + 16 * s < L ? t + 16 * s : t;  // a half behind the end is not used
-        int page = a.c.table[(int64_t)r * a.c.max_pages + (tt >> a.c.shift)];
+        const int tt = t + 16 * s < L ? t + 16 * s : t;  // nor is a half
+        int page = t + 16 * s < L ? num.page[s] : num.page[0];
         if ((unsigned)page >= (unsigned)a.c.num_pages) {
             x.bad |= 1 << s;
             page = 0;
@@ -316,13 +337,54 @@ __device__ __forceinline__ bool odd_word(uint32_t w) {  // a NaN or an infinity 
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-// Whether the row of node v (position pos) sees token t < L.
-__device__ __forceinline__ bool sees(const AttnArgs &a, int t, int ctx, int n, int v, int pos,
-                                     const uint32_t *mrow) {
-    if (t < ctx) return !a.window || t > pos - a.window;
-    const int u = t - ctx;
-    if (u >= n) return false;
-    return mrow ? (mrow[u >> 5] >> (u & 31)) & 1u : u <= v && (!a.window || v - u < a.window);
+// The low k bits, k clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t ones(int k) {
+    return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u;
+}
+// Tokens tok .. tok + 31 that the row of node v (position pos, mask row mrow)
+// sees, one bit each.
+__device__ __forceinline__ uint32_t sees(const AttnArgs &a, int tok, int ctx, int n, int v, int pos,
+                                         const uint32_t *mrow) {
+    const int k = ctx - tok;  // tokens of the context
+    const uint32_t old = ones(k);
+    uint32_t tree;
+    if (mrow) {
+        const int w = -k >> 5, sh = -k & 31;  // tree slot -k at bit 0
+        const uint32_t lo = w >= 0 && w < a.W ? mrow[w] : 0u;
+        const uint32_t hi = w >= -1 && w + 1 < a.W ? mrow[w + 1] : 0u;
+        tree = (uint32_t)(((uint64_t)hi << 32 | lo) >> sh) & ones(k + n);
+    } else {
+        tree = ones(k + v + 1);
+        if (a.window) tree &= ~ones(k + v + 1 - a.window);
+    }
+    const uint32_t near = a.window ? old & ~ones(pos - tok + 1 - a.window) : old;
+    return near | (tree & ~old);
+}
+// Bit i: token i of this lane group's eight.
+__device__ __forceinline__ uint32_t lane_bits(uint32_t seen, int g) {
+    return (seen >> (4 * g) & 15u) | (seen >> (4 * g + 16) & 15u) << 4;
+}
+
+// Tokens that every row of a wave sees: steps inside need no mask.
+struct Plain {
+    int lo, hi;
+};
+// For rows from `row0` on at positions pos[] of all lanes, up to token t1.
+template <int RT>
+__device__ __forceinline__ Plain plain_of(const AttnArgs &a, const Req &rq, int row0,
+                                          const int (&pos)[RT], int t1) {
+    Plain p;
+    p.lo = 0;
+    p.hi = rq.ctx;
+    if (!a.mask && !a.window) p.hi += row0 / a.G + 1;
+    if (a.window) {
+        int far = pos[0];
+#pragma unroll
+        for (int x = 1; x < RT; ++x) far = max(far, pos[x]);
+        p.lo = wave_max_i(far) - a.window + 1;
+    }
+    p.hi = min(p.hi, t1);
+    return p;
 }
 
 // ---------------------------------------------------------------------------
@@ -330,7 +392,7 @@ __device__ __forceinline__ bool sees(const AttnArgs &a, int t, int ctx, int n, i
 // ---------------------------------------------------------------------------
 
 template <int D, int RT> constexpr int waves_per_simd() {
-    return D * RT <= 128 ? 2 : 1;
+    return D <= 128 && D * RT <= 256 ? 2 : 1;
 }
 
 template <bool FP8, int D, int RT>
@@ -344,9 +406,12 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
     int grp = blockIdx.x;
-    const Place at = find_unit<TR, true>(a, grp);
-    if (grp < 0) return;
-    int64_t left = border(at, grp + 1) - border(at, grp);
+    const Place at = find_unit<TR>(a, grp);
+    if (grp < 0) {
+        if (at.parts == 0 && blockIdx.x == 0 && tid == 0) *a.n_cuts = 0;
+        return;
+    }
+    int left = border(at, grp + 1) - border(at, grp);
     int r = at.r;
     Req rq = request_of<TR>(a, r);
     const Item it = item_of<TR>(a, rq, at.off);
@@ -355,7 +420,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
         // ---- one item (r, h, t), its units from u0 on
         const int end = tile_end<TR>(a, rq, t);
         const int units = tile_units<TR>(a, rq, t);
-        const int u1 = (int)min((int64_t)units, u0 + left);
+        const int u1 = min(units, u0 + left);
         const int t0 = rq.lo + u0 * kUnit, t1 = min(end, rq.lo + u1 * kUnit);
         const bool whole = u0 == 0 && u1 == units;
         // ---- the rows of this lane's column
@@ -383,22 +448,20 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
 #pragma unroll
             for (int j = 0; j < DV; ++j) acc[x][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
-        // tokens before `plain` are seen by every row of the tile
-        int plain = rq.ctx;
-        if (!a.mask) plain += t * TR / a.G + 1;
-        if (a.window) plain = 0;
-        plain = min(plain, t1);
+        const Plain plain = plain_of<RT>(a, rq, t * TR, pos, t1);
         int tok = t0 + wave * kStep;
         if (rq.ok && tok < t1) {
             TT kv;
-            Half cur = halves_of(a, r, h, tok, end);
+            Half cur = halves_of(a, numbers_of(a, r, tok, end), h, tok, end);
+            Numbers num = numbers_of(a, r, tok + kUnit, end);
             load_k<FP8, D>(a, cur, lane, kv);
             load_v<FP8, D>(a, cur, lane, kv);
             while (true) {
                 const int nxt = tok + kUnit;
                 const bool more = nxt < t1;
                 Half nh = cur;
-                if (more) nh = halves_of(a, r, h, nxt, end);
+                if (more) nh = halves_of(a, num, h, nxt, end);
+                num = numbers_of(a, r, nxt + kUnit, end);
                 // ---- scores
                 f32x4_t s[RT][2];
 #pragma unroll
@@ -435,7 +498,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                 }
                 if (more) load_k<FP8, D>(a, nh, lane, kv);
                 __builtin_amdgcn_sched_barrier(0);
-                const bool masked = tok + kStep > plain || cur.bad;
+                const bool masked = tok < plain.lo || tok + kStep > plain.hi || cur.bad;
                 uint32_t seen[RT];  // bit i: this lane's token i is seen by its row
                 uint4 pw[RT];
 #pragma unroll
@@ -446,14 +509,10 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                     seen[x] = 0xffu;
                     if (masked) {
                         const uint32_t *mrow = a.mask ? a.mask + ((size_t)r * a.M + node[x]) * a.W : nullptr;
-                        seen[x] = 0u;
+                        seen[x] = lane_bits(sees(a, tok, rq.ctx, rq.n, node[x], pos[x], mrow), g);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int tt = tok + 16 * (i >> 2) + 4 * g + (i & 3);
-                            const bool see = sees(a, tt, rq.ctx, rq.n, node[x], pos[x], mrow);
-                            seen[x] |= (uint32_t)see << i;
-                            p[i] = !see ? -INFINITY : (cur.bad >> (i >> 2)) & 1 ? NAN : p[i];
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            p[i] = !(seen[x] >> i & 1u) ? -INFINITY : cur.bad >> (i >> 2) & 1 ? NAN : p[i];
                     }
                     float tm = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])),
                                      fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
@@ -568,7 +627,10 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
         for (int x = 0; x < RT; ++x) {
             l[x] += __shfl_xor(l[x], 16, 64);
             l[x] += __shfl_xor(l[x], 32, 64);
-            if (rowbad[x]) l[x] = NAN;
+            if (rowbad[x]) {
+                l[x] = NAN;
+                atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+            }
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -611,8 +673,6 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                                                         pack_bf16(o[j + 2] * inv, o[j + 3] * inv));
                     if ((tid & 15) == 0) {
                         if (a.lse) a.lse[orow] = (mm + log2f(sum)) * (float)kLn2;
-                        if (!rq.ok || (a.positions && a.positions[(size_t)r * a.M + nd] < rq.ctx))
-                            atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
                     }
                 } else {
                     float *pp = a.part + (size_t)(2 * grp + (u0 == 0)) * a.part_stride;
@@ -628,7 +688,383 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
         }
         // ---- the next item
         left -= u1 - u0;
-        if (left <= 0) return;
+        if (left <= 0) {
+            if (tid == 0) write_cut<TR>(a, at, grp, u0 == 0 && !whole, r, rq, h, t, units - u1);
+            return;
+        }
+        u0 = 0;
+        if (++t >= rq.tiles) {
+            t = 0;
+            if (++h >= a.c.heads) {
+                h = 0;
+                do {
+                    if (++r >= a.R) return;
+                    rq = request_of<TR>(a, r);
+                } while (rq.tiles == 0);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// many rows to a key head
+// ---------------------------------------------------------------------------
+
+constexpr int kTile = 64;              // tokens staged at a time
+
+// The same arithmetic with the waves side by side in the rows (16 RT each)
+// instead of the tokens: 64 tokens of K and V go to shared memory once per
+// workgroup, already in operand layout (converted and transposed on the way),
+// while the previous 64 are multiplied, and every wave reads them from there.
+template <bool FP8, int D> struct Stage {
+    typedef Tile<FP8, D> TT;
+    uint4 k[TT::KV];
+    uint32_t v[4][TT::VW];
+    float sc;
+    int flags;                         // bit 16: the 16 tokens lie in a bad page
+};
+template <bool FP8, int D> struct Shared {
+    uint4 k[2][4][D / 32][64];         // [buffer][16 tokens][contraction step][lane]
+    uint2 v[2][2][D / 16][2][64];      // [buffer][32 tokens][output tile][half][lane]
+    float ks[2][kTile], vs[2][kTile];
+    int flags[2][4];                   // per 16 tokens: bits 0-15 odd tokens, 16 bad page
+};
+
+// The page number of this wave's 16 tokens of the tile at token t0; those
+// behind the end take the last token's page, and are not used.
+__device__ __forceinline__ int stage_page(const AttnArgs &a, int r, int t0, int end, int wave) {
+    return a.c.table[(int64_t)r * a.c.max_pages + (min(t0 + 16 * wave, end - 1) >> a.c.shift)];
+}
+
+// Loads this wave's 16 tokens of the tile at token t0 (rows [t0, end) exist).
+template <bool FP8, int D>
+__device__ __forceinline__ void stage_load(const AttnArgs &a, int page, int h, int t0, int end, int wave,
+                                           int lane, Stage<FP8, D> &s) {
+    typedef Tile<FP8, D> TT;
+    const int c = lane & 15, g = lane >> 4;
+    const int tt = t0 + 16 * wave < end ? t0 + 16 * wave : (end - 1) & ~15;
+    s.flags = 0;
+    if ((unsigned)page >= (unsigned)a.c.num_pages) {
+        s.flags = 1 << 16;
+        page = 0;
+    }
+    const int64_t row = ((int64_t)page * a.c.heads + h) * a.c.size + (tt & (a.c.size - 1));
+    const char *kp = (const char *)a.c.k + (row + c) * (D * TT::EB) + g * 16;
+#pragma unroll
+    for (int i = 0; i < TT::KV; ++i) s.k[i] = *(const uint4 *)(kp + i * 64);
+    const char *vp = (const char *)a.c.v + (row + 4 * g) * (D * TT::EB) + c * (TT::VW * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_words(vp + i * (D * TT::EB), s.v[i]);
+    if constexpr (FP8) s.sc = (lane & 16 ? a.c.v_scale : a.c.k_scale)[row + c];
+}
+
+// Writes them to buffer b.  `part`: the tile holds tokens that some row does
+// not see (or that do not exist, from `end` on): values of V that a weight of
+// 0 would not cancel leave the tile and are marked.
+template <bool FP8, int D>
+__device__ __forceinline__ void stage_store(const AttnArgs &a, Shared<FP8, D> &sh, int b, int t0,
+                                            int end, bool part, int wave, int lane,
+                                            Stage<FP8, D> &s) {
+    typedef Tile<FP8, D> TT;
+    const int g = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < TT::KV; ++i) {
+        if constexpr (!FP8) {
+            sh.k[b][wave][i][lane] = s.k[i];
+        } else {
+            const uint4 w = s.k[i];
+            sh.k[b][wave][2 * i][lane] = make_uint4(e4m3_bf16<false>(w.x), e4m3_bf16<true>(w.x),
+                                                    e4m3_bf16<false>(w.y), e4m3_bf16<true>(w.y));
+            sh.k[b][wave][2 * i + 1][lane] = make_uint4(e4m3_bf16<false>(w.z), e4m3_bf16<true>(w.z),
+                                                        e4m3_bf16<false>(w.w), e4m3_bf16<true>(w.w));
+        }
+    }
+    uint32_t v[4][TT::DV / 2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int w = 0; w < TT::DV / 2; ++w) {
+            if constexpr (!FP8) v[i][w] = s.v[i][w];
+            else v[i][w] = w & 1 ? e4m3_bf16<true>(s.v[i][w >> 1]) : e4m3_bf16<false>(s.v[i][w >> 1]);
+        }
+    int flags = s.flags;
+    if (part) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool live = t0 + 16 * wave + 4 * g + i < end;
+            bool odd = false;
+#pragma unroll
+            for (int w = 0; w < TT::DV / 2; ++w) {
+                v[i][w] = live ? v[i][w] : 0u;
+                odd |= odd_word(v[i][w]);
+            }
+            const uint64_t bal = __ballot(odd);
+            if (bal) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (bal >> (16 * q) & 0xffffu) flags |= 1 << (4 * q + i);
+#pragma unroll
+                for (int w = 0; w < TT::DV / 2; ++w) v[i][w] = bal >> (16 * g) & 0xffffu ? 0u : v[i][w];
+            }
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < TT::DV / 2; ++w) {
+        sh.v[b][wave >> 1][2 * w][wave & 1][lane] =
+            make_uint2(__builtin_amdgcn_perm(v[1][w], v[0][w], 0x05040100),
+                       __builtin_amdgcn_perm(v[3][w], v[2][w], 0x05040100));
+        sh.v[b][wave >> 1][2 * w + 1][wave & 1][lane] =
+            make_uint2(__builtin_amdgcn_perm(v[1][w], v[0][w], 0x07060302),
+                       __builtin_amdgcn_perm(v[3][w], v[2][w], 0x07060302));
+    }
+    if constexpr (FP8) {
+        if (lane < 16) sh.ks[b][16 * wave + lane] = s.sc * a.scale2;
+        else if (lane < 32) sh.vs[b][16 * wave + (lane & 15)] = s.sc;
+    }
+    if (lane == 0) sh.flags[b][wave] = flags;
+}
+
+template <bool FP8, int D, int RT>
+__global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(AttnArgs a) {
+    typedef Tile<FP8, D> TT;
+    constexpr int KS = TT::KS, DV = TT::DV, TR = 64 * RT;
+    __shared__ Shared<FP8, D> sh;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    int grp = blockIdx.x;
+    const Place at = find_unit<TR>(a, grp);
+    if (grp < 0) {
+        if (at.parts == 0 && blockIdx.x == 0 && tid == 0) *a.n_cuts = 0;
+        return;
+    }
+    int left = border(at, grp + 1) - border(at, grp);
+    int r = at.r;
+    Req rq = request_of<TR>(a, r);
+    const Item it = item_of<TR>(a, rq, at.off);
+    int h = it.h, t = it.t, u0 = it.u;
+    while (true) {
+        const int end = tile_end<TR>(a, rq, t);
+        const int units = tile_units<TR>(a, rq, t);
+        const int u1 = min(units, u0 + left);
+        const int t0 = rq.lo + u0 * kUnit, t1 = min(end, rq.lo + u1 * kUnit);
+        const bool whole = u0 == 0 && u1 == units;
+        const int row0 = t * TR + wave * 16 * RT;  // the wave's rows
+        bf16x8_t qf[RT][KS];
+        int node[RT], pos[RT];
+#pragma unroll
+        for (int x = 0; x < RT; ++x) {
+            const int row = min(row0 + x * 16 + c, rq.rows - 1);
+            node[x] = row / a.G;
+            const size_t nd = (size_t)r * a.M + node[x];
+            pos[x] = a.positions ? a.positions[nd] : rq.ctx + node[x];
+            const uint16_t *qp = a.q + (nd * a.Hq + h * a.G + (row - node[x] * a.G)) * D;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                qf[x][ks] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(qp + q_chunk<FP8>(ks, g)));
+        }
+        f32x4_t acc[RT][DV];
+        float m[RT], l[RT];
+#pragma unroll
+        for (int x = 0; x < RT; ++x) {
+            m[x] = -INFINITY;
+            l[x] = 0.f;
+#pragma unroll
+            for (int j = 0; j < DV; ++j) acc[x][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+        const Plain plain = plain_of<RT>(a, rq, row0, pos, t1);
+        // the workgroup's: its first rows see the least of a chain; of a window nothing is said
+        const int common = a.window ? 0 : min(rq.ctx + (a.mask ? 0 : t * TR / a.G + 1), t1);
+        // a chain's wave sees nothing behind its last row's node
+        const int wend = a.mask ? t1 : min(t1, rq.ctx + (min(row0 + 16 * RT, rq.rows) - 1) / a.G + 1);
+        const bool idle = row0 >= rq.rows || !rq.ok;
+        if (rq.ok) {
+            Stage<FP8, D> st;
+            stage_load<FP8, D>(a, stage_page(a, r, t0, end, wave), h, t0, end, wave, lane, st);
+            int page = stage_page(a, r, t0 + kTile, end, wave);
+            __syncthreads();  // the last item's reads are done
+            stage_store<FP8, D>(a, sh, 0, t0, end, t0 + kTile > common, wave, lane, st);
+            __syncthreads();
+            int b = 0;
+            for (int tile = t0; tile < t1; tile += kTile, b ^= 1) {
+                const bool more = tile + kTile < t1;
+                if (more) stage_load<FP8, D>(a, page, h, tile + kTile, end, wave, lane, st);
+                page = stage_page(a, r, tile + 2 * kTile, end, wave);  // in time for the next load
+                int flags[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) flags[i] = __builtin_amdgcn_readfirstlane(sh.flags[b][i]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int tok = tile + kStep * half;
+                    if (idle || tok >= wend) break;
+                    // ---- scores
+                    f32x4_t s[RT][2];
+#pragma unroll
+                    for (int x = 0; x < RT; ++x)
+                        for (int hf = 0; hf < 2; ++hf) s[x][hf] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) {
+                            const bf16x8_t kf = __builtin_bit_cast(bf16x8_t, sh.k[b][2 * half + hf][ks][lane]);
+#pragma unroll
+                            for (int x = 0; x < RT; ++x)
+                                s[x][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[x][ks], s[x][hf], 0, 0, 0);
+                        }
+                    float4 ksc[2], vsc[2];
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            ksc[hf] = *(const float4 *)&sh.ks[b][kStep * half + 16 * hf + 4 * g];
+                            vsc[hf] = *(const float4 *)&sh.vs[b][kStep * half + 16 * hf + 4 * g];
+                        }
+                    }
+                    const int fl0 = half ? flags[2] : flags[0], fl1 = half ? flags[3] : flags[1];
+                    const bool bad = (fl0 | fl1) >> 16;
+                    const bool masked = tok < plain.lo || tok + kStep > plain.hi || bad;
+                    uint32_t seen[RT];
+                    uint4 pw[RT];
+#pragma unroll
+                    for (int x = 0; x < RT; ++x) {
+                        float p[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            p[i] = s[x][i >> 2][i & 3];
+                            if constexpr (FP8) p[i] *= (&ksc[i >> 2].x)[i & 3];
+                            else p[i] *= a.scale2;
+                        }
+                        seen[x] = 0xffu;
+                        if (masked) {
+                            const uint32_t *mrow = a.mask ? a.mask + ((size_t)r * a.M + node[x]) * a.W : nullptr;
+                            seen[x] = lane_bits(sees(a, tok, rq.ctx, rq.n, node[x], pos[x], mrow), g);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                p[i] = !(seen[x] >> i & 1u) ? -INFINITY
+                                       : (i >> 2 ? fl1 : fl0) >> 16 ? NAN : p[i];
+                        }
+                        float tm = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])),
+                                         fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
+                        tm = fmaxf(tm, __shfl_xor(tm, 16, 64));
+                        tm = fmaxf(tm, __shfl_xor(tm, 32, 64));
+                        if (__any(tm > m[x] + kLazy)) {
+                            const float mn = fmaxf(m[x], tm);
+                            const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[x] - mn);
+                            l[x] *= al;
+#pragma unroll
+                            for (int j = 0; j < DV; ++j) acc[x][j] *= al;
+                            m[x] = mn;
+                        }
+                        const float ref = m[x] == -INFINITY ? 0.f : m[x];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            p[i] = __builtin_amdgcn_exp2f(p[i] - ref);
+                            l[x] += p[i];
+                        }
+                        if constexpr (FP8) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float vv = p[i] * (&vsc[i >> 2].x)[i & 3];
+                                p[i] = !masked || (seen[x] >> i & 1u) ? vv : 0.f;
+                            }
+                        }
+                        pw[x] = make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]),
+                                           pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+                    }
+                    // ---- tokens whose V rows left the tile, one by one
+                    const uint32_t odd = (fl0 & 0xffff) | (uint32_t)(fl1 & 0xffff) << 16;
+                    if (odd) {
+#pragma unroll 1
+                        for (int q = 0; q < 32; ++q) {
+                            if (!(odd >> q & 1u)) continue;
+                            const int tg = q >> 2 & 3, ti = (q & 3) | (q >> 2 & 4);
+                            const Half x16 = halves_of(a, numbers_of(a, r, tok + (q & 16), end), h, tok + (q & 16), end);
+                            const int64_t row = x16.row[0] + (q & 15);
+#pragma unroll
+                            for (int x = 0; x < RT; ++x) {
+                                const uint32_t lo = ti & 4 ? (ti & 2 ? pw[x].w : pw[x].z)
+                                                           : (ti & 2 ? pw[x].y : pw[x].x);
+                                const float mine = ti & 1 ? bf16_hi(lo) : bf16_lo(lo);
+                                const float pv = __shfl(mine, tg * 16 + c, 64);
+                                const bool see = __shfl((int)seen[x], tg * 16 + c, 64) >> ti & 1;
+#pragma unroll
+                                for (int j = 0; j < DV; ++j)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const int64_t e = row * D + DV * (4 * g + i) + j;
+                                        float val;
+                                        if constexpr (FP8) val = bf16_lo(e4m3_bf16<false>(((const uint8_t *)a.c.v)[e]));
+                                        else val = bf16_lo(((const uint16_t *)a.c.v)[e]);
+                                        if (see) acc[x][j][i] += pv * val;
+                                    }
+                            }
+                        }
+                    }
+                    // ---- product
+#pragma unroll
+                    for (int j = 0; j < DV; ++j) {
+                        const uint2 lo = sh.v[b][half][j][0][lane], hi = sh.v[b][half][j][1][lane];
+                        const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, make_uint4(lo.x, lo.y, hi.x, hi.y));
+#pragma unroll
+                        for (int x = 0; x < RT; ++x)
+                            acc[x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                vf, __builtin_bit_cast(bf16x8_t, pw[x]), acc[x][j], 0, 0, 0);
+                    }
+                    if (bad && lane == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+                }
+                if (more)
+                    stage_store<FP8, D>(a, sh, b ^ 1, tile + kTile, end, tile + 2 * kTile > common, wave, lane, st);
+                __syncthreads();
+            }
+        }
+        // ---- the wave's rows
+#pragma unroll
+        for (int x = 0; x < RT; ++x) {
+            l[x] += __shfl_xor(l[x], 16, 64);
+            l[x] += __shfl_xor(l[x], 32, 64);
+            const int lr = wave * 16 * RT + x * 16 + c, row = t * TR + lr;
+            if (row >= rq.rows) continue;
+            const bool fault = !rq.ok || pos[x] < rq.ctx;
+            if (fault) {
+                l[x] = NAN;
+                if (g == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+            }
+            if (whole) {
+                const size_t orow = ((size_t)r * a.M + node[x]) * a.Hq + h * a.G + (row - node[x] * a.G);
+                if (l[x] == 0.f) {  // nothing seen: o is 0
+                    l[x] = 1.f;
+                    m[x] = -INFINITY;
+                }
+                const float inv = 1.f / l[x];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint16_t *op = a.out + orow * D + DV * (4 * g + i);
+#pragma unroll
+                    for (int j = 0; j < DV; j += 4)
+                        *(uint2 *)(op + j) = make_uint2(pack_bf16(acc[x][j][i] * inv, acc[x][j + 1][i] * inv),
+                                                        pack_bf16(acc[x][j + 2][i] * inv, acc[x][j + 3][i] * inv));
+                }
+                if (g == 0 && a.lse) a.lse[orow] = (m[x] + log2f(l[x])) * (float)kLn2;
+            } else {
+                float *pp = a.part + (size_t)(2 * grp + (u0 == 0)) * a.part_stride;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float *po = pp + (size_t)lr * D + DV * (4 * g + i);
+#pragma unroll
+                    for (int j = 0; j < DV; j += 4)
+                        *(float4 *)(po + j) = make_float4(acc[x][j][i], acc[x][j + 1][i], acc[x][j + 2][i], acc[x][j + 3][i]);
+                }
+                if (g == 0) {
+                    pp[TR * D + lr] = m[x];
+                    pp[TR * D + TR + lr] = l[x];
+                }
+            }
+        }
+        // ---- the next item
+        left -= u1 - u0;
+        if (left <= 0) {
+            if (tid == 0) write_cut<TR>(a, at, grp, u0 == 0 && !whole, r, rq, h, t, units - u1);
+            return;
+        }
         u0 = 0;
         if (++t >= rq.tiles) {
             t = 0;
@@ -648,107 +1084,127 @@ __device__ __forceinline__ void load_part(const float *p, float (&x)[E]) {
     VecLoad<float, E>::run(p, 0, x);
 }
 
-// Joins the parts of the item that the border between groups b - 1 and b cuts
-// first (workgroup x = b - 1), in token order; one wave per row, its lanes
-// D / 64 values each.
-template <int D, int TR>
+// Joins the parts of the item that range blockIdx.x began and did not finish,
+// in token order; a wave's lanes take D / 64 values each of one row.  The
+// parts come from other XCDs' memory, a long way off: one load for the cut,
+// then every load of up to kJoinParts parts at once.  SPLIT: the four waves
+// divide one row's parts (few rows cut into many parts); otherwise each takes
+// rows of its own (many rows, in two or three parts).
+constexpr int kJoinParts = 16;
+
+template <int D, int TR, bool SPLIT>
 __global__ void __launch_bounds__(kBlock) attn_join_kernel(AttnArgs a) {
     constexpr int E = D / 64;
-    int b = blockIdx.x + 1;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Place at = find_unit<TR, false>(a, b);
-    if (b < 0) return;
-    const Req rq = request_of<TR>(a, at.r);
-    const Item it = item_of<TR>(a, rq, at.off);
-    const int64_t first = border(at, b) - it.u, last = first + it.units;  // the item's units
-    if (it.u == 0 || border(at, b - 1) > first) return;  // not cut, or cut by an earlier border
-    int e = b;                                           // the last range with units of the item
-    while (e + 1 < at.parts && border(at, e + 1) < last) ++e;
-    const int h = it.h, t = it.t;
-    const int lr = blockIdx.y * kWaves + wave, row = t * TR + lr;
-    if (row >= rq.rows) return;
-    const int f = b - 1, n = e - f + 1;
+    __shared__ float o_s[kWaves][D], m_s[kWaves], l_s[kWaves];
+    const int f = blockIdx.x, n_cuts = *a.n_cuts;
+    const Cut cut = a.cuts[f];
+    if (f >= n_cuts || cut.rows == 0) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lr = SPLIT ? blockIdx.y : blockIdx.y * kWaves + wave;
+    if (lr >= cut.rows) return;
+    const int n = cut.parts;
     auto slot = [&](int i) -> const float * {
         return a.part + (size_t)(2 * (f + i) + (i == 0)) * a.part_stride;
     };
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 64) M = fmaxf(M, slot(i)[TR * D + lr]);
-    M = wave_max(M);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float sum = 0.f, o[E];
+    float m = -INFINITY, sum = 0.f, o[E];
     for (int q = 0; q < E; ++q) o[q] = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 64) {
-        float w = 0.f, l = 0.f;
-        if (i0 + lane < n) {
-            const float *p = slot(i0 + lane);
-            w = __builtin_amdgcn_exp2f(p[TR * D + lr] - ref);
-            l = p[TR * D + TR + lr];
-        }
-        sum += wave_sum_f(w * l);
-        const int cnt = min(64, n - i0);
-        for (int i = 0; i < cnt; i += 8) {  // eight loads in flight
-            float x[8][E];
+    for (int i0 = SPLIT ? wave * kJoinParts : 0; i0 < n; i0 += SPLIT ? kBlock / 64 * kJoinParts : kJoinParts) {
+        const int cnt = min(kJoinParts, n - i0);
+        const float *p = slot(min(i0 + lane, n - 1)) + TR * D + lr;
+        const float mi = lane < cnt ? p[0] : -INFINITY, li = lane < cnt ? p[TR] : 0.f;
+        float x[kJoinParts][E];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                load_part(slot(i0 + min(i + k, cnt - 1)) + (size_t)lr * D + lane * E, x[k]);
+        for (int k = 0; k < kJoinParts; ++k)
+            if (k < cnt) load_part(slot(i0 + k) + (size_t)lr * D + lane * E, x[k]);
+        const float top = fmaxf(wave_max(mi), m);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float w = __builtin_amdgcn_exp2f(mi - ref), back = __builtin_amdgcn_exp2f(m - ref);
+        sum = sum * back + wave_sum_f(w * li);
+        for (int q = 0; q < E; ++q) o[q] *= back;
+        m = top;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float wi = i + k < cnt ? readlane_f(w, i + k) : 0.f;
-                if (i + k < cnt) {
+        for (int k = 0; k < kJoinParts; ++k)
+            if (k < cnt) {
+                const float wk = readlane_f(w, k);
 #pragma unroll
-                    for (int q = 0; q < E; ++q) o[q] += wi * x[k][q];
-                }
+                for (int q = 0; q < E; ++q) o[q] += wk * x[k][q];
             }
+    }
+    if constexpr (SPLIT) {
+        for (int q = 0; q < E; ++q) o_s[wave][lane * E + q] = o[q];
+        if (lane == 0) {
+            m_s[wave] = m;
+            l_s[wave] = sum;
+        }
+        __syncthreads();
+        if (wave) return;
+        m = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
+        const float ref = m == -INFINITY ? 0.f : m;
+        sum = 0.f;
+        for (int q = 0; q < E; ++q) o[q] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float wk = __builtin_amdgcn_exp2f(m_s[w] - ref);
+            sum += wk * l_s[w];
+            for (int q = 0; q < E; ++q) o[q] += wk * o_s[w][lane * E + q];
         }
     }
-    const int nd = row / a.G;
-    const size_t node = (size_t)at.r * a.M + nd;
-    const size_t orow = node * a.Hq + h * a.G + (row - nd * a.G);
+    const int row = cut.row0 + lr, nd = row / a.G;
+    const size_t orow = (size_t)(cut.node0 + nd) * a.Hq + cut.h * a.G + (row - nd * a.G);
     if (sum == 0.f) {  // nothing seen: o is 0
         sum = 1.f;
-        M = -INFINITY;
+        m = -INFINITY;
     }
     const float inv = 1.f / sum;
     uint16_t *op = a.out + orow * D + lane * E;
     if constexpr (E == 1) op[0] = (uint16_t)pack_bf16(o[0] * inv, 0.f);
     else if constexpr (E == 2) *(uint32_t *)op = pack_bf16(o[0] * inv, o[1] * inv);
     else *(uint2 *)op = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-    if (lane == 0) {
-        if (a.lse) a.lse[orow] = (M + log2f(sum)) * (float)kLn2;
-        if (a.positions && a.positions[node] < rq.ctx)
-            atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
-    }
+    if (lane == 0 && a.lse) a.lse[orow] = (m + log2f(sum)) * (float)kLn2;
 }
 
-// Row tiles of 16, 32 or 64 rows: the smallest that takes all rows of the
-// largest request; 32 at D = 256, whose accumulators fill the registers.
-inline int row_tiles(int64_t rows, int D) {
-    return rows <= 16 ? 1 : rows <= 32 || D == 256 ? 2 : 4;
+// Which launch a call takes and its row tile.  A request's largest count of
+// rows per key head decides: up to 32 the waves of a workgroup divide the
+// tokens and keep everything in registers; more rows divide the waves.
+struct Shape {
+    bool wide;
+    int RT, TR, groups;
+};
+inline Shape shape_of(int64_t rows, int D) {
+    Shape s;
+    s.wide = rows > 32;
+    if (!s.wide) s.RT = rows <= 16 ? 1 : 2;
+    else s.RT = D == 256 || rows <= 64 ? 1 : 2;
+    s.TR = 16 * s.RT * (s.wide ? kWaves : 1);
+    s.groups = D <= 128 ? kMaxGroups : kMaxGroups / 2;
+    return s;
 }
-inline int groups_of(int RT, int D) { return D * RT <= 128 ? kMaxGroups : kMaxGroups / 2; }
 
-template <bool FP8, int D, int RT>
-static void launch_attn(AttnArgs a, hipStream_t st) {
-    a.groups = groups_of(RT, D);
-    a.part_stride = 16 * RT * (D + 2);
-    hipLaunchKernelGGL((attn_kernel<FP8, D, RT>), dim3(a.groups), dim3(kBlock), 0, st, a);
-    hipLaunchKernelGGL((attn_join_kernel<D, 16 * RT>), dim3(a.groups - 1, 16 * RT / kWaves),
+template <bool FP8, int D, int RT, bool WIDE>
+static void launch_attn(const AttnArgs &a, hipStream_t st) {
+    constexpr int TR = 16 * RT * (WIDE ? kWaves : 1);
+    if constexpr (WIDE)
+        hipLaunchKernelGGL((attn_wide_kernel<FP8, D, RT>), dim3(a.groups), dim3(kBlock), 0, st, a);
+    else
+        hipLaunchKernelGGL((attn_kernel<FP8, D, RT>), dim3(a.groups), dim3(kBlock), 0, st, a);
+    hipLaunchKernelGGL((attn_join_kernel<D, TR, !WIDE>), dim3(a.groups - 1, WIDE ? TR / kWaves : TR),
                        dim3(kBlock), 0, st, a);
 }
-template <bool FP8>
-static void launch_attn(const AttnArgs &a, int D, int RT, hipStream_t st) {
-    if (D == 64) {
-        if (RT == 1) launch_attn<FP8, 64, 1>(a, st);
-        else if (RT == 2) launch_attn<FP8, 64, 2>(a, st);
-        else launch_attn<FP8, 64, 4>(a, st);
-    } else if (D == 128) {
-        if (RT == 1) launch_attn<FP8, 128, 1>(a, st);
-        else if (RT == 2) launch_attn<FP8, 128, 2>(a, st);
-        else launch_attn<FP8, 128, 4>(a, st);
+template <bool FP8, int D>
+static void launch_attn(const AttnArgs &a, const Shape &s, hipStream_t st) {
+    if (s.wide) {
+        if (s.RT == 1) launch_attn<FP8, D, 1, true>(a, st);
+        else if constexpr (D <= 128) launch_attn<FP8, D, 2, true>(a, st);
     } else {
-        if (RT == 1) launch_attn<FP8, 256, 1>(a, st);
-        else launch_attn<FP8, 256, 2>(a, st);
+        if (s.RT == 1) launch_attn<FP8, D, 1, false>(a, st);
+        else launch_attn<FP8, D, 2, false>(a, st);
     }
+}
+template <bool FP8>
+static void launch_attn(const AttnArgs &a, int D, const Shape &s, hipStream_t st) {
+    if (D == 64) launch_attn<FP8, 64>(a, s, st);
+    else if (D == 128) launch_attn<FP8, 128>(a, s, st);
+    else launch_attn<FP8, 256>(a, s, st);
 }
 
 }  // namespace sv
@@ -761,8 +1217,9 @@ size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D)
     if (R < 0 || M < 1 || M > SPEC_TREE_MAX_NODES || Hkv < 1 || Hq < 1 || Hq % Hkv ||
         Hq / Hkv > 64 || (D != 64 && D != 128 && D != 256))
         return 0;
-    const int RT = row_tiles((int64_t)M * (Hq / Hkv), D);
-    return sizeof(Control) + (size_t)2 * groups_of(RT, D) * 16 * RT * (D + 2) * sizeof(float);
+    const Shape s = shape_of((int64_t)M * (Hq / Hkv), D);
+    return sizeof(Control) + sizeof(Cut) * (kMaxGroups + 1) +
+           (size_t)2 * s.groups * s.TR * (D + 2) * sizeof(float);
 }
 
 int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const void *v_cache,
@@ -802,10 +1259,18 @@ int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const v
     a.out = (uint16_t *)out;
     a.lse = out_lse;
     a.ctl = (Control *)workspace;
-    a.part = (float *)((char *)workspace + sizeof(Control));
-    const int RT = row_tiles((int64_t)M * a.G, D);
-    if (cache_dtype == SPEC_E4M3) launch_attn<true>(a, D, RT, (hipStream_t)stream);
-    else launch_attn<false>(a, D, RT, (hipStream_t)stream);
+    a.cuts = (Cut *)((char *)workspace + sizeof(Control));
+    a.n_cuts = (int *)(a.cuts + kMaxGroups);
+    a.part = (float *)(a.cuts + kMaxGroups + 1);
+    const Shape s = shape_of((int64_t)M * a.G, D);
+    a.groups = s.groups;
+    a.part_stride = s.TR * (D + 2);
+    // the batch's units must count in 31 bits
+    const int64_t tiles = ((int64_t)M * a.G + s.TR - 1) / s.TR;
+    const int64_t units = (((int64_t)max_pages << a.c.shift) + kUnit - 1) / kUnit + 1;
+    if ((double)R * Hkv * (double)tiles * (double)units >= 2147483647.0) return SPEC_EUNSUPPORTED;
+    if (cache_dtype == SPEC_E4M3) launch_attn<true>(a, D, s, (hipStream_t)stream);
+    else launch_attn<false>(a, D, s, (hipStream_t)stream);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
 }
 
