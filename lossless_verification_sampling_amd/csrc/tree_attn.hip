@@ -36,6 +36,10 @@ struct Cut;
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+// (vector types of the language, not the runtime's structs: arrays of those
+// end up in scratch memory)
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kStep = 32;              // tokens a wave takes at a time
 constexpr int kUnit = kStep * kWaves;  // tokens of one unit of work
@@ -48,7 +52,8 @@ struct AttnArgs {
     const int32_t *ctx_len, *n_nodes;
     const uint32_t *mask;        // [R][M][W], null: chain
     const int32_t *positions;    // [R][M], null: ctx + v
-    float scale2;                // scale * log2(e)
+    float scale2;                // |scale| * log2(e), above 0
+    uint32_t flip;               // sign bits for q where scale is negative
     int window, R, M, W, Hq, G;
     uint16_t *out;
     float *lse;
@@ -217,15 +222,22 @@ __device__ __forceinline__ void write_cut(const AttnArgs &a, const Place &p, int
 // one wave's step
 // ---------------------------------------------------------------------------
 
+// v, opaque to the compiler: what is derived from it stays where it is used
+// instead of being computed ahead of the token loop, whose registers are short.
+__device__ __forceinline__ int here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 template <bool FP8, int D> struct Tile {
     static constexpr int KS = D / 32;              // contraction steps of Q K^T
     static constexpr int DV = D / 16;              // values of V a lane holds per token
     static constexpr int EB = FP8 ? 1 : 2;
     static constexpr int KV = D * EB / 64;         // 16-byte K loads per 16 tokens
     static constexpr int VW = DV * EB / 4;         // 32-bit words of V per token
-    uint4 k[2][KV];
+    u32x4_t k[2][KV];
     uint32_t v[8][VW];
-    float4 ks[2], vs[2];                           // scales (FP8)
+    float sc;                                      // scales (FP8), see load_scale
 };
 
 // N consecutive 32-bit words (N a multiple of 4, or 1 or 2: aligned to them).
@@ -234,13 +246,13 @@ __device__ __forceinline__ void load_words(const char *p, uint32_t (&w)[N]) {
     if constexpr (N == 1) {
         w[0] = *(const uint32_t *)p;
     } else if constexpr (N == 2) {
-        const uint2 x = *(const uint2 *)p;
+        const u32x2_t x = *(const u32x2_t *)p;
         w[0] = x.x;
         w[1] = x.y;
     } else {
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
-            const uint4 x = *(const uint4 *)(p + 4 * i);
+            const u32x4_t x = *(const u32x4_t *)(p + 4 * i);
             w[i] = x.x;
             w[i + 1] = x.y;
             w[i + 2] = x.z;
@@ -255,6 +267,13 @@ struct Half {
     int bad;                     // bit h: half h lies in a bad page
 };
 
+// A page number, by a scalar load (the index is the wave's, and nothing in a
+// launch writes the table).
+__device__ __forceinline__ int page_number(const AttnArgs &a, int r, int index) {
+    typedef const __attribute__((address_space(4))) int32_t *table_t;
+    return ((table_t)(uintptr_t)(a.c.table + (int64_t)r * a.c.max_pages))[index];
+}
+
 // The page numbers of a step's halves, one load ahead of their use: a wave
 // that waited for them before it could ask for the rows stood still for a
 // memory round trip each step.
@@ -263,10 +282,9 @@ struct Numbers {
 };
 __device__ __forceinline__ Numbers numbers_of(const AttnArgs &a, int r, int t, int L) {
     Numbers x;
-    const int32_t *row = a.c.table + (int64_t)r * a.c.max_pages;
     t = min(t, L - 1);                                  // a step behind the end is not used
-    x.page[0] = row[t >> a.c.shift];
-    x.page[1] = row[min(t + 16, L - 1) >> a.c.shift];
+    x.page[0] = page_number(a, r, t >> a.c.shift);
+    x.page[1] = page_number(a, r, min(t + 16, L - 1) >> a.c.shift);
     return x;
 }
 __device__ __forceinline__ Half halves_of(const AttnArgs &a, const Numbers &num, int h, int t, int L) {
@@ -287,26 +305,36 @@ __device__ __forceinline__ Half halves_of(const AttnArgs &a, const Numbers &num,
 
 template <bool FP8, int D>
 __device__ __forceinline__ void load_k(const AttnArgs &a, const Half &x, int lane, Tile<FP8, D> &t) {
-    const int c = lane & 15, g = lane >> 4;
+    const int hl = here(lane), c = hl & 15, g = hl >> 4;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const char *p = (const char *)a.c.k + (x.row[s] + c) * (D * Tile<FP8, D>::EB) + g * 16;
+        // a wave's base, and a lane's 32-bit offset
+        const char *p = (const char *)a.c.k + x.row[s] * (D * Tile<FP8, D>::EB);
+        const uint32_t lane_at = c * (D * Tile<FP8, D>::EB) + g * 16;
 #pragma unroll
-        for (int i = 0; i < Tile<FP8, D>::KV; ++i) t.k[s][i] = *(const uint4 *)(p + i * 64);
-        if constexpr (FP8) t.ks[s] = *(const float4 *)(a.c.k_scale + x.row[s] + 4 * g);
+        for (int i = 0; i < Tile<FP8, D>::KV; ++i) t.k[s][i] = *(const u32x4_t *)(p + lane_at + i * 64);
     }
 }
 template <bool FP8, int D>
 __device__ __forceinline__ void load_v(const AttnArgs &a, const Half &x, int lane, Tile<FP8, D> &t) {
     typedef Tile<FP8, D> TT;
-    const int c = lane & 15, g = lane >> 4;
+    const int hl = here(lane), c = hl & 15, g = hl >> 4;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const char *p = (const char *)a.c.v + (x.row[s] + 4 * g) * (D * TT::EB) + c * (TT::VW * 4);
+        const char *p = (const char *)a.c.v + x.row[s] * (D * TT::EB);
+        const uint32_t lane_at = g * (4 * D * TT::EB) + c * (TT::VW * 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_words(p + i * (D * TT::EB), t.v[4 * s + i]);
-        if constexpr (FP8) t.vs[s] = *(const float4 *)(a.c.v_scale + x.row[s] + 4 * g);
+        for (int i = 0; i < 4; ++i) load_words(p + lane_at + i * (D * TT::EB), t.v[4 * s + i]);
     }
+}
+
+// A step's 64 scales, one a lane: lane group g holds those of its own tokens,
+// K's of its eight in lanes 0-7 and V's in lanes 8-15, for row_times to take by row broadcasts.
+__device__ __forceinline__ float load_scale(const AttnArgs &a, const Half &x, int lane) {
+    const int hl = here(lane), c = hl & 15, g = hl >> 4;
+    const float *k = a.c.k_scale + x.row[0], *v = a.c.v_scale + x.row[0];
+    const int64_t at = (c & 4 ? x.row[1] - x.row[0] : 0) + 4 * g + (c & 3);
+    return (c & 8 ? v : k)[at];
 }
 
 // The A operand of contraction step ks of the 16 tokens of half s.
@@ -315,10 +343,10 @@ __device__ __forceinline__ bf16x8_t k_frag(const Tile<FP8, D> &t, int s, int ks)
     if constexpr (!FP8) {
         return __builtin_bit_cast(bf16x8_t, t.k[s][ks]);
     } else {
-        const uint4 w = t.k[s][ks >> 1];
+        const u32x4_t w = t.k[s][ks >> 1];
         const uint32_t x = ks & 1 ? w.z : w.x, y = ks & 1 ? w.w : w.y;
-        return __builtin_bit_cast(bf16x8_t, make_uint4(e4m3_bf16<false>(x), e4m3_bf16<true>(x),
-                                                       e4m3_bf16<false>(y), e4m3_bf16<true>(y)));
+        return __builtin_bit_cast(bf16x8_t, u32x4_t{e4m3_bf16<false>(x), e4m3_bf16<true>(x),
+                                                       e4m3_bf16<false>(y), e4m3_bf16<true>(y)});
     }
 }
 // First of the 8 values of q that lane group g pairs with it.
@@ -333,22 +361,29 @@ __device__ __forceinline__ uint32_t v_word(const Tile<FP8, D> &t, int tok, int w
     else return w & 1 ? e4m3_bf16<true>(t.v[tok][w >> 1]) : e4m3_bf16<false>(t.v[tok][w >> 1]);
 }
 
-__device__ __forceinline__ bool odd_word(uint32_t w) {  // a NaN or an infinity in it
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// Whether a raw word of V holds a NaN or an infinity (e4m3: a NaN, seven ones).
+template <bool FP8>
+__device__ __forceinline__ bool odd_word(uint32_t w) {
+    if constexpr (!FP8) return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+    const uint32_t y = ~w & 0x7f7f7f7fu;  // a byte of zeros
+    return (y - 0x01010101u) & ~y & 0x80808080u;
 }
 
 // The low k bits, k clamped to 0 .. 32.
 __device__ __forceinline__ uint32_t ones(int k) {
     return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u;
 }
-// Tokens tok .. tok + 31 that the row of node v (position pos, mask row mrow)
+// Tokens tok .. tok + 31 that the row of node v (position pos) of request r
 // sees, one bit each.
-__device__ __forceinline__ uint32_t sees(const AttnArgs &a, int tok, int ctx, int n, int v, int pos,
-                                         const uint32_t *mrow) {
+__device__ __forceinline__ uint32_t sees(const AttnArgs &a, int r, int tok, int ctx, int n, int v,
+                                         int pos) {
+    v = here(v);
+    pos = here(pos);
     const int k = ctx - tok;  // tokens of the context
     const uint32_t old = ones(k);
     uint32_t tree;
-    if (mrow) {
+    if (a.mask) {
+        const uint32_t *mrow = a.mask + ((size_t)r * a.M + v) * a.W;
         const int w = -k >> 5, sh = -k & 31;  // tree slot -k at bit 0
         const uint32_t lo = w >= 0 && w < a.W ? mrow[w] : 0u;
         const uint32_t hi = w >= -1 && w + 1 < a.W ? mrow[w + 1] : 0u;
@@ -363,6 +398,117 @@ __device__ __forceinline__ uint32_t sees(const AttnArgs &a, int tok, int ctx, in
 // Bit i: token i of this lane group's eight.
 __device__ __forceinline__ uint32_t lane_bits(uint32_t seen, int g) {
     return (seen >> (4 * g) & 15u) | (seen >> (4 * g + 16) & 15u) << 4;
+}
+
+// Maximum (NaN if one is) of a lane's eight scores, and over the four lanes
+// that share a column; the latter's sum.
+__device__ __forceinline__ float max2(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+__device__ __forceinline__ float max8(const float (&p)[8]) {
+    return max2(max2(max2(p[0], p[1]), max2(p[2], p[3])), max2(max2(p[4], p[5]), max2(p[6], p[7])));
+}
+__device__ __forceinline__ float column_max(float v) {
+    uint32_t lo, hi;
+    lane_pair<16>(__float_as_uint(v), lo, hi);
+    v = max2(__uint_as_float(lo), __uint_as_float(hi));
+    lane_pair<32>(__float_as_uint(v), lo, hi);
+    return max2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ float column_sum(float v) {
+    uint32_t lo, hi;
+    lane_pair<16>(__float_as_uint(v), lo, hi);
+    v = __uint_as_float(lo) + __uint_as_float(hi);
+    lane_pair<32>(__float_as_uint(v), lo, hi);
+    return __uint_as_float(lo) + __uint_as_float(hi);
+}
+
+// p[i] times the value that lane FIRST + i of the lane group holds (the
+// broadcast is an operand modifier of the multiply).
+template <int N>
+__device__ __forceinline__ float row_lane(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x150 + N, 0xf, 0xf, true));
+}
+template <int FIRST>
+__device__ __forceinline__ void row_times(float (&p)[8], float v) {
+    p[0] *= row_lane<FIRST>(v);
+    p[1] *= row_lane<FIRST + 1>(v);
+    p[2] *= row_lane<FIRST + 2>(v);
+    p[3] *= row_lane<FIRST + 3>(v);
+    p[4] *= row_lane<FIRST + 4>(v);
+    p[5] *= row_lane<FIRST + 5>(v);
+    p[6] *= row_lane<FIRST + 6>(v);
+    p[7] *= row_lane<FIRST + 7>(v);
+}
+
+// The running softmax's step for one row: scores s of the lane's eight tokens
+// become weights (bf16, 2^-8 relative like the output's own rounding; V's
+// scale goes in first), and m, l and acc follow.  The maximum may lag by
+// kLazy: weights then reach 2^kLazy, which costs no precision, and most steps
+// rescale nothing.  seen: bit i, the row sees token i; bad: bit h, tokens
+// 4 h .. 4 h + 3 lie in a bad page (both only where masked).
+template <bool FP8, int DV>
+__device__ __forceinline__ u32x4_t weigh(const f32x4_t (&s)[2], float sc, float scale2,
+                                         bool masked, uint32_t seen, int bad, float &m, float &l,
+                                         f32x4_t (&acc)[DV]) {
+    float p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = s[i >> 2][i & 3];
+    if constexpr (FP8) row_times<0>(p, sc * scale2);
+    if (masked) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            p[i] = !(seen >> i & 1u) ? -INFINITY : bad >> (i >> 2) & 1 ? NAN : p[i];
+    }
+    float top = column_max(max8(p));
+    if constexpr (!FP8) top *= scale2;
+    if (__any(top > m + kLazy)) {
+        const float mn = max2(m, top);
+        const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+        l *= al;
+#pragma unroll
+        for (int j = 0; j < DV; ++j) acc[j] *= al;
+        m = mn;
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(FP8 ? p[i] - ref : fmaf(p[i], scale2, -ref));
+        l += p[i];
+    }
+    if constexpr (FP8) {
+        row_times<8>(p, sc);
+        if (masked) {  // a scale of an unseen row may be anything
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = seen >> i & 1u ? p[i] : 0.f;
+        }
+    }
+    return u32x4_t{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
+                   pack_bf16(p[6], p[7])};
+}
+
+// Adds token `row` of V (weights pw of the lane group tg's token ti) where it
+// is seen: the way of tokens whose row holds a NaN or an infinity, which a
+// weight of 0 would not cancel in the product.
+template <bool FP8, int D>
+__device__ __forceinline__ void add_token(const AttnArgs &a, int64_t row, int tg, int ti, int lane,
+                                          u32x4_t pw, uint32_t seen, f32x4_t (&acc)[D / 16]) {
+    constexpr int DV = D / 16;
+    lane = here(lane);
+    const int c = lane & 15, g = lane >> 4;
+    const uint32_t w = ti & 4 ? (ti & 2 ? pw[3] : pw[2]) : (ti & 2 ? pw[1] : pw[0]);
+    const float pv = __shfl(ti & 1 ? bf16_hi(w) : bf16_lo(w), tg * 16 + c, 64);
+    const bool see = __shfl((int)seen, tg * 16 + c, 64) >> ti & 1;
+#pragma unroll
+    for (int j = 0; j < DV; ++j) {
+        __builtin_amdgcn_sched_barrier(0);  // few loads in flight: registers are short here
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t e = row * D + DV * (4 * g + i) + j;
+            float val;
+            if constexpr (FP8) val = bf16_lo(e4m3_bf16<false>(((const uint8_t *)a.c.v)[e]));
+            else val = bf16_lo(((const uint16_t *)a.c.v)[e]);
+            if (see) acc[j][i] += pv * val;
+        }
+    }
 }
 
 // Tokens that every row of a wave sees: steps inside need no mask.
@@ -435,9 +581,10 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
             pos[x] = a.positions ? a.positions[nd] : rq.ctx + node[x];
             rowbad[x] = !rq.ok || pos[x] < rq.ctx;
             const uint16_t *qp = a.q + (nd * a.Hq + h * a.G + (row - node[x] * a.G)) * D;
+            const int qg = here(g);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
-                qf[x][ks] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(qp + q_chunk<FP8>(ks, g)));
+                qf[x][ks] = __builtin_bit_cast(bf16x8_t, *(const u32x4_t *)(qp + q_chunk<FP8>(ks, qg)) ^ a.flip);
         }
         f32x4_t acc[RT][DV];
         float m[RT], l[RT];
@@ -455,6 +602,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
             Half cur = halves_of(a, numbers_of(a, r, tok, end), h, tok, end);
             Numbers num = numbers_of(a, r, tok + kUnit, end);
             load_k<FP8, D>(a, cur, lane, kv);
+            if constexpr (FP8) kv.sc = load_scale(a, cur, lane);
             load_v<FP8, D>(a, cur, lane, kv);
             while (true) {
                 const int nxt = tok + kUnit;
@@ -477,69 +625,22 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                             s[x][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[x][ks], s[x][hf], 0, 0, 0);
                     }
                 }
-                float ksc[8], vsc[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ksc[i] = a.scale2;
-                    vsc[i] = 1.f;
+                const float sc = FP8 ? kv.sc : 0.f;
+                if (more) {
+                    load_k<FP8, D>(a, nh, lane, kv);
+                    if constexpr (FP8) kv.sc = load_scale(a, nh, lane);
                 }
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        ksc[4 * hf] *= kv.ks[hf].x;
-                        ksc[4 * hf + 1] *= kv.ks[hf].y;
-                        ksc[4 * hf + 2] *= kv.ks[hf].z;
-                        ksc[4 * hf + 3] *= kv.ks[hf].w;
-                        vsc[4 * hf] = kv.vs[hf].x;
-                        vsc[4 * hf + 1] = kv.vs[hf].y;
-                        vsc[4 * hf + 2] = kv.vs[hf].z;
-                        vsc[4 * hf + 3] = kv.vs[hf].w;
-                    }
-                }
-                if (more) load_k<FP8, D>(a, nh, lane, kv);
                 __builtin_amdgcn_sched_barrier(0);
                 const bool masked = tok < plain.lo || tok + kStep > plain.hi || cur.bad;
-                uint32_t seen[RT];  // bit i: this lane's token i is seen by its row
-                uint4 pw[RT];
+                uint32_t seen[RT];  // bit i: the row sees this lane's token i
+                u32x4_t pw[RT];
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
-                    float p[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) p[i] = s[x][i >> 2][i & 3] * ksc[i];
                     seen[x] = 0xffu;
                     if (masked) {
-                        const uint32_t *mrow = a.mask ? a.mask + ((size_t)r * a.M + node[x]) * a.W : nullptr;
-                        seen[x] = lane_bits(sees(a, tok, rq.ctx, rq.n, node[x], pos[x], mrow), g);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            p[i] = !(seen[x] >> i & 1u) ? -INFINITY : cur.bad >> (i >> 2) & 1 ? NAN : p[i];
+                        seen[x] = lane_bits(sees(a, r, tok, rq.ctx, rq.n, node[x], pos[x]), g);
                     }
-                    float tm = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])),
-                                     fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
-                    tm = fmaxf(tm, __shfl_xor(tm, 16, 64));
-                    tm = fmaxf(tm, __shfl_xor(tm, 32, 64));
-                    if (__any(tm > m[x] + kLazy)) {
-                        const float mn = fmaxf(m[x], tm);
-                        const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[x] - mn);
-                        l[x] *= al;
-#pragma unroll
-                        for (int j = 0; j < DV; ++j) acc[x][j] *= al;
-                        m[x] = mn;
-                    }
-                    const float ref = m[x] == -INFINITY ? 0.f : m[x];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        p[i] = __builtin_amdgcn_exp2f(p[i] - ref);
-                        l[x] += p[i];
-                    }
-                    if constexpr (FP8) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            p[i] = !masked || (seen[x] >> i & 1u) ? p[i] * vsc[i] : 0.f;
-                    }
-                    // weights in bf16 (2^-8 relative, as the output's own rounding)
-                    pw[x] = make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]),
-                                       pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+                    pw[x] = weigh<FP8, DV>(s[x], sc, a.scale2, masked, seen[x], cur.bad, m[x], l[x], acc[x]);
                 }
                 uint32_t odd = 0u;  // bit i: token i of this lane holds a NaN or an infinity
                 if (masked) {
@@ -550,7 +651,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                         for (int w = 0; w < TT::VW; ++w) kv.v[i][w] = live ? kv.v[i][w] : 0u;
                         bool o = false;
 #pragma unroll
-                        for (int w = 0; w < DV / 2; ++w) o |= odd_word(v_word<FP8, D>(kv, i, w));
+                        for (int w = 0; w < TT::VW; ++w) o |= odd_word<FP8>(kv.v[i][w]);
                         odd |= (uint32_t)o << i;
                     }
                 }
@@ -569,34 +670,20 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                     for (int q = 0; q < 32; ++q) {
                         const int tg = q >> 3, ti = q & 7;  // lane group and index of the token
                         if (!(__shfl((int)all, tg * 16, 64) >> ti & 1)) continue;
-                        const int64_t row = (ti & 4 ? cur.row[1] : cur.row[0]) + 4 * tg + (ti & 3);
+                        const int64_t row = cur.row[0] + (ti & 4 ? cur.row[1] - cur.row[0] : 0) + 4 * tg + (ti & 3);
 #pragma unroll
-                        for (int x = 0; x < RT; ++x) {
-                            const uint32_t lo = ti & 4 ? (ti & 2 ? pw[x].w : pw[x].z)
-                                                       : (ti & 2 ? pw[x].y : pw[x].x);
-                            const float mine = ti & 1 ? bf16_hi(lo) : bf16_lo(lo);
-                            const float pv = __shfl(mine, tg * 16 + c, 64);
-                            const bool see = __shfl((int)seen[x], tg * 16 + c, 64) >> ti & 1;
-#pragma unroll
-                            for (int j = 0; j < DV; ++j)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int64_t e = row * D + DV * (4 * g + i) + j;
-                                    float val;
-                                    if constexpr (FP8) val = bf16_lo(e4m3_bf16<false>(((const uint8_t *)a.c.v)[e]));
-                                    else val = bf16_lo(((const uint16_t *)a.c.v)[e]);
-                                    if (see) acc[x][j][i] += pv * val;
-                                }
-                        }
+                        for (int x = 0; x < RT; ++x)
+                            add_token<FP8, D>(a, row, tg, ti, lane, pw[x], seen[x], acc[x]);
                     }
                 }
                 // ---- product
 #pragma unroll
                 for (int w = 0; w < DV / 2; ++w) {
+                    __builtin_amdgcn_sched_barrier(0);  // one word's operands in registers at a time
                     uint32_t b[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) b[i] = v_word<FP8, D>(kv, i, w);
-                    uint4 f0, f1;
+                    u32x4_t f0, f1;
                     f0.x = __builtin_amdgcn_perm(b[1], b[0], 0x05040100);
                     f0.y = __builtin_amdgcn_perm(b[3], b[2], 0x05040100);
                     f0.z = __builtin_amdgcn_perm(b[5], b[4], 0x05040100);
@@ -623,10 +710,10 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
             }
         }
         // ---- join the four waves, 16 rows at a time
+        const int et = here(tid), ec = et & 15, eg = et >> 4 & 3;
 #pragma unroll
         for (int x = 0; x < RT; ++x) {
-            l[x] += __shfl_xor(l[x], 16, 64);
-            l[x] += __shfl_xor(l[x], 32, 64);
+            l[x] = column_sum(l[x]);
             if (rowbad[x]) {
                 l[x] = NAN;
                 atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
@@ -636,14 +723,14 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < DV; j += 4)
-                    *(float4 *)&o_s[wave][c][DV * (4 * g + i) + j] =
-                        make_float4(acc[x][j][i], acc[x][j + 1][i], acc[x][j + 2][i], acc[x][j + 3][i]);
-            if (g == 0) {
-                m_s[wave][c] = m[x];
-                l_s[wave][c] = l[x];
+                    *(f32x4_t *)&o_s[wave][ec][DV * (4 * eg + i) + j] =
+                        f32x4_t{acc[x][j][i], acc[x][j + 1][i], acc[x][j + 2][i], acc[x][j + 3][i]};
+            if (eg == 0) {
+                m_s[wave][ec] = m[x];
+                l_s[wave][ec] = l[x];
             }
             __syncthreads();
-            const int jr = tid >> 4, e0 = (tid & 15) * DV;  // this thread's row and values
+            const int jr = et >> 4, e0 = (et & 15) * DV;  // this thread's row and values
             const int row = t * TR + x * 16 + jr;
             float mm = fmaxf(fmaxf(m_s[0][jr], m_s[1][jr]), fmaxf(m_s[2][jr], m_s[3][jr]));
             const float ref = mm == -INFINITY ? 0.f : mm;
@@ -669,17 +756,17 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                     uint16_t *op = a.out + orow * D + e0;
 #pragma unroll
                     for (int j = 0; j < DV; j += 4)
-                        *(uint2 *)(op + j) = make_uint2(pack_bf16(o[j] * inv, o[j + 1] * inv),
-                                                        pack_bf16(o[j + 2] * inv, o[j + 3] * inv));
-                    if ((tid & 15) == 0) {
+                        *(u32x2_t *)(op + j) = u32x2_t{pack_bf16(o[j] * inv, o[j + 1] * inv),
+                                                        pack_bf16(o[j + 2] * inv, o[j + 3] * inv)};
+                    if ((et & 15) == 0) {
                         if (a.lse) a.lse[orow] = (mm + log2f(sum)) * (float)kLn2;
                     }
                 } else {
                     float *pp = a.part + (size_t)(2 * grp + (u0 == 0)) * a.part_stride;
                     float *po = pp + (size_t)(x * 16 + jr) * D + e0;
 #pragma unroll
-                    for (int j = 0; j < DV; j += 4) *(float4 *)(po + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                    if ((tid & 15) == 0) {
+                    for (int j = 0; j < DV; j += 4) *(f32x4_t *)(po + j) = f32x4_t{o[j], o[j + 1], o[j + 2], o[j + 3]};
+                    if ((et & 15) == 0) {
                         pp[TR * D + x * 16 + jr] = mm;
                         pp[TR * D + TR + x * 16 + jr] = sum;
                     }
@@ -718,22 +805,22 @@ constexpr int kTile = 64;              // tokens staged at a time
 // while the previous 64 are multiplied, and every wave reads them from there.
 template <bool FP8, int D> struct Stage {
     typedef Tile<FP8, D> TT;
-    uint4 k[TT::KV];
+    u32x4_t k[TT::KV];
     uint32_t v[4][TT::VW];
     float sc;
     int flags;                         // bit 16: the 16 tokens lie in a bad page
 };
 template <bool FP8, int D> struct Shared {
-    uint4 k[2][4][D / 32][64];         // [buffer][16 tokens][contraction step][lane]
-    uint2 v[2][2][D / 16][2][64];      // [buffer][32 tokens][output tile][half][lane]
-    float ks[2][kTile], vs[2][kTile];
+    u32x4_t k[2][4][D / 32][64];         // [buffer][16 tokens][contraction step][lane]
+    u32x2_t v[2][2][D / 16][2][64];      // [buffer][32 tokens][output tile][half][lane]
+    float sc[2][2][64];                // [buffer][32 tokens][lane], as load_scale's
     int flags[2][4];                   // per 16 tokens: bits 0-15 odd tokens, 16 bad page
 };
 
 // The page number of this wave's 16 tokens of the tile at token t0; those
 // behind the end take the last token's page, and are not used.
 __device__ __forceinline__ int stage_page(const AttnArgs &a, int r, int t0, int end, int wave) {
-    return a.c.table[(int64_t)r * a.c.max_pages + (min(t0 + 16 * wave, end - 1) >> a.c.shift)];
+    return page_number(a, r, min(t0 + 16 * wave, end - 1) >> a.c.shift);
 }
 
 // Loads this wave's 16 tokens of the tile at token t0 (rows [t0, end) exist).
@@ -741,7 +828,7 @@ template <bool FP8, int D>
 __device__ __forceinline__ void stage_load(const AttnArgs &a, int page, int h, int t0, int end, int wave,
                                            int lane, Stage<FP8, D> &s) {
     typedef Tile<FP8, D> TT;
-    const int c = lane & 15, g = lane >> 4;
+    const int hl = here(lane), c = hl & 15, g = hl >> 4;
     const int tt = t0 + 16 * wave < end ? t0 + 16 * wave : (end - 1) & ~15;
     s.flags = 0;
     if ((unsigned)page >= (unsigned)a.c.num_pages) {
@@ -749,13 +836,15 @@ __device__ __forceinline__ void stage_load(const AttnArgs &a, int page, int h, i
         page = 0;
     }
     const int64_t row = ((int64_t)page * a.c.heads + h) * a.c.size + (tt & (a.c.size - 1));
-    const char *kp = (const char *)a.c.k + (row + c) * (D * TT::EB) + g * 16;
+    const char *kp = (const char *)a.c.k + row * (D * TT::EB);
+    const uint32_t k_at = c * (D * TT::EB) + g * 16;
 #pragma unroll
-    for (int i = 0; i < TT::KV; ++i) s.k[i] = *(const uint4 *)(kp + i * 64);
-    const char *vp = (const char *)a.c.v + (row + 4 * g) * (D * TT::EB) + c * (TT::VW * 4);
+    for (int i = 0; i < TT::KV; ++i) s.k[i] = *(const u32x4_t *)(kp + k_at + i * 64);
+    const char *vp = (const char *)a.c.v + row * (D * TT::EB);
+    const uint32_t v_at = g * (4 * D * TT::EB) + c * (TT::VW * 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_words(vp + i * (D * TT::EB), s.v[i]);
-    if constexpr (FP8) s.sc = (lane & 16 ? a.c.v_scale : a.c.k_scale)[row + c];
+    for (int i = 0; i < 4; ++i) load_words(vp + v_at + i * (D * TT::EB), s.v[i]);
+    if constexpr (FP8) s.sc = lane & 16 ? (a.c.v_scale + row)[c] : (a.c.k_scale + row)[c];
 }
 
 // Writes them to buffer b.  `part`: the tile holds tokens that some row does
@@ -772,11 +861,32 @@ __device__ __forceinline__ void stage_store(const AttnArgs &a, Shared<FP8, D> &s
         if constexpr (!FP8) {
             sh.k[b][wave][i][lane] = s.k[i];
         } else {
-            const uint4 w = s.k[i];
-            sh.k[b][wave][2 * i][lane] = make_uint4(e4m3_bf16<false>(w.x), e4m3_bf16<true>(w.x),
-                                                    e4m3_bf16<false>(w.y), e4m3_bf16<true>(w.y));
-            sh.k[b][wave][2 * i + 1][lane] = make_uint4(e4m3_bf16<false>(w.z), e4m3_bf16<true>(w.z),
-                                                        e4m3_bf16<false>(w.w), e4m3_bf16<true>(w.w));
+            const u32x4_t w = s.k[i];
+            sh.k[b][wave][2 * i][lane] = u32x4_t{e4m3_bf16<false>(w.x), e4m3_bf16<true>(w.x),
+                                                    e4m3_bf16<false>(w.y), e4m3_bf16<true>(w.y)};
+            sh.k[b][wave][2 * i + 1][lane] = u32x4_t{e4m3_bf16<false>(w.z), e4m3_bf16<true>(w.z),
+                                                        e4m3_bf16<false>(w.w), e4m3_bf16<true>(w.w)};
+        }
+    }
+    int flags = s.flags;
+    if (part) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool live = t0 + 16 * wave + 4 * g + i < end;
+            bool odd = false;
+#pragma unroll
+            for (int w = 0; w < TT::VW; ++w) {
+                s.v[i][w] = live ? s.v[i][w] : 0u;
+                odd |= odd_word<FP8>(s.v[i][w]);
+            }
+            const uint64_t bal = __ballot(odd);
+            if (bal) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (bal >> (16 * q) & 0xffffu) flags |= 1 << (4 * q + i);
+#pragma unroll
+                for (int w = 0; w < TT::VW; ++w) s.v[i][w] = bal >> (16 * g) & 0xffffu ? 0u : s.v[i][w];
+            }
         }
     }
     uint32_t v[4][TT::DV / 2];
@@ -787,39 +897,20 @@ __device__ __forceinline__ void stage_store(const AttnArgs &a, Shared<FP8, D> &s
             if constexpr (!FP8) v[i][w] = s.v[i][w];
             else v[i][w] = w & 1 ? e4m3_bf16<true>(s.v[i][w >> 1]) : e4m3_bf16<false>(s.v[i][w >> 1]);
         }
-    int flags = s.flags;
-    if (part) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool live = t0 + 16 * wave + 4 * g + i < end;
-            bool odd = false;
-#pragma unroll
-            for (int w = 0; w < TT::DV / 2; ++w) {
-                v[i][w] = live ? v[i][w] : 0u;
-                odd |= odd_word(v[i][w]);
-            }
-            const uint64_t bal = __ballot(odd);
-            if (bal) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (bal >> (16 * q) & 0xffffu) flags |= 1 << (4 * q + i);
-#pragma unroll
-                for (int w = 0; w < TT::DV / 2; ++w) v[i][w] = bal >> (16 * g) & 0xffffu ? 0u : v[i][w];
-            }
-        }
-    }
 #pragma unroll
     for (int w = 0; w < TT::DV / 2; ++w) {
         sh.v[b][wave >> 1][2 * w][wave & 1][lane] =
-            make_uint2(__builtin_amdgcn_perm(v[1][w], v[0][w], 0x05040100),
-                       __builtin_amdgcn_perm(v[3][w], v[2][w], 0x05040100));
+            u32x2_t{__builtin_amdgcn_perm(v[1][w], v[0][w], 0x05040100),
+                       __builtin_amdgcn_perm(v[3][w], v[2][w], 0x05040100)};
         sh.v[b][wave >> 1][2 * w + 1][wave & 1][lane] =
-            make_uint2(__builtin_amdgcn_perm(v[1][w], v[0][w], 0x07060302),
-                       __builtin_amdgcn_perm(v[3][w], v[2][w], 0x07060302));
+            u32x2_t{__builtin_amdgcn_perm(v[1][w], v[0][w], 0x07060302),
+                       __builtin_amdgcn_perm(v[3][w], v[2][w], 0x07060302)};
     }
     if constexpr (FP8) {
-        if (lane < 16) sh.ks[b][16 * wave + lane] = s.sc * a.scale2;
-        else if (lane < 32) sh.vs[b][16 * wave + (lane & 15)] = s.sc;
+        // lane c of K's (0-15) or V's (16-31): token c of the wave's 16
+        const int c = lane & 15;
+        if (lane < 32)
+            sh.sc[b][wave >> 1][16 * (c >> 2) + (lane & 16 ? 8 : 0) + 4 * (wave & 1) + (c & 3)] = s.sc;
     }
     if (lane == 0) sh.flags[b][wave] = flags;
 }
@@ -859,9 +950,10 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
             const size_t nd = (size_t)r * a.M + node[x];
             pos[x] = a.positions ? a.positions[nd] : rq.ctx + node[x];
             const uint16_t *qp = a.q + (nd * a.Hq + h * a.G + (row - node[x] * a.G)) * D;
+            const int qg = here(g);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
-                qf[x][ks] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(qp + q_chunk<FP8>(ks, g)));
+                qf[x][ks] = __builtin_bit_cast(bf16x8_t, *(const u32x4_t *)(qp + q_chunk<FP8>(ks, qg)) ^ a.flip);
         }
         f32x4_t acc[RT][DV];
         float m[RT], l[RT];
@@ -911,64 +1003,19 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                             for (int x = 0; x < RT; ++x)
                                 s[x][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[x][ks], s[x][hf], 0, 0, 0);
                         }
-                    float4 ksc[2], vsc[2];
-                    if constexpr (FP8) {
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            ksc[hf] = *(const float4 *)&sh.ks[b][kStep * half + 16 * hf + 4 * g];
-                            vsc[hf] = *(const float4 *)&sh.vs[b][kStep * half + 16 * hf + 4 * g];
-                        }
-                    }
+                    const float sc = FP8 ? sh.sc[b][half][lane] : 0.f;
                     const int fl0 = half ? flags[2] : flags[0], fl1 = half ? flags[3] : flags[1];
-                    const bool bad = (fl0 | fl1) >> 16;
+                    const int bad = fl0 >> 16 | (fl1 >> 16) << 1;
                     const bool masked = tok < plain.lo || tok + kStep > plain.hi || bad;
                     uint32_t seen[RT];
-                    uint4 pw[RT];
+                    u32x4_t pw[RT];
 #pragma unroll
                     for (int x = 0; x < RT; ++x) {
-                        float p[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            p[i] = s[x][i >> 2][i & 3];
-                            if constexpr (FP8) p[i] *= (&ksc[i >> 2].x)[i & 3];
-                            else p[i] *= a.scale2;
-                        }
                         seen[x] = 0xffu;
                         if (masked) {
-                            const uint32_t *mrow = a.mask ? a.mask + ((size_t)r * a.M + node[x]) * a.W : nullptr;
-                            seen[x] = lane_bits(sees(a, tok, rq.ctx, rq.n, node[x], pos[x], mrow), g);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                p[i] = !(seen[x] >> i & 1u) ? -INFINITY
-                                       : (i >> 2 ? fl1 : fl0) >> 16 ? NAN : p[i];
+                            seen[x] = lane_bits(sees(a, r, tok, rq.ctx, rq.n, node[x], pos[x]), g);
                         }
-                        float tm = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])),
-                                         fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
-                        tm = fmaxf(tm, __shfl_xor(tm, 16, 64));
-                        tm = fmaxf(tm, __shfl_xor(tm, 32, 64));
-                        if (__any(tm > m[x] + kLazy)) {
-                            const float mn = fmaxf(m[x], tm);
-                            const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[x] - mn);
-                            l[x] *= al;
-#pragma unroll
-                            for (int j = 0; j < DV; ++j) acc[x][j] *= al;
-                            m[x] = mn;
-                        }
-                        const float ref = m[x] == -INFINITY ? 0.f : m[x];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            p[i] = __builtin_amdgcn_exp2f(p[i] - ref);
-                            l[x] += p[i];
-                        }
-                        if constexpr (FP8) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float vv = p[i] * (&vsc[i >> 2].x)[i & 3];
-                                p[i] = !masked || (seen[x] >> i & 1u) ? vv : 0.f;
-                            }
-                        }
-                        pw[x] = make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]),
-                                           pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+                        pw[x] = weigh<FP8, DV>(s[x], sc, a.scale2, masked, seen[x], bad, m[x], l[x], acc[x]);
                     }
                     // ---- tokens whose V rows left the tile, one by one
                     const uint32_t odd = (fl0 & 0xffff) | (uint32_t)(fl1 & 0xffff) << 16;
@@ -980,30 +1027,15 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                             const Half x16 = halves_of(a, numbers_of(a, r, tok + (q & 16), end), h, tok + (q & 16), end);
                             const int64_t row = x16.row[0] + (q & 15);
 #pragma unroll
-                            for (int x = 0; x < RT; ++x) {
-                                const uint32_t lo = ti & 4 ? (ti & 2 ? pw[x].w : pw[x].z)
-                                                           : (ti & 2 ? pw[x].y : pw[x].x);
-                                const float mine = ti & 1 ? bf16_hi(lo) : bf16_lo(lo);
-                                const float pv = __shfl(mine, tg * 16 + c, 64);
-                                const bool see = __shfl((int)seen[x], tg * 16 + c, 64) >> ti & 1;
-#pragma unroll
-                                for (int j = 0; j < DV; ++j)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const int64_t e = row * D + DV * (4 * g + i) + j;
-                                        float val;
-                                        if constexpr (FP8) val = bf16_lo(e4m3_bf16<false>(((const uint8_t *)a.c.v)[e]));
-                                        else val = bf16_lo(((const uint16_t *)a.c.v)[e]);
-                                        if (see) acc[x][j][i] += pv * val;
-                                    }
-                            }
+                            for (int x = 0; x < RT; ++x)
+                                add_token<FP8, D>(a, row, tg, ti, lane, pw[x], seen[x], acc[x]);
                         }
                     }
                     // ---- product
 #pragma unroll
                     for (int j = 0; j < DV; ++j) {
-                        const uint2 lo = sh.v[b][half][j][0][lane], hi = sh.v[b][half][j][1][lane];
-                        const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, make_uint4(lo.x, lo.y, hi.x, hi.y));
+                        const u32x2_t lo = sh.v[b][half][j][0][lane], hi = sh.v[b][half][j][1][lane];
+                        const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, u32x4_t{lo.x, lo.y, hi.x, hi.y});
 #pragma unroll
                         for (int x = 0; x < RT; ++x)
                             acc[x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -1017,16 +1049,16 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
             }
         }
         // ---- the wave's rows
+        const int el = here(lane), ec = el & 15, eg = el >> 4;
 #pragma unroll
         for (int x = 0; x < RT; ++x) {
-            l[x] += __shfl_xor(l[x], 16, 64);
-            l[x] += __shfl_xor(l[x], 32, 64);
-            const int lr = wave * 16 * RT + x * 16 + c, row = t * TR + lr;
+            l[x] = column_sum(l[x]);
+            const int lr = wave * 16 * RT + x * 16 + ec, row = t * TR + lr;
             if (row >= rq.rows) continue;
             const bool fault = !rq.ok || pos[x] < rq.ctx;
             if (fault) {
                 l[x] = NAN;
-                if (g == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+                if (eg == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
             }
             if (whole) {
                 const size_t orow = ((size_t)r * a.M + node[x]) * a.Hq + h * a.G + (row - node[x] * a.G);
@@ -1037,23 +1069,23 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                 const float inv = 1.f / l[x];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint16_t *op = a.out + orow * D + DV * (4 * g + i);
+                    uint16_t *op = a.out + orow * D + DV * (4 * eg + i);
 #pragma unroll
                     for (int j = 0; j < DV; j += 4)
-                        *(uint2 *)(op + j) = make_uint2(pack_bf16(acc[x][j][i] * inv, acc[x][j + 1][i] * inv),
-                                                        pack_bf16(acc[x][j + 2][i] * inv, acc[x][j + 3][i] * inv));
+                        *(u32x2_t *)(op + j) = u32x2_t{pack_bf16(acc[x][j][i] * inv, acc[x][j + 1][i] * inv),
+                                                        pack_bf16(acc[x][j + 2][i] * inv, acc[x][j + 3][i] * inv)};
                 }
-                if (g == 0 && a.lse) a.lse[orow] = (m[x] + log2f(l[x])) * (float)kLn2;
+                if (eg == 0 && a.lse) a.lse[orow] = (m[x] + log2f(l[x])) * (float)kLn2;
             } else {
                 float *pp = a.part + (size_t)(2 * grp + (u0 == 0)) * a.part_stride;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float *po = pp + (size_t)lr * D + DV * (4 * g + i);
+                    float *po = pp + (size_t)lr * D + DV * (4 * eg + i);
 #pragma unroll
                     for (int j = 0; j < DV; j += 4)
-                        *(float4 *)(po + j) = make_float4(acc[x][j][i], acc[x][j + 1][i], acc[x][j + 2][i], acc[x][j + 3][i]);
+                        *(f32x4_t *)(po + j) = f32x4_t{acc[x][j][i], acc[x][j + 1][i], acc[x][j + 2][i], acc[x][j + 3][i]};
                 }
-                if (g == 0) {
+                if (eg == 0) {
                     pp[TR * D + lr] = m[x];
                     pp[TR * D + TR + lr] = l[x];
                 }
@@ -1249,7 +1281,10 @@ int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const v
     a.n_nodes = n_nodes;
     a.mask = mask;
     a.positions = positions;
-    a.scale2 = (float)(scale * kLog2e);
+    // a positive factor, so that the largest score is the largest product; 0
+    // becomes the smallest normal number (-inf times it is still -inf)
+    a.scale2 = fmaxf((float)(fabs((double)scale) * kLog2e), 1.17549435e-38f);
+    a.flip = scale < 0.0f ? 0x80008000u : 0u;
     a.R = R;
     a.window = window;
     a.M = M;
