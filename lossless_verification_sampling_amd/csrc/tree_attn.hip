@@ -373,13 +373,23 @@ __device__ __forceinline__ bool odd_word(uint32_t w) {
 __device__ __forceinline__ uint32_t ones(int k) {
     return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u;
 }
-// Tokens tok .. tok + 31 that the row of node v (position pos) of request r
-// sees, one bit each.
-__device__ __forceinline__ uint32_t sees(const AttnArgs &a, int r, int tok, int ctx, int n, int v,
-                                         int pos) {
-    v = here(v);
-    pos = here(pos);
-    const int k = ctx - tok;  // tokens of the context
+// Node and position of query row `row` of request r (rows past the last
+// stand for it).
+struct Query {
+    int node, pos;
+};
+__device__ __forceinline__ Query query_of(const AttnArgs &a, const Req &rq, int r, int row) {
+    Query q;
+    q.node = min(row, rq.rows - 1) / a.G;
+    q.pos = a.positions ? a.positions[(size_t)r * a.M + q.node] : rq.ctx + q.node;
+    return q;
+}
+// Tokens tok .. tok + 31 that query row `row` of request r sees, one bit each.
+// Worked out anew where a step needs it: few do, and registers are short.
+__device__ __forceinline__ uint32_t sees(const AttnArgs &a, const Req &rq, int r, int tok, int row) {
+    const Query q = query_of(a, rq, r, here(row));
+    const int v = q.node, pos = q.pos, n = rq.n;
+    const int k = rq.ctx - tok;  // tokens of the context
     const uint32_t old = ones(k);
     uint32_t tree;
     if (a.mask) {
@@ -398,6 +408,19 @@ __device__ __forceinline__ uint32_t sees(const AttnArgs &a, int r, int tok, int 
 // Bit i: token i of this lane group's eight.
 __device__ __forceinline__ uint32_t lane_bits(uint32_t seen, int g) {
     return (seen >> (4 * g) & 15u) | (seen >> (4 * g + 16) & 15u) << 4;
+}
+
+// The B operands of query row `row`: lane group g holds its values of every
+// contraction step.
+template <bool FP8, int D>
+__device__ __forceinline__ void load_q(const AttnArgs &a, const Req &rq, int r, int h, int row, int lane,
+                                       bf16x8_t (&qf)[D / 32]) {
+    row = min(here(row), rq.rows - 1);
+    const int node = row / a.G, g = here(lane) >> 4;
+    const uint16_t *qp = a.q + (((size_t)r * a.M + node) * a.Hq + h * a.G + (row - node * a.G)) * D;
+#pragma unroll
+    for (int ks = 0; ks < D / 32; ++ks)
+        qf[ks] = __builtin_bit_cast(bf16x8_t, *(const u32x4_t *)(qp + q_chunk<FP8>(ks, g)) ^ a.flip);
 }
 
 // Maximum (NaN if one is) of a lane's eight scores, and over the four lanes
@@ -458,10 +481,10 @@ __device__ __forceinline__ u32x4_t weigh(const f32x4_t (&s)[2], float sc, float 
         for (int i = 0; i < 8; ++i)
             p[i] = !(seen >> i & 1u) ? -INFINITY : bad >> (i >> 2) & 1 ? NAN : p[i];
     }
-    float top = column_max(max8(p));
+    float top = max8(p);  // m is the column's, so a lane's own maximum tells
     if constexpr (!FP8) top *= scale2;
     if (__any(top > m + kLazy)) {
-        const float mn = max2(m, top);
+        const float mn = max2(m, column_max(top));
         const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
         l *= al;
 #pragma unroll
@@ -515,18 +538,18 @@ __device__ __forceinline__ void add_token(const AttnArgs &a, int64_t row, int tg
 struct Plain {
     int lo, hi;
 };
-// For rows from `row0` on at positions pos[] of all lanes, up to token t1.
+// For the 16 RT rows from `row0` on, up to token t1.
 template <int RT>
-__device__ __forceinline__ Plain plain_of(const AttnArgs &a, const Req &rq, int row0,
-                                          const int (&pos)[RT], int t1) {
+__device__ __forceinline__ Plain plain_of(const AttnArgs &a, const Req &rq, int r, int row0, int c,
+                                          int t1) {
     Plain p;
     p.lo = 0;
     p.hi = rq.ctx;
     if (!a.mask && !a.window) p.hi += row0 / a.G + 1;
     if (a.window) {
-        int far = pos[0];
+        int far = 0;
 #pragma unroll
-        for (int x = 1; x < RT; ++x) far = max(far, pos[x]);
+        for (int x = 0; x < RT; ++x) far = max(far, query_of(a, rq, r, row0 + x * 16 + c).pos);
         p.lo = wave_max_i(far) - a.window + 1;
     }
     p.hi = min(p.hi, t1);
@@ -571,21 +594,8 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
         const bool whole = u0 == 0 && u1 == units;
         // ---- the rows of this lane's column
         bf16x8_t qf[RT][KS];
-        int node[RT], pos[RT];
-        bool rowbad[RT];
 #pragma unroll
-        for (int x = 0; x < RT; ++x) {
-            const int row = min(t * TR + x * 16 + c, rq.rows - 1);
-            node[x] = row / a.G;
-            const size_t nd = (size_t)r * a.M + node[x];
-            pos[x] = a.positions ? a.positions[nd] : rq.ctx + node[x];
-            rowbad[x] = !rq.ok || pos[x] < rq.ctx;
-            const uint16_t *qp = a.q + (nd * a.Hq + h * a.G + (row - node[x] * a.G)) * D;
-            const int qg = here(g);
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                qf[x][ks] = __builtin_bit_cast(bf16x8_t, *(const u32x4_t *)(qp + q_chunk<FP8>(ks, qg)) ^ a.flip);
-        }
+        for (int x = 0; x < RT; ++x) load_q<FP8, D>(a, rq, r, h, t * TR + x * 16 + c, lane, qf[x]);
         f32x4_t acc[RT][DV];
         float m[RT], l[RT];
 #pragma unroll
@@ -595,7 +605,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
 #pragma unroll
             for (int j = 0; j < DV; ++j) acc[x][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
-        const Plain plain = plain_of<RT>(a, rq, t * TR, pos, t1);
+        const Plain plain = plain_of<RT>(a, rq, r, t * TR, c, t1);
         int tok = t0 + wave * kStep;
         if (rq.ok && tok < t1) {
             TT kv;
@@ -638,7 +648,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                 for (int x = 0; x < RT; ++x) {
                     seen[x] = 0xffu;
                     if (masked) {
-                        seen[x] = lane_bits(sees(a, r, tok, rq.ctx, rq.n, node[x], pos[x]), g);
+                        seen[x] = lane_bits(sees(a, rq, r, tok, t * TR + x * 16 + c), g);
                     }
                     pw[x] = weigh<FP8, DV>(s[x], sc, a.scale2, masked, seen[x], cur.bad, m[x], l[x], acc[x]);
                 }
@@ -714,7 +724,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
 #pragma unroll
         for (int x = 0; x < RT; ++x) {
             l[x] = column_sum(l[x]);
-            if (rowbad[x]) {
+            if (!rq.ok || query_of(a, rq, r, t * TR + x * 16 + ec).pos < rq.ctx) {
                 l[x] = NAN;
                 atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
             }
@@ -942,19 +952,8 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
         const bool whole = u0 == 0 && u1 == units;
         const int row0 = t * TR + wave * 16 * RT;  // the wave's rows
         bf16x8_t qf[RT][KS];
-        int node[RT], pos[RT];
 #pragma unroll
-        for (int x = 0; x < RT; ++x) {
-            const int row = min(row0 + x * 16 + c, rq.rows - 1);
-            node[x] = row / a.G;
-            const size_t nd = (size_t)r * a.M + node[x];
-            pos[x] = a.positions ? a.positions[nd] : rq.ctx + node[x];
-            const uint16_t *qp = a.q + (nd * a.Hq + h * a.G + (row - node[x] * a.G)) * D;
-            const int qg = here(g);
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                qf[x][ks] = __builtin_bit_cast(bf16x8_t, *(const u32x4_t *)(qp + q_chunk<FP8>(ks, qg)) ^ a.flip);
-        }
+        for (int x = 0; x < RT; ++x) load_q<FP8, D>(a, rq, r, h, row0 + x * 16 + c, lane, qf[x]);
         f32x4_t acc[RT][DV];
         float m[RT], l[RT];
 #pragma unroll
@@ -964,7 +963,7 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
 #pragma unroll
             for (int j = 0; j < DV; ++j) acc[x][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
-        const Plain plain = plain_of<RT>(a, rq, row0, pos, t1);
+        const Plain plain = plain_of<RT>(a, rq, r, row0, c, t1);
         // the workgroup's: its first rows see the least of a chain; of a window nothing is said
         const int common = a.window ? 0 : min(rq.ctx + (a.mask ? 0 : t * TR / a.G + 1), t1);
         // a chain's wave sees nothing behind its last row's node
@@ -994,15 +993,22 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
 #pragma unroll
                     for (int x = 0; x < RT; ++x)
                         for (int hf = 0; hf < 2; ++hf) s[x][hf] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                    // operands come from shared memory well ahead of their products
+                    u32x4_t kf[2][KS];
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) kf[hf][ks] = sh.k[b][2 * half + hf][ks][lane];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) {
-                            const bf16x8_t kf = __builtin_bit_cast(bf16x8_t, sh.k[b][2 * half + hf][ks][lane]);
+                        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                             for (int x = 0; x < RT; ++x)
-                                s[x][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[x][ks], s[x][hf], 0, 0, 0);
-                        }
+                                s[x][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                    __builtin_bit_cast(bf16x8_t, kf[hf][ks]), qf[x][ks], s[x][hf], 0, 0, 0);
                     const float sc = FP8 ? sh.sc[b][half][lane] : 0.f;
                     const int fl0 = half ? flags[2] : flags[0], fl1 = half ? flags[3] : flags[1];
                     const int bad = fl0 >> 16 | (fl1 >> 16) << 1;
@@ -1013,7 +1019,7 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                     for (int x = 0; x < RT; ++x) {
                         seen[x] = 0xffu;
                         if (masked) {
-                            seen[x] = lane_bits(sees(a, r, tok, rq.ctx, rq.n, node[x], pos[x]), g);
+                            seen[x] = lane_bits(sees(a, rq, r, tok, row0 + x * 16 + c), g);
                         }
                         pw[x] = weigh<FP8, DV>(s[x], sc, a.scale2, masked, seen[x], bad, m[x], l[x], acc[x]);
                     }
@@ -1033,13 +1039,20 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                     }
                     // ---- product
 #pragma unroll
-                    for (int j = 0; j < DV; ++j) {
-                        const u32x2_t lo = sh.v[b][half][j][0][lane], hi = sh.v[b][half][j][1][lane];
-                        const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, u32x4_t{lo.x, lo.y, hi.x, hi.y});
+                    for (int j0 = 0; j0 < DV; j0 += 4) {
+                        u32x4_t vf[4];
 #pragma unroll
-                        for (int x = 0; x < RT; ++x)
-                            acc[x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                vf, __builtin_bit_cast(bf16x8_t, pw[x]), acc[x][j], 0, 0, 0);
+                        for (int j = 0; j < 4; ++j) {
+                            const u32x2_t lo = sh.v[b][half][j0 + j][0][lane], hi = sh.v[b][half][j0 + j][1][lane];
+                            vf[j] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int x = 0; x < RT; ++x)
+                                acc[x][j0 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                    __builtin_bit_cast(bf16x8_t, vf[j]), __builtin_bit_cast(bf16x8_t, pw[x]),
+                                    acc[x][j0 + j], 0, 0, 0);
                     }
                     if (bad && lane == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
                 }
@@ -1055,13 +1068,13 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
             l[x] = column_sum(l[x]);
             const int lr = wave * 16 * RT + x * 16 + ec, row = t * TR + lr;
             if (row >= rq.rows) continue;
-            const bool fault = !rq.ok || pos[x] < rq.ctx;
-            if (fault) {
+            const Query q = query_of(a, rq, r, row);
+            if (!rq.ok || q.pos < rq.ctx) {
                 l[x] = NAN;
                 if (eg == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
             }
             if (whole) {
-                const size_t orow = ((size_t)r * a.M + node[x]) * a.Hq + h * a.G + (row - node[x] * a.G);
+                const size_t orow = ((size_t)r * a.M + q.node) * a.Hq + h * a.G + (row - q.node * a.G);
                 if (l[x] == 0.f) {  // nothing seen: o is 0
                     l[x] = 1.f;
                     m[x] = -INFINITY;
@@ -1204,9 +1217,9 @@ struct Shape {
 };
 inline Shape shape_of(int64_t rows, int D) {
     Shape s;
-    s.wide = rows > 32;
+    s.wide = rows > (D == 256 ? 16 : 32);
     if (!s.wide) s.RT = rows <= 16 ? 1 : 2;
-    else s.RT = D == 256 || rows <= 64 ? 1 : 2;
+    else s.RT = D == 256 || rows <= 64 ? 1 : rows <= 128 ? 2 : 3;
     s.TR = 16 * s.RT * (s.wide ? kWaves : 1);
     s.groups = D <= 128 ? kMaxGroups : kMaxGroups / 2;
     return s;
@@ -1226,10 +1239,10 @@ template <bool FP8, int D>
 static void launch_attn(const AttnArgs &a, const Shape &s, hipStream_t st) {
     if (s.wide) {
         if (s.RT == 1) launch_attn<FP8, D, 1, true>(a, st);
-        else if constexpr (D <= 128) launch_attn<FP8, D, 2, true>(a, st);
+        else if constexpr (D <= 128) { if (s.RT == 2) launch_attn<FP8, D, 2, true>(a, st); else launch_attn<FP8, D, 3, true>(a, st); }
     } else {
         if (s.RT == 1) launch_attn<FP8, D, 1, false>(a, st);
-        else launch_attn<FP8, D, 2, false>(a, st);
+        else if constexpr (D <= 128) launch_attn<FP8, D, 2, false>(a, st);
     }
 }
 template <bool FP8>
