@@ -11,6 +11,11 @@ constexpr float kMinScale = 1.17549435e-38f;       // 2^-126, so that x / scale 
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
+// (vector types of the language, not the runtime's structs: arrays of those
+// end up in scratch memory)
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 // One layer's pages.  Token t of request r: page table[r * max_pages + (t >>
 // shift)], offset t & (size - 1); the row of head h starts at element

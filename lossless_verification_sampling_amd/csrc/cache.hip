@@ -1,10 +1,11 @@
 // cache.hip -- writing, reading and moving rows of the paged key/value cache
 // on gfx950.
 //
-// A head row of D values belongs to D / 8 lanes, 8 values (16 bytes of bf16)
-// each, so a wave holds 512 / D rows and every sum, maximum or exchange over a
-// row stays inside it.
+// A head row of D values belongs to D / 8 lanes, 8 values each, so a wave
+// holds 512 / D rows and every sum or maximum over a row stays inside it.
 #include <math.h>
+
+#include <type_traits>
 
 #include "cache.h"
 
@@ -28,142 +29,220 @@ struct WriteArgs {
     Control *ctl;
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        VecLoad<T, 8>::run(p, 0, x);
-    } else {
-        VecLoad<T, 4>::run(p, 0, x);
-        VecLoad<T, 4>::run(p, 4, x + 4);
-    }
+__device__ __forceinline__ u32x4_t bf16x8(const float (&x)[8]) {
+    return u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                   pack_bf16(x[6], x[7])};
 }
 
-__device__ __forceinline__ uint4 bf16x8(const float (&x)[8]) {
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                      pack_bf16(x[6], x[7]));
-}
-
-// Sum and maximum over the D / 8 lanes of a row.
+// Sum and maximum over the D / 8 lanes of a row, by lane moves.
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) v += __shfl_xor(v, o, 64);
+    v += dpp_f<kDppSwap1>(v);
+    v += dpp_f<kDppSwap2>(v);
+    v += dpp_f<kDppHalfMirror>(v);
+    if constexpr (LPR >= 16) v += dpp_f<kDppMirror>(v);
+    if constexpr (LPR == 32) {
+        uint32_t lo, hi;
+        lane_pair<16>(__float_as_uint(v), lo, hi);
+        v = __uint_as_float(lo) + __uint_as_float(hi);
+    }
     return v;
 }
 template <int LPR>
 __device__ __forceinline__ float row_max(float v) {
-#pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    v = fmaxf(v, dpp_f<kDppSwap1>(v));
+    v = fmaxf(v, dpp_f<kDppSwap2>(v));
+    v = fmaxf(v, dpp_f<kDppHalfMirror>(v));
+    if constexpr (LPR >= 16) v = fmaxf(v, dpp_f<kDppMirror>(v));
+    if constexpr (LPR == 32) {
+        uint32_t lo, hi;
+        lane_pair<16>(__float_as_uint(v), lo, hi);
+        v = fmaxf(__uint_as_float(lo), __uint_as_float(hi));
+    }
     return v;
 }
 
-// One workgroup per token (x) and group of 2048 / D head rows (y).
-template <typename T, bool FP8, int D>
+// The two groups of four values a lane holds, from elements a and b on.  The
+// two halves of a rotation are half elements apart: a lane that turns takes
+// four of each, so that both values of a pair are its own; the other lanes,
+// and all of them for interleaved pairs, take eight in a row.
+struct Place {
+    int a, b;
+    bool in;                     // the lane's values turn
+};
+__device__ __forceinline__ Place place_of(const WriteArgs &w, int l) {
+    Place p;
+    const int split = w.interleaved ? 0 : w.half / 4;  // lanes that hold both halves
+    p.a = l < split ? 4 * l : 2 * (w.interleaved ? 0 : w.half) + 8 * (l - split);
+    p.b = l < split ? w.half + 4 * l : p.a + 4;
+    p.in = w.interleaved ? p.a < 2 * w.half : l < split;
+    return p;
+}
+
+// Four values as they lie in memory.
+template <typename T> struct Raw4 {
+    uint32_t w[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Raw4<T> load4(const T *p) {
+    Raw4<T> r;
+    if constexpr (sizeof(T) == 2) {
+        const u32x2_t x = *(const u32x2_t *)p;
+        r.w[0] = x[0];
+        r.w[1] = x[1];
+    } else {
+        const u32x4_t x = *(const u32x4_t *)p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = x[i];
+    }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ float value(const Raw4<T> &r, int i) {
+    if constexpr (sizeof(T) == 2) return i & 1 ? bf16_hi(r.w[i >> 1]) : bf16_lo(r.w[i >> 1]);
+    else return __uint_as_float(r.w[i]);
+}
+
+// One workgroup per token: its lanes keep the same values of every head row,
+// so the rotation and the weights are read once; ROWS head rows a thread are
+// asked for before the first is used.  Few tokens: ROWS = 1 and workgroups
+// (y) share a token's rows.  Several tokens a workgroup with the next one's
+// rows in flight was slower (150 us against 125 for 16 k tokens of 48 rows:
+// the registers cost more waves than the waits).
+// Bound by HBM: the projections read, q and the cache written.
+template <typename T, bool FP8, int D, int ROWS>
 __global__ void __launch_bounds__(kBlock) qkv_write_kernel(WriteArgs a) {
     constexpr int LPR = D / 8, RPB = kBlock / LPR;
     const int token = blockIdx.x, r = token / a.M, v = token - r * a.M;
-    const int tid = threadIdx.x, l = tid & (LPR - 1), e = l * 8;
+    const int tid = threadIdx.x, l = tid & (LPR - 1);
     const int n = a.n_nodes[r], ctx = a.ctx_len[r];
     const bool sane = n >= 0 && n <= a.M && in_table(ctx, n, a.c.max_pages, a.c.shift);
     if (sane && v >= n) return;
     const int Hkv = a.c.heads, rows = a.Hq + 2 * Hkv;
-    const int row = blockIdx.y * RPB + tid / LPR;
-    if (row >= rows) return;
+    const int first = blockIdx.y * RPB + tid / LPR, step = gridDim.y * RPB;
     if (!sane) {
-        if (row < a.Hq) {
-            const float nan8[8] = {NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN};
-            *(uint4 *)(a.out_q + ((size_t)token * a.Hq + row) * D + e) = bf16x8(nan8);
-        }
-        if (row == 0 && l == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+        const uint32_t nan2 = pack_bf16(NAN, NAN);
+        for (int row = first; row < a.Hq; row += step)
+            *(u32x4_t *)(a.out_q + ((size_t)token * a.Hq + row) * D + 8 * l) = u32x4_t{nan2, nan2, nan2, nan2};
+        if (first == 0 && l == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
         return;
     }
-    const int kind = row < a.Hq ? 0 : row < a.Hq + Hkv ? 1 : 2;  // q, k, v
-    const int head = kind == 0 ? row : kind == 1 ? row - a.Hq : row - a.Hq - Hkv;
-    const T *src = kind == 0 ? (const T *)a.q + (int64_t)token * a.ld_q
-                 : kind == 1 ? (const T *)a.k + (int64_t)token * a.ld_k
-                             : (const T *)a.v + (int64_t)token * a.ld_v;
-    float x[8];
-    load8(src + head * D + e, x);
-    if (kind < 2) {
-        const T *w = (const T *)(kind == 0 ? a.q_weight : a.k_weight);
-        if (w) {
-            float wt[8], ss = 0.f;
-            load8(w + e, wt);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-            ss = row_sum<LPR>(ss);
-            const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * wt[i];
-        }
-        if (a.half) {
-            const int pos = a.positions ? a.positions[token] : ctx + v;
-            const bool there = pos >= 0 && pos < a.max_pos;
-            const float2 *cs = a.rope + (size_t)(there ? pos : 0) * a.half;
-            if (a.interleaved) {
-                if (e < 2 * a.half) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 t = cs[e / 2 + i];
-                        const float p = x[2 * i], q = x[2 * i + 1];
-                        x[2 * i] = p * t.x - q * t.y;
-                        x[2 * i + 1] = q * t.x + p * t.y;
-                    }
-                }
-            } else {
-                // the partner of lane l < half / 8 is lane l + half / 8
-                const int hl = a.half / 8;
-                const int lo = l < hl, in = l < 2 * hl;
-                const int from = (tid & 63) + (in ? (lo ? hl : -hl) : 0);
-                const int i0 = lo ? e : e - a.half;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float other = __shfl(x[i], from, 64);
-                    if (in) {
-                        const float2 t = cs[i0 + i];
-                        x[i] = lo ? x[i] * t.x - other * t.y : x[i] * t.x + other * t.y;
-                    }
-                }
-            }
-            if (!there) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = NAN;
-                if (l == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
-            }
-        }
-    }
-    if (kind == 0) {
-        *(uint4 *)(a.out_q + ((size_t)token * a.Hq + head) * D + e) = bf16x8(x);
-        return;
-    }
+    const Place at = place_of(a, l);
+    // the token's place in the cache and its angles
     const int t = ctx + v;
     const int page = a.c.table[(size_t)r * a.c.max_pages + (t >> a.c.shift)];
     const bool good = page >= 0 && page < a.c.num_pages;
-    if (!good) {
-        if (l == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
-        return;
+    const int pos = a.half && a.positions ? a.positions[token] : t;
+    const bool there = !a.half || (pos >= 0 && pos < a.max_pos);
+    if ((!good || !there) && first == 0 && l == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+    f32x4_t cs[2] = {};          // (cos, sin) of the lane's four pairs
+    if (at.in) {
+        const f32x4_t *p = (const f32x4_t *)(a.rope + (size_t)(there ? pos : 0) * a.half +
+                                             (a.interleaved ? at.a / 2 : at.a));
+        cs[0] = p[0];
+        cs[1] = p[1];
     }
-    const size_t slot = ((size_t)page * Hkv + head) * a.c.size + (t & (a.c.size - 1));
-    if constexpr (!FP8) {
-        *(uint4 *)((uint16_t *)(kind == 1 ? a.c.k : a.c.v) + slot * D + e) = bf16x8(x);
-    } else {
-        float m = 0.f;
-        int bad = 0;
+    Raw4<T> qw[2], kw[2];
+    if (a.q_weight) {
+        qw[0] = load4((const T *)a.q_weight + at.a);
+        qw[1] = load4((const T *)a.q_weight + at.b);
+    }
+    if (a.k_weight) {
+        kw[0] = load4((const T *)a.k_weight + at.a);
+        kw[1] = load4((const T *)a.k_weight + at.b);
+    }
+    for (int row0 = first; row0 < rows; row0 += ROWS * step) {
+        Raw4<T> raw[ROWS][2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            m = fmaxf(m, fabsf(x[i]));
-            bad |= !(fabsf(x[i]) <= 3.40282347e38f);
+        for (int i = 0; i < ROWS; ++i) {
+            const int row = row0 + i * step;
+            if (row < rows) {
+                const T *src = row < a.Hq ? (const T *)a.q + (int64_t)token * a.ld_q + row * D
+                             : row < a.Hq + Hkv ? (const T *)a.k + (int64_t)token * a.ld_k + (row - a.Hq) * D
+                                                : (const T *)a.v + (int64_t)token * a.ld_v + (row - a.Hq - Hkv) * D;
+                raw[i][0] = load4(src + at.a);
+                raw[i][1] = load4(src + at.b);
+            }
         }
-        m = row_max<LPR>(bad ? INFINITY : m);
-        const bool fin = m <= 3.40282347e38f;
-        const float s = fin ? fmaxf(m / kE4m3Max, kMinScale) : NAN;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fin ? x[i] / s : 0.f;
-        uint2 w;
-        w.x = pack_e4m3(x[0], x[1], x[2], x[3]);
-        w.y = pack_e4m3(x[4], x[5], x[6], x[7]);
-        *(uint2 *)((uint8_t *)(kind == 1 ? a.c.k : a.c.v) + slot * D + e) = w;
-        if (l == 0) (kind == 1 ? a.c.k_scale : a.c.v_scale)[slot] = s;
+        for (int i = 0; i < ROWS; ++i) {
+            const int row = row0 + i * step;
+            if (row >= rows) break;
+            const int kind = row < a.Hq ? 0 : row < a.Hq + Hkv ? 1 : 2;  // q, k, v
+            const int head = row - (kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + Hkv);
+            float x[8];          // values a .. a + 3, then b .. b + 3
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = value(raw[i][q >> 2], q & 3);
+            if (kind < 2) {
+                if (kind == 0 ? a.q_weight != nullptr : a.k_weight != nullptr) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) ss = fmaf(x[q], x[q], ss);
+                    const float inv = 1.0f / sqrtf(row_sum<LPR>(ss) * (1.0f / D) + a.eps);
+                    if (kind == 0) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) x[q] = x[q] * inv * value(qw[q >> 2], q & 3);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) x[q] = x[q] * inv * value(kw[q >> 2], q & 3);
+                    }
+                }
+                if (at.in) {
+                    float y[8];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float c = cs[q >> 1][2 * (q & 1)], s = cs[q >> 1][2 * (q & 1) + 1];
+                        const float p0 = a.interleaved ? x[2 * q] : x[q], p1 = a.interleaved ? x[2 * q + 1] : x[4 + q];
+                        const float y0 = p0 * c - p1 * s, y1 = p1 * c + p0 * s;
+                        y[2 * q] = y0;
+                        y[2 * q + 1] = y1;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) x[q] = a.interleaved ? y[q] : q < 4 ? y[2 * q] : y[2 * (q - 4) + 1];
+                }
+                if (!there) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) x[q] = NAN;
+                }
+            }
+            if (kind == 0) {
+                const u32x4_t w = bf16x8(x);
+                uint16_t *o = a.out_q + ((size_t)token * a.Hq + head) * D;
+                *(u32x2_t *)(o + at.a) = u32x2_t{w[0], w[1]};
+                *(u32x2_t *)(o + at.b) = u32x2_t{w[2], w[3]};
+                continue;
+            }
+            if (!good) continue;
+            const size_t slot = ((size_t)page * Hkv + head) * a.c.size + (t & (a.c.size - 1));
+            if constexpr (!FP8) {
+                const u32x4_t w = bf16x8(x);
+                uint16_t *o = (uint16_t *)(kind == 1 ? a.c.k : a.c.v) + slot * D;
+                *(u32x2_t *)(o + at.a) = u32x2_t{w[0], w[1]};
+                *(u32x2_t *)(o + at.b) = u32x2_t{w[2], w[3]};
+            } else {
+                float m = 0.f;
+                int bad = 0;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    m = fmaxf(m, fabsf(x[q]));
+                    bad |= !(fabsf(x[q]) <= 3.40282347e38f);
+                }
+                m = row_max<LPR>(bad ? INFINITY : m);
+                const bool fin = m <= 3.40282347e38f;
+                const float s = fin ? fmaxf(m / kE4m3Max, kMinScale) : 1.0f;
+                // x / s: the product with the reciprocal and one correction
+                const float inv = 1.0f / s;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float d = x[q] * inv;
+                    x[q] = fin ? fmaf(fmaf(-d, s, x[q]), inv, d) : 0.f;
+                }
+                uint8_t *o = (uint8_t *)(kind == 1 ? a.c.k : a.c.v) + slot * D;
+                *(uint32_t *)(o + at.a) = pack_e4m3(x[0], x[1], x[2], x[3]);
+                *(uint32_t *)(o + at.b) = pack_e4m3(x[4], x[5], x[6], x[7]);
+                if (l == 0) (kind == 1 ? a.c.k_scale : a.c.v_scale)[slot] = fin ? s : NAN;
+            }
+        }
     }
 }
 
@@ -182,51 +261,79 @@ struct ReadArgs {
 template <typename T>
 __device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
     if constexpr (sizeof(T) == 2) {
-        *(uint4 *)p = bf16x8(x);
+        *(u32x4_t *)p = bf16x8(x);
     } else {
-        *(float4 *)p = make_float4(x[0], x[1], x[2], x[3]);
-        *(float4 *)(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        *(f32x4_t *)p = f32x4_t{x[0], x[1], x[2], x[3]};
+        *(f32x4_t *)(p + 4) = f32x4_t{x[4], x[5], x[6], x[7]};
     }
 }
 
-// One workgroup per token of a request (y); thread: 8 values of a head row.
+constexpr int kReadTokens = 4;
+
+// One workgroup per kReadTokens tokens of a request (y); a thread takes 8
+// values of a head row of each, all loads before the first store.
+// Bound by HBM: pages read, rows written.
 template <typename T, bool FP8, int D>
 __global__ void __launch_bounds__(kBlock) kv_read_kernel(ReadArgs a) {
-    const int r = blockIdx.y, i = blockIdx.x;
+    const int r = blockIdx.y, i0 = blockIdx.x * kReadTokens;
     const int n = a.len[r], st = a.start[r];
     const bool sane = n >= 0 && n <= a.L && in_table(st, n, a.c.max_pages, a.c.shift);
-    if (sane && i >= n) return;
-    int page = -1;
-    const int t = st + i;
-    if (sane) {
-        page = a.c.table[(size_t)r * a.c.max_pages + (t >> a.c.shift)];
-        if (page < 0 || page >= a.c.num_pages) page = -1;
-    }
-    if (page < 0 && threadIdx.x == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+    const int end = sane ? n : a.L;  // rows of this request that are written
+    if (i0 >= end) return;
     const int Hkv = a.c.heads;
-    for (int j = threadIdx.x; j < 2 * Hkv * (D / 8); j += kBlock) {
-        const int half = Hkv * (D / 8);
+    int64_t slot[kReadTokens];       // of head 0; -1: a bad page or request
+    bool bad = false;
+#pragma unroll
+    for (int q = 0; q < kReadTokens; ++q) {
+        const int t = st + min(i0 + q, end - 1);
+        const int page = sane ? a.c.table[(size_t)r * a.c.max_pages + (t >> a.c.shift)] : -1;
+        const bool good = page >= 0 && page < a.c.num_pages;
+        slot[q] = good ? (int64_t)page * Hkv * a.c.size + (t & (a.c.size - 1)) : -1;
+        bad |= !good;
+    }
+    if (bad && threadIdx.x == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+    const int half = Hkv * (D / 8);
+    for (int j = threadIdx.x; j < 2 * half; j += kBlock) {
         const bool isv = j >= half;
         const int jj = isv ? j - half : j, head = jj / (D / 8), e = (jj % (D / 8)) * 8;
-        T *dst = (T *)(isv ? a.out_v : a.out_k) + (((size_t)r * a.L + i) * Hkv + head) * D + e;
-        float x[8] = {NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN};
-        if (page >= 0) {
-            const size_t slot = ((size_t)page * Hkv + head) * a.c.size + (t & (a.c.size - 1));
-            if constexpr (!FP8) {
-                VecLoad<uint16_t, 8>::run((const uint16_t *)(isv ? a.c.v : a.c.k) + slot * D, e, x);
-            } else {
-                const uint2 w = *(const uint2 *)((const uint8_t *)(isv ? a.c.v : a.c.k) + slot * D + e);
-                const float s = (isv ? a.c.v_scale : a.c.k_scale)[slot];
-                const uint32_t b[4] = {e4m3_bf16<false>(w.x), e4m3_bf16<true>(w.x),
-                                       e4m3_bf16<false>(w.y), e4m3_bf16<true>(w.y)};
+        T *dst = (T *)(isv ? a.out_v : a.out_k) + (((size_t)r * a.L + i0) * Hkv + head) * D + e;
+        const char *pages = (const char *)(isv ? a.c.v : a.c.k);
+        const float *scales = isv ? a.c.v_scale : a.c.k_scale;
+        typedef typename std::conditional<FP8, u32x2_t, u32x4_t>::type raw_t;
+        raw_t w[kReadTokens];
+        float s[kReadTokens];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    x[2 * q] = bf16_lo(b[q]) * s;
-                    x[2 * q + 1] = bf16_hi(b[q]) * s;
+        for (int q = 0; q < kReadTokens; ++q) {
+            const int64_t at = max(slot[q], (int64_t)0) + (int64_t)head * a.c.size;  // slot 0 is there
+            w[q] = *(const raw_t *)(pages + (at * D + e) * (FP8 ? 1 : 2));
+            if constexpr (FP8) s[q] = scales[at];
+        }
+#pragma unroll
+        for (int q = 0; q < kReadTokens; ++q) {
+            if (i0 + q >= end) break;
+            float x[8];
+            if constexpr (!FP8) {
+                const uint32_t b[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[2 * i] = bf16_lo(b[i]);
+                    x[2 * i + 1] = bf16_hi(b[i]);
+                }
+            } else {
+                const uint32_t b[4] = {e4m3_bf16<false>(w[q].x), e4m3_bf16<true>(w[q].x),
+                                       e4m3_bf16<false>(w[q].y), e4m3_bf16<true>(w[q].y)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[2 * i] = bf16_lo(b[i]) * s[q];
+                    x[2 * i + 1] = bf16_hi(b[i]) * s[q];
                 }
             }
+            if (slot[q] < 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = NAN;
+            }
+            store8(dst + (size_t)q * Hkv * D, x);
         }
-        store8(dst, x);
     }
 }
 
@@ -243,9 +350,10 @@ struct CommitArgs {
 };
 
 // One workgroup per request.  Every column (16 bytes of one head row of K or
-// V, or one scale) belongs to one thread, which moves its rows in ascending
-// order: path[i] > i, and the path rises, so a row is read before any move
-// writes to it.
+// V, or one scale) belongs to one thread, which moves its rows eight at a time
+// in ascending order, reading the eight before it writes them: the path rises
+// from path[i] >= i + 1 on, so a later row's source path[j] >= j + 1 lies
+// behind every slot i + 1 <= j written for earlier ones.
 __global__ void __launch_bounds__(kBlock) kv_commit_kernel(CommitArgs a) {
     __shared__ int64_t from_s[SPEC_TREE_MAX_NODES], to_s[SPEC_TREE_MAX_NODES];
     const int r = blockIdx.x, tid = threadIdx.x;
@@ -280,27 +388,53 @@ __global__ void __launch_bounds__(kBlock) kv_commit_kernel(CommitArgs a) {
     const int cols = a.row_bytes / 16, all = 2 * a.c.heads * cols;
     for (int j = tid; j < all; j += kBlock) {
         const int head = j / cols % a.c.heads, col = j % cols;
-        char *base = (char *)(j >= a.c.heads * cols ? a.c.v : a.c.k) + col * 16;
-        for (int i = 0; i < nA; ++i) {
-            const int64_t hs = (int64_t)head * a.c.size;
-            const uint4 w = *(const uint4 *)(base + (from_s[i] + hs) * a.row_bytes);
-            *(uint4 *)(base + (to_s[i] + hs) * a.row_bytes) = w;
+        char *base = (char *)(j >= a.c.heads * cols ? a.c.v : a.c.k) +
+                     (int64_t)head * a.c.size * a.row_bytes + col * 16;
+        for (int i0 = 0; i0 < nA; i0 += 8) {
+            u32x4_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < nA) w[i] = *(const u32x4_t *)(base + from_s[i0 + i] * a.row_bytes);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < nA) *(u32x4_t *)(base + to_s[i0 + i] * a.row_bytes) = w[i];
         }
     }
     if (a.c.k_scale) {
         for (int j = tid; j < 2 * a.c.heads; j += kBlock) {
             float *base = (j >= a.c.heads ? a.c.v_scale : a.c.k_scale) +
                           (int64_t)(j % a.c.heads) * a.c.size;
-            for (int i = 0; i < nA; ++i) base[to_s[i]] = base[from_s[i]];
+            for (int i0 = 0; i0 < nA; i0 += 8) {
+                float w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i0 + i < nA) w[i] = base[from_s[i0 + i]];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i0 + i < nA) base[to_s[i0 + i]] = w[i];
+            }
         }
     }
 }
 
+// Few tokens: one head row a thread, so that latency is a row's; from about
+// 2000 tokens (eight workgroups to a compute unit) on, a workgroup per token.
+template <typename T, bool FP8, int D>
+static void launch_write(const WriteArgs &a, int64_t tokens, int rows, hipStream_t st) {
+    constexpr int RPB = kBlock / (D / 8);
+    const int y = (rows + RPB - 1) / RPB;
+    if (tokens < 2048)
+        hipLaunchKernelGGL((qkv_write_kernel<T, FP8, D, 1>), dim3((unsigned)tokens, (unsigned)y),
+                           dim3(kBlock), 0, st, a);
+    else
+        hipLaunchKernelGGL((qkv_write_kernel<T, FP8, D, 4>), dim3((unsigned)tokens), dim3(kBlock), 0,
+                           st, a);
+}
 template <typename T, bool FP8>
-static void launch_write(const WriteArgs &a, int D, dim3 grid, hipStream_t st) {
-    if (D == 64) hipLaunchKernelGGL((qkv_write_kernel<T, FP8, 64>), grid, dim3(kBlock), 0, st, a);
-    else if (D == 128) hipLaunchKernelGGL((qkv_write_kernel<T, FP8, 128>), grid, dim3(kBlock), 0, st, a);
-    else hipLaunchKernelGGL((qkv_write_kernel<T, FP8, 256>), grid, dim3(kBlock), 0, st, a);
+static void launch_write(const WriteArgs &a, int D, int64_t tokens, int rows, hipStream_t st) {
+    if (D == 64) launch_write<T, FP8, 64>(a, tokens, rows, st);
+    else if (D == 128) launch_write<T, FP8, 128>(a, tokens, rows, st);
+    else launch_write<T, FP8, 256>(a, tokens, rows, st);
 }
 
 template <typename T, bool FP8>
@@ -372,15 +506,14 @@ int spec_qkv_write(const void *q, const void *k, const void *v, int dtype, int64
     a.ctl = (Control *)workspace;
     const int rpb = kBlock / (D / 8), rows = Hq + 2 * Hkv;
     if ((rows + rpb - 1) / rpb > 65535) return SPEC_EUNSUPPORTED;
-    const dim3 grid((unsigned)tokens, (unsigned)((rows + rpb - 1) / rpb));
     hipStream_t st = (hipStream_t)stream;
     const bool fp8 = cache_dtype == SPEC_E4M3;
     if (dtype == SPEC_BF16) {
-        if (fp8) launch_write<uint16_t, true>(a, D, grid, st);
-        else launch_write<uint16_t, false>(a, D, grid, st);
+        if (fp8) launch_write<uint16_t, true>(a, D, tokens, rows, st);
+        else launch_write<uint16_t, false>(a, D, tokens, rows, st);
     } else {
-        if (fp8) launch_write<float, true>(a, D, grid, st);
-        else launch_write<float, false>(a, D, grid, st);
+        if (fp8) launch_write<float, true>(a, D, tokens, rows, st);
+        else launch_write<float, false>(a, D, tokens, rows, st);
     }
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
 }
@@ -409,7 +542,7 @@ int spec_kv_read(const void *k_cache, const void *v_cache, int cache_dtype, cons
     a.out_k = out_k;
     a.out_v = out_v;
     a.ctl = (Control *)workspace;
-    const dim3 grid((unsigned)max_len, (unsigned)R);
+    const dim3 grid((unsigned)((max_len + kReadTokens - 1) / kReadTokens), (unsigned)R);
     hipStream_t st = (hipStream_t)stream;
     const bool fp8 = cache_dtype == SPEC_E4M3;
     if (out_dtype == SPEC_BF16) {

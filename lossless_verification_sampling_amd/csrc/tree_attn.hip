@@ -35,11 +35,6 @@ namespace sv {
 struct Cut;
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-// (vector types of the language, not the runtime's structs: arrays of those
-// end up in scratch memory)
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kStep = 32;              // tokens a wave takes at a time
 constexpr int kUnit = kStep * kWaves;  // tokens of one unit of work

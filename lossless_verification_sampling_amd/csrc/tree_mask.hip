@@ -62,9 +62,16 @@ __global__ void __launch_bounds__(kMaskNodes) tree_mask_kernel(MaskArgs a) {
     __syncthreads();
     const int cnt = min(kMaskNodes, a.M - v0) * a.W;
     uint32_t *out = a.mask + (rb + v0) * a.W;
+    const int down = kMaskNodes / a.W, right = kMaskNodes - down * a.W;
+    int row = tid / a.W, col = tid - row * a.W;
     for (int i = tid; i < cnt; i += kMaskNodes) {
-        const int row = i / a.W;
-        out[i] = rows[row * ld + (i - row * a.W)];
+        out[i] = rows[row * ld + col];
+        row += down;
+        col += right;
+        if (col >= a.W) {
+            col -= a.W;
+            ++row;
+        }
     }
     if (!ok && tid == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
 }
