@@ -629,49 +629,74 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+def _all(dev: int, *specs):
+    """Checks (tensor, name, dtype, shape) for dense tensors on device `dev`;
+    a tensor may be None.  (The quick way through; _check words the error.)"""
+    for t, name, dtype, shape in specs:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or
+                              t.get_device() != dev or not t.is_contiguous()):
+            _check(t, name, dtype, shape, torch.device("cuda", dev))
+
+
+def _stream_of(stream: Optional[torch.cuda.Stream], dev: int) -> int:
+    return (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+
+
+_CACHE_CODES = {torch.bfloat16: SPEC_BF16, torch.float8_e4m3fn: SPEC_E4M3}
+
+
 def _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev):
-    """Checks a layer's pages and returns (dtype code, P, Hkv, page size, D,
-    page table width)."""
-    _need(k_cache.dim() == 4, "k_cache must be [pages, heads, page size, D]")
-    P, Hkv, size, D = shape = tuple(k_cache.shape)
-    code = SPEC_BF16 if k_cache.dtype == torch.bfloat16 else SPEC_E4M3
-    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise TypeError(f"cache pages must be bfloat16 or float8_e4m3fn, got {k_cache.dtype}")
-    _check(k_cache, "k_cache", None, None, dev)
-    _check(v_cache, "v_cache", k_cache.dtype, shape, dev)
-    if code == SPEC_E4M3:
-        _need(k_scale is not None and v_scale is not None, "e4m3 pages need k_scale and v_scale")
-        _check(k_scale, "k_scale", torch.float32, shape[:3], dev)
-        _check(v_scale, "v_scale", torch.float32, shape[:3], dev)
-    else:
-        _need(k_scale is None and v_scale is None, "bfloat16 pages have no scales")
+    """Checks a layer's pages on device `dev` and returns (dtype code, P, Hkv,
+    page size, D, page table width)."""
+    dtype = k_cache.dtype
+    code = _CACHE_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"cache pages must be bfloat16 or float8_e4m3fn, got {dtype}")
+    shape = k_cache.shape
+    _need(len(shape) == 4, "k_cache must be [pages, heads, page size, D]")
     _need(page_table.dim() == 2, "page_table must be [R, max_pages]")
     wide = page_table.shape[1]
-    _check(page_table, "page_table", torch.int32, (R, wide), dev)
+    if code == SPEC_E4M3:
+        _need(k_scale is not None and v_scale is not None, "e4m3 pages need k_scale and v_scale")
+    else:
+        _need(k_scale is None and v_scale is None, "bfloat16 pages have no scales")
+    _all(dev, (k_cache, "k_cache", dtype, shape), (v_cache, "v_cache", dtype, shape),
+         (k_scale, "k_scale", torch.float32, shape[:3]),
+         (v_scale, "v_scale", torch.float32, shape[:3]),
+         (page_table, "page_table", torch.int32, (R, wide)))
+    P, Hkv, size, D = shape
     return code, P, Hkv, size, D, wide
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    _need(dev >= 0, f"{name} must be a device tensor")
+    return dev
 
 
 def _raw(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _ordered_heads(t: torch.Tensor, name: str, dev) -> int:
+def _ordered_heads(t: torch.Tensor, name: str, dev: int) -> int:
     """Elements from one token's heads to the next of [R, M, H, D] whose
     tokens are evenly spaced and whose heads are dense."""
-    _need(t.is_cuda and t.device == dev, f"{name} must be on {dev}")
+    _need(t.get_device() == dev, f"{name} must be on cuda:{dev}")
     R, M, H, D = t.shape
-    s = t.stride()
-    ld = s[1] if M > 1 else s[0] if R > 1 else H * D
-    _need((D == 1 or s[3] == 1) and (H == 1 or s[2] == D) and ld >= H * D and
-          (R == 1 or M == 1 or s[0] == M * ld),
+    s0, s1, s2, s3 = t.stride()
+    ld = s1 if M > 1 else s0 if R > 1 else H * D
+    _need((D == 1 or s3 == 1) and (H == 1 or s2 == D) and ld >= H * D and
+          (R == 1 or M == 1 or s0 == M * ld),
           f"{name} must hold dense heads at evenly spaced tokens")
     return ld
 
 
-def _cache_buf(workspace, dev, need, stream):
-    ws = workspace or default_workspace(dev)
+def _cache_buf(workspace, dev: int, need: int, stream):
+    ws = workspace or _default_ws.get(("cuda", dev)) or default_workspace(torch.device("cuda", dev))
     buf = ws.buf
-    return buf if buf is not None and buf.numel() >= need else ws.ensure(need, stream)
+    if buf is None or buf.numel() < need:
+        buf = ws.ensure(need, stream)
+    return buf.data_ptr(), buf.numel()
 
 
 def spec_tree_mask(parent: torch.Tensor, n_nodes: torch.Tensor, ctx_len: torch.Tensor, *,
@@ -681,23 +706,22 @@ def spec_tree_mask(parent: torch.Tensor, n_nodes: torch.Tensor, ctx_len: torch.T
     """Positions and ancestor bits of drafted trees, once a step for all
     layers.  parent [R, M], n_nodes [R], ctx_len [R] int32.  Returns
     (positions [R, M] int32, mask [R, M, (M + 31) // 32] int32 bit words)."""
-    R, M = parent.shape
-    dev = parent.device
-    W = (M + 31) // 32
-    _check(parent, "parent", torch.int32, None, dev)
-    _check(n_nodes, "n_nodes", torch.int32, (R,), dev)
-    _check(ctx_len, "ctx_len", torch.int32, (R,), dev)
-    pos = out_positions if out_positions is not None else torch.empty((R, M), dtype=torch.int32,
-                                                                      device=dev)
-    mask = out_mask if out_mask is not None else torch.empty((R, M, W), dtype=torch.int32,
-                                                             device=dev)
-    _check(pos, "out_positions", torch.int32, (R, M), dev)
-    _check(mask, "out_mask", torch.int32, (R, M, W), dev)
-    buf = _cache_buf(workspace, dev, 256, stream)
+    R, M = shape = parent.shape
+    dev = _device(parent, "parent")
+    words = (R, M, (M + 31) // 32)
+    i32 = torch.int32
+    pos = out_positions if out_positions is not None else torch.empty(shape, dtype=i32,
+                                                                      device=parent.device)
+    mask = out_mask if out_mask is not None else torch.empty(words, dtype=i32, device=parent.device)
+    _all(dev, (parent, "parent", i32, shape), (n_nodes, "n_nodes", i32, (R,)),
+         (ctx_len, "ctx_len", i32, (R,)), (pos, "out_positions", i32, shape),
+         (mask, "out_mask", i32, words))
+    buf, size = _cache_buf(workspace, dev, 256, stream)
     st = _lib.spec_tree_mask(parent.data_ptr(), n_nodes.data_ptr(), ctx_len.data_ptr(), R, M,
-                             int(window), pos.data_ptr(), mask.data_ptr(), buf.data_ptr(),
-                             buf.numel(), _stream_ptr(stream, dev))
-    _raise(st, "spec_tree_mask")
+                             int(window), pos.data_ptr(), mask.data_ptr(), buf, size,
+                             _stream_of(stream, dev))
+    if st:
+        _raise(st, "spec_tree_mask")
     return pos, mask
 
 
@@ -717,43 +741,47 @@ def spec_qkv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     positions [R, M] int32 (ctx_len + index without).  Token v < n_nodes[r] of
     request r goes to cache token ctx_len[r] + v.  Returns the queries
     [R, M, Hq, D] bfloat16 (out_q), or None without q."""
-    _need(k.dim() == 4 and v.dim() == 4, "k and v must be [R, M, heads, D]")
-    R, M, Hkv, D = shape = tuple(k.shape)
-    dev = k.device
+    shape = k.shape
+    _need(len(shape) == 4 and v.shape == shape, "k and v must be [R, M, heads, D], both alike")
+    R, M, Hkv, D = shape
+    dev = _device(k, "k")
     code, P, H, size, Dc, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev)
-    _need(H == Hkv and Dc == D and tuple(v.shape) == shape, "k, v and the cache differ in heads or D")
+    _need(H == Hkv and Dc == D, "k, v and the cache differ in heads or D")
+    dtype = k.dtype
     dt = _dtype(k)
-    _need(v.dtype == k.dtype and (q is None or q.dtype == k.dtype), "q, k and v differ in type")
+    _need(v.dtype is dtype and (q is None or q.dtype is dtype), "q, k and v differ in type")
     ld_k, ld_v = _ordered_heads(k, "k", dev), _ordered_heads(v, "v", dev)
     Hq = ld_q = 0
     if q is not None:
-        _need(q.dim() == 4 and q.shape[0] == R and q.shape[1] == M and q.shape[3] == D,
-              "q must be [R, M, Hq, D]")
-        Hq, ld_q = q.shape[2], _ordered_heads(q, "q", dev)
+        qs = q.shape
+        _need(len(qs) == 4 and qs[0] == R and qs[1] == M and qs[3] == D, "q must be [R, M, Hq, D]")
+        Hq, ld_q = qs[2], _ordered_heads(q, "q", dev)
         if out_q is None:
-            out_q = torch.empty((R, M, Hq, D), dtype=torch.bfloat16, device=dev)
-        _check(out_q, "out_q", torch.bfloat16, (R, M, Hq, D), dev)
+            out_q = torch.empty(qs, dtype=torch.bfloat16, device=k.device)
     else:
+        qs = None
         _need(q_weight is None and out_q is None, "q_weight and out_q belong to q")
-    _check(q_weight, "q_weight", k.dtype, (D,), dev)
-    _check(k_weight, "k_weight", k.dtype, (D,), dev)
     max_pos = rot = 0
+    rs = None
     if rope is not None:
-        _need(rope.dim() == 3 and rope.shape[2] == 2, "rope must be [max_pos, rot / 2, 2]")
-        _check(rope, "rope", torch.float32, None, dev)
-        max_pos, rot = rope.shape[0], 2 * rope.shape[1]
-    _check(positions, "positions", torch.int32, (R, M), dev)
-    _check(ctx_len, "ctx_len", torch.int32, (R,), dev)
-    _check(n_nodes, "n_nodes", torch.int32, (R,), dev)
-    buf = _cache_buf(workspace, dev, 256, stream)
+        rs = rope.shape
+        _need(len(rs) == 3 and rs[2] == 2, "rope must be [max_pos, rot / 2, 2]")
+        max_pos, rot = rs[0], 2 * rs[1]
+    i32 = torch.int32
+    _all(dev, (out_q, "out_q", torch.bfloat16, qs), (q_weight, "q_weight", dtype, (D,)),
+         (k_weight, "k_weight", dtype, (D,)), (rope, "rope", torch.float32, rs),
+         (positions, "positions", i32, (R, M)), (ctx_len, "ctx_len", i32, (R,)),
+         (n_nodes, "n_nodes", i32, (R,)))
+    buf, room = _cache_buf(workspace, dev, 256, stream)
     st = _lib.spec_qkv_write(_raw(q), k.data_ptr(), v.data_ptr(), dt, ld_q, ld_k, ld_v,
                              _raw(q_weight), _raw(k_weight), eps, _raw(rope), max_pos, rot,
                              int(interleaved), _raw(positions), ctx_len.data_ptr(),
                              n_nodes.data_ptr(), page_table.data_ptr(), wide, R, M, Hq, Hkv, D,
                              k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
-                             _raw(v_scale), P, size, _raw(out_q), buf.data_ptr(), buf.numel(),
-                             _stream_ptr(stream, dev))
-    _raise(st, "spec_qkv_write")
+                             _raw(v_scale), P, size, _raw(out_q), buf, room,
+                             _stream_of(stream, dev))
+    if st:
+        _raise(st, "spec_qkv_write")
     return out_q
 
 
@@ -765,27 +793,28 @@ def spec_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
                  stream=None):
     """Reads tokens start[r] .. start[r] + length[r] - 1 of every request.
     Returns (k, v) [R, max_len, Hkv, D] in `dtype` (bfloat16 or float32, or
-    that of the given outputs); rows past length[r] are left as they were."""
-    R, dev = page_table.shape[0], k_cache.device
+    that of a given output); rows past length[r] are left as they were."""
+    R, dev = page_table.shape[0], _device(k_cache, "k_cache")
     code, P, Hkv, size, D, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev)
-    _check(start, "start", torch.int32, (R,), dev)
-    _check(length, "length", torch.int32, (R,), dev)
-    if out_k is not None:
-        dtype = out_k.dtype
-    shape = (R, int(max_len), Hkv, D)
+    max_len = int(max_len)
+    _need(max_len >= 0, "max_len must not be negative")
+    given = out_k if out_k is not None else out_v
+    if given is not None:
+        dtype = given.dtype
+    shape = (R, max_len, Hkv, D)
     if out_k is None:
-        out_k = torch.empty(shape, dtype=dtype, device=dev)
+        out_k = torch.empty(shape, dtype=dtype, device=k_cache.device)
     if out_v is None:
-        out_v = torch.empty(shape, dtype=dtype, device=dev)
-    _check(out_k, "out_k", dtype, shape, dev)
-    _check(out_v, "out_v", dtype, shape, dev)
-    buf = _cache_buf(workspace, dev, 256, stream)
+        out_v = torch.empty(shape, dtype=dtype, device=k_cache.device)
+    _all(dev, (start, "start", torch.int32, (R,)), (length, "length", torch.int32, (R,)),
+         (out_k, "out_k", dtype, shape), (out_v, "out_v", dtype, shape))
+    buf, room = _cache_buf(workspace, dev, 256, stream)
     st = _lib.spec_kv_read(k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
                            _raw(v_scale), P, size, page_table.data_ptr(), wide, start.data_ptr(),
-                           length.data_ptr(), R, int(max_len), Hkv, D, out_k.data_ptr(),
-                           out_v.data_ptr(), _dtype(out_k), buf.data_ptr(), buf.numel(),
-                           _stream_ptr(stream, dev))
-    _raise(st, "spec_kv_read")
+                           length.data_ptr(), R, max_len, Hkv, D, out_k.data_ptr(),
+                           out_v.data_ptr(), _dtype(out_k), buf, room, _stream_of(stream, dev))
+    if st:
+        _raise(st, "spec_kv_read")
     return out_k, out_v
 
 
@@ -797,21 +826,20 @@ def spec_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: tor
     """Moves the accepted path's rows (spec_tree_verify's accepted [R] and path
     [R, M]) behind the context, in place.  Returns the new context lengths."""
     R, M = path.shape
-    dev = k_cache.device
+    dev = _device(k_cache, "k_cache")
     code, P, Hkv, size, D, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev)
-    _check(ctx_len, "ctx_len", torch.int32, (R,), dev)
-    _check(accepted, "accepted", torch.int32, (R,), dev)
-    _check(path, "path", torch.int32, (R, M), dev)
+    i32 = torch.int32
     if out_ctx_len is None:
-        out_ctx_len = torch.empty((R,), dtype=torch.int32, device=dev)
-    _check(out_ctx_len, "out_ctx_len", torch.int32, (R,), dev)
-    buf = _cache_buf(workspace, dev, 256, stream)
+        out_ctx_len = torch.empty((R,), dtype=i32, device=k_cache.device)
+    _all(dev, (ctx_len, "ctx_len", i32, (R,)), (accepted, "accepted", i32, (R,)),
+         (path, "path", i32, (R, M)), (out_ctx_len, "out_ctx_len", i32, (R,)))
+    buf, room = _cache_buf(workspace, dev, 256, stream)
     st = _lib.spec_kv_commit(k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
                              _raw(v_scale), P, size, page_table.data_ptr(), wide,
                              ctx_len.data_ptr(), accepted.data_ptr(), path.data_ptr(), R, M, Hkv,
-                             D, out_ctx_len.data_ptr(), buf.data_ptr(), buf.numel(),
-                             _stream_ptr(stream, dev))
-    _raise(st, "spec_kv_commit")
+                             D, out_ctx_len.data_ptr(), buf, room, _stream_of(stream, dev))
+    if st:
+        _raise(st, "spec_kv_commit")
     return out_ctx_len
 
 
@@ -828,32 +856,32 @@ def spec_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     cache: the context and, by `mask` (spec_tree_mask), their ancestors; without
     a mask the tokens are a chain.  scale defaults to D ** -0.5.  Returns
     (out [R, M, Hq, D] bfloat16, log-sum-exp [R, M, Hq] float32 or None)."""
-    _need(q.dim() == 4, "q must be [R, M, Hq, D]")
-    R, M, Hq, D = shape = tuple(q.shape)
-    dev = q.device
+    shape = q.shape
+    _need(len(shape) == 4, "q must be [R, M, Hq, D]")
+    R, M, Hq, D = shape
+    dev = _device(q, "q")
     code, P, Hkv, size, Dc, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev)
     _need(Dc == D, "q and the cache differ in D")
-    _check(q, "q", torch.bfloat16, None, dev)
-    _check(ctx_len, "ctx_len", torch.int32, (R,), dev)
-    _check(n_nodes, "n_nodes", torch.int32, (R,), dev)
-    _check(mask, "mask", torch.int32, (R, M, (M + 31) // 32), dev)
-    _check(positions, "positions", torch.int32, (R, M), dev)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _check(out, "out", torch.bfloat16, shape, dev)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     if out_lse is None and want_lse:
-        out_lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
-    _check(out_lse, "out_lse", torch.float32, shape[:3], dev)
+        out_lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+    i32 = torch.int32
+    _all(dev, (q, "q", torch.bfloat16, shape), (ctx_len, "ctx_len", i32, (R,)),
+         (n_nodes, "n_nodes", i32, (R,)), (mask, "mask", i32, (R, M, (M + 31) // 32)),
+         (positions, "positions", i32, (R, M)), (out, "out", torch.bfloat16, shape),
+         (out_lse, "out_lse", torch.float32, shape[:3]))
     need = _lib.spec_tree_attention_workspace_bytes(R, M, Hq, Hkv, D)
     if need == 0:
         raise SpecError(-5, "spec_tree_attention_workspace_bytes")
-    buf = _cache_buf(workspace, dev, need, stream)
+    buf, room = _cache_buf(workspace, dev, need, stream)
     st = _lib.spec_tree_attention(q.data_ptr(), SPEC_BF16, k_cache.data_ptr(), v_cache.data_ptr(),
                                   code, _raw(k_scale), _raw(v_scale), P, size,
                                   page_table.data_ptr(), wide, ctx_len.data_ptr(),
                                   n_nodes.data_ptr(), _raw(mask), _raw(positions),
                                   D ** -0.5 if scale is None else scale, int(window), R, M, Hq,
-                                  Hkv, D, out.data_ptr(), _raw(out_lse), buf.data_ptr(),
-                                  buf.numel(), _stream_ptr(stream, dev))
-    _raise(st, "spec_tree_attention")
+                                  Hkv, D, out.data_ptr(), _raw(out_lse), buf, room,
+                                  _stream_of(stream, dev))
+    if st:
+        _raise(st, "spec_tree_attention")
     return out, out_lse

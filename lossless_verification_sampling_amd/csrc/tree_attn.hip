@@ -1204,8 +1204,11 @@ __global__ void __launch_bounds__(kBlock) attn_join_kernel(AttnArgs a) {
 }
 
 // Which launch a call takes and its row tile.  A request's largest count of
-// rows per key head decides: up to 32 the waves of a workgroup divide the
-// tokens and keep everything in registers; more rows divide the waves.
+// rows per key head decides: up to 32 (16 at D = 256, for the registers) the
+// waves of a workgroup divide the tokens; more rows divide the waves.  There
+// three 16-row tiles a wave reach 781 TFLOP/s on long chunks against 649 with
+// two (D = 128, e4m3: each operand from shared memory serves three products),
+// so two are taken where they leave over 13% fewer rows empty.
 struct Shape {
     bool wide;
     int RT, TR, groups;
@@ -1214,7 +1217,11 @@ inline Shape shape_of(int64_t rows, int D) {
     Shape s;
     s.wide = rows > (D == 256 ? 16 : 32);
     if (!s.wide) s.RT = rows <= 16 ? 1 : 2;
-    else s.RT = D == 256 || rows <= 64 ? 1 : rows <= 128 ? 2 : 3;
+    else if (D == 256 || rows <= 64) s.RT = 1;
+    else {
+        const int64_t two = (rows + 127) / 128 * 128, three = (rows + 191) / 192 * 192;
+        s.RT = two * 100 < three * 87 ? 2 : 3;
+    }
     s.TR = 16 * s.RT * (s.wide ? kWaves : 1);
     s.groups = D <= 128 ? kMaxGroups : kMaxGroups / 2;
     return s;
@@ -1227,14 +1234,22 @@ static void launch_attn(const AttnArgs &a, hipStream_t st) {
         hipLaunchKernelGGL((attn_wide_kernel<FP8, D, RT>), dim3(a.groups), dim3(kBlock), 0, st, a);
     else
         hipLaunchKernelGGL((attn_kernel<FP8, D, RT>), dim3(a.groups), dim3(kBlock), 0, st, a);
-    hipLaunchKernelGGL((attn_join_kernel<D, TR, !WIDE>), dim3(a.groups - 1, WIDE ? TR / kWaves : TR),
-                       dim3(kBlock), 0, st, a);
+    // items enough for every eighth range: eight parts an item at most, on the
+    // average; fewer items: more parts than one wave reads at a time
+    const int64_t items = (int64_t)a.R * a.c.heads * ((a.M * a.G + TR - 1) / TR);
+    if (WIDE || items * 8 >= a.groups)
+        hipLaunchKernelGGL((attn_join_kernel<D, TR, false>), dim3(a.groups - 1, TR / kWaves), dim3(kBlock), 0, st, a);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<D, TR, true>), dim3(a.groups - 1, TR), dim3(kBlock), 0, st, a);
 }
 template <bool FP8, int D>
 static void launch_attn(const AttnArgs &a, const Shape &s, hipStream_t st) {
     if (s.wide) {
         if (s.RT == 1) launch_attn<FP8, D, 1, true>(a, st);
-        else if constexpr (D <= 128) { if (s.RT == 2) launch_attn<FP8, D, 2, true>(a, st); else launch_attn<FP8, D, 3, true>(a, st); }
+        else if constexpr (D <= 128) {
+            if (s.RT == 2) launch_attn<FP8, D, 2, true>(a, st);
+            else launch_attn<FP8, D, 3, true>(a, st);
+        }
     } else {
         if (s.RT == 1) launch_attn<FP8, D, 1, false>(a, st);
         else if constexpr (D <= 128) launch_attn<FP8, D, 2, false>(a, st);
