@@ -642,6 +642,14 @@ def _stream_of(stream: Optional[torch.cuda.Stream], dev: int) -> int:
     return (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
+def _run(dev: int, call, *args) -> int:
+    """call(*args) with `dev` current: stream 0 is the current device's."""
+    if torch._C._cuda_getDevice() == dev:
+        return call(*args)
+    with torch.cuda.device(dev):
+        return call(*args)
+
+
 _CACHE_CODES = {torch.bfloat16: SPEC_BF16, torch.float8_e4m3fn: SPEC_E4M3}
 
 
@@ -683,6 +691,8 @@ def _ordered_heads(t: torch.Tensor, name: str, dev: int) -> int:
     tokens are evenly spaced and whose heads are dense."""
     _need(t.get_device() == dev, f"{name} must be on cuda:{dev}")
     R, M, H, D = t.shape
+    if t.numel() == 0:
+        return H * D
     s0, s1, s2, s3 = t.stride()
     ld = s1 if M > 1 else s0 if R > 1 else H * D
     _need((D == 1 or s3 == 1) and (H == 1 or s2 == D) and ld >= H * D and
@@ -717,7 +727,7 @@ def spec_tree_mask(parent: torch.Tensor, n_nodes: torch.Tensor, ctx_len: torch.T
          (ctx_len, "ctx_len", i32, (R,)), (pos, "out_positions", i32, shape),
          (mask, "out_mask", i32, words))
     buf, size = _cache_buf(workspace, dev, 256, stream)
-    st = _lib.spec_tree_mask(parent.data_ptr(), n_nodes.data_ptr(), ctx_len.data_ptr(), R, M,
+    st = _run(dev, _lib.spec_tree_mask, parent.data_ptr(), n_nodes.data_ptr(), ctx_len.data_ptr(), R, M,
                              int(window), pos.data_ptr(), mask.data_ptr(), buf, size,
                              _stream_of(stream, dev))
     if st:
@@ -773,7 +783,7 @@ def spec_qkv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
          (positions, "positions", i32, (R, M)), (ctx_len, "ctx_len", i32, (R,)),
          (n_nodes, "n_nodes", i32, (R,)))
     buf, room = _cache_buf(workspace, dev, 256, stream)
-    st = _lib.spec_qkv_write(_raw(q), k.data_ptr(), v.data_ptr(), dt, ld_q, ld_k, ld_v,
+    st = _run(dev, _lib.spec_qkv_write, _raw(q), k.data_ptr(), v.data_ptr(), dt, ld_q, ld_k, ld_v,
                              _raw(q_weight), _raw(k_weight), eps, _raw(rope), max_pos, rot,
                              int(interleaved), _raw(positions), ctx_len.data_ptr(),
                              n_nodes.data_ptr(), page_table.data_ptr(), wide, R, M, Hq, Hkv, D,
@@ -809,7 +819,7 @@ def spec_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
     _all(dev, (start, "start", torch.int32, (R,)), (length, "length", torch.int32, (R,)),
          (out_k, "out_k", dtype, shape), (out_v, "out_v", dtype, shape))
     buf, room = _cache_buf(workspace, dev, 256, stream)
-    st = _lib.spec_kv_read(k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
+    st = _run(dev, _lib.spec_kv_read, k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
                            _raw(v_scale), P, size, page_table.data_ptr(), wide, start.data_ptr(),
                            length.data_ptr(), R, max_len, Hkv, D, out_k.data_ptr(),
                            out_v.data_ptr(), _dtype(out_k), buf, room, _stream_of(stream, dev))
@@ -834,7 +844,7 @@ def spec_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: tor
     _all(dev, (ctx_len, "ctx_len", i32, (R,)), (accepted, "accepted", i32, (R,)),
          (path, "path", i32, (R, M)), (out_ctx_len, "out_ctx_len", i32, (R,)))
     buf, room = _cache_buf(workspace, dev, 256, stream)
-    st = _lib.spec_kv_commit(k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
+    st = _run(dev, _lib.spec_kv_commit, k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
                              _raw(v_scale), P, size, page_table.data_ptr(), wide,
                              ctx_len.data_ptr(), accepted.data_ptr(), path.data_ptr(), R, M, Hkv,
                              D, out_ctx_len.data_ptr(), buf, room, _stream_of(stream, dev))
@@ -875,7 +885,7 @@ def spec_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if need == 0:
         raise SpecError(-5, "spec_tree_attention_workspace_bytes")
     buf, room = _cache_buf(workspace, dev, need, stream)
-    st = _lib.spec_tree_attention(q.data_ptr(), SPEC_BF16, k_cache.data_ptr(), v_cache.data_ptr(),
+    st = _run(dev, _lib.spec_tree_attention, q.data_ptr(), SPEC_BF16, k_cache.data_ptr(), v_cache.data_ptr(),
                                   code, _raw(k_scale), _raw(v_scale), P, size,
                                   page_table.data_ptr(), wide, ctx_len.data_ptr(),
                                   n_nodes.data_ptr(), _raw(mask), _raw(positions),

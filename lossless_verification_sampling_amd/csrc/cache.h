@@ -52,17 +52,16 @@ __device__ __forceinline__ bool in_table(int first, int count, int max_pages, in
 }
 
 // Host checks of a cache's arguments that every entry point shares; 0 or a
-// negative spec_status.
+// negative spec_status.  (A missing page table is looked for once it is known
+// that the call has anything to do.)
 inline int check_pages(const void *k, const void *v, int dtype, const float *ks, const float *vs,
-                       int num_pages, int page_size, const int32_t *table, int max_pages, int Hkv,
-                       int D) {
+                       int num_pages, int page_size, int max_pages, int Hkv, int D) {
     if (num_pages < 1 || max_pages < 0 || Hkv < 1 || D < 1 || page_size < 1) return SPEC_EINVAL;
     if (dtype != SPEC_BF16 && dtype != SPEC_E4M3) return SPEC_EDTYPE;
     if (D != 64 && D != 128 && D != 256) return SPEC_EUNSUPPORTED;
     if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)))
         return SPEC_EUNSUPPORTED;
     if (!k || !v) return SPEC_EINVAL;
-    if (max_pages > 0 && !table) return SPEC_EINVAL;
     if (dtype == SPEC_E4M3 && (!ks || !vs)) return SPEC_EINVAL;
     if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)ks | (uintptr_t)vs) & 15u) return SPEC_EINVAL;
     return SPEC_OK;

@@ -464,14 +464,14 @@ int spec_qkv_write(const void *q, const void *k, const void *v, int dtype, int64
         return SPEC_EINVAL;
     if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_EDTYPE;
     const int bad = check_pages(k_cache, v_cache, cache_dtype, k_scale, v_scale, num_pages,
-                                page_size, page_table, max_pages, Hkv, D);
+                                page_size, max_pages, Hkv, D);
     if (bad) return bad;
     if (rot_dim > D || rot_dim % 16) return SPEC_EUNSUPPORTED;
     const int64_t tokens = (int64_t)R * M;
     if (tokens > 0x7fffffff) return SPEC_EUNSUPPORTED;
     if (q ? Hq < 1 || Hq % Hkv : Hq != 0) return SPEC_EINVAL;
     if (tokens == 0) return SPEC_OK;
-    if (!k || !v || !ctx_len || !n_nodes || (q && !out_q) || (rot_dim > 0) != (rope != nullptr))
+    if (!k || !v || !ctx_len || !n_nodes || (max_pages > 0 && !page_table) || (q && !out_q) || (rot_dim > 0) != (rope != nullptr))
         return SPEC_EINVAL;
     const int64_t per = dtype == SPEC_BF16 ? 8 : 4;  // elements of 16 bytes
     if ((q && (ld_q < (int64_t)Hq * D || ld_q % per)) || ld_k < (int64_t)Hkv * D || ld_k % per ||
@@ -525,12 +525,12 @@ int spec_kv_read(const void *k_cache, const void *v_cache, int cache_dtype, cons
                  size_t workspace_bytes, void *stream) {
     if (R < 0 || max_len < 0) return SPEC_EINVAL;
     const int bad = check_pages(k_cache, v_cache, cache_dtype, k_scale, v_scale, num_pages,
-                                page_size, page_table, max_pages, Hkv, D);
+                                page_size, max_pages, Hkv, D);
     if (bad) return bad;
     if (out_dtype != SPEC_BF16 && out_dtype != SPEC_F32) return SPEC_EDTYPE;
     if (R > 65535) return SPEC_EUNSUPPORTED;
     if (R == 0 || max_len == 0) return SPEC_OK;
-    if (!start || !len || !out_k || !out_v) return SPEC_EINVAL;
+    if (!start || !len || !out_k || !out_v || (max_pages > 0 && !page_table)) return SPEC_EINVAL;
     if (((uintptr_t)out_k | (uintptr_t)out_v) & 15u) return SPEC_EINVAL;
     if (bad_workspace(workspace, workspace_bytes, sizeof(Control))) return SPEC_EWORKSPACE;
     ReadArgs a{};
@@ -562,11 +562,12 @@ int spec_kv_commit(void *k_cache, void *v_cache, int cache_dtype, float *k_scale
                    size_t workspace_bytes, void *stream) {
     if (R < 0 || M < 1) return SPEC_EINVAL;
     const int bad = check_pages(k_cache, v_cache, cache_dtype, k_scale, v_scale, num_pages,
-                                page_size, page_table, max_pages, Hkv, D);
+                                page_size, max_pages, Hkv, D);
     if (bad) return bad;
     if (M > SPEC_TREE_MAX_NODES) return SPEC_EUNSUPPORTED;
     if (R == 0) return SPEC_OK;
-    if (!ctx_len || !accepted || !path || out_ctx_len == ctx_len) return SPEC_EINVAL;
+    if (!ctx_len || !accepted || !path || out_ctx_len == ctx_len || (max_pages > 0 && !page_table))
+        return SPEC_EINVAL;
     if (bad_workspace(workspace, workspace_bytes, sizeof(Control))) return SPEC_EWORKSPACE;
     CommitArgs a{};
     a.c = make_pages(k_cache, v_cache, cache_dtype == SPEC_E4M3 ? k_scale : nullptr,

@@ -356,14 +356,6 @@ __device__ __forceinline__ uint32_t v_word(const Tile<FP8, D> &t, int tok, int w
     else return w & 1 ? e4m3_bf16<true>(t.v[tok][w >> 1]) : e4m3_bf16<false>(t.v[tok][w >> 1]);
 }
 
-// Whether a raw word of V holds a NaN or an infinity (e4m3: a NaN, seven ones).
-template <bool FP8>
-__device__ __forceinline__ bool odd_word(uint32_t w) {
-    if constexpr (!FP8) return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-    const uint32_t y = ~w & 0x7f7f7f7fu;  // a byte of zeros
-    return (y - 0x01010101u) & ~y & 0x80808080u;
-}
-
 // The low k bits, k clamped to 0 .. 32.
 __device__ __forceinline__ uint32_t ones(int k) {
     return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u;
@@ -379,25 +371,23 @@ __device__ __forceinline__ Query query_of(const AttnArgs &a, const Req &rq, int 
     q.pos = a.positions ? a.positions[(size_t)r * a.M + q.node] : rq.ctx + q.node;
     return q;
 }
-// Tokens tok .. tok + 31 that query row `row` of request r sees, one bit each.
-// Worked out anew where a step needs it: few do, and registers are short.
-__device__ __forceinline__ uint32_t sees(const AttnArgs &a, const Req &rq, int r, int tok, int row) {
-    const Query q = query_of(a, rq, r, here(row));
-    const int v = q.node, pos = q.pos, n = rq.n;
+// The low k bits of 64, k clamped to 0 .. 64.
+__device__ __forceinline__ uint64_t ones64(int k) {
+    return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1ull;
+}
+// Tokens tok .. tok + 63 that a row sees, one bit each: the row's node v (its
+// tree bits from slot ctx - tok on in `tree`, for a mask) at position pos.
+__device__ __forceinline__ uint64_t sees(const AttnArgs &a, const Req &rq, int tok, int v, int pos,
+                                         uint64_t tree) {
     const int k = rq.ctx - tok;  // tokens of the context
-    const uint32_t old = ones(k);
-    uint32_t tree;
+    const uint64_t old = ones64(k);
     if (a.mask) {
-        const uint32_t *mrow = a.mask + ((size_t)r * a.M + v) * a.W;
-        const int w = -k >> 5, sh = -k & 31;  // tree slot -k at bit 0
-        const uint32_t lo = w >= 0 && w < a.W ? mrow[w] : 0u;
-        const uint32_t hi = w >= -1 && w + 1 < a.W ? mrow[w + 1] : 0u;
-        tree = (uint32_t)(((uint64_t)hi << 32 | lo) >> sh) & ones(k + n);
+        tree &= ones64(k + rq.n);
     } else {
-        tree = ones(k + v + 1);
-        if (a.window) tree &= ~ones(k + v + 1 - a.window);
+        tree = ones64(k + v + 1);
+        if (a.window) tree &= ~ones64(k + v + 1 - a.window);
     }
-    const uint32_t near = a.window ? old & ~ones(pos - tok + 1 - a.window) : old;
+    const uint64_t near = a.window ? old & ~ones64(pos - tok + 1 - a.window) : old;
     return near | (tree & ~old);
 }
 // Bit i: token i of this lane group's eight.
@@ -503,28 +493,59 @@ __device__ __forceinline__ u32x4_t weigh(const f32x4_t (&s)[2], float sc, float 
                    pack_bf16(p[6], p[7])};
 }
 
-// Adds token `row` of V (weights pw of the lane group tg's token ti) where it
-// is seen: the way of tokens whose row holds a NaN or an infinity, which a
-// weight of 0 would not cancel in the product.
+// NaN and infinities in V.  A weight of 0 would not cancel them in a product,
+// and rows that do not see such a token must not meet it: where some row does
+// not see a token, the values leave the operand (take_rare) and are added
+// after the token loop to the rows that do (add_rare).  Few calls ever hold
+// one; what matters is that the loop has no part in it but the look.
+template <bool FP8, int N>
+__device__ __forceinline__ bool take_rare(uint32_t (&w)[N], bool live) {
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        uint32_t v = live ? w[i] : 0u;
+        if constexpr (!FP8) {
+            const bool lo = (v & 0x7f80u) == 0x7f80u, hi = (v & 0x7f800000u) == 0x7f800000u;
+            odd |= lo || hi;
+            v &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+        } else {
+#pragma unroll
+            for (int s = 0; s < 32; s += 8) {  // e4m3: seven ones are a NaN
+                const bool nan = (v >> s & 0x7fu) == 0x7fu;
+                odd |= nan;
+                v &= nan ? ~(0xffu << s) : ~0u;
+            }
+        }
+        w[i] = v;
+    }
+    return odd;
+}
+// Tokens [from, to) of the request, for the row whose sums acc holds.
 template <bool FP8, int D>
-__device__ __forceinline__ void add_token(const AttnArgs &a, int64_t row, int tg, int ti, int lane,
-                                          u32x4_t pw, uint32_t seen, f32x4_t (&acc)[D / 16]) {
+__device__ __forceinline__ void add_rare(const AttnArgs &a, const Req &rq, int r, int h, int row,
+                                         int from, int to, int lane, f32x4_t (&acc)[D / 16]) {
     constexpr int DV = D / 16;
-    lane = here(lane);
-    const int c = lane & 15, g = lane >> 4;
-    const uint32_t w = ti & 4 ? (ti & 2 ? pw[3] : pw[2]) : (ti & 2 ? pw[1] : pw[0]);
-    const float pv = __shfl(ti & 1 ? bf16_hi(w) : bf16_lo(w), tg * 16 + c, 64);
-    const bool see = __shfl((int)seen, tg * 16 + c, 64) >> ti & 1;
+    const int g = here(lane) >> 4;
+    const Query q = query_of(a, rq, r, here(row));
+    const uint32_t *mrow = a.mask ? a.mask + ((size_t)r * a.M + q.node) * a.W : nullptr;
+#pragma unroll 1
+    for (int t = from; t < to; ++t) {
+        const int page = page_number(a, r, t >> a.c.shift), u = t - rq.ctx;
+        if ((unsigned)page >= (unsigned)a.c.num_pages) continue;
+        const uint64_t tree = mrow && u >= 0 && u < rq.n ? mrow[u >> 5] >> (u & 31) & 1u : 0u;
+        const bool see = sees(a, rq, t, q.node, q.pos, tree) & 1u;
+        const int64_t at = (((int64_t)page * a.c.heads + h) * a.c.size + (t & (a.c.size - 1))) * D;
 #pragma unroll
-    for (int j = 0; j < DV; ++j) {
-        __builtin_amdgcn_sched_barrier(0);  // few loads in flight: registers are short here
+        for (int j = 0; j < DV; ++j) {
+            __builtin_amdgcn_sched_barrier(0);  // few loads at a time: registers are short
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t e = row * D + DV * (4 * g + i) + j;
-            float val;
-            if constexpr (FP8) val = bf16_lo(e4m3_bf16<false>(((const uint8_t *)a.c.v)[e]));
-            else val = bf16_lo(((const uint16_t *)a.c.v)[e]);
-            if (see) acc[j][i] += pv * val;
+            for (int i = 0; i < 4; ++i) {
+                const int64_t e = at + DV * (4 * g + i) + j;
+                float val;
+                if constexpr (FP8) val = bf16_lo(e4m3_bf16<false>(((const uint8_t *)a.c.v)[e]));
+                else val = bf16_lo(((const uint16_t *)a.c.v)[e]);
+                acc[j][i] += see && val - val != 0.f ? val : 0.f;
+            }
         }
     }
 }
@@ -591,6 +612,14 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
         bf16x8_t qf[RT][KS];
 #pragma unroll
         for (int x = 0; x < RT; ++x) load_q<FP8, D>(a, rq, r, h, t * TR + x * 16 + c, lane, qf[x]);
+        // the rows' tree bits (at most 32 nodes here) and positions, for masks
+        uint32_t bits[RT];
+        Query at_row[RT];
+#pragma unroll
+        for (int x = 0; x < RT; ++x) {
+            at_row[x] = query_of(a, rq, r, t * TR + x * 16 + c);
+            bits[x] = a.mask ? a.mask[((size_t)r * a.M + at_row[x].node) * a.W] : 0u;
+        }
         f32x4_t acc[RT][DV];
         float m[RT], l[RT];
 #pragma unroll
@@ -602,6 +631,11 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
         }
         const Plain plain = plain_of<RT>(a, rq, r, t * TR, c, t1);
         int tok = t0 + wave * kStep;
+        int bad = 0;        // a bad page was met
+        bool rare = false;  // values left the products
+        // (no load but the next step's is under way inside the loop.  A load
+        // that a branch may issue makes the compiler wait for all of them
+        // where the branch joins.)
         if (rq.ok && tok < t1) {
             TT kv;
             Half cur = halves_of(a, numbers_of(a, r, tok, end), h, tok, end);
@@ -643,43 +677,19 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                 for (int x = 0; x < RT; ++x) {
                     seen[x] = 0xffu;
                     if (masked) {
-                        seen[x] = lane_bits(sees(a, rq, r, tok, t * TR + x * 16 + c), g);
+                        const int k = rq.ctx - tok;  // tree slot 0 is bit k
+                        const uint64_t tree = k >= 64 ? 0ull : k >= 0 ? (uint64_t)bits[x] << k
+                                            : k > -32 ? bits[x] >> -k : 0u;
+                        seen[x] = lane_bits((uint32_t)sees(a, rq, tok, at_row[x].node, at_row[x].pos, tree), g);
                     }
                     pw[x] = weigh<FP8, DV>(s[x], sc, a.scale2, masked, seen[x], cur.bad, m[x], l[x], acc[x]);
                 }
-                uint32_t odd = 0u;  // bit i: token i of this lane holds a NaN or an infinity
                 if (masked) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const bool live = tok + 16 * (i >> 2) + 4 * g + (i & 3) < t1;
-#pragma unroll
-                        for (int w = 0; w < TT::VW; ++w) kv.v[i][w] = live ? kv.v[i][w] : 0u;
-                        bool o = false;
-#pragma unroll
-                        for (int w = 0; w < TT::VW; ++w) o |= odd_word<FP8>(kv.v[i][w]);
-                        odd |= (uint32_t)o << i;
-                    }
-                }
-                if (__any(odd != 0u)) {
-                    // weight 0 times such a value is not 0: rows that do not
-                    // see the token must not meet it.  These tokens leave the
-                    // product and are added one by one where they are seen.
-                    uint32_t all = odd;  // over the 16 lanes that hold a token's row
-#pragma unroll
-                    for (int o = 1; o < 16; o <<= 1) all |= __shfl_xor(all, o, 64);
+                    bool odd = false;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-#pragma unroll
-                        for (int w = 0; w < TT::VW; ++w) kv.v[i][w] = all >> i & 1u ? 0u : kv.v[i][w];
-#pragma unroll 1
-                    for (int q = 0; q < 32; ++q) {
-                        const int tg = q >> 3, ti = q & 7;  // lane group and index of the token
-                        if (!(__shfl((int)all, tg * 16, 64) >> ti & 1)) continue;
-                        const int64_t row = cur.row[0] + (ti & 4 ? cur.row[1] - cur.row[0] : 0) + 4 * tg + (ti & 3);
-#pragma unroll
-                        for (int x = 0; x < RT; ++x)
-                            add_token<FP8, D>(a, row, tg, ti, lane, pw[x], seen[x], acc[x]);
-                    }
+                        odd |= take_rare<FP8>(kv.v[i], tok + 16 * (i >> 2) + 4 * g + (i & 3) < t1);
+                    rare |= __any(odd);
                 }
                 // ---- product
 #pragma unroll
@@ -706,7 +716,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                             __builtin_bit_cast(bf16x8_t, f1), pf, acc[x][2 * w + 1], 0, 0, 0);
                     }
                 }
-                if (cur.bad && lane == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+                bad |= cur.bad;
                 if (!more) break;
                 load_v<FP8, D>(a, nh, lane, kv);
                 __builtin_amdgcn_sched_barrier(0);
@@ -714,6 +724,16 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                 tok = nxt;
             }
         }
+        if (rare) {
+#pragma unroll 1
+            for (int s = t0 + wave * kStep; s < t1; s += kUnit) {
+                if (s >= plain.lo && s + kStep <= plain.hi) continue;
+#pragma unroll
+                for (int x = 0; x < RT; ++x)
+                    add_rare<FP8, D>(a, rq, r, h, t * TR + x * 16 + c, s, min(s + kStep, t1), lane, acc[x]);
+            }
+        }
+        if (bad && lane == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
         // ---- join the four waves, 16 rows at a time
         const int et = here(tid), ec = et & 15, eg = et >> 4 & 3;
 #pragma unroll
@@ -813,13 +833,15 @@ template <bool FP8, int D> struct Stage {
     u32x4_t k[TT::KV];
     uint32_t v[4][TT::VW];
     float sc;
-    int flags;                         // bit 16: the 16 tokens lie in a bad page
+    int flags;                         // bit 1: the 16 tokens lie in a bad page
+    uint32_t bits[3];                  // tree bits of this thread's row, see stage_sight
 };
-template <bool FP8, int D> struct Shared {
+template <bool FP8, int D, int TR> struct Shared {
     u32x4_t k[2][4][D / 32][64];         // [buffer][16 tokens][contraction step][lane]
     u32x2_t v[2][2][D / 16][2][64];      // [buffer][32 tokens][output tile][half][lane]
     float sc[2][2][64];                // [buffer][32 tokens][lane], as load_scale's
-    int flags[2][4];                   // per 16 tokens: bits 0-15 odd tokens, 16 bad page
+    int flags[2][4];                   // per 16 tokens: bit 0 rare values left V, bit 1 a bad page
+    uint64_t sight[2][TR];             // per row: the tokens of the tile that it sees
 };
 
 // The page number of this wave's 16 tokens of the tile at token t0; those
@@ -837,7 +859,7 @@ __device__ __forceinline__ void stage_load(const AttnArgs &a, int page, int h, i
     const int tt = t0 + 16 * wave < end ? t0 + 16 * wave : (end - 1) & ~15;
     s.flags = 0;
     if ((unsigned)page >= (unsigned)a.c.num_pages) {
-        s.flags = 1 << 16;
+        s.flags = 2;
         page = 0;
     }
     const int64_t row = ((int64_t)page * a.c.heads + h) * a.c.size + (tt & (a.c.size - 1));
@@ -852,13 +874,35 @@ __device__ __forceinline__ void stage_load(const AttnArgs &a, int page, int h, i
     if constexpr (FP8) s.sc = lane & 16 ? (a.c.v_scale + row)[c] : (a.c.k_scale + row)[c];
 }
 
-// Writes them to buffer b.  `part`: the tile holds tokens that some row does
-// not see (or that do not exist, from `end` on): values of V that a weight of
-// 0 would not cancel leave the tile and are marked.
+// A row's mask words that hold the tree slots of the 64 tokens from t0 on.
 template <bool FP8, int D>
-__device__ __forceinline__ void stage_store(const AttnArgs &a, Shared<FP8, D> &sh, int b, int t0,
-                                            int end, bool part, int wave, int lane,
-                                            Stage<FP8, D> &s) {
+__device__ __forceinline__ void load_bits(const AttnArgs &a, const Req &rq, int r, int node, int t0,
+                                          Stage<FP8, D> &s) {
+    const uint32_t *row = a.mask + ((size_t)r * a.M + node) * a.W;
+    const int w = (t0 - rq.ctx) >> 5;  // of slot t0 - ctx
+#pragma unroll
+    for (int i = 0; i < 3; ++i) s.bits[i] = w + i >= 0 && w + i < a.W ? row[w + i] : 0u;
+}
+// Which of them the row sees (thread `tid`'s, of the workgroup's row tile).
+template <bool FP8, int D>
+__device__ __forceinline__ uint64_t stage_sight(const AttnArgs &a, const Req &rq, int t0, Query q,
+                                                const Stage<FP8, D> &s) {
+    uint64_t tree = 0ull;
+    if (a.mask) {
+        const int sh = (t0 - rq.ctx) & 31;
+        const uint32_t b0 = here(s.bits[0]), b1 = here(s.bits[1]), b2 = here(s.bits[2]);  // not waited for before
+        tree = ((uint64_t)b1 << 32 | b0) >> sh;
+        if (sh) tree |= (uint64_t)b2 << (64 - sh);
+    }
+    return sees(a, rq, t0, q.node, q.pos, tree);
+}
+
+// Writes them to buffer b.  `part`: the tile holds tokens that some row does
+// not see, or that do not exist (from `end` on, V becomes 0): values of V that
+// a weight of 0 would not cancel are looked for.
+template <bool FP8, int D, typename SH>
+__device__ __forceinline__ void stage_store(const AttnArgs &a, SH &sh, int b, int t0, int end,
+                                            bool part, int wave, int lane, Stage<FP8, D> &s) {
     typedef Tile<FP8, D> TT;
     const int g = lane >> 4;
 #pragma unroll
@@ -875,24 +919,10 @@ __device__ __forceinline__ void stage_store(const AttnArgs &a, Shared<FP8, D> &s
     }
     int flags = s.flags;
     if (part) {
+        bool odd = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool live = t0 + 16 * wave + 4 * g + i < end;
-            bool odd = false;
-#pragma unroll
-            for (int w = 0; w < TT::VW; ++w) {
-                s.v[i][w] = live ? s.v[i][w] : 0u;
-                odd |= odd_word<FP8>(s.v[i][w]);
-            }
-            const uint64_t bal = __ballot(odd);
-            if (bal) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (bal >> (16 * q) & 0xffffu) flags |= 1 << (4 * q + i);
-#pragma unroll
-                for (int w = 0; w < TT::VW; ++w) s.v[i][w] = bal >> (16 * g) & 0xffffu ? 0u : s.v[i][w];
-            }
-        }
+        for (int i = 0; i < 4; ++i) odd |= take_rare<FP8>(s.v[i], t0 + 16 * wave + 4 * g + i < end);
+        flags |= __any(odd) ? 1 : 0;
     }
     uint32_t v[4][TT::DV / 2];
 #pragma unroll
@@ -924,7 +954,7 @@ template <bool FP8, int D, int RT>
 __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(AttnArgs a) {
     typedef Tile<FP8, D> TT;
     constexpr int KS = TT::KS, DV = TT::DV, TR = 64 * RT;
-    __shared__ Shared<FP8, D> sh;
+    __shared__ Shared<FP8, D, TR> sh;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
@@ -958,23 +988,42 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
 #pragma unroll
             for (int j = 0; j < DV; ++j) acc[x][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
-        const Plain plain = plain_of<RT>(a, rq, r, row0, c, t1);
-        // the workgroup's: its first rows see the least of a chain; of a window nothing is said
-        const int common = a.window ? 0 : min(rq.ctx + (a.mask ? 0 : t * TR / a.G + 1), t1);
+        // tiles [mid0, mid1) are seen whole by every row of the workgroup
+        const Plain plain = plain_of<RT * kWaves>(a, rq, r, t * TR, c, t1);
+        const int mid0 = min(t0 + max(0, plain.lo - t0 + kTile - 1) / kTile * kTile, t1);
+        const int mid1 = max(mid0, t0 + (max(plain.hi, t0) - t0) / kTile * kTile);
         // a chain's wave sees nothing behind its last row's node
         const int wend = a.mask ? t1 : min(t1, rq.ctx + (min(row0 + 16 * RT, rq.rows) - 1) / a.G + 1);
         const bool idle = row0 >= rq.rows || !rq.ok;
+        int bad = 0;        // a bad page was met
+        bool rare = false;  // values left the products
+        // (no load but the next tile's is under way while this one is worked
+        // on: masks are laid beside the tile.  A load that a branch may issue
+        // makes the compiler wait for all of them where the branch joins.)
         if (rq.ok) {
             Stage<FP8, D> st;
-            stage_load<FP8, D>(a, stage_page(a, r, t0, end, wave), h, t0, end, wave, lane, st);
+            // the next tile's, and this thread's row's sight of it
+            const auto ask = [&](int page, int t_at) {
+                stage_load<FP8, D>(a, page, h, t_at, end, wave, lane, st);
+                if (a.mask && tid < TR && (t_at < mid0 || t_at >= mid1))
+                    load_bits<FP8, D>(a, rq, r, query_of(a, rq, r, t * TR + here(tid)).node, t_at, st);
+            };
+            const auto keep = [&](int buf, int t_at) {
+                const bool part = t_at < mid0 || t_at >= mid1;
+                stage_store<FP8, D>(a, sh, buf, t_at, end, part, wave, lane, st);
+                if (part && tid < TR)
+                    sh.sight[buf][tid] = stage_sight<FP8, D>(a, rq, t_at, query_of(a, rq, r, t * TR + here(tid)), st);
+            };
+            ask(stage_page(a, r, t0, end, wave), t0);
             int page = stage_page(a, r, t0 + kTile, end, wave);
             __syncthreads();  // the last item's reads are done
-            stage_store<FP8, D>(a, sh, 0, t0, end, t0 + kTile > common, wave, lane, st);
+            keep(0, t0);
             __syncthreads();
             int b = 0;
             for (int tile = t0; tile < t1; tile += kTile, b ^= 1) {
                 const bool more = tile + kTile < t1;
-                if (more) stage_load<FP8, D>(a, page, h, tile + kTile, end, wave, lane, st);
+                const bool part = tile < mid0 || tile >= mid1;
+                if (more) ask(page, tile + kTile);
                 page = stage_page(a, r, tile + 2 * kTile, end, wave);  // in time for the next load
                 int flags[4];
 #pragma unroll
@@ -1006,32 +1055,21 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                                     __builtin_bit_cast(bf16x8_t, kf[hf][ks]), qf[x][ks], s[x][hf], 0, 0, 0);
                     const float sc = FP8 ? sh.sc[b][half][lane] : 0.f;
                     const int fl0 = half ? flags[2] : flags[0], fl1 = half ? flags[3] : flags[1];
-                    const int bad = fl0 >> 16 | (fl1 >> 16) << 1;
-                    const bool masked = tok < plain.lo || tok + kStep > plain.hi || bad;
+                    const int off = fl0 >> 1 | (fl1 & 2);  // halves in a bad page
+                    bad |= off;
+                    const bool masked = part || off;
                     uint32_t seen[RT];
                     u32x4_t pw[RT];
 #pragma unroll
                     for (int x = 0; x < RT; ++x) {
                         seen[x] = 0xffu;
-                        if (masked) {
-                            seen[x] = lane_bits(sees(a, rq, r, tok, row0 + x * 16 + c), g);
+                        if (part) {
+                            const uint64_t sight = sh.sight[b][wave * 16 * RT + x * 16 + c];
+                            seen[x] = lane_bits((uint32_t)(half ? sight >> 32 : sight), g);
                         }
-                        pw[x] = weigh<FP8, DV>(s[x], sc, a.scale2, masked, seen[x], bad, m[x], l[x], acc[x]);
+                        pw[x] = weigh<FP8, DV>(s[x], sc, a.scale2, masked, seen[x], off, m[x], l[x], acc[x]);
                     }
-                    // ---- tokens whose V rows left the tile, one by one
-                    const uint32_t odd = (fl0 & 0xffff) | (uint32_t)(fl1 & 0xffff) << 16;
-                    if (odd) {
-#pragma unroll 1
-                        for (int q = 0; q < 32; ++q) {
-                            if (!(odd >> q & 1u)) continue;
-                            const int tg = q >> 2 & 3, ti = (q & 3) | (q >> 2 & 4);
-                            const Half x16 = halves_of(a, numbers_of(a, r, tok + (q & 16), end), h, tok + (q & 16), end);
-                            const int64_t row = x16.row[0] + (q & 15);
-#pragma unroll
-                            for (int x = 0; x < RT; ++x)
-                                add_token<FP8, D>(a, row, tg, ti, lane, pw[x], seen[x], acc[x]);
-                        }
-                    }
+                    rare |= (fl0 | fl1) & 1;
                     // ---- product
 #pragma unroll
                     for (int j0 = 0; j0 < DV; j0 += 4) {
@@ -1049,13 +1087,21 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                                     __builtin_bit_cast(bf16x8_t, vf[j]), __builtin_bit_cast(bf16x8_t, pw[x]),
                                     acc[x][j0 + j], 0, 0, 0);
                     }
-                    if (bad && lane == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
                 }
-                if (more)
-                    stage_store<FP8, D>(a, sh, b ^ 1, tile + kTile, end, tile + 2 * kTile > common, wave, lane, st);
+                if (more) keep(b ^ 1, tile + kTile);
                 __syncthreads();
             }
         }
+        if (rare) {
+#pragma unroll 1
+            for (int s = t0; s < wend; s += kTile) {
+                if (s >= mid0 && s < mid1) continue;
+#pragma unroll
+                for (int x = 0; x < RT; ++x)
+                    add_rare<FP8, D>(a, rq, r, h, row0 + x * 16 + c, s, min(s + kTile, wend), lane, acc[x]);
+            }
+        }
+        if (bad && lane == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
         // ---- the wave's rows
         const int el = here(lane), ec = el & 15, eg = el >> 4;
 #pragma unroll
@@ -1287,13 +1333,13 @@ int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const v
     if (R < 0 || M < 1 || Hq < 1 || window < 0 || !isfinite(scale)) return SPEC_EINVAL;
     if (q_dtype != SPEC_BF16) return SPEC_EDTYPE;
     const int bad = check_pages(k_cache, v_cache, cache_dtype, k_scale, v_scale, num_pages,
-                                page_size, page_table, max_pages, Hkv, D);
+                                page_size, max_pages, Hkv, D);
     if (bad) return bad;
     if (Hq % Hkv) return SPEC_EINVAL;
     const size_t need = spec_tree_attention_workspace_bytes(R, M, Hq, Hkv, D);
     if (!need || R > 65535) return SPEC_EUNSUPPORTED;
     if (R == 0) return SPEC_OK;
-    if (!q || !ctx_len || !n_nodes || !out) return SPEC_EINVAL;
+    if (!q || !ctx_len || !n_nodes || !out || (max_pages > 0 && !page_table)) return SPEC_EINVAL;
     if (((uintptr_t)q | (uintptr_t)out) & 15u) return SPEC_EINVAL;
     if (bad_workspace(workspace, workspace_bytes, need)) return SPEC_EWORKSPACE;
     AttnArgs a{};
