@@ -447,17 +447,16 @@ __device__ __forceinline__ void row_times(float (&p)[8], float v) {
     p[7] *= row_lane<FIRST + 7>(v);
 }
 
-// The running softmax's step for one row: scores s of the lane's eight tokens
-// become weights (bf16, 2^-8 relative like the output's own rounding; V's
-// scale goes in first), and m, l and acc follow.  The maximum may lag by
-// kLazy: weights then reach 2^kLazy, which costs no precision, and most steps
-// rescale nothing.  seen: bit i, the row sees token i; bad: bit h, tokens
+// The running softmax's step for a lane's eight tokens of each of its RT
+// columns, in three parts, so that a caller can lay the products of one column
+// between the exponents of the next.
+//
+// Scores s become p, ready for the exponent but for scale2 (bf16), and top
+// their maximum.  seen: bit i, the row sees token i; bad: bit h, tokens
 // 4 h .. 4 h + 3 lie in a bad page (both only where masked).
-template <bool FP8, int DV>
-__device__ __forceinline__ u32x4_t weigh(const f32x4_t (&s)[2], float sc, float scale2,
-                                         bool masked, uint32_t seen, int bad, float &m, float &l,
-                                         f32x4_t (&acc)[DV]) {
-    float p[8];
+template <bool FP8>
+__device__ __forceinline__ float peak(const f32x4_t (&s)[2], float sc, float scale2, bool masked,
+                                      uint32_t seen, int bad, float (&p)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = s[i >> 2][i & 3];
     if constexpr (FP8) row_times<0>(p, sc * scale2);
@@ -466,37 +465,48 @@ __device__ __forceinline__ u32x4_t weigh(const f32x4_t (&s)[2], float sc, float 
         for (int i = 0; i < 8; ++i)
             p[i] = !(seen >> i & 1u) ? -INFINITY : bad >> (i >> 2) & 1 ? NAN : p[i];
     }
-    float top = max8(p);  // m is the column's, so a lane's own maximum tells
-    if constexpr (!FP8) top *= scale2;
-    if (__any(top > m + kLazy)) {
-        const float mn = max2(m, column_max(top));
-        const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
-        l *= al;
+    const float top = max8(p);  // m is the column's, so a lane's own maximum tells
+    return FP8 ? top : top * scale2;
+}
+// The maximum may lag by kLazy: weights then reach 2^kLazy, which costs no
+// precision, and most steps rescale nothing.
+template <int RT, int DV>
+__device__ __forceinline__ void lift(const float (&top)[RT], float (&m)[RT], float (&l)[RT],
+                                     f32x4_t (&acc)[RT][DV]) {
+    bool up = false;
 #pragma unroll
-        for (int j = 0; j < DV; ++j) acc[j] *= al;
-        m = mn;
+    for (int x = 0; x < RT; ++x) up |= top[x] > m[x] + kLazy;
+    if (!__any(up)) return;
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+        const float most = column_max(top[x]);
+        const bool due = most > m[x] + kLazy;  // a row's own affair, whatever its neighbours do
+        const float al = due ? __builtin_amdgcn_exp2f(m[x] - most) : 1.f;
+        l[x] *= al;
+#pragma unroll
+        for (int j = 0; j < DV; ++j) acc[x][j] *= al;
+        m[x] = due ? most : m[x];
     }
+}
+// The weights (bf16, 2^-8 relative like the output's own rounding; V's scale
+// goes in first), and their sum into l.
+template <bool FP8>
+__device__ __forceinline__ u32x4_t weigh(float (&p)[8], float sc, float scale2, float m, float &l) {
     const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         p[i] = __builtin_amdgcn_exp2f(FP8 ? p[i] - ref : fmaf(p[i], scale2, -ref));
         l += p[i];
     }
-    if constexpr (FP8) {
-        row_times<8>(p, sc);
-        if (masked) {  // a scale of an unseen row may be anything
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = seen >> i & 1u ? p[i] : 0.f;
-        }
-    }
+    if constexpr (FP8) row_times<8>(p, sc);
     return u32x4_t{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
                    pack_bf16(p[6], p[7])};
 }
 
-// NaN and infinities in V.  A weight of 0 would not cancel them in a product,
-// and rows that do not see such a token must not meet it: where some row does
-// not see a token, the values leave the operand (take_rare) and are added
-// after the token loop to the rows that do (add_rare).  Few calls ever hold
+// NaN and infinities in V or its scale.  A weight of 0 would not cancel them in
+// a product, and rows that do not see such a token must not meet it: where
+// some row does not see a token, the values leave the operand (take_rare) and
+// are added after the token loop to the rows that do (add_rare).  Few calls ever hold
 // one; what matters is that the loop has no part in it but the look.
 template <bool FP8, int N>
 __device__ __forceinline__ bool take_rare(uint32_t (&w)[N], bool live) {
@@ -520,6 +530,12 @@ __device__ __forceinline__ bool take_rare(uint32_t (&w)[N], bool live) {
     }
     return odd;
 }
+// The same of a token's scale.
+__device__ __forceinline__ bool take_rare(float &sc, bool live) {
+    const bool odd = !(fabsf(sc) < INFINITY);
+    sc = odd ? 0.f : sc;
+    return odd && live;
+}
 // Tokens [from, to) of the request, for the row whose sums acc holds.
 template <bool FP8, int D>
 __device__ __forceinline__ void add_rare(const AttnArgs &a, const Req &rq, int r, int h, int row,
@@ -534,7 +550,8 @@ __device__ __forceinline__ void add_rare(const AttnArgs &a, const Req &rq, int r
         if ((unsigned)page >= (unsigned)a.c.num_pages) continue;
         const uint64_t tree = mrow && u >= 0 && u < rq.n ? mrow[u >> 5] >> (u & 31) & 1u : 0u;
         const bool see = sees(a, rq, t, q.node, q.pos, tree) & 1u;
-        const int64_t at = (((int64_t)page * a.c.heads + h) * a.c.size + (t & (a.c.size - 1))) * D;
+        const int64_t slot = ((int64_t)page * a.c.heads + h) * a.c.size + (t & (a.c.size - 1)), at = slot * D;
+        const float sc = FP8 ? a.c.v_scale[slot] : 1.f;
 #pragma unroll
         for (int j = 0; j < DV; ++j) {
             __builtin_amdgcn_sched_barrier(0);  // few loads at a time: registers are short
@@ -542,9 +559,9 @@ __device__ __forceinline__ void add_rare(const AttnArgs &a, const Req &rq, int r
             for (int i = 0; i < 4; ++i) {
                 const int64_t e = at + DV * (4 * g + i) + j;
                 float val;
-                if constexpr (FP8) val = bf16_lo(e4m3_bf16<false>(((const uint8_t *)a.c.v)[e]));
+                if constexpr (FP8) val = sc * bf16_lo(e4m3_bf16<false>(((const uint8_t *)a.c.v)[e]));
                 else val = bf16_lo(((const uint16_t *)a.c.v)[e]);
-                acc[j][i] += see && val - val != 0.f ? val : 0.f;
+                acc[j][i] += see && !(fabsf(val) < INFINITY) ? val : 0.f;
             }
         }
     }
@@ -664,7 +681,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                             s[x][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[x][ks], s[x][hf], 0, 0, 0);
                     }
                 }
-                const float sc = FP8 ? kv.sc : 0.f;
+                float sc = FP8 ? kv.sc : 0.f;
                 if (more) {
                     load_k<FP8, D>(a, nh, lane, kv);
                     if constexpr (FP8) kv.sc = load_scale(a, nh, lane);
@@ -672,7 +689,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                 __builtin_amdgcn_sched_barrier(0);
                 const bool masked = tok < plain.lo || tok + kStep > plain.hi || cur.bad;
                 uint32_t seen[RT];  // bit i: the row sees this lane's token i
-                u32x4_t pw[RT];
+                float p[RT][8], top[RT];
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
                     seen[x] = 0xffu;
@@ -682,15 +699,22 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                                             : k > -32 ? bits[x] >> -k : 0u;
                         seen[x] = lane_bits((uint32_t)sees(a, rq, tok, at_row[x].node, at_row[x].pos, tree), g);
                     }
-                    pw[x] = weigh<FP8, DV>(s[x], sc, a.scale2, masked, seen[x], cur.bad, m[x], l[x], acc[x]);
+                    top[x] = peak<FP8>(s[x], sc, a.scale2, masked, seen[x], cur.bad, p[x]);
                 }
+                lift(top, m, l, acc);
                 if (masked) {
                     bool odd = false;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         odd |= take_rare<FP8>(kv.v[i], tok + 16 * (i >> 2) + 4 * g + (i & 3) < t1);
+                    if constexpr (FP8) {
+                        if (lane & 8) odd |= take_rare(sc, tok + 16 * (lane >> 2 & 1) + 4 * g + (lane & 3) < t1);
+                    }
                     rare |= __any(odd);
                 }
+                u32x4_t pw[RT];
+#pragma unroll
+                for (int x = 0; x < RT; ++x) pw[x] = weigh<FP8>(p[x], sc, a.scale2, m[x], l[x]);
                 // ---- product
 #pragma unroll
                 for (int w = 0; w < DV / 2; ++w) {
@@ -922,6 +946,9 @@ __device__ __forceinline__ void stage_store(const AttnArgs &a, SH &sh, int b, in
         bool odd = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) odd |= take_rare<FP8>(s.v[i], t0 + 16 * wave + 4 * g + i < end);
+        if constexpr (FP8) {
+            if (lane & 16) odd |= take_rare(s.sc, t0 + 16 * wave + (lane & 15) < end);
+        }
         flags |= __any(odd) ? 1 : 0;
     }
     uint32_t v[4][TT::DV / 2];
@@ -1059,7 +1086,7 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                     bad |= off;
                     const bool masked = part || off;
                     uint32_t seen[RT];
-                    u32x4_t pw[RT];
+                    float p[RT][8], top[RT];
 #pragma unroll
                     for (int x = 0; x < RT; ++x) {
                         seen[x] = 0xffu;
@@ -1067,10 +1094,14 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                             const uint64_t sight = sh.sight[b][wave * 16 * RT + x * 16 + c];
                             seen[x] = lane_bits((uint32_t)(half ? sight >> 32 : sight), g);
                         }
-                        pw[x] = weigh<FP8, DV>(s[x], sc, a.scale2, masked, seen[x], off, m[x], l[x], acc[x]);
+                        top[x] = peak<FP8>(s[x], sc, a.scale2, masked, seen[x], off, p[x]);
                     }
                     rare |= (fl0 | fl1) & 1;
+                    lift(top, m, l, acc);
                     // ---- product
+                    u32x4_t pw[RT];
+#pragma unroll
+                    for (int x = 0; x < RT; ++x) pw[x] = weigh<FP8>(p[x], sc, a.scale2, m[x], l[x]);
 #pragma unroll
                     for (int j0 = 0; j0 < DV; j0 += 4) {
                         u32x4_t vf[4];

@@ -211,3 +211,36 @@ def test_same_call_same_bits(sv, dev):
     a, b = c.run(sv, dev), c.run(sv, dev)
     np.testing.assert_array_equal(a[0], b[0])
     np.testing.assert_array_equal(a[1], b[1])
+
+
+# rows per key head: 8, 30 and 16 (waves divide the tokens), 96, 192 and 80 (waves divide the rows)
+@pytest.mark.parametrize("M,G,Dh", [(8, 1, 64), (30, 1, 128), (8, 2, 256), (48, 2, 64), (64, 3, 128), (20, 4, 256)])
+@pytest.mark.parametrize("what,value", [("k_scale", np.nan), ("k_scale", np.inf), ("v_scale", np.nan),
+                                        ("v_scale", np.inf), ("codes", np.nan)])
+def test_unseen_scales_and_codes(sv, dev, M, G, Dh, what, value):
+    """e4m3: a token's scales or codes are no numbers.  Rows that do not see it
+    are as if it were not there; what the others give is the formula's."""
+    bad, dirty = 3, Case(20, 1, M, G, 1, Dh, 16, "e4m3", [37], True)
+    clean = Case(20, 1, M, G, 1, Dh, 16, "e4m3", [37], True)
+    at = int(dirty.c.table[0, (37 + bad) // 16]), 0, (37 + bad) % 16
+    if what == "codes":
+        for x in dirty.c.dev:
+            x.view(torch.uint8)[at] = 0x7f
+    else:
+        dirty.c.scales[what == "v_scale"][at] = value
+    got, good = dirty.run(sv, dev), clean.run(sv, dev)
+    blind = ~dirty.see[0, :, bad]
+    assert blind.any() and not blind.all()
+    for a, b in zip(got, good):
+        np.testing.assert_array_equal(a[0, blind], b[0, blind])
+    seeing = got[0][0, ~blind]
+    if what == "v_scale" and value == np.inf:  # inf times a code: its sign, or NaN for 0
+        code = dirty.c.dev[1][at].float().cpu().numpy()
+        with np.errstate(invalid="ignore"):
+            assert np.array_equal(seeing, np.broadcast_to(code * np.inf, seeing.shape), equal_nan=True)
+    elif what == "k_scale" and value == np.inf:
+        assert not np.isnan(got[1][0, blind]).any()
+    else:
+        assert np.isnan(seeing).all()
+    if what == "v_scale":                     # the scores have nothing of it
+        np.testing.assert_array_equal(got[1], good[1])
