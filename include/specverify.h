@@ -445,8 +445,8 @@ int spec_tree_verify(const void *logits, int dtype, const int32_t *parent, const
  * Common rules:
  *  - page_size is a power of two, 16 .. 1024; D is 64, 128 or 256; Hkv >= 1 and
  *    Hq is a multiple of Hkv (query head h reads key head h / (Hq / Hkv)).
- *  - Pointers to activations, pages and out_q / out_k / out_v / out are
- *    16-byte aligned (SPEC_EINVAL otherwise).
+ *  - Pointers to activations, weights, rope, pages, scales and out_q / out_k /
+ *    out_v / out are 16-byte aligned (SPEC_EINVAL otherwise).
  *  - n_nodes[r] may be 0 (an idle slot of a padded batch).  Rows v >=
  *    n_nodes[r] are neither read nor written, in inputs, outputs or cache.
  *  - Data faults (each sets SPEC_DEV_BAD_REQUEST): n_nodes outside [0, M],
@@ -501,7 +501,7 @@ int spec_tree_mask(const int32_t *parent, const int32_t *n_nodes, const int32_t 
  *   rope      [max_pos][rot_dim / 2][2]  fp32 (cos, sin), NULL iff rot_dim == 0
  *   positions [R][M]          int32, nullable (ctx_len + v)
  *   out_q     [R][M][Hq][D]   bf16
- * rot_dim is a multiple of 16, at most D.  A position outside [0, max_pos) is
+ * rot_dim is a multiple of 16, at most D (max_pos >= 1 with it).  A position outside [0, max_pos) is
  * a data fault (with rot_dim > 0): the token's out_q rows and its k rows
  * become NaN.  A faulty request's out_q rows become NaN and its tokens are
  * not written.  Sizes: R, M >= 0.
@@ -570,14 +570,16 @@ size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D)
  * Scores, softmax sums and products are held in fp32.
  *   q         [R][M][Hq][D]  SPEC_BF16
  *   mask      [R][M][W]      uint32 as spec_tree_mask writes it, nullable
- *   positions [R][M]         int32, nullable (ctx_len + v); read when a window
- * XX
+ *   positions [R][M]         int32 as spec_tree_mask writes it, nullable
+ *                            (ctx_len + v); at least ctx_len (below is a data
+ *                            fault of the node), and only a window uses it
  *   out       [R][M][Hq][D]  bf16
  *   out_lse   [R][M][Hq]     fp32, nullable: natural log of the softmax sum
  * A faulty request's or node's rows become NaN, and so do the rows that see a
  * token in a bad page.  The tokens of the tree must be in the cache
- * (spec_qkv_write).  Results do not depend on what else is in the batch's
- * padding; the order of sums depends on the lengths in the batch.
+ * (spec_qkv_write).  A call repeated gives the same bits; the order of a
+ * row's sums depends on the lengths in the batch, and on nothing that the
+ * row does not see.
  * Sizes: R >= 0, 1 <= M <= SPEC_TREE_MAX_NODES, Hq / Hkv <= 64, window >= 0.
  */
 int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const void *v_cache,

@@ -39,6 +39,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 constexpr int kStep = 32;              // tokens a wave takes at a time
 constexpr int kUnit = kStep * kWaves;  // tokens of one unit of work
 constexpr int kMaxGroups = 512;        // workgroups of the attention launch
+constexpr int kFewUnits = 2048;        // below, one workgroup per compute unit
 constexpr float kLazy = 8.0f;          // a maximum may lag by this many powers of two
 
 struct AttnArgs {
@@ -107,7 +108,12 @@ __device__ __forceinline__ int head_units(const AttnArgs &a, const Req &q) {
 }
 
 // Ranges of the batch's `total` units (below 2^31, checked on the host): the
-// first `extra` of `parts` ranges have `each` + 1 of them.
+// first `extra` of `parts` ranges have `each` + 1 of them.  There are as many
+// ranges as compute units, or two for each (fewer parts to join, against waits
+// that hide each other): one user's 30 k tokens, 1880 units, take 29.2 us with
+// 256 ranges and 32.6 with 512, 8 users of 4 k 22.7 and 24.7, 16 users (2300
+// units) 35.3 and 34.6, 32 users 78 (288 ranges) and 65.0.  Numbers between
+// leave some compute units twice the work of others.
 struct Place {
     int r;                       // the request of the range's first unit
     int off;                     // units into it
@@ -144,7 +150,7 @@ __device__ __forceinline__ Place find_unit(const AttnArgs &a, int &num) {
         p.total += sum_s[w];
     }
     p.total = __builtin_amdgcn_readfirstlane(p.total);
-    p.parts = min(a.groups, p.total);
+    p.parts = min(min(a.groups, p.total < kFewUnits ? kMaxGroups / 2 : kMaxGroups), p.total);
     p.each = p.parts ? p.total / p.parts : 0;
     p.extra = p.total - p.each * p.parts;
     p.r = a.R;
@@ -385,9 +391,9 @@ __device__ __forceinline__ uint64_t sees(const AttnArgs &a, const Req &rq, int t
         tree &= ones64(k + rq.n);
     } else {
         tree = ones64(k + v + 1);
-        if (a.window) tree &= ~ones64(k + v + 1 - a.window);
+        if (a.window) tree &= ~ones64(max(k + v + 1, 0) - a.window);
     }
-    const uint64_t near = a.window ? old & ~ones64(pos - tok + 1 - a.window) : old;
+    const uint64_t near = a.window ? old & ~ones64(max(pos - a.window + 1, 0) - tok) : old;
     return near | (tree & ~old);
 }
 // Bit i: token i of this lane group's eight.
@@ -1162,14 +1168,17 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                 }
                 if (eg == 0 && a.lse) a.lse[orow] = (m[x] + log2f(l[x])) * (float)kLn2;
             } else {
+                // as the lanes hold it, a kilobyte a store (rows side by side, as the
+                // output has them, were 16 bytes a line: 24.0 us against 17.3 for one
+                // tree of 48 nodes behind 4 k tokens)
                 float *pp = a.part + (size_t)(2 * grp + (u0 == 0)) * a.part_stride;
+                float *po = pp + (wave * RT + x) * 16 * D + 4 * el;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float *po = pp + (size_t)lr * D + DV * (4 * eg + i);
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < DV; j += 4)
-                        *(f32x4_t *)(po + j) = f32x4_t{acc[x][j][i], acc[x][j + 1][i], acc[x][j + 2][i], acc[x][j + 3][i]};
-                }
+                        *(f32x4_t *)(po + (i * (DV / 4) + j / 4) * 256) =
+                            f32x4_t{acc[x][j][i], acc[x][j + 1][i], acc[x][j + 2][i], acc[x][j + 3][i]};
                 if (eg == 0) {
                     pp[TR * D + lr] = m[x];
                     pp[TR * D + TR + lr] = l[x];
@@ -1280,19 +1289,83 @@ __global__ void __launch_bounds__(kBlock) attn_join_kernel(AttnArgs a) {
     if (lane == 0 && a.lse) a.lse[orow] = (m + log2f(sum)) * (float)kLn2;
 }
 
+// The same for attn_wide_kernel's parts, which lie as its lanes held them: a
+// wave takes 16 rows by 16 of their values, a kilobyte of each part.
+template <int D, int TR>
+__global__ void __launch_bounds__(kBlock) attn_wide_join_kernel(AttnArgs a) {
+    constexpr int DV = D / 16;
+    const int f = blockIdx.x, n_cuts = *a.n_cuts;
+    const Cut cut = a.cuts[f];
+    if (f >= n_cuts) return;
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int unit = blockIdx.y * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rb = unit / DV, piece = unit - rb * DV, lr = 16 * rb + c;
+    if (16 * rb >= cut.rows) return;
+    const int n = cut.parts;
+    float m = -INFINITY, sum = 0.f;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < n; i0 += kJoinParts) {
+        const int cnt = min(kJoinParts, n - i0);
+        float mi[kJoinParts], li[kJoinParts];
+        f32x4_t x[kJoinParts];
+#pragma unroll
+        for (int k = 0; k < kJoinParts; ++k) {
+            mi[k] = -INFINITY;
+            if (k < cnt) {
+                const float *p = a.part + (size_t)(2 * (f + i0 + k) + (i0 + k == 0)) * a.part_stride;
+                mi[k] = p[TR * D + lr];
+                li[k] = p[TR * D + TR + lr];
+                x[k] = *(const f32x4_t *)(p + unit * 256 + 4 * lane);
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < kJoinParts; ++k) top = fmaxf(top, mi[k]);
+        const float ref = top == -INFINITY ? 0.f : top, back = __builtin_amdgcn_exp2f(m - ref);
+        sum *= back;
+        o *= back;
+        m = top;
+#pragma unroll
+        for (int k = 0; k < kJoinParts; ++k)
+            if (k < cnt) {
+                const float w = __builtin_amdgcn_exp2f(mi[k] - ref);
+                sum += w * li[k];
+                o += w * x[k];
+            }
+    }
+    if (lr >= cut.rows) return;
+    const int row = cut.row0 + lr, nd = row / a.G;
+    const size_t orow = (size_t)(cut.node0 + nd) * a.Hq + cut.h * a.G + (row - nd * a.G);
+    if (sum == 0.f) {  // nothing seen: o is 0
+        sum = 1.f;
+        m = -INFINITY;
+    }
+    o *= 1.f / sum;
+    // piece = i (DV / 4) + j / 4: the lane's values d = DV (4 g + i) + j on
+    const int i = piece / (DV / 4), j = 4 * (piece - i * (DV / 4));
+    *(u32x2_t *)(a.out + orow * D + DV * (4 * g + i) + j) = u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+    if (piece == 0 && g == 0 && a.lse) a.lse[orow] = (m + log2f(sum)) * (float)kLn2;
+}
+
 // Which launch a call takes and its row tile.  A request's largest count of
-// rows per key head decides: up to 32 (16 at D = 256, for the registers) the
-// waves of a workgroup divide the tokens; more rows divide the waves.  There
-// three 16-row tiles a wave reach 781 TFLOP/s on long chunks against 649 with
-// two (D = 128, e4m3: each operand from shared memory serves three products),
-// so two are taken where they leave over 13% fewer rows empty.
+// rows per key head decides.  Up to 16 the waves of a workgroup divide the
+// tokens; more rows divide the waves, which read K and V from HBM once for all
+// of them.  For e4m3 the first form holds up to 32 rows (two tiles a wave) and
+// is the faster one there (64 users, 32 rows, 4 k tokens: 91.6 us, the other
+// 95; the other way round for bf16, 136.5 and 134.3), but for D = 256, where two
+// tiles leave too few registers (24 rows: 162 us, the other 156).
+// Beside each other three 16-row tiles a wave reach 781 TFLOP/s on long chunks
+// against 649 with two (D = 128, e4m3: each operand from shared memory serves
+// three products), so two are taken where they leave over 13% fewer rows
+// empty (16 trees of 64 nodes, 256 rows: 97 us against 104; 192 rows: 81.8
+// against 80.3).
 struct Shape {
     bool wide;
     int RT, TR, groups;
 };
-inline Shape shape_of(int64_t rows, int D) {
+inline Shape shape_of(int64_t rows, int D, bool fp8) {
     Shape s;
-    s.wide = rows > (D == 256 ? 16 : 32);
+    s.wide = rows > (fp8 && D <= 128 ? 32 : 16);
     if (!s.wide) s.RT = rows <= 16 ? 1 : 2;
     else if (D == 256 || rows <= 64) s.RT = 1;
     else {
@@ -1307,17 +1380,21 @@ inline Shape shape_of(int64_t rows, int D) {
 template <bool FP8, int D, int RT, bool WIDE>
 static void launch_attn(const AttnArgs &a, hipStream_t st) {
     constexpr int TR = 16 * RT * (WIDE ? kWaves : 1);
-    if constexpr (WIDE)
+    if constexpr (WIDE) {
         hipLaunchKernelGGL((attn_wide_kernel<FP8, D, RT>), dim3(a.groups), dim3(kBlock), 0, st, a);
-    else
+        hipLaunchKernelGGL((attn_wide_join_kernel<D, TR>), dim3(a.groups - 1, TR * D / 256 / kWaves), dim3(kBlock), 0, st, a);
+    } else {
         hipLaunchKernelGGL((attn_kernel<FP8, D, RT>), dim3(a.groups), dim3(kBlock), 0, st, a);
-    // items enough for every eighth range: eight parts an item at most, on the
-    // average; fewer items: more parts than one wave reads at a time
-    const int64_t items = (int64_t)a.R * a.c.heads * ((a.M * a.G + TR - 1) / TR);
-    if (WIDE || items * 8 >= a.groups)
-        hipLaunchKernelGGL((attn_join_kernel<D, TR, false>), dim3(a.groups - 1, TR / kWaves), dim3(kBlock), 0, st, a);
-    else
-        hipLaunchKernelGGL((attn_join_kernel<D, TR, true>), dim3(a.groups - 1, TR), dim3(kBlock), 0, st, a);
+        // items enough for every eighth range: eight parts an item at most, on
+        // the average; fewer items: more parts than one wave reads at a time
+        // (one user's 30 k tokens: 32.6 us with the parts divided, 36.0
+        // without; 64 users, 32 rows: 141.5 and 137.2)
+        const int64_t items = (int64_t)a.R * a.c.heads * ((a.M * a.G + TR - 1) / TR);
+        if (items * 8 >= a.groups)
+            hipLaunchKernelGGL((attn_join_kernel<D, TR, false>), dim3(a.groups - 1, TR / kWaves), dim3(kBlock), 0, st, a);
+        else
+            hipLaunchKernelGGL((attn_join_kernel<D, TR, true>), dim3(a.groups - 1, TR), dim3(kBlock), 0, st, a);
+    }
 }
 template <bool FP8, int D>
 static void launch_attn(const AttnArgs &a, const Shape &s, hipStream_t st) {
@@ -1329,7 +1406,7 @@ static void launch_attn(const AttnArgs &a, const Shape &s, hipStream_t st) {
         }
     } else {
         if (s.RT == 1) launch_attn<FP8, D, 1, false>(a, st);
-        else if constexpr (D <= 128) launch_attn<FP8, D, 2, false>(a, st);
+        else if constexpr (FP8 && D <= 128) launch_attn<FP8, D, 2, false>(a, st);
     }
 }
 template <bool FP8>
@@ -1349,7 +1426,7 @@ size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D)
     if (R < 0 || M < 1 || M > SPEC_TREE_MAX_NODES || Hkv < 1 || Hq < 1 || Hq % Hkv ||
         Hq / Hkv > 64 || (D != 64 && D != 128 && D != 256))
         return 0;
-    const Shape s = shape_of((int64_t)M * (Hq / Hkv), D);
+    const Shape s = shape_of((int64_t)M * (Hq / Hkv), D, false);  // the larger tiles
     return sizeof(Control) + sizeof(Cut) * (kMaxGroups + 1) +
            (size_t)2 * s.groups * s.TR * (D + 2) * sizeof(float);
 }
@@ -1397,7 +1474,7 @@ int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const v
     a.cuts = (Cut *)((char *)workspace + sizeof(Control));
     a.n_cuts = (int *)(a.cuts + kMaxGroups);
     a.part = (float *)(a.cuts + kMaxGroups + 1);
-    const Shape s = shape_of((int64_t)M * a.G, D);
+    const Shape s = shape_of((int64_t)M * a.G, D, cache_dtype == SPEC_E4M3);
     a.groups = s.groups;
     a.part_stride = s.TR * (D + 2);
     // the batch's units must count in 31 bits

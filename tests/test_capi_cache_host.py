@@ -110,6 +110,7 @@ def test_qkv_write_arguments(write):
     for k in ("k", "v", "ctx", "n", "out_q", "rope"):
         assert write(**{k: None}) == EINVAL, k
     assert write(rot=0) == EINVAL                                   # a table without a rotation
+    assert write(max_pos=0) == EINVAL                               # a rotation without a table
     assert write(ld_q=31 * 128) == EINVAL and write(ld_k=8 * 128 - 8) == EINVAL
     assert write(ld_v=8 * 128 + 4) == EINVAL                        # not 16 bytes
     for k in ("q", "k", "v", "qw", "kw", "rope", "out_q"):

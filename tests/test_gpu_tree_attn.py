@@ -244,3 +244,20 @@ def test_unseen_scales_and_codes(sv, dev, M, G, Dh, what, value):
         assert np.isnan(seeing).all()
     if what == "v_scale":                     # the scores have nothing of it
         np.testing.assert_array_equal(got[1], good[1])
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("M,G", [(6, 2), (40, 2)])
+def test_largest_window_and_position(sv, dev, tree, M, G):
+    """2^31 - 1 is as good as no window; a position of 2^31 - 1 is behind every
+    token by more than a small window."""
+    c = Case(21, 1, M, 2 * G, 2, 64, 16, "bf16", [100], tree)
+    free = c.run(sv, dev)
+    c.window = 2 ** 31 - 1
+    for a, b in zip(c.run(sv, dev), free):
+        np.testing.assert_array_equal(a, b)
+    c.window = 5
+    far = np.full(c.pos.shape, 2 ** 31 - 1, np.int32)
+    got = c.run(sv, dev, positions=D(far, dev))
+    c.pos = far.astype(np.int64)
+    c.check(got)
