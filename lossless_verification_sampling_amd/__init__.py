@@ -260,6 +260,7 @@ class Workspace:
     def __init__(self, device=None, nbytes: int = 0):
         self.device = torch.device(device if device is not None else "cuda")
         self.buf: Optional[torch.Tensor] = None
+        self._outgrown = []  # captured graphs go on writing to them
         if nbytes:
             self.ensure(nbytes)
 
@@ -267,6 +268,8 @@ class Workspace:
         if self.buf is None or self.buf.numel() < nbytes:
             n = max(int(nbytes), 1 << 16)
             n = (n + 255) // 256 * 256
+            if self.buf is not None:
+                self._outgrown.append(self.buf)
             self.buf = torch.empty(n, dtype=torch.uint8, device=self.device)
             _raise(_lib.spec_workspace_init(_ptr(self.buf), n, _stream_ptr(stream, self.device)),
                    "spec_workspace_init")

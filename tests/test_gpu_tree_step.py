@@ -175,6 +175,28 @@ def test_two_graphs_share_a_workspace(sv, dev):
             assert torch.equal(x, y)
 
 
+def test_a_graph_keeps_a_workspace_that_was_outgrown(sv, dev):
+    """A larger call after the capture takes a new buffer; the replay still
+    writes to the old one, which nobody else may have got meanwhile."""
+    s = Step(39, "bf16", dev)
+    need = sv.spec_tree_attention_workspace_bytes(3, 12, 4, 2, 64)
+    ws = sv.Workspace(dev, need)
+    run, fill = calls(sv, s, dev, 1, ws)
+    g, out = capture(run)
+    size = ws.nbytes
+    ws.ensure(2 * size)
+    others = [torch.full((size,), 77, dtype=torch.uint8, device=dev) for _ in range(3)]
+    fill(1)
+    want = [x.clone() for x in run()]
+    for t in out:
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(out, want):
+        assert torch.equal(x, y)
+    assert all((o == 77).all() for o in others)
+
+
 def test_two_streams_with_workspaces_of_their_own(sv, dev):
     steps = [Step(35 + i, "e4m3", dev, M=20) for i in range(2)]
     spaces = [sv.Workspace(dev, sv.spec_tree_attention_workspace_bytes(3, 20, 4, 2, 64)) for _ in steps]
