@@ -282,3 +282,45 @@ def test_refusals(sv, dev):
         sv.spec_kv_read(k, k, tb, z, z, -1)
     with pytest.raises(sv.SpecError):
         sv.spec_kv_commit(k, k, tb, z, z, torch.zeros(2, 3, dtype=torch.int32, device=dev), out_ctx_len=z)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("M", [3, 24])
+def test_pages_past_32_bits(sv, dev, kind, M):
+    """The same step over pages whose byte offsets pass 2^32: the same bits."""
+    s = Step(40, kind, dev, M=M + 3, Dh=128, page=64)
+    near, far = s.c, Step(40, kind, dev, M=M + 3, Dh=128, page=64).c
+    shape = near.dev[0].shape
+    gap = (1 << 32) // (shape[1] * shape[2] * shape[3] * near.dev[0].element_size())
+    for w in (0, 1):
+        big = torch.empty((gap + shape[0],) + shape[1:], dtype=near.dev[w].dtype, device=dev)
+        big[gap:].copy_(near.dev[w])
+        far.dev[w] = big
+        if kind == "e4m3":
+            sc = torch.empty((gap + shape[0],) + shape[1:3], device=dev)
+            sc[gap:].copy_(near.scales[w])
+            far.scales[w] = sc
+    far.P, far.t = gap + shape[0], near.t + gap
+    outs = []
+    n, parent, qkv = s.draft()
+    for c in (near, far):
+        s.c = c
+        R, M1, Hq, Hkv, Dh, V = s.dims
+        x, nd, ctx = qkv.to(dev), D(n, dev), D(s.ctx, dev)
+        pos, mask = sv.spec_tree_mask(D(parent, dev), nd, ctx)
+        q = sv.spec_qkv_write(x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:], *c.args(), ctx, nd,
+                              q=x[:, :, :Hq], rope=D(s.rope, dev), positions=pos, **c.kw())
+        o = torch.zeros_like(q)
+        _, lse = sv.spec_tree_attention(q, *c.args(), ctx, nd, mask=mask, positions=pos, out=o,
+                                        out_lse=torch.zeros(R, M1, Hq, device=dev), **c.kw())
+        path = torch.full((R, M1), -1, dtype=torch.int32, device=dev)
+        path[0, :2] = torch.tensor([2, M1 - 1])
+        acc = torch.tensor([2, 0, 0], dtype=torch.int32, device=dev)
+        new = sv.spec_kv_commit(*c.args(), ctx, acc, path, **c.kw())
+        kv = sv.spec_kv_read(*c.args(), torch.zeros_like(ctx), ctx + nd, 60 + M1,
+                             out_k=torch.zeros(R, 60 + M1, Hkv, Dh, device=dev),
+                             out_v=torch.zeros(R, 60 + M1, Hkv, Dh, device=dev), **c.kw())
+        outs.append((o, lse, new, *kv))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert outs[0][0].abs().sum() > 0 and outs[0][3].abs().sum() > 0
