@@ -599,6 +599,9 @@ __device__ __forceinline__ Plain plain_of(const AttnArgs &a, const Req &rq, int 
 // the attention launch
 // ---------------------------------------------------------------------------
 
+// Bound by HBM: a workgroup's waves keep one step of K and V each in flight.
+// One token behind 30011 (bf16): 27.2 us, 4.5 TB/s; 64 chains of 8 behind up to
+// 4 k (e4m3): 83 us, 3.8 TB/s (two waves a SIMD, for the registers).
 template <int D, int RT> constexpr int waves_per_simd() {
     return D <= 128 && D * RT <= 256 ? 2 : 1;
 }
@@ -858,6 +861,10 @@ constexpr int kTile = 64;              // tokens staged at a time
 // instead of the tokens: 64 tokens of K and V go to shared memory once per
 // workgroup, already in operand layout (converted and transposed on the way),
 // while the previous 64 are multiplied, and every wave reads them from there.
+// Bound by HBM for trees (64 of 48 nodes behind up to 4 k tokens, bf16: 177 us,
+// 3.6 TB/s; with the arithmetic left out 150), by the issue of matrix and
+// vector instructions for prompt chunks (4 of 1000 behind 12 k, five heads a
+// key head, e4m3: 803 us, 798 TFLOP/s, the matrix pipes 32% busy).
 template <bool FP8, int D> struct Stage {
     typedef Tile<FP8, D> TT;
     u32x4_t k[TT::KV];
@@ -1169,7 +1176,7 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                 if (eg == 0 && a.lse) a.lse[orow] = (m[x] + log2f(l[x])) * (float)kLn2;
             } else {
                 // as the lanes hold it, a kilobyte a store (rows side by side, as the
-                // output has them, were 16 bytes a line: 24.0 us against 17.3 for one
+                // output has them, were 16 bytes a line: 24.0 us against 19.4 for one
                 // tree of 48 nodes behind 4 k tokens)
                 float *pp = a.part + (size_t)(2 * grp + (u0 == 0)) * a.part_stride;
                 float *po = pp + (wave * RT + x) * 16 * D + 4 * el;
