@@ -261,3 +261,19 @@ def test_largest_window_and_position(sv, dev, tree, M, G):
     got = c.run(sv, dev, positions=D(far, dev))
     c.pos = far.astype(np.int64)
     c.check(got)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("shape", [
+    (1, 30, 8, 2, 128, 32, [150], True, 0, None),               # 120 rows: two tiles a wave
+    (2, 24, 8, 2, 128, 64, [9000, 5], True, 0, [24, 9]),        # an item in many parts, many rows
+    (2, 24, 6, 1, 256, 128, [5000, 0], False, 900, None),
+    (1, 70, 9, 3, 64, 16, [3001], True, 40, None),
+    (4, 1, 8, 8, 64, 64, [9000, 8900, 9000, 8999], False, 0, None),  # units for two ranges a compute unit
+    (3, 8, 4, 1, 128, 16, [2000, 1, 700], False, 0, [8, 8, 5]),  # 32 rows
+])
+def test_splits_and_joins(sv, dev, shape, kind):
+    R, M, Hq, Hkv, Dh, page, ctx, tree, window, n = shape
+    print(f"[attn] {shape} {kind}", flush=True)
+    c = Case(sum(ctx) + M, R, M, Hq, Hkv, Dh, page, kind, ctx, tree, window, n)
+    c.check(c.run(sv, dev))
