@@ -681,7 +681,8 @@ def _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev):
 
 def _device(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
-    _need(dev >= 0, f"{name} must be a device tensor")
+    if dev < 0:
+        raise ValueError(f"{name} must be a device tensor")
     return dev
 
 
@@ -689,19 +690,19 @@ def _raw(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _ordered_heads(t: torch.Tensor, name: str, dev: int) -> int:
+def _ordered_heads(t: torch.Tensor, name: str, shape, dev: int) -> int:
     """Elements from one token's heads to the next of [R, M, H, D] whose
     tokens are evenly spaced and whose heads are dense."""
-    _need(t.get_device() == dev, f"{name} must be on cuda:{dev}")
-    R, M, H, D = t.shape
-    if t.numel() == 0:
-        return H * D
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    R, M, H, D = shape
     s0, s1, s2, s3 = t.stride()
-    ld = s1 if M > 1 else s0 if R > 1 else H * D
-    _need((D == 1 or s3 == 1) and (H == 1 or s2 == D) and ld >= H * D and
-          (R == 1 or M == 1 or s0 == M * ld),
-          f"{name} must hold dense heads at evenly spaced tokens")
-    return ld
+    row = H * D
+    ld = s1 if M > 1 else s0 if R > 1 else row
+    if ((s3 != 1 and D > 1) or (s2 != D and H > 1) or ld < row or
+            (s0 != M * ld and R > 1 and M > 1)) and t.numel():
+        raise ValueError(f"{name} must hold dense heads at evenly spaced tokens")
+    return ld if ld > row else row
 
 
 def _cache_buf(workspace, dev: int, need: int, stream):
@@ -763,12 +764,12 @@ def spec_qkv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     dtype = k.dtype
     dt = _dtype(k)
     _need(v.dtype is dtype and (q is None or q.dtype is dtype), "q, k and v differ in type")
-    ld_k, ld_v = _ordered_heads(k, "k", dev), _ordered_heads(v, "v", dev)
+    ld_k, ld_v = _ordered_heads(k, "k", shape, dev), _ordered_heads(v, "v", shape, dev)
     Hq = ld_q = 0
     if q is not None:
         qs = q.shape
         _need(len(qs) == 4 and qs[0] == R and qs[1] == M and qs[3] == D, "q must be [R, M, Hq, D]")
-        Hq, ld_q = qs[2], _ordered_heads(q, "q", dev)
+        Hq, ld_q = qs[2], _ordered_heads(q, "q", qs, dev)
         if out_q is None:
             out_q = torch.empty(qs, dtype=torch.bfloat16, device=k.device)
     else:
