@@ -551,7 +551,8 @@ int spec_kv_commit(void *k_cache, void *v_cache, int cache_dtype, float *k_scale
                    int M, int Hkv, int D, int32_t *out_ctx_len, void *workspace,
                    size_t workspace_bytes, void *stream);
 
-/* Workspace bytes for spec_tree_attention (0 for sizes it does not accept). */
+/* Workspace bytes for spec_tree_attention with these sizes or smaller R and M
+ * (0 for sizes it does not accept). */
 size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D);
 
 /*
@@ -578,8 +579,8 @@ size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D)
  * A faulty request's or node's rows become NaN, and so do the rows that see a
  * token in a bad page.  The tokens of the tree must be in the cache
  * (spec_qkv_write).  A call repeated gives the same bits; the order of a
- * row's sums depends on the lengths in the batch, and on nothing that the
- * row does not see.
+ * row's sums depends on R, M and the lengths in the batch, and on nothing
+ * else that the row does not see.
  * Sizes: R >= 0, 1 <= M <= SPEC_TREE_MAX_NODES, Hq / Hkv <= 64, window >= 0.
  */
 int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const void *v_cache,

@@ -14,6 +14,7 @@ importing this module without it raises, there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -705,6 +706,11 @@ def _ordered_heads(t: torch.Tensor, name: str, shape, dev: int) -> int:
     return ld if ld > row else row
 
 
+@functools.lru_cache(maxsize=256)
+def _attention_bytes(*sizes) -> int:
+    return _lib.spec_tree_attention_workspace_bytes(*sizes)
+
+
 def _cache_buf(workspace, dev: int, need: int, stream):
     ws = workspace or _default_ws.get(("cuda", dev)) or default_workspace(torch.device("cuda", dev))
     buf = ws.buf
@@ -885,7 +891,7 @@ def spec_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
          (n_nodes, "n_nodes", i32, (R,)), (mask, "mask", i32, (R, M, (M + 31) // 32)),
          (positions, "positions", i32, (R, M)), (out, "out", torch.bfloat16, shape),
          (out_lse, "out_lse", torch.float32, shape[:3]))
-    need = _lib.spec_tree_attention_workspace_bytes(R, M, Hq, Hkv, D)
+    need = _attention_bytes(R, M, Hq, Hkv, D)
     if need == 0:
         raise SpecError(-5, "spec_tree_attention_workspace_bytes")
     buf, room = _cache_buf(workspace, dev, need, stream)

@@ -1365,16 +1365,22 @@ __global__ void __launch_bounds__(kBlock) attn_wide_join_kernel(AttnArgs a) {
 // against 649 with two (D = 128, e4m3: each operand from shared memory serves
 // three products), so two are taken where they leave over 13% fewer rows
 // empty (16 trees of 64 nodes, 256 rows: 97 us against 104; 192 rows: 81.8
-// against 80.3).
+// against 80.3).  A small batch, up to 48 rows to a compute unit, takes one:
+// more workgroups with less to store for the join, for pages read again from
+// L2 (one tree of 48 nodes behind 200 tokens 14.0 us against 20.1, behind 4 k
+// 27.7 and 31.4, behind 30 k 72 and 68; 8 trees 50.3 and 53.6, 16 trees 93 and
+// 81).
 struct Shape {
     bool wide;
     int RT, TR, groups;
 };
-inline Shape shape_of(int64_t rows, int D, bool fp8) {
+constexpr int64_t kSmallBatch = 48 * (kMaxGroups / 2);
+// rows: a request's per key head; heads: key heads of all requests.
+inline Shape shape_of(int64_t rows, int64_t heads, int D, bool fp8) {
     Shape s;
     s.wide = rows > (fp8 && D <= 128 ? 32 : 16);
     if (!s.wide) s.RT = rows <= 16 ? 1 : 2;
-    else if (D == 256 || rows <= 64) s.RT = 1;
+    else if (D == 256 || rows <= 64 || rows * heads <= kSmallBatch) s.RT = 1;
     else {
         const int64_t two = (rows + 127) / 128 * 128, three = (rows + 191) / 192 * 192;
         s.RT = two * 100 < three * 87 ? 2 : 3;
@@ -1433,9 +1439,11 @@ size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D)
     if (R < 0 || M < 1 || M > SPEC_TREE_MAX_NODES || Hkv < 1 || Hq < 1 || Hq % Hkv ||
         Hq / Hkv > 64 || (D != 64 && D != 128 && D != 256))
         return 0;
-    const Shape s = shape_of((int64_t)M * (Hq / Hkv), D, false);  // the larger tiles
-    return sizeof(Control) + sizeof(Cut) * (kMaxGroups + 1) +
-           (size_t)2 * s.groups * s.TR * (D + 2) * sizeof(float);
+    // the largest tiles that these sizes or smaller ones take
+    const int rows = M * (Hq / Hkv);
+    const size_t TR = rows <= 16 ? 16 : D == 256 || rows <= 64 ? 64 : 192;
+    const size_t groups = D <= 128 ? kMaxGroups : kMaxGroups / 2;
+    return sizeof(Control) + sizeof(Cut) * (kMaxGroups + 1) + 2 * groups * TR * (D + 2) * sizeof(float);
 }
 
 int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const void *v_cache,
@@ -1481,7 +1489,7 @@ int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const v
     a.cuts = (Cut *)((char *)workspace + sizeof(Control));
     a.n_cuts = (int *)(a.cuts + kMaxGroups);
     a.part = (float *)(a.cuts + kMaxGroups + 1);
-    const Shape s = shape_of((int64_t)M * a.G, D, cache_dtype == SPEC_E4M3);
+    const Shape s = shape_of((int64_t)M * a.G, (int64_t)R * Hkv, D, cache_dtype == SPEC_E4M3);
     a.groups = s.groups;
     a.part_stride = s.TR * (D + 2);
     // the batch's units must count in 31 bits

@@ -150,3 +150,14 @@ def test_tree_attention_arguments(lib, attn):
     for k in ("q", "ctx", "n", "out"):
         assert attn(**{k: None}) == EINVAL, k
     assert attn(q=A + 8) == EINVAL and attn(out=A + 8) == EINVAL
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 4, 7])
+def test_attention_workspace_covers_smaller_calls(lib, D, G):
+    lib.spec_tree_attention_workspace_bytes.restype = S
+    last = 0
+    for M in list(range(1, 200)) + [256, 1000, 1024]:
+        need = lib.spec_tree_attention_workspace_bytes(64, M, 2 * G, 2, D)
+        assert need >= last > -1 and need == lib.spec_tree_attention_workspace_bytes(1, M, 2 * G, 2, D)
+        last = need

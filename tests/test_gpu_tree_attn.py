@@ -277,3 +277,44 @@ def test_splits_and_joins(sv, dev, shape, kind):
     print(f"[attn] {shape} {kind}", flush=True)
     c = Case(sum(ctx) + M, R, M, Hq, Hkv, Dh, page, kind, ctx, tree, window, n)
     c.check(c.run(sv, dev))
+
+
+def ragged(R, top, seed):
+    g = np.random.default_rng(seed)
+    return [int(x) for x in g.integers(0, top, R)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("shape", [                             # batches of more than 12288 rows
+    (33, 48, 16, 4, 128, 32, ragged(33, 300, 1), True, 0, ragged(33, 49, 2)),   # three tiles a wave
+    (40, 64, 8, 2, 128, 16, ragged(40, 200, 3), True, 30, None),                # two
+    (70, 100, 4, 2, 64, 64, ragged(70, 130, 4), False, 0, ragged(70, 101, 5)),  # three, D = 64
+    (60, 33, 21, 3, 64, 32, ragged(60, 500, 6), False, 77, None),               # two, D = 64
+    (30, 10, 128, 2, 256, 16, ragged(30, 90, 7), True, 0, None),                # one, D = 256
+    (1, 1024, 16, 2, 64, 128, [1100], False, 0, None),                          # few items in many parts
+])
+def test_large_batches(sv, dev, shape, kind):
+    R, M, Hq, Hkv, Dh, page, ctx, tree, window, n = shape
+    print(f"[attn] {shape} {kind}", flush=True)
+    c = Case(sum(ctx) + M, R, M, Hq, Hkv, Dh, page, kind, ctx, tree, window, n)
+    c.check(c.run(sv, dev))
+
+
+@pytest.mark.parametrize("what,value", [("none", 0.0), ("v_scale", np.nan), ("codes", np.nan)])
+def test_unseen_in_large_batches(sv, dev, what, value):
+    R, M, bad = 30, 48, 3
+    a, b = [Case(22, R, M, 12, 3, 128, 16, "e4m3", [37] * R, True) for _ in range(2)]
+    for r in range(R):
+        at = int(a.c.table[r, (37 + bad) // 16]), 1, (37 + bad) % 16
+        if what == "v_scale":
+            a.c.scales[1][at] = value
+        elif what == "codes":
+            a.c.dev[1].view(torch.uint8)[at] = 0x7f
+    got, good = a.run(sv, dev), b.run(sv, dev)
+    for r in range(R):
+        blind = ~a.see[r, :, bad]
+        for x, y in zip(got, good):
+            np.testing.assert_array_equal(x[r, blind], y[r, blind])
+        if what != "none":
+            assert np.isnan(got[0][r, ~blind, 4:8]).all()
+            np.testing.assert_array_equal(got[0][r, ~blind, :4], good[0][r, ~blind, :4])
