@@ -716,6 +716,8 @@ def _cache_buf(workspace, dev: int, need: int, stream):
     buf = ws.buf
     if buf is None or buf.numel() < need:
         buf = ws.ensure(need, stream)
+    if buf.get_device() != dev:
+        raise ValueError(f"workspace is on {buf.device}, expected cuda:{dev}")
     return buf.data_ptr(), buf.numel()
 
 
@@ -737,9 +739,9 @@ def spec_tree_mask(parent: torch.Tensor, n_nodes: torch.Tensor, ctx_len: torch.T
          (ctx_len, "ctx_len", i32, (R,)), (pos, "out_positions", i32, shape),
          (mask, "out_mask", i32, words))
     buf, size = _cache_buf(workspace, dev, 256, stream)
-    st = _run(dev, _lib.spec_tree_mask, parent.data_ptr(), n_nodes.data_ptr(), ctx_len.data_ptr(), R, M,
-                             int(window), pos.data_ptr(), mask.data_ptr(), buf, size,
-                             _stream_of(stream, dev))
+    st = _run(dev, _lib.spec_tree_mask, parent.data_ptr(), n_nodes.data_ptr(), ctx_len.data_ptr(),
+              R, M, int(window), pos.data_ptr(), mask.data_ptr(), buf, size,
+              _stream_of(stream, dev))
     if st:
         _raise(st, "spec_tree_mask")
     return pos, mask
@@ -794,12 +796,10 @@ def spec_qkv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
          (n_nodes, "n_nodes", i32, (R,)))
     buf, room = _cache_buf(workspace, dev, 256, stream)
     st = _run(dev, _lib.spec_qkv_write, _raw(q), k.data_ptr(), v.data_ptr(), dt, ld_q, ld_k, ld_v,
-                             _raw(q_weight), _raw(k_weight), eps, _raw(rope), max_pos, rot,
-                             int(interleaved), _raw(positions), ctx_len.data_ptr(),
-                             n_nodes.data_ptr(), page_table.data_ptr(), wide, R, M, Hq, Hkv, D,
-                             k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
-                             _raw(v_scale), P, size, _raw(out_q), buf, room,
-                             _stream_of(stream, dev))
+              _raw(q_weight), _raw(k_weight), eps, _raw(rope), max_pos, rot, int(interleaved),
+              _raw(positions), ctx_len.data_ptr(), n_nodes.data_ptr(), page_table.data_ptr(), wide,
+              R, M, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
+              _raw(v_scale), P, size, _raw(out_q), buf, room, _stream_of(stream, dev))
     if st:
         _raise(st, "spec_qkv_write")
     return out_q
@@ -830,9 +830,9 @@ def spec_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
          (out_k, "out_k", dtype, shape), (out_v, "out_v", dtype, shape))
     buf, room = _cache_buf(workspace, dev, 256, stream)
     st = _run(dev, _lib.spec_kv_read, k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
-                           _raw(v_scale), P, size, page_table.data_ptr(), wide, start.data_ptr(),
-                           length.data_ptr(), R, max_len, Hkv, D, out_k.data_ptr(),
-                           out_v.data_ptr(), _dtype(out_k), buf, room, _stream_of(stream, dev))
+              _raw(v_scale), P, size, page_table.data_ptr(), wide, start.data_ptr(),
+              length.data_ptr(), R, max_len, Hkv, D, out_k.data_ptr(), out_v.data_ptr(),
+              _dtype(out_k), buf, room, _stream_of(stream, dev))
     if st:
         _raise(st, "spec_kv_read")
     return out_k, out_v
@@ -855,9 +855,9 @@ def spec_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: tor
          (path, "path", i32, (R, M)), (out_ctx_len, "out_ctx_len", i32, (R,)))
     buf, room = _cache_buf(workspace, dev, 256, stream)
     st = _run(dev, _lib.spec_kv_commit, k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
-                             _raw(v_scale), P, size, page_table.data_ptr(), wide,
-                             ctx_len.data_ptr(), accepted.data_ptr(), path.data_ptr(), R, M, Hkv,
-                             D, out_ctx_len.data_ptr(), buf, room, _stream_of(stream, dev))
+              _raw(v_scale), P, size, page_table.data_ptr(), wide, ctx_len.data_ptr(),
+              accepted.data_ptr(), path.data_ptr(), R, M, Hkv, D, out_ctx_len.data_ptr(), buf, room,
+              _stream_of(stream, dev))
     if st:
         _raise(st, "spec_kv_commit")
     return out_ctx_len
@@ -895,13 +895,11 @@ def spec_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if need == 0:
         raise SpecError(-5, "spec_tree_attention_workspace_bytes")
     buf, room = _cache_buf(workspace, dev, need, stream)
-    st = _run(dev, _lib.spec_tree_attention, q.data_ptr(), SPEC_BF16, k_cache.data_ptr(), v_cache.data_ptr(),
-                                  code, _raw(k_scale), _raw(v_scale), P, size,
-                                  page_table.data_ptr(), wide, ctx_len.data_ptr(),
-                                  n_nodes.data_ptr(), _raw(mask), _raw(positions),
-                                  D ** -0.5 if scale is None else scale, int(window), R, M, Hq,
-                                  Hkv, D, out.data_ptr(), _raw(out_lse), buf, room,
-                                  _stream_of(stream, dev))
+    st = _run(dev, _lib.spec_tree_attention, q.data_ptr(), SPEC_BF16, k_cache.data_ptr(),
+              v_cache.data_ptr(), code, _raw(k_scale), _raw(v_scale), P, size,
+              page_table.data_ptr(), wide, ctx_len.data_ptr(), n_nodes.data_ptr(), _raw(mask),
+              _raw(positions), D ** -0.5 if scale is None else scale, int(window), R, M, Hq, Hkv, D,
+              out.data_ptr(), _raw(out_lse), buf, room, _stream_of(stream, dev))
     if st:
         _raise(st, "spec_tree_attention")
     return out, out_lse

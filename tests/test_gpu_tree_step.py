@@ -324,3 +324,19 @@ def test_pages_past_32_bits(sv, dev, kind, M):
     for a, b in zip(*outs):
         assert torch.equal(a, b)
     assert outs[0][0].abs().sum() > 0 and outs[0][3].abs().sum() > 0
+
+
+def test_a_workspace_elsewhere_is_refused(sv, dev):
+    ws = sv.Workspace(dev, 256)
+    ws.buf = torch.zeros(1 << 26, dtype=torch.uint8)
+    k = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16, device=dev)
+    z = torch.zeros(2, dtype=torch.int32, device=dev)
+    tb = torch.zeros(2, 1, dtype=torch.int32, device=dev)
+    q = torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16, device=dev)
+    for call in (lambda: sv.spec_tree_mask(tb, z, z, workspace=ws),
+                 lambda: sv.spec_tree_attention(q, k, k, tb, z, z, workspace=ws),
+                 lambda: sv.spec_qkv_write(q[:, :, :1], q[:, :, 1:], k, k, tb, z, z, workspace=ws),
+                 lambda: sv.spec_kv_read(k, k, tb, z, z, 3, workspace=ws),
+                 lambda: sv.spec_kv_commit(k, k, tb, z, z, tb, workspace=ws)):
+        with pytest.raises(ValueError):
+            call()
