@@ -1111,25 +1111,32 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                     }
                     rare |= (fl0 | fl1) & 1;
                     lift(top, m, l, acc);
-                    // ---- product
-                    u32x4_t pw[RT];
-#pragma unroll
-                    for (int x = 0; x < RT; ++x) pw[x] = weigh<FP8>(p[x], sc, a.scale2, m[x], l[x]);
-#pragma unroll
-                    for (int j0 = 0; j0 < DV; j0 += 4) {
-                        u32x4_t vf[4];
+                    // ---- product; the first operands come while the weights are made
+                    const auto load_vf = [&](int j0, u32x4_t (&vf)[4]) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const u32x2_t lo = sh.v[b][half][j0 + j][0][lane], hi = sh.v[b][half][j0 + j][1][lane];
                             vf[j] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
                         }
+                    };
+                    u32x4_t vf[DV / 4][4];
+                    load_vf(0, vf[0]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    u32x4_t pw[RT];
+#pragma unroll
+                    for (int x = 0; x < RT; ++x) pw[x] = weigh<FP8>(p[x], sc, a.scale2, m[x], l[x]);
+#pragma unroll
+                    for (int q = 0; q < DV / 4; ++q) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (q + 1 < DV / 4) load_vf(4 * (q + 1), vf[q + 1]);
+                        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
                             for (int x = 0; x < RT; ++x)
-                                acc[x][j0 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                    __builtin_bit_cast(bf16x8_t, vf[j]), __builtin_bit_cast(bf16x8_t, pw[x]),
-                                    acc[x][j0 + j], 0, 0, 0);
+                                acc[x][4 * q + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                    __builtin_bit_cast(bf16x8_t, vf[q][j]), __builtin_bit_cast(bf16x8_t, pw[x]),
+                                    acc[x][4 * q + j], 0, 0, 0);
                     }
                 }
                 if (more) keep(b ^ 1, tile + kTile);
