@@ -45,10 +45,11 @@ __device__ __forceinline__ uint32_t e4m3_bf16(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
 }
 
-// Whether count tokens from first lie inside the page table.
+// Whether count tokens from first lie inside the page table, and far enough
+// below 2^31 for token numbers a few steps ahead to be 32-bit ones.
 __device__ __forceinline__ bool in_table(int first, int count, int max_pages, int shift) {
     return first >= 0 && count >= 0 &&
-           (int64_t)first + count <= ((int64_t)max_pages << shift);
+           (int64_t)first + count <= min((int64_t)max_pages << shift, (int64_t)0x7ffff000);
 }
 
 // Host checks of a cache's arguments that every entry point shares; 0 or a

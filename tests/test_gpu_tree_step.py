@@ -340,3 +340,28 @@ def test_a_workspace_elsewhere_is_refused(sv, dev):
                  lambda: sv.spec_kv_commit(k, k, tb, z, z, tb, workspace=ws)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_token_numbers_past_31_bits_are_faults(sv, dev):
+    """A table wide enough for more than 2^31 tokens (its pages repeat)."""
+    k = torch.zeros(1, 1, 1024, 64, dtype=torch.bfloat16, device=dev)
+    tb = torch.zeros(1, (1 << 21) + 8, dtype=torch.int32, device=dev)
+    ctx = torch.tensor([2 ** 31 - 1000], dtype=torch.int32, device=dev)
+    n = torch.tensor([1010], dtype=torch.int32, device=dev)
+    few = torch.tensor([3], dtype=torch.int32, device=dev)
+    q = torch.ones(1, 1024, 1, 64, dtype=torch.bfloat16, device=dev)
+    ws = sv.Workspace(dev, sv.spec_tree_attention_workspace_bytes(1, 1024, 1, 1, 64))
+
+    def bad():
+        return sv.spec_get_device_status(ws) == sv.SPEC_DEV_BAD_REQUEST
+    for m in (n, few):
+        x = q[:, :int(m)].contiguous()
+        out, _ = sv.spec_tree_attention(x, k, k, tb, ctx, m, workspace=ws)
+        assert bad() and torch.isnan(out).all()
+        out = sv.spec_qkv_write(x, x, k, k, tb, ctx, m, q=x, workspace=ws)
+        assert bad() and torch.isnan(out).all() and not k.any()
+        out, _ = sv.spec_kv_read(k, k, tb, ctx, m, int(m), workspace=ws)
+        assert bad() and torch.isnan(out).all()
+    path = torch.tensor([[2, 3, -1, -1]], dtype=torch.int32, device=dev)
+    new = sv.spec_kv_commit(k, k, tb, ctx, few - 1, path, workspace=ws)
+    assert bad() and int(new) == -1
