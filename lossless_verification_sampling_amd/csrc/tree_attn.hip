@@ -589,7 +589,9 @@ __device__ __forceinline__ Plain plain_of(const AttnArgs &a, const Req &rq, int 
         int far = 0;
 #pragma unroll
         for (int x = 0; x < RT; ++x) far = max(far, query_of(a, rq, r, row0 + x * 16 + c).pos);
-        p.lo = wave_max_i(far) - a.window + 1;
+        // (a position may be anything up to 2^31 - 1: inside the item, lo can be
+        // rounded up to a tile in 32 bits)
+        p.lo = min(max(wave_max_i(far) - a.window + 1, 0), t1);
     }
     p.hi = min(p.hi, t1);
     return p;

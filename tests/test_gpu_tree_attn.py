@@ -318,3 +318,14 @@ def test_unseen_in_large_batches(sv, dev, what, value):
         if what != "none":
             assert np.isnan(got[0][r, ~blind, 4:8]).all()
             np.testing.assert_array_equal(got[0][r, ~blind, :4], good[0][r, ~blind, :4])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("ctx,window", [(20, 5), (40, 34), (64, 34), (70, 50), (93, 63)])
+def test_a_far_position_beside_others(sv, dev, kind, ctx, window):
+    """One node's position is 2^31 - 1, the others' are ordinary; the context's
+    first tokens are out of everybody's window."""
+    c = Case(23, 1, 40, 4, 2, 64, 16, kind, [ctx], True, window)
+    c.pos = c.pos.copy()
+    c.pos[0, 7] = 2 ** 31 - 1
+    c.check(c.run(sv, dev))
