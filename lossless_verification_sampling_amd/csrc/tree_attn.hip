@@ -808,9 +808,11 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                 if (whole) {
                     const int nd = row / a.G;
                     const size_t orow = ((size_t)r * a.M + nd) * a.Hq + h * a.G + (row - nd * a.G);
-                    if (sum == 0.f) {  // nothing seen: o is 0
+                    if (sum == 0.f) {  // no weight at all: o is 0, whatever V holds
                         sum = 1.f;
                         mm = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < DV; ++j) o[j] = 0.f;
                     }
                     const float inv = 1.f / sum;
                     uint16_t *op = a.out + orow * D + e0;
@@ -1169,9 +1171,11 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
             }
             if (whole) {
                 const size_t orow = ((size_t)r * a.M + q.node) * a.Hq + h * a.G + (row - q.node * a.G);
-                if (l[x] == 0.f) {  // nothing seen: o is 0
+                if (l[x] == 0.f) {  // no weight at all: o is 0, whatever V holds
                     l[x] = 1.f;
                     m[x] = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < DV; ++j) acc[x][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
                 }
                 const float inv = 1.f / l[x];
 #pragma unroll
@@ -1293,9 +1297,10 @@ __global__ void __launch_bounds__(kBlock) attn_join_kernel(AttnArgs a) {
     }
     const int row = cut.row0 + lr, nd = row / a.G;
     const size_t orow = (size_t)(cut.node0 + nd) * a.Hq + cut.h * a.G + (row - nd * a.G);
-    if (sum == 0.f) {  // nothing seen: o is 0
+    if (sum == 0.f) {  // no weight at all: o is 0, whatever V holds
         sum = 1.f;
         m = -INFINITY;
+        for (int q = 0; q < E; ++q) o[q] = 0.f;
     }
     const float inv = 1.f / sum;
     uint16_t *op = a.out + orow * D + lane * E;
@@ -1352,9 +1357,10 @@ __global__ void __launch_bounds__(kBlock) attn_wide_join_kernel(AttnArgs a) {
     if (lr >= cut.rows) return;
     const int row = cut.row0 + lr, nd = row / a.G;
     const size_t orow = (size_t)(cut.node0 + nd) * a.Hq + cut.h * a.G + (row - nd * a.G);
-    if (sum == 0.f) {  // nothing seen: o is 0
+    if (sum == 0.f) {  // no weight at all: o is 0, whatever V holds
         sum = 1.f;
         m = -INFINITY;
+        o = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
     o *= 1.f / sum;
     // piece = i (DV / 4) + j / 4: the lane's values d = DV (4 g + i) + j on

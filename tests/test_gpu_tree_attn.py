@@ -329,3 +329,15 @@ def test_a_far_position_beside_others(sv, dev, kind, ctx, window):
     c.pos = c.pos.copy()
     c.pos[0, 7] = 2 ** 31 - 1
     c.check(c.run(sv, dev))
+
+
+@pytest.mark.parametrize("M,G", [(8, 2), (40, 2)])
+@pytest.mark.parametrize("ctx", [0, 300, 5000])
+def test_scores_of_minus_infinity(sv, dev, M, G, ctx):
+    """Every score is -inf: the row is 0, whatever V holds."""
+    c = Case(24, 1, M, G, 1, 64, 16, "bf16", [ctx], False)
+    c.q[..., 5] = c.q[..., 5].abs() + 1
+    c.c.dev[0][..., 5] = -float("inf")
+    c.c.dev[1][..., 9] = float("inf")
+    out, lse = c.run(sv, dev)
+    assert not out.any() and (lse == -np.inf).all()
