@@ -451,8 +451,11 @@ int spec_tree_verify(const void *logits, int dtype, const int32_t *parent, const
  *    n_nodes[r] are neither read nor written, in inputs, outputs or cache.
  *  - Data faults (each sets SPEC_DEV_BAD_REQUEST): n_nodes outside [0, M],
  *    ctx_len < 0 or ctx_len + n_nodes past the page table (or 2^31 - 4096
- *    tokens, whatever the table's width) mark the whole request; a page number outside [0, num_pages) marks the tokens in it.
- *    Nothing outside the given arrays is read or written for them.
+ *    tokens, whatever the table's width) mark the whole request; a page number
+ *    outside [0, num_pages) marks the tokens in it.  Nothing outside the given
+ *    arrays is read or written for them.  Only page numbers of tokens that a call
+ *    reads or writes are looked at; attention with a window reads those from
+ *    ctx_len - window + 1 on, so pages before may have been given back.
  *  - Two requests may share pages that only hold context (a common prefix);
  *    a page that one call writes must belong to one request.
  */

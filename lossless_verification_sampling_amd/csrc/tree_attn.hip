@@ -66,7 +66,7 @@ struct AttnArgs {
 
 struct Req {
     int n, ctx, rows, tiles;     // live nodes, context, query rows per key head, row tiles
-    int lo;                      // first token any row sees
+    int lo;                      // the 16 tokens with the first one that any row sees
     bool ok;
 };
 
@@ -82,7 +82,9 @@ __device__ __forceinline__ Req request_of(const AttnArgs &a, int r) {
     }
     q.rows = q.n * a.G;
     q.tiles = (q.rows + TR - 1) / TR;
-    q.lo = a.window ? max(0, q.ctx - a.window + 1) & ~(kStep - 1) : 0;
+    // (no lower: 16 tokens always share a page, 32 need not, and the page before
+    // the first token seen may have been given back)
+    q.lo = a.window ? max(0, q.ctx - a.window + 1) & ~15 : 0;
     return q;
 }
 

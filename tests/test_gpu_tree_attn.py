@@ -341,3 +341,17 @@ def test_scores_of_minus_infinity(sv, dev, M, G, ctx):
     c.c.dev[1][..., 9] = float("inf")
     out, lse = c.run(sv, dev)
     assert not out.any() and (lse == -np.inf).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("M,G", [(8, 2), (40, 2)])
+@pytest.mark.parametrize("ctx,window", [(69, 20), (79, 32), (500, 21)])
+def test_pages_before_the_window_are_not_looked_at(sv, dev, kind, tree, M, G, ctx, window):
+    """Pages of 16 tokens that lie before token ctx - window + 1 were given back."""
+    c = Case(25, 1, M, G, 1, 64, 16, kind, [ctx], tree, window)
+    c.c.table[0, :(ctx - window + 1) // 16] = -1
+    ws = sv.Workspace(dev, sv.spec_tree_attention_workspace_bytes(1, M, G, 1, 64))
+    got = c.run(sv, dev, workspace=ws)
+    assert sv.spec_get_device_status(ws) == 0
+    c.check(got)
