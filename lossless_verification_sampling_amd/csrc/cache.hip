@@ -475,8 +475,9 @@ int spec_qkv_write(const void *q, const void *k, const void *v, int dtype, int64
     if (rot_dim > 0 && max_pos < 1) return SPEC_EINVAL;
     const int64_t tokens = (int64_t)R * M;
     if (tokens > 0x7fffffff) return SPEC_EUNSUPPORTED;
-    if (q ? Hq < 1 || Hq % Hkv : Hq != 0) return SPEC_EINVAL;
-    if (tokens == 0) return SPEC_OK;
+    if (Hq % Hkv) return SPEC_EINVAL;
+    if (tokens == 0) return SPEC_OK;  // (an empty q may well be null)
+    if ((q != nullptr) != (Hq > 0)) return SPEC_EINVAL;
     if (!k || !v || !ctx_len || !n_nodes || (max_pages > 0 && !page_table) || (q && !out_q) || (rot_dim > 0) != (rope != nullptr))
         return SPEC_EINVAL;
     const int64_t per = dtype == SPEC_BF16 ? 8 : 4;  // elements of 16 bytes

@@ -161,3 +161,12 @@ def test_attention_workspace_covers_smaller_calls(lib, D, G):
         need = lib.spec_tree_attention_workspace_bytes(64, M, 2 * G, 2, D)
         assert need >= last > -1 and need == lib.spec_tree_attention_workspace_bytes(1, M, 2 * G, 2, D)
         last = need
+
+
+def test_an_empty_write_is_no_fault_whatever_is_null(write):
+    """An empty tensor's pointer is null."""
+    for size in (dict(R=0), dict(M=0), dict(R=0, M=0)):
+        assert write(q=None, out_q=None, **size) == OK
+        assert write(q=None, k=None, v=None, out_q=None, ctx=None, n=None, table=None, **size) == OK
+        assert write(q=None, Hq=0, out_q=None, **size) == OK
+        assert write(Hq=30, **size) == EINVAL and write(Hq=-8, **size) == EINVAL

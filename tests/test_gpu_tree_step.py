@@ -365,3 +365,17 @@ def test_token_numbers_past_31_bits_are_faults(sv, dev):
     path = torch.tensor([[2, 3, -1, -1]], dtype=torch.int32, device=dev)
     new = sv.spec_kv_commit(k, k, tb, ctx, few - 1, path, workspace=ws)
     assert bad() and int(new) == -1
+
+
+@pytest.mark.parametrize("R,M", [(0, 3), (2, 0), (0, 0)])
+def test_empty_writes_with_queries(sv, dev, R, M):
+    e = lambda *s, t=torch.int32: torch.empty(s, dtype=t, device=dev)  # noqa: E731
+    c = torch.ones(2, 1, 16, 64, dtype=torch.bfloat16, device=dev)
+    x = e(R, M, 4, 64, t=torch.bfloat16)
+    w = torch.ones(64, dtype=torch.bfloat16, device=dev)
+    out = e(R, M, 2, 64, t=torch.bfloat16)
+    for given in (None, out):
+        got = sv.spec_qkv_write(x[:, :, 2:3], x[:, :, 3:], c, c.clone(), e(R, 3), e(R), e(R), q=x[:, :, :2],
+                                q_weight=w, k_weight=w, out_q=given)
+        assert got.shape == (R, M, 2, 64) and (given is None or got is given)
+    assert (c == 1).all()
