@@ -5,7 +5,8 @@ Argument marshalling only: every step of the computation runs in the HIP
 kernels behind the C ABI declared in include/specverify.h.  The functions keep
 the C names.  Tensors must be contiguous CUDA (HIP) tensors on one device;
 logits are torch.float32 or torch.bfloat16.  Work is enqueued on the current
-torch stream and nothing synchronises except spec_get_device_status.
+torch stream of that device, or on `stream` (one of that device), and nothing
+synchronises except spec_get_device_status.
 
 The library must have been built (``python -m
 lossless_verification_sampling_amd._build`` or ``__graft_entry__.build()``);
@@ -217,8 +218,19 @@ def spec_tree_attention_workspace_bytes(R: int, M: int, Hq: int, Hkv: int, D: in
 # ---------------------------------------------------------------------------
 
 def _stream_ptr(stream: Optional[torch.cuda.Stream], device) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    if device.index is not None and stream.device.index != device.index:
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
+    return stream.cuda_stream
+
+
+def _run(dev: int, call, *args) -> int:
+    """call(*args) with device `dev` current: stream 0 is the current device's."""
+    if torch._C._cuda_getDevice() == dev:
+        return call(*args)
+    with torch.cuda.device(dev):
+        return call(*args)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -253,6 +265,11 @@ def _raise(status: int, what: str):
         raise SpecError(status, what)
 
 
+def _init(buf: torch.Tensor, stream):
+    _raise(_run(buf.get_device(), _lib.spec_workspace_init, _ptr(buf), buf.numel(),
+                _stream_ptr(stream, buf.device)), "spec_workspace_init")
+
+
 class Workspace:
     """A device buffer for the library's cross-workgroup exchange, initialised
     once with spec_workspace_init and grown on demand.  Calls that share a
@@ -269,11 +286,11 @@ class Workspace:
         if self.buf is None or self.buf.numel() < nbytes:
             n = max(int(nbytes), 1 << 16)
             n = (n + 255) // 256 * 256
+            buf = torch.empty(n, dtype=torch.uint8, device=self.device)
+            _init(buf, stream)
             if self.buf is not None:
                 self._outgrown.append(self.buf)
-            self.buf = torch.empty(n, dtype=torch.uint8, device=self.device)
-            _raise(_lib.spec_workspace_init(_ptr(self.buf), n, _stream_ptr(stream, self.device)),
-                   "spec_workspace_init")
+            self.buf = buf
         return self.buf
 
     @property
@@ -295,11 +312,8 @@ def default_workspace(device) -> Workspace:
 
 
 def spec_workspace_init(workspace: Workspace, stream=None) -> None:
-    buf = workspace.buf
-    if buf is None:
-        return
-    _raise(_lib.spec_workspace_init(_ptr(buf), buf.numel(), _stream_ptr(stream, buf.device)),
-           "spec_workspace_init")
+    if workspace.buf is not None:
+        _init(workspace.buf, stream)
 
 
 def spec_get_device_status(workspace: Workspace, clear: bool = True, stream=None) -> int:
@@ -308,9 +322,8 @@ def spec_get_device_status(workspace: Workspace, clear: bool = True, stream=None
     buf = workspace.buf
     if buf is None:
         return 0
-    _raise(_lib.spec_get_device_status(_ptr(buf), ctypes.byref(bits), int(clear),
-                                       _stream_ptr(stream, buf.device)),
-           "spec_get_device_status")
+    _raise(_run(buf.get_device(), _lib.spec_get_device_status, _ptr(buf), ctypes.byref(bits),
+                int(clear), _stream_ptr(stream, buf.device)), "spec_get_device_status")
     return int(bits.value)
 
 
@@ -379,12 +392,11 @@ def spec_verify_batch(target_logits: torch.Tensor, draft_logits: Optional[torch.
         raise SpecError(-5, "spec_verify_workspace_bytes")
     buf = ws.ensure(need, stream)
     d_dtype = _dtype(draft_logits) if draft_logits is not None else SPEC_F32
-    st = _lib.spec_verify_batch(_ptr(target_logits), _dtype(target_logits), _ptr(draft_logits),
-                                d_dtype, _ptr(draft_tokens), _ptr(verify_len), _ptr(temperature),
-                                _ptr(u_accept), _ptr(u_sample), R, gamma, V, _ptr(o["tokens"]),
-                                _ptr(o["num_accepted"]), _ptr(o["cstar"]),
-                                _ptr(o["resid_mass"]), _ptr(o["logq"]), _ptr(buf),
-                                buf.numel(), _stream_ptr(stream, dev))
+    st = _run(dev.index, _lib.spec_verify_batch, _ptr(target_logits), _dtype(target_logits),
+              _ptr(draft_logits), d_dtype, _ptr(draft_tokens), _ptr(verify_len), _ptr(temperature),
+              _ptr(u_accept), _ptr(u_sample), R, gamma, V, _ptr(o["tokens"]),
+              _ptr(o["num_accepted"]), _ptr(o["cstar"]), _ptr(o["resid_mass"]), _ptr(o["logq"]),
+              _ptr(buf), buf.numel(), _stream_ptr(stream, dev))
     _raise(st, "spec_verify_batch")
     return o
 
@@ -405,13 +417,11 @@ def spec_verify_batch_noalloc(target_logits: torch.Tensor, draft_logits: Optiona
                                 temperature, u_accept, u_sample, out, False, False, False)
     dev = target_logits.device
     d_dtype = _dtype(draft_logits) if draft_logits is not None else SPEC_F32
-    st = _lib.spec_verify_batch_noalloc(_ptr(target_logits), _dtype(target_logits),
-                                        _ptr(draft_logits), d_dtype, _ptr(draft_tokens),
-                                        _ptr(verify_len), _ptr(temperature), _ptr(u_accept),
-                                        _ptr(u_sample), R, gamma, V, _ptr(o["tokens"]),
-                                        _ptr(o["num_accepted"]), _ptr(o["cstar"]),
-                                        _ptr(o["resid_mass"]), _ptr(o["logq"]),
-                                        _stream_ptr(stream, dev))
+    st = _run(dev.index, _lib.spec_verify_batch_noalloc, _ptr(target_logits), _dtype(target_logits),
+              _ptr(draft_logits), d_dtype, _ptr(draft_tokens), _ptr(verify_len), _ptr(temperature),
+              _ptr(u_accept), _ptr(u_sample), R, gamma, V, _ptr(o["tokens"]),
+              _ptr(o["num_accepted"]), _ptr(o["cstar"]), _ptr(o["resid_mass"]), _ptr(o["logq"]),
+              _stream_ptr(stream, dev))
     _raise(st, "spec_verify_batch_noalloc")
     return o
 
@@ -450,9 +460,9 @@ def spec_tv_accept_rate(draft_logits: torch.Tensor, target_logits: torch.Tensor,
     if need == 0:
         raise SpecError(-5, "spec_tv_workspace_bytes")
     buf = ws.ensure(need, stream)
-    st = _lib.spec_tv_accept_rate(_ptr(draft_logits), _ptr(target_logits), _dtype(target_logits),
-                                  _ptr(temperature), N, V, _ptr(cs), _ptr(rs), _ptr(buf),
-                                  buf.numel(), _stream_ptr(stream, dev))
+    st = _run(dev.index, _lib.spec_tv_accept_rate, _ptr(draft_logits), _ptr(target_logits),
+              _dtype(target_logits), _ptr(temperature), N, V, _ptr(cs), _ptr(rs), _ptr(buf),
+              buf.numel(), _stream_ptr(stream, dev))
     _raise(st, "spec_tv_accept_rate")
     return cs, rs
 
@@ -477,9 +487,9 @@ def spec_schedule_verify_len(confidence: torch.Tensor, sps: torch.Tensor, *, top
     _check(th, "out_theta", torch.float64, (1,), dev)
     ws = workspace or default_workspace(dev)
     buf = ws.ensure(spec_schedule_workspace_bytes(), stream)
-    st = _lib.spec_schedule_verify_len(_ptr(confidence), _ptr(sps), R, gamma, sps.numel() - 1,
-                                       int(topk), _ptr(ln), _ptr(th), _ptr(buf), buf.numel(),
-                                       _stream_ptr(stream, dev))
+    st = _run(dev.index, _lib.spec_schedule_verify_len, _ptr(confidence), _ptr(sps), R, gamma,
+              sps.numel() - 1, int(topk), _ptr(ln), _ptr(th), _ptr(buf), buf.numel(),
+              _stream_ptr(stream, dev))
     _raise(st, "spec_schedule_verify_len")
     return ln, th
 
@@ -506,10 +516,10 @@ def spec_sts_calibrate(conf_logits: torch.Tensor, accepted_len: torch.Tensor, gr
         raise ValueError(f"spec_sts_calibrate: unsupported sizes N={N} G={G} bins={bins}")
     ws = workspace or default_workspace(dev)
     buf = ws.ensure(need, stream)
-    st = _lib.spec_sts_calibrate(_ptr(conf_logits), _ptr(accepted_len), _ptr(grid), N, gamma, G,
-                                 int(bins), _ptr(temps), _ptr(ece),
-                                 _ptr(curve) if curve is not None else None, _ptr(buf),
-                                 buf.numel(), _stream_ptr(stream, dev))
+    st = _run(dev.index, _lib.spec_sts_calibrate, _ptr(conf_logits), _ptr(accepted_len), _ptr(grid),
+              N, gamma, G, int(bins), _ptr(temps), _ptr(ece),
+              _ptr(curve) if curve is not None else None, _ptr(buf), buf.numel(),
+              _stream_ptr(stream, dev))
     _raise(st, "spec_sts_calibrate")
     return temps, ece, curve
 
@@ -536,9 +546,9 @@ def spec_tree_verify(logits: torch.Tensor, parent: torch.Tensor, tokens: torch.T
         raise ValueError(f"spec_tree_verify: unsupported sizes M={M} V={V}")
     ws = workspace or default_workspace(dev)
     buf = ws.ensure(need, stream)
-    st = _lib.spec_tree_verify(_ptr(logits), _dtype(logits), _ptr(parent), _ptr(tokens),
-                               _ptr(n_nodes), R, M, V, int(max_depth), _ptr(acc), _ptr(path),
-                               _ptr(tok), _ptr(buf), buf.numel(), _stream_ptr(stream, dev))
+    st = _run(dev.index, _lib.spec_tree_verify, _ptr(logits), _dtype(logits), _ptr(parent),
+              _ptr(tokens), _ptr(n_nodes), R, M, V, int(max_depth), _ptr(acc), _ptr(path),
+              _ptr(tok), _ptr(buf), buf.numel(), _stream_ptr(stream, dev))
     _raise(st, "spec_tree_verify")
     return acc, path, tok
 
@@ -578,11 +588,10 @@ def spec_rnn_draft_sample(U: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor,
     if need == 0:
         raise SpecError(-5, "spec_rnn_workspace_bytes")
     buf = ws.ensure(need, stream)
-    st = _lib.spec_rnn_draft_sample(_ptr(U), _dtype(U), _ptr(W1), _ptr(W2), SPEC_BF16,
-                                    _ptr(hidden_states), hidden, _ptr(Wg), _ptr(bg), _ptr(anchor),
-                                    _ptr(temperature), _ptr(u_draft), R, gamma, V, rank, _ptr(tok),
-                                    _ptr(lg), _ptr(stt), _ptr(buf), buf.numel(),
-                                    _stream_ptr(stream, dev))
+    st = _run(dev.index, _lib.spec_rnn_draft_sample, _ptr(U), _dtype(U), _ptr(W1), _ptr(W2),
+              SPEC_BF16, _ptr(hidden_states), hidden, _ptr(Wg), _ptr(bg), _ptr(anchor),
+              _ptr(temperature), _ptr(u_draft), R, gamma, V, rank, _ptr(tok), _ptr(lg), _ptr(stt),
+              _ptr(buf), buf.numel(), _stream_ptr(stream, dev))
     _raise(st, "spec_rnn_draft_sample")
     return tok, lg, stt
 
@@ -616,10 +625,9 @@ def spec_markov_draft_sample(U: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor
     if need == 0:
         raise SpecError(-5, "spec_markov_workspace_bytes")
     buf = ws.ensure(need, stream)
-    st = _lib.spec_markov_draft_sample(_ptr(U), _dtype(U), _ptr(W1), _ptr(W2), SPEC_BF16,
-                                       _ptr(anchor), _ptr(temperature), _ptr(u_draft), R, gamma,
-                                       V, rank, _ptr(tok), _ptr(lg), _ptr(buf), buf.numel(),
-                                       _stream_ptr(stream, dev))
+    st = _run(dev.index, _lib.spec_markov_draft_sample, _ptr(U), _dtype(U), _ptr(W1), _ptr(W2),
+              SPEC_BF16, _ptr(anchor), _ptr(temperature), _ptr(u_draft), R, gamma, V, rank,
+              _ptr(tok), _ptr(lg), _ptr(buf), buf.numel(), _stream_ptr(stream, dev))
     _raise(st, "spec_markov_draft_sample")
     return tok, lg
 
@@ -643,15 +651,9 @@ def _all(dev: int, *specs):
 
 
 def _stream_of(stream: Optional[torch.cuda.Stream], dev: int) -> int:
-    return (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
-
-
-def _run(dev: int, call, *args) -> int:
-    """call(*args) with `dev` current: stream 0 is the current device's."""
-    if torch._C._cuda_getDevice() == dev:
-        return call(*args)
-    with torch.cuda.device(dev):
-        return call(*args)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream_ptr(stream, torch.device("cuda", dev))
 
 
 _CACHE_CODES = {torch.bfloat16: SPEC_BF16, torch.float8_e4m3fn: SPEC_E4M3}
