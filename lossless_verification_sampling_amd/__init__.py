@@ -6,7 +6,10 @@ kernels behind the C ABI declared in include/specverify.h.  The functions keep
 the C names.  Tensors must be contiguous CUDA (HIP) tensors on one device;
 logits are torch.float32 or torch.bfloat16.  Work is enqueued on the current
 torch stream of that device, or on `stream` (one of that device), and nothing
-synchronises except spec_get_device_status.
+synchronises except spec_get_device_status.  Outputs that are not given are
+memory of the stream that the call runs on, as torch's own would be under
+torch.cuda.stream(stream), and are not given away before the current stream is
+done with them.
 
 The library must have been built (``python -m
 lossless_verification_sampling_amd._build`` or ``__graft_entry__.build()``);
@@ -265,6 +268,19 @@ def _raise(status: int, what: str):
         raise SpecError(status, what)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """torch.empty from the memory of the stream the call runs on: what the
+    current stream frees may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if here.cuda_stream != stream.cuda_stream:
+        t.record_stream(here)
+    return t
+
+
 def _init(buf: torch.Tensor, stream):
     _raise(_run(buf.get_device(), _lib.spec_workspace_init, _ptr(buf), buf.numel(),
                 _stream_ptr(stream, buf.device)), "spec_workspace_init")
@@ -279,6 +295,7 @@ class Workspace:
         self.device = torch.device(device if device is not None else "cuda")
         self.buf: Optional[torch.Tensor] = None
         self._outgrown = []  # captured graphs go on writing to them
+        self._streams = set()  # handles of the streams that buf is known to be used on
         if nbytes:
             self.ensure(nbytes)
 
@@ -286,11 +303,17 @@ class Workspace:
         if self.buf is None or self.buf.numel() < nbytes:
             n = max(int(nbytes), 1 << 16)
             n = (n + 255) // 256 * 256
-            buf = torch.empty(n, dtype=torch.uint8, device=self.device)
+            buf = _empty((n,), torch.uint8, self.device, stream)
             _init(buf, stream)
             if self.buf is not None:
                 self._outgrown.append(self.buf)
             self.buf = buf
+            self._streams = {_stream_ptr(stream, buf.device)}
+        handle = _stream_ptr(stream, self.buf.device)
+        if handle not in self._streams:  # its memory stays until that stream is done, too
+            self.buf.record_stream(stream if stream is not None else
+                                   torch.cuda.current_stream(self.buf.device))
+            self._streams.add(handle)
         return self.buf
 
     @property
@@ -332,7 +355,7 @@ def spec_get_device_status(workspace: Workspace, clear: bool = True, stream=None
 # ---------------------------------------------------------------------------
 
 def _verify_io(target_logits, draft_logits, draft_tokens, verify_len, temperature, u_accept,
-               u_sample, out, want_cstar, want_resid, want_logq):
+               u_sample, out, want_cstar, want_resid, want_logq, stream):
     """Checks the inputs of a verification call and returns (R, gamma, V, outputs)
     with the missing output tensors allocated."""
     R, G1, V = target_logits.shape
@@ -349,19 +372,19 @@ def _verify_io(target_logits, draft_logits, draft_tokens, verify_len, temperatur
         out = {}
     o_tok = out.get("tokens")
     if o_tok is None:
-        o_tok = torch.empty((R, G1), dtype=torch.int32, device=dev)
+        o_tok = _empty((R, G1), torch.int32, dev, stream)
     o_n = out.get("num_accepted")
     if o_n is None:
-        o_n = torch.empty((R,), dtype=torch.int32, device=dev)
+        o_n = _empty((R,), torch.int32, dev, stream)
     o_cs = out.get("cstar")
     if o_cs is None and want_cstar:
-        o_cs = torch.empty((R, gamma), dtype=torch.float32, device=dev)
+        o_cs = _empty((R, gamma), torch.float32, dev, stream)
     o_rs = out.get("resid_mass")
     if o_rs is None and want_resid:
-        o_rs = torch.empty((R, gamma), dtype=torch.float32, device=dev)
+        o_rs = _empty((R, gamma), torch.float32, dev, stream)
     o_lq = out.get("logq")
     if o_lq is None and want_logq:
-        o_lq = torch.empty((R, G1), dtype=torch.float32, device=dev)
+        o_lq = _empty((R, G1), torch.float32, dev, stream)
     _check(o_tok, "out tokens", torch.int32, (R, G1), dev)
     _check(o_n, "out num_accepted", torch.int32, (R,), dev)
     _check(o_cs, "out cstar", torch.float32, (R, gamma), dev)
@@ -384,7 +407,7 @@ def spec_verify_batch(target_logits: torch.Tensor, draft_logits: Optional[torch.
     resid_mass, logq); `out` may supply preallocated output tensors."""
     R, gamma, V, o = _verify_io(target_logits, draft_logits, draft_tokens, verify_len,
                                 temperature, u_accept, u_sample, out, want_cstar, want_resid,
-                                want_logq)
+                                want_logq, stream)
     dev = target_logits.device
     ws = workspace or default_workspace(dev)
     need = spec_verify_workspace_bytes(R, gamma, V)
@@ -414,7 +437,8 @@ def spec_verify_batch_noalloc(target_logits: torch.Tensor, draft_logits: Optiona
             raise ValueError(f"spec_verify_batch_noalloc: out[{k!r}] must be given "
                              "(a tensor, or None for an optional output)")
     R, gamma, V, o = _verify_io(target_logits, draft_logits, draft_tokens, verify_len,
-                                temperature, u_accept, u_sample, out, False, False, False)
+                                temperature, u_accept, u_sample, out, False, False, False,
+                                stream)
     dev = target_logits.device
     d_dtype = _dtype(draft_logits) if draft_logits is not None else SPEC_F32
     st = _run(dev.index, _lib.spec_verify_batch_noalloc, _ptr(target_logits), _dtype(target_logits),
@@ -453,8 +477,8 @@ def spec_tv_accept_rate(draft_logits: torch.Tensor, target_logits: torch.Tensor,
     _check(target_logits, "target_logits", device=dev)
     _check(draft_logits, "draft_logits", target_logits.dtype, (N, V), dev)
     _check(temperature, "temperature", torch.float32, (N,), dev)
-    cs = torch.empty((N,), dtype=torch.float32, device=dev)
-    rs = torch.empty((N,), dtype=torch.float32, device=dev) if want_resid else None
+    cs = _empty((N,), torch.float32, dev, stream)
+    rs = _empty((N,), torch.float32, dev, stream) if want_resid else None
     ws = workspace or default_workspace(dev)
     need = spec_tv_workspace_bytes(N, V)
     if need == 0:
@@ -481,8 +505,8 @@ def spec_schedule_verify_len(confidence: torch.Tensor, sps: torch.Tensor, *, top
     _check(sps, "sps", torch.float32, None, dev)
     if sps.dim() != 1 or sps.numel() < 1:
         raise ValueError("sps must be a non-empty 1-D table")
-    ln = out_len if out_len is not None else torch.empty((R,), dtype=torch.int32, device=dev)
-    th = out_theta if out_theta is not None else torch.empty((1,), dtype=torch.float64, device=dev)
+    ln = out_len if out_len is not None else _empty((R,), torch.int32, dev, stream)
+    th = out_theta if out_theta is not None else _empty((1,), torch.float64, dev, stream)
     _check(ln, "out_len", torch.int32, (R,), dev)
     _check(th, "out_theta", torch.float64, (1,), dev)
     ws = workspace or default_workspace(dev)
@@ -508,9 +532,9 @@ def spec_sts_calibrate(conf_logits: torch.Tensor, accepted_len: torch.Tensor, gr
     _check(conf_logits, "conf_logits", torch.float32, (N, gamma), dev)
     _check(accepted_len, "accepted_len", torch.int32, (N,), dev)
     _check(grid, "grid", torch.float64, (G,), dev)
-    temps = torch.empty((gamma,), dtype=torch.float64, device=dev)
-    ece = torch.empty((gamma,), dtype=torch.float64, device=dev)
-    curve = torch.empty((gamma, G), dtype=torch.float64, device=dev) if want_curve else None
+    temps = _empty((gamma,), torch.float64, dev, stream)
+    ece = _empty((gamma,), torch.float64, dev, stream)
+    curve = _empty((gamma, G), torch.float64, dev, stream) if want_curve else None
     need = spec_sts_workspace_bytes(max(N, 1), gamma, G, bins)
     if need == 0:
         raise ValueError(f"spec_sts_calibrate: unsupported sizes N={N} G={G} bins={bins}")
@@ -538,9 +562,9 @@ def spec_tree_verify(logits: torch.Tensor, parent: torch.Tensor, tokens: torch.T
     for t, nm in ((parent, "parent"), (tokens, "tokens")):
         _check(t, nm, torch.int32, (R, M), dev)
     _check(n_nodes, "n_nodes", torch.int32, (R,), dev)
-    acc = torch.empty((R,), dtype=torch.int32, device=dev)
-    path = torch.empty((R, M), dtype=torch.int32, device=dev)
-    tok = torch.empty((R, M), dtype=torch.int32, device=dev)
+    acc = _empty((R,), torch.int32, dev, stream)
+    path = _empty((R, M), torch.int32, dev, stream)
+    tok = _empty((R, M), torch.int32, dev, stream)
     need = spec_tree_workspace_bytes(max(R, 1), M, V)
     if need == 0:
         raise ValueError(f"spec_tree_verify: unsupported sizes M={M} V={V}")
@@ -576,11 +600,9 @@ def spec_rnn_draft_sample(U: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor,
     _check(anchor, "anchor", torch.int32, (R,), dev)
     _check(temperature, "temperature", torch.float32, (R,), dev)
     _check(u_draft, "u_draft", torch.float32, (R, gamma), dev)
-    tok = out_tokens if out_tokens is not None else torch.empty((R, gamma), dtype=torch.int32,
-                                                                 device=dev)
-    lg = out_logits if out_logits is not None else torch.empty((R, gamma, V),
-                                                                dtype=torch.float32, device=dev)
-    stt = torch.empty((R, gamma, rank), dtype=torch.float32, device=dev) if want_state else None
+    tok = out_tokens if out_tokens is not None else _empty((R, gamma), torch.int32, dev, stream)
+    lg = out_logits if out_logits is not None else _empty((R, gamma, V), torch.float32, dev, stream)
+    stt = _empty((R, gamma, rank), torch.float32, dev, stream) if want_state else None
     _check(tok, "out_tokens", torch.int32, (R, gamma), dev)
     _check(lg, "out_logits", torch.float32, (R, gamma, V), dev)
     ws = workspace or default_workspace(dev)
@@ -614,10 +636,8 @@ def spec_markov_draft_sample(U: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor
     _check(anchor, "anchor", torch.int32, (R,), dev)
     _check(temperature, "temperature", torch.float32, (R,), dev)
     _check(u_draft, "u_draft", torch.float32, (R, gamma), dev)
-    tok = out_tokens if out_tokens is not None else torch.empty((R, gamma), dtype=torch.int32,
-                                                                 device=dev)
-    lg = out_logits if out_logits is not None else torch.empty((R, gamma, V),
-                                                                dtype=torch.float32, device=dev)
+    tok = out_tokens if out_tokens is not None else _empty((R, gamma), torch.int32, dev, stream)
+    lg = out_logits if out_logits is not None else _empty((R, gamma, V), torch.float32, dev, stream)
     _check(tok, "out_tokens", torch.int32, (R, gamma), dev)
     _check(lg, "out_logits", torch.float32, (R, gamma, V), dev)
     ws = workspace or default_workspace(dev)
@@ -714,13 +734,17 @@ def _attention_bytes(*sizes) -> int:
 
 
 def _cache_buf(workspace, dev: int, need: int, stream):
+    """(address, bytes, handle of the stream the call runs on)."""
     ws = workspace or _default_ws.get(("cuda", dev)) or default_workspace(torch.device("cuda", dev))
+    handle = _stream_of(stream, dev)
     buf = ws.buf
-    if buf is None or buf.numel() < need:
+    if buf is None or buf.numel() < need or handle not in ws._streams:
+        if ws.device.index not in (None, dev):
+            raise ValueError(f"workspace is on {ws.device}, expected cuda:{dev}")
         buf = ws.ensure(need, stream)
     if buf.get_device() != dev:
         raise ValueError(f"workspace is on {buf.device}, expected cuda:{dev}")
-    return buf.data_ptr(), buf.numel()
+    return buf.data_ptr(), buf.numel(), handle
 
 
 def spec_tree_mask(parent: torch.Tensor, n_nodes: torch.Tensor, ctx_len: torch.Tensor, *,
@@ -734,16 +758,14 @@ def spec_tree_mask(parent: torch.Tensor, n_nodes: torch.Tensor, ctx_len: torch.T
     dev = _device(parent, "parent")
     words = (R, M, (M + 31) // 32)
     i32 = torch.int32
-    pos = out_positions if out_positions is not None else torch.empty(shape, dtype=i32,
-                                                                      device=parent.device)
-    mask = out_mask if out_mask is not None else torch.empty(words, dtype=i32, device=parent.device)
+    pos = out_positions if out_positions is not None else _empty(shape, i32, parent.device, stream)
+    mask = out_mask if out_mask is not None else _empty(words, i32, parent.device, stream)
     _all(dev, (parent, "parent", i32, shape), (n_nodes, "n_nodes", i32, (R,)),
          (ctx_len, "ctx_len", i32, (R,)), (pos, "out_positions", i32, shape),
          (mask, "out_mask", i32, words))
-    buf, size = _cache_buf(workspace, dev, 256, stream)
+    buf, size, queue = _cache_buf(workspace, dev, 256, stream)
     st = _run(dev, _lib.spec_tree_mask, parent.data_ptr(), n_nodes.data_ptr(), ctx_len.data_ptr(),
-              R, M, int(window), pos.data_ptr(), mask.data_ptr(), buf, size,
-              _stream_of(stream, dev))
+              R, M, int(window), pos.data_ptr(), mask.data_ptr(), buf, size, queue)
     if st:
         _raise(st, "spec_tree_mask")
     return pos, mask
@@ -781,7 +803,7 @@ def spec_qkv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
         _need(len(qs) == 4 and qs[0] == R and qs[1] == M and qs[3] == D, "q must be [R, M, Hq, D]")
         Hq, ld_q = qs[2], _ordered_heads(q, "q", qs, dev)
         if out_q is None:
-            out_q = torch.empty(qs, dtype=torch.bfloat16, device=k.device)
+            out_q = _empty(qs, torch.bfloat16, k.device, stream)
     else:
         qs = None
         _need(q_weight is None and out_q is None, "q_weight and out_q belong to q")
@@ -796,12 +818,12 @@ def spec_qkv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
          (k_weight, "k_weight", dtype, (D,)), (rope, "rope", torch.float32, rs),
          (positions, "positions", i32, (R, M)), (ctx_len, "ctx_len", i32, (R,)),
          (n_nodes, "n_nodes", i32, (R,)))
-    buf, room = _cache_buf(workspace, dev, 256, stream)
+    buf, room, queue = _cache_buf(workspace, dev, 256, stream)
     st = _run(dev, _lib.spec_qkv_write, _raw(q), k.data_ptr(), v.data_ptr(), dt, ld_q, ld_k, ld_v,
               _raw(q_weight), _raw(k_weight), eps, _raw(rope), max_pos, rot, int(interleaved),
               _raw(positions), ctx_len.data_ptr(), n_nodes.data_ptr(), page_table.data_ptr(), wide,
               R, M, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
-              _raw(v_scale), P, size, _raw(out_q), buf, room, _stream_of(stream, dev))
+              _raw(v_scale), P, size, _raw(out_q), buf, room, queue)
     if st:
         _raise(st, "spec_qkv_write")
     return out_q
@@ -825,16 +847,16 @@ def spec_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
         dtype = given.dtype
     shape = (R, max_len, Hkv, D)
     if out_k is None:
-        out_k = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        out_k = _empty(shape, dtype, k_cache.device, stream)
     if out_v is None:
-        out_v = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        out_v = _empty(shape, dtype, k_cache.device, stream)
     _all(dev, (start, "start", torch.int32, (R,)), (length, "length", torch.int32, (R,)),
          (out_k, "out_k", dtype, shape), (out_v, "out_v", dtype, shape))
-    buf, room = _cache_buf(workspace, dev, 256, stream)
+    buf, room, queue = _cache_buf(workspace, dev, 256, stream)
     st = _run(dev, _lib.spec_kv_read, k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
               _raw(v_scale), P, size, page_table.data_ptr(), wide, start.data_ptr(),
               length.data_ptr(), R, max_len, Hkv, D, out_k.data_ptr(), out_v.data_ptr(),
-              _dtype(out_k), buf, room, _stream_of(stream, dev))
+              _dtype(out_k), buf, room, queue)
     if st:
         _raise(st, "spec_kv_read")
     return out_k, out_v
@@ -852,14 +874,14 @@ def spec_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: tor
     code, P, Hkv, size, D, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev)
     i32 = torch.int32
     if out_ctx_len is None:
-        out_ctx_len = torch.empty((R,), dtype=i32, device=k_cache.device)
+        out_ctx_len = _empty((R,), i32, k_cache.device, stream)
     _all(dev, (ctx_len, "ctx_len", i32, (R,)), (accepted, "accepted", i32, (R,)),
          (path, "path", i32, (R, M)), (out_ctx_len, "out_ctx_len", i32, (R,)))
-    buf, room = _cache_buf(workspace, dev, 256, stream)
+    buf, room, queue = _cache_buf(workspace, dev, 256, stream)
     st = _run(dev, _lib.spec_kv_commit, k_cache.data_ptr(), v_cache.data_ptr(), code, _raw(k_scale),
               _raw(v_scale), P, size, page_table.data_ptr(), wide, ctx_len.data_ptr(),
               accepted.data_ptr(), path.data_ptr(), R, M, Hkv, D, out_ctx_len.data_ptr(), buf, room,
-              _stream_of(stream, dev))
+              queue)
     if st:
         _raise(st, "spec_kv_commit")
     return out_ctx_len
@@ -885,9 +907,9 @@ def spec_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     code, P, Hkv, size, Dc, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev)
     _need(Dc == D, "q and the cache differ in D")
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = _empty(shape, torch.bfloat16, q.device, stream)
     if out_lse is None and want_lse:
-        out_lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+        out_lse = _empty(shape[:3], torch.float32, q.device, stream)
     i32 = torch.int32
     _all(dev, (q, "q", torch.bfloat16, shape), (ctx_len, "ctx_len", i32, (R,)),
          (n_nodes, "n_nodes", i32, (R,)), (mask, "mask", i32, (R, M, (M + 31) // 32)),
@@ -896,12 +918,12 @@ def spec_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     need = _attention_bytes(R, M, Hq, Hkv, D)
     if need == 0:
         raise SpecError(-5, "spec_tree_attention_workspace_bytes")
-    buf, room = _cache_buf(workspace, dev, need, stream)
+    buf, room, queue = _cache_buf(workspace, dev, need, stream)
     st = _run(dev, _lib.spec_tree_attention, q.data_ptr(), SPEC_BF16, k_cache.data_ptr(),
               v_cache.data_ptr(), code, _raw(k_scale), _raw(v_scale), P, size,
               page_table.data_ptr(), wide, ctx_len.data_ptr(), n_nodes.data_ptr(), _raw(mask),
               _raw(positions), D ** -0.5 if scale is None else scale, int(window), R, M, Hq, Hkv, D,
-              out.data_ptr(), _raw(out_lse), buf, room, _stream_of(stream, dev))
+              out.data_ptr(), _raw(out_lse), buf, room, queue)
     if st:
         _raise(st, "spec_tree_attention")
     return out, out_lse

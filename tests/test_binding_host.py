@@ -49,3 +49,25 @@ def test_a_stream_of_another_device_is_refused(sv, gpu, name):
         assert len(gpu.calls) == before
     call()                                      # and nothing is left half done
     assert [n for n, *_ in gpu.calls[-2:]] == ["spec_workspace_init", name]
+
+
+@pytest.mark.parametrize("name", fake_gpu.NAMES)
+def test_a_given_stream_writes_memory_of_its_own(sv, gpu, name):
+    """A block that the current stream freed may still be read by what is queued
+    there: neither an output nor a workspace for another stream may be one."""
+    st = fake_gpu.Stream(1, 9)
+    fake_gpu.calls(sv, 1)[name](stream=st)
+    assert gpu.taken and all(t.pool is st for t in gpu.taken)
+    assert all(t.used == [0] for t in gpu.taken)        # the caller's stream may read them
+    assert {n: s for n, _, s, _ in gpu.calls} == {"spec_workspace_init": 9, name: 9}
+    assert gpu.streams[1].cuda_stream == 0 and gpu.current == 0
+
+
+@pytest.mark.parametrize("name", fake_gpu.NAMES)
+def test_a_workspace_outlasts_every_stream_it_is_used_on(sv, gpu, name):
+    call, ws = fake_gpu.calls(sv, 1)[name], sv.Workspace("cuda:1", 256)
+    for st in (9, 9, 8, 9):
+        call(stream=fake_gpu.Stream(1, st), workspace=ws)
+    with torch.cuda.stream(fake_gpu.Stream(1, 5)):
+        call(workspace=ws)
+    assert ws.buf.pool.cuda_stream == 0 and ws.buf.used == [9, 8, 5]

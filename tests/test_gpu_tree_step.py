@@ -379,3 +379,38 @@ def test_empty_writes_with_queries(sv, dev, R, M):
                                 q_weight=w, k_weight=w, out_q=given)
         assert got.shape == (R, M, 2, 64) and (given is None or got is given)
     assert (c == 1).all()
+
+
+def test_a_given_stream_takes_no_memory_of_the_current_one(sv, dev):
+    """Blocks that the current stream has just freed, each of an output's size,
+    may still be in use there."""
+    s = Step(42, "bf16", dev)
+    R, M, Hq, Hkv, Dh, V = s.dims
+    n, parent, qkv = s.draft()
+    x, nd, pd, ctx = qkv.to(dev), D(n, dev), D(parent, dev), D(s.ctx, dev)
+    q = x[:, :, :Hq].contiguous()
+    st = torch.cuda.Stream()
+    ws = sv.Workspace(dev, sv.spec_tree_attention_workspace_bytes(R, M, Hq, Hkv, Dh))
+    acc, path = torch.zeros_like(ctx), torch.full((R, M), -1, dtype=torch.int32, device=dev)
+    torch.cuda.synchronize()
+
+    def run(**kw):
+        pos, mask = sv.spec_tree_mask(pd, nd, ctx, workspace=ws, **kw)
+        qo = sv.spec_qkv_write(x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:], *s.c.args(), ctx, nd, q=q,
+                               workspace=ws, **kw)
+        o, l = sv.spec_tree_attention(q, *s.c.args(), ctx, nd, mask=mask, positions=pos, want_lse=True,
+                                      workspace=ws, **kw)
+        k, v = sv.spec_kv_read(*s.c.args(), torch.zeros_like(ctx), ctx, 40, workspace=ws, **kw)
+        return pos, mask, qo, o, l, k, v, sv.spec_kv_commit(*s.c.args(), ctx, acc, path, workspace=ws, **kw)
+    want = run()
+    free = [torch.empty_like(t) for t in want for _ in range(2)]
+    taken = {t.data_ptr() for t in free}
+    torch.cuda.synchronize()
+    del free
+    got = run(stream=st)
+    st.synchronize()
+    assert not taken & {t.data_ptr() for t in got}
+    for r in range(R):
+        m = int(n[r])
+        for a, b in zip(got[:5], want[:5]):
+            assert torch.equal(a[r, :m], b[r, :m])
