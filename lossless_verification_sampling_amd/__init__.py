@@ -288,20 +288,22 @@ def _init(buf: torch.Tensor, stream):
 
 class Workspace:
     """A device buffer for the library's cross-workgroup exchange, initialised
-    once with spec_workspace_init and grown on demand.  Calls that share a
-    workspace must be stream-ordered."""
+    once with spec_workspace_init and grown on demand, to twice its size at
+    least.  The buffers it outgrew, together smaller than the present one, are
+    kept for as long as it is: captured graphs go on writing to them.  Calls that
+    share a workspace must be stream-ordered."""
 
     def __init__(self, device=None, nbytes: int = 0):
         self.device = torch.device(device if device is not None else "cuda")
         self.buf: Optional[torch.Tensor] = None
-        self._outgrown = []  # captured graphs go on writing to them
+        self._outgrown = []
         self._streams = set()  # handles of the streams that buf is known to be used on
         if nbytes:
             self.ensure(nbytes)
 
     def ensure(self, nbytes: int, stream=None) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
-            n = max(int(nbytes), 1 << 16)
+            n = max(int(nbytes), 1 << 16, 2 * self.nbytes)
             n = (n + 255) // 256 * 256
             buf = _empty((n,), torch.uint8, self.device, stream)
             _init(buf, stream)

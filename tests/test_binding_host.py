@@ -71,3 +71,12 @@ def test_a_workspace_outlasts_every_stream_it_is_used_on(sv, gpu, name):
     with torch.cuda.stream(fake_gpu.Stream(1, 5)):
         call(workspace=ws)
     assert ws.buf.pool.cuda_stream == 0 and ws.buf.used == [9, 8, 5]
+
+
+def test_a_workspace_that_grows_in_small_steps_keeps_little(sv, gpu):
+    """The buffers that it outgrew are kept for captured graphs."""
+    ws, last = sv.Workspace("cuda:1", 256), 0
+    for need in range(70000, 3000000, 4096):
+        assert ws.ensure(need).numel() >= need and ws.nbytes == ws.buf.numel()
+        last = need
+    assert sum(t.numel() for t in gpu.taken) <= 4 * last
