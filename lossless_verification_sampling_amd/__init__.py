@@ -342,14 +342,18 @@ def spec_workspace_init(workspace: Workspace, stream=None) -> None:
 
 
 def spec_get_device_status(workspace: Workspace, clear: bool = True, stream=None) -> int:
-    """Synchronises the stream and returns the OR of SPEC_DEV_* bits."""
-    bits = ctypes.c_uint32(0)
-    buf = workspace.buf
-    if buf is None:
-        return 0
-    _raise(_run(buf.get_device(), _lib.spec_get_device_status, _ptr(buf), ctypes.byref(bits),
-                int(clear), _stream_ptr(stream, buf.device)), "spec_get_device_status")
-    return int(bits.value)
+    """Synchronises the stream and returns the OR of SPEC_DEV_* bits, those in
+    the buffers that the workspace outgrew (a replayed graph's, or from before
+    it grew) among them."""
+    found = 0
+    for buf in workspace._outgrown + [workspace.buf]:
+        if buf is not None:
+            bits = ctypes.c_uint32(0)
+            _raise(_run(buf.get_device(), _lib.spec_get_device_status, _ptr(buf),
+                        ctypes.byref(bits), int(clear), _stream_ptr(stream, buf.device)),
+                   "spec_get_device_status")
+            found |= bits.value
+    return found
 
 
 # ---------------------------------------------------------------------------

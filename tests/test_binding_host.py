@@ -80,3 +80,19 @@ def test_a_workspace_that_grows_in_small_steps_keeps_little(sv, gpu):
         assert ws.ensure(need).numel() >= need and ws.nbytes == ws.buf.numel()
         last = need
     assert sum(t.numel() for t in gpu.taken) <= 4 * last
+
+
+def test_status_words_of_outgrown_buffers_count(sv, gpu):
+    ws = sv.Workspace("cuda:1", 1 << 16)
+    for _ in range(2):
+        ws.ensure(ws.nbytes + 1)
+    first, second, last = (t.data_ptr() for t in gpu.taken)
+    gpu.status = {first: 1, second: 2}          # a replay's, and one from before the growth
+    assert sv.spec_get_device_status(ws, clear=False) == 3
+    assert sv.spec_get_device_status(ws) == 3
+    assert sv.spec_get_device_status(ws) == 0
+    gpu.status[last] = 1
+    assert sv.spec_get_device_status(ws) == 1 and not any(gpu.status.values())
+    sv.spec_get_device_status(ws, stream=fake_gpu.Stream(1, 9))
+    assert [(d, s) for _, d, s, _ in gpu.calls[-3:]] == [(1, 9)] * 3
+    assert sv.spec_get_device_status(sv.Workspace("cuda:1")) == 0

@@ -414,3 +414,31 @@ def test_a_given_stream_takes_no_memory_of_the_current_one(sv, dev):
         m = int(n[r])
         for a, b in zip(got[:5], want[:5]):
             assert torch.equal(a[r, :m], b[r, :m])
+
+
+def test_faults_in_an_outgrown_buffer_are_seen(sv, dev):
+    """A fault raised before the workspace grew, and one by a replay after it."""
+    s = Step(43, "bf16", dev)
+    R, M, Hq, Hkv, Dh, V = s.dims
+    n, parent, qkv = s.draft()
+    q, ctx = qkv.to(dev)[:, :, :Hq].contiguous(), D(s.ctx, dev)
+    good, bad = D(n, dev), D(np.array([M + 1, M, M], np.int32), dev)
+    nd = good.clone()
+    ws = sv.Workspace(dev, sv.spec_tree_attention_workspace_bytes(R, M, Hq, Hkv, Dh))
+    g, out = capture(lambda: sv.spec_tree_attention(q, *s.c.args(), ctx, nd, workspace=ws)[:1])
+    assert sv.spec_get_device_status(ws) == 0
+    nd.copy_(bad)
+    sv.spec_tree_attention(q, *s.c.args(), ctx, nd, workspace=ws)
+    nd.copy_(good)
+    ws.ensure(ws.nbytes + 1)
+    assert sv.spec_get_device_status(ws) == sv.SPEC_DEV_BAD_REQUEST
+    for k in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert sv.spec_get_device_status(ws) == 0
+        nd.copy_(bad)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.isnan(out[0][0]).all()
+        assert sv.spec_get_device_status(ws) == sv.SPEC_DEV_BAD_REQUEST
+        nd.copy_(good)
