@@ -281,6 +281,13 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
     return t
 
 
+def _capturing(stream) -> bool:
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _init(buf: torch.Tensor, stream):
     _raise(_run(buf.get_device(), _lib.spec_workspace_init, _ptr(buf), buf.numel(),
                 _stream_ptr(stream, buf.device)), "spec_workspace_init")
@@ -291,18 +298,22 @@ class Workspace:
     once with spec_workspace_init and grown on demand, to twice its size at
     least.  The buffers it outgrew, together smaller than the present one, are
     kept for as long as it is: captured graphs go on writing to them.  Calls that
-    share a workspace must be stream-ordered."""
+    share a workspace must be stream-ordered.  Give it its size before a capture:
+    a buffer taken inside one is cleared by every replay, its status word too."""
 
     def __init__(self, device=None, nbytes: int = 0):
         self.device = torch.device(device if device is not None else "cuda")
         self.buf: Optional[torch.Tensor] = None
         self._outgrown = []
+        self._recorded = False  # buf was taken inside a capture: cleared by the replays alone
         self._streams = set()  # handles of the streams that buf is known to be used on
         if nbytes:
             self.ensure(nbytes)
 
     def ensure(self, nbytes: int, stream=None) -> torch.Tensor:
-        if self.buf is None or self.buf.numel() < nbytes:
+        small = self.buf is None or self.buf.numel() < nbytes
+        inside = (small or self._recorded) and _capturing(stream)
+        if small or self._recorded and not inside:
             n = max(int(nbytes), 1 << 16, 2 * self.nbytes)
             n = (n + 255) // 256 * 256
             buf = _empty((n,), torch.uint8, self.device, stream)
@@ -310,6 +321,7 @@ class Workspace:
             if self.buf is not None:
                 self._outgrown.append(self.buf)
             self.buf = buf
+            self._recorded = inside
             self._streams = {_stream_ptr(stream, buf.device)}
         handle = _stream_ptr(stream, self.buf.device)
         if handle not in self._streams:  # its memory stays until that stream is done, too
@@ -352,7 +364,10 @@ def spec_get_device_status(workspace: Workspace, clear: bool = True, stream=None
             _raise(_run(buf.get_device(), _lib.spec_get_device_status, _ptr(buf),
                         ctypes.byref(bits), int(clear), _stream_ptr(stream, buf.device)),
                    "spec_get_device_status")
-            found |= bits.value
+            # (unknown bits: taken inside a capture and not replayed yet, the word
+            # is what its memory held before)
+            if not bits.value & ~(SPEC_DEV_BAD_REQUEST | SPEC_DEV_SPIN_TIMEOUT):
+                found |= bits.value
     return found
 
 
@@ -744,7 +759,7 @@ def _cache_buf(workspace, dev: int, need: int, stream):
     ws = workspace or _default_ws.get(("cuda", dev)) or default_workspace(torch.device("cuda", dev))
     handle = _stream_of(stream, dev)
     buf = ws.buf
-    if buf is None or buf.numel() < need or handle not in ws._streams:
+    if buf is None or buf.numel() < need or handle not in ws._streams or ws._recorded:
         if ws.device.index not in (None, dev):
             raise ValueError(f"workspace is on {ws.device}, expected cuda:{dev}")
         buf = ws.ensure(need, stream)

@@ -96,3 +96,38 @@ def test_status_words_of_outgrown_buffers_count(sv, gpu):
     sv.spec_get_device_status(ws, stream=fake_gpu.Stream(1, 9))
     assert [(d, s) for _, d, s, _ in gpu.calls[-3:]] == [(1, 9)] * 3
     assert sv.spec_get_device_status(sv.Workspace("cuda:1")) == 0
+
+
+@pytest.mark.parametrize("name", fake_gpu.NAMES)
+def test_a_workspace_taken_inside_a_capture_is_the_graphs(sv, gpu, name):
+    """What a capture records has not run: the buffer that it took holds whatever
+    its memory held.  Calls outside take one of their own, and clear it."""
+    call = fake_gpu.calls(sv, 1)[name]
+    gpu.capturing = True
+    call()
+    call()
+    assert [n for n, *_ in gpu.calls] == ["spec_workspace_init", name, name]
+    inside = gpu.calls[0][3][0].value
+    gpu.capturing = False
+    gpu.calls.clear()
+    call()
+    call()
+    gpu.capturing = True                        # a later capture finds a cleared one
+    call()
+    assert [n for n, *_ in gpu.calls] == ["spec_workspace_init", name, name, name]
+    assert gpu.calls[0][3][0].value != inside
+
+
+def test_the_status_of_a_workspace_taken_inside_a_capture(sv, gpu):
+    """Its status word counts, unless it holds what no call writes."""
+    ws = sv.Workspace("cuda:1")
+    gpu.capturing = True
+    ws.ensure(256)
+    gpu.capturing = False
+    first = ws.buf.data_ptr()
+    ws.ensure(256)
+    last = ws.buf.data_ptr()
+    gpu.status = {first: 0xffffffff, last: 1}
+    assert sv.spec_get_device_status(ws) == 1
+    gpu.status = {first: 2, last: 1}
+    assert sv.spec_get_device_status(ws) == 3 and not any(gpu.status.values())

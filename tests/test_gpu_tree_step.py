@@ -442,3 +442,22 @@ def test_faults_in_an_outgrown_buffer_are_seen(sv, dev):
         assert torch.isnan(out[0][0]).all()
         assert sv.spec_get_device_status(ws) == sv.SPEC_DEV_BAD_REQUEST
         nd.copy_(good)
+
+
+def test_a_workspace_taken_inside_a_capture(sv, dev):
+    """Its clearing is recorded, not done."""
+    s = Step(44, "bf16", dev)
+    calls(sv, s, dev, 1, sv.Workspace(dev))[0]()    # all code is loaded
+    ws = sv.Workspace(dev)
+    run, fill = calls(sv, s, dev, 1, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    ws.buf.fill_(255)                           # what the memory may have held
+    assert sv.spec_get_device_status(ws) == 0
+    ws.buf.fill_(255)
+    run()
+    assert sv.spec_get_device_status(ws) == 0
+    replay_and_compare(g, out, fill, run)
+    assert sv.spec_get_device_status(ws) == 0
