@@ -228,6 +228,14 @@ def _stream_ptr(stream: Optional[torch.cuda.Stream], device) -> int:
     return stream.cuda_stream
 
 
+def _c_int(value, name: str) -> int:
+    """`value` as a C int (ctypes keeps the low 32 bits of any integer)."""
+    value = int(value)
+    if not -1 << 31 <= value < 1 << 31:
+        raise ValueError(f"{name} is not a 32-bit number: {value}")
+    return value
+
+
 def _run(dev: int, call, *args) -> int:
     """call(*args) with device `dev` current: stream 0 is the current device's."""
     if torch._C._cuda_getDevice() == dev:
@@ -533,7 +541,7 @@ def spec_schedule_verify_len(confidence: torch.Tensor, sps: torch.Tensor, *, top
     ws = workspace or default_workspace(dev)
     buf = ws.ensure(spec_schedule_workspace_bytes(), stream)
     st = _run(dev.index, _lib.spec_schedule_verify_len, _ptr(confidence), _ptr(sps), R, gamma,
-              sps.numel() - 1, int(topk), _ptr(ln), _ptr(th), _ptr(buf), buf.numel(),
+              sps.numel() - 1, _c_int(topk, "topk"), _ptr(ln), _ptr(th), _ptr(buf), buf.numel(),
               _stream_ptr(stream, dev))
     _raise(st, "spec_schedule_verify_len")
     return ln, th
@@ -562,7 +570,7 @@ def spec_sts_calibrate(conf_logits: torch.Tensor, accepted_len: torch.Tensor, gr
     ws = workspace or default_workspace(dev)
     buf = ws.ensure(need, stream)
     st = _run(dev.index, _lib.spec_sts_calibrate, _ptr(conf_logits), _ptr(accepted_len), _ptr(grid),
-              N, gamma, G, int(bins), _ptr(temps), _ptr(ece),
+              N, gamma, G, _c_int(bins, "bins"), _ptr(temps), _ptr(ece),
               _ptr(curve) if curve is not None else None, _ptr(buf), buf.numel(),
               _stream_ptr(stream, dev))
     _raise(st, "spec_sts_calibrate")
@@ -592,8 +600,8 @@ def spec_tree_verify(logits: torch.Tensor, parent: torch.Tensor, tokens: torch.T
     ws = workspace or default_workspace(dev)
     buf = ws.ensure(need, stream)
     st = _run(dev.index, _lib.spec_tree_verify, _ptr(logits), _dtype(logits), _ptr(parent),
-              _ptr(tokens), _ptr(n_nodes), R, M, V, int(max_depth), _ptr(acc), _ptr(path),
-              _ptr(tok), _ptr(buf), buf.numel(), _stream_ptr(stream, dev))
+              _ptr(tokens), _ptr(n_nodes), R, M, V, _c_int(max_depth, "max_depth"), _ptr(acc),
+              _ptr(path), _ptr(tok), _ptr(buf), buf.numel(), _stream_ptr(stream, dev))
     _raise(st, "spec_tree_verify")
     return acc, path, tok
 
@@ -786,7 +794,7 @@ def spec_tree_mask(parent: torch.Tensor, n_nodes: torch.Tensor, ctx_len: torch.T
          (mask, "out_mask", i32, words))
     buf, size, queue = _cache_buf(workspace, dev, 256, stream)
     st = _run(dev, _lib.spec_tree_mask, parent.data_ptr(), n_nodes.data_ptr(), ctx_len.data_ptr(),
-              R, M, int(window), pos.data_ptr(), mask.data_ptr(), buf, size, queue)
+              R, M, _c_int(window, "window"), pos.data_ptr(), mask.data_ptr(), buf, size, queue)
     if st:
         _raise(st, "spec_tree_mask")
     return pos, mask
@@ -861,7 +869,7 @@ def spec_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
     that of a given output); rows past length[r] are left as they were."""
     R, dev = page_table.shape[0], _device(k_cache, "k_cache")
     code, P, Hkv, size, D, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev)
-    max_len = int(max_len)
+    max_len = _c_int(max_len, "max_len")
     _need(max_len >= 0, "max_len must not be negative")
     given = out_k if out_k is not None else out_v
     if given is not None:
@@ -943,8 +951,8 @@ def spec_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     st = _run(dev, _lib.spec_tree_attention, q.data_ptr(), SPEC_BF16, k_cache.data_ptr(),
               v_cache.data_ptr(), code, _raw(k_scale), _raw(v_scale), P, size,
               page_table.data_ptr(), wide, ctx_len.data_ptr(), n_nodes.data_ptr(), _raw(mask),
-              _raw(positions), D ** -0.5 if scale is None else scale, int(window), R, M, Hq, Hkv, D,
-              out.data_ptr(), _raw(out_lse), buf, room, queue)
+              _raw(positions), D ** -0.5 if scale is None else scale, _c_int(window, "window"), R,
+              M, Hq, Hkv, D, out.data_ptr(), _raw(out_lse), buf, room, queue)
     if st:
         _raise(st, "spec_tree_attention")
     return out, out_lse

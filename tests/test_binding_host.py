@@ -131,3 +131,15 @@ def test_the_status_of_a_workspace_taken_inside_a_capture(sv, gpu):
     assert sv.spec_get_device_status(ws) == 1
     gpu.status = {first: 2, last: 1}
     assert sv.spec_get_device_status(ws) == 3 and not any(gpu.status.values())
+
+
+@pytest.mark.parametrize("name,arg", [("spec_tree_mask", "window"), ("spec_tree_attention", "window"),
+                                      ("spec_schedule_verify_len", "topk"), ("spec_sts_calibrate", "bins")])
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1, 2 ** 64 + 1])
+def test_numbers_past_32_bits_are_refused(sv, gpu, name, arg, value):
+    """ctypes would keep their low 32 bits: a window of 2^32 + 5 would be one of 5."""
+    with pytest.raises(ValueError):
+        fake_gpu.calls(sv, 1)[name](**{arg: value})
+    assert not [n for n, *_ in gpu.calls if n == name]
+    fake_gpu.calls(sv, 1)[name](**{arg: 2 ** 31 - 1})
+    assert [n for n, *_ in gpu.calls if n == name]
