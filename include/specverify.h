@@ -574,9 +574,10 @@ size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D)
  * Scores, softmax sums and products are held in fp32.
  *   q         [R][M][Hq][D]  SPEC_BF16
  *   mask      [R][M][W]      uint32 as spec_tree_mask writes it, nullable
- *   positions [R][M]         int32 as spec_tree_mask writes it, nullable
- *                            (ctx_len + v); at least ctx_len (below is a data
- *                            fault of the node), and only a window uses it
+ *   positions [R][M]         int32 as spec_tree_mask writes it, at least ctx_len
+ *                            (below is a data fault of the node); only a window
+ *                            uses it.  Nullable (a chain's, ctx_len + v), but
+ *                            not for a mask with a window (SPEC_EINVAL)
  *   out       [R][M][Hq][D]  bf16
  *   out_lse   [R][M][Hq]     fp32, nullable: natural log of the softmax sum
  * A faulty request's or node's rows become NaN, and so do the rows that see a

@@ -927,7 +927,8 @@ def spec_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
                         workspace: Optional[Workspace] = None, stream=None):
     """Attention of the drafted tokens q [R, M, Hq, D] bfloat16 over the paged
     cache: the context and, by `mask` (spec_tree_mask), their ancestors; without
-    a mask the tokens are a chain.  scale defaults to D ** -0.5.  Returns
+    a mask the tokens are a chain.  A mask with a window needs `positions`
+    (spec_tree_mask) too.  scale defaults to D ** -0.5.  Returns
     (out [R, M, Hq, D] bfloat16, log-sum-exp [R, M, Hq] float32 or None)."""
     shape = q.shape
     _need(len(shape) == 4, "q must be [R, M, Hq, D]")

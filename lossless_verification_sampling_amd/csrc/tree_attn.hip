@@ -1480,6 +1480,7 @@ int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const v
     if (!need || R > 65535) return SPEC_EUNSUPPORTED;
     if (R == 0) return SPEC_OK;
     if (!q || !ctx_len || !n_nodes || !out || (max_pages > 0 && !page_table)) return SPEC_EINVAL;
+    if (mask && window > 0 && !positions) return SPEC_EINVAL;  // a node's index is not its level
     if (((uintptr_t)q | (uintptr_t)out) & 15u) return SPEC_EINVAL;
     if (bad_workspace(workspace, workspace_bytes, need)) return SPEC_EWORKSPACE;
     AttnArgs a{};

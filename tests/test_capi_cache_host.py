@@ -170,3 +170,11 @@ def test_an_empty_write_is_no_fault_whatever_is_null(write):
         assert write(q=None, k=None, v=None, out_q=None, ctx=None, n=None, table=None, **size) == OK
         assert write(q=None, Hq=0, out_q=None, **size) == OK
         assert write(Hq=30, **size) == EINVAL and write(Hq=-8, **size) == EINVAL
+
+
+def test_a_window_over_a_tree_needs_positions(attn):
+    """A mask says who is whose ancestor, not how far the context is."""
+    assert attn(window=5, pos=None, ws=None) == EINVAL
+    # with them, or without a window, or for a chain, the next check is reached
+    assert attn(window=5, ws=None) == EWORKSPACE and attn(pos=None, ws=None) == EWORKSPACE
+    assert attn(window=5, mask=None, pos=None, ws=None) == EWORKSPACE
