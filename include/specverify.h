@@ -478,7 +478,8 @@ size_t spec_cache_workspace_bytes(void);
  * n_nodes outside [0, M], a negative ctx_len, ctx_len + M past 2^31 - 1 or a
  * parent outside [0, v) gets that in all its rows and sets
  * SPEC_DEV_BAD_REQUEST.
- * Sizes: R >= 0, 1 <= M <= SPEC_TREE_MAX_NODES, window >= 0 (0: no window).
+ * Sizes: 0 <= R <= 65535, 1 <= M <= SPEC_TREE_MAX_NODES, window >= 0 (0: no
+ * window).
  */
 int spec_tree_mask(const int32_t *parent, const int32_t *n_nodes, const int32_t *ctx_len, int R,
                    int M, int window, int32_t *out_positions, uint32_t *out_mask, void *workspace,
@@ -504,10 +505,10 @@ int spec_tree_mask(const int32_t *parent, const int32_t *n_nodes, const int32_t 
  *   rope      [max_pos][rot_dim / 2][2]  fp32 (cos, sin), NULL iff rot_dim == 0
  *   positions [R][M]          int32, nullable (ctx_len + v)
  *   out_q     [R][M][Hq][D]   bf16
- * rot_dim is a multiple of 16, at most D (max_pos >= 1 with it).  A position outside [0, max_pos) is
- * a data fault (with rot_dim > 0): the token's out_q rows and its k rows
- * become NaN.  A faulty request's out_q rows become NaN and its tokens are
- * not written.  Sizes: R, M >= 0.
+ * rot_dim is a multiple of 16, at most D (max_pos >= 1 with it).  A position
+ * outside [0, max_pos) is a data fault (with rot_dim > 0): the token's out_q
+ * rows and its k rows become NaN.  A faulty request's out_q rows become NaN and
+ * its tokens are not written.  Sizes: R, M >= 0, R * M < 2^24.
  */
 int spec_qkv_write(const void *q, const void *k, const void *v, int dtype, int64_t ld_q,
                    int64_t ld_k, int64_t ld_v, const void *q_weight, const void *k_weight,
@@ -524,7 +525,7 @@ int spec_qkv_write(const void *q, const void *k, const void *v, int dtype, int64
  *                 code * scale rounded once); rows past len[r] are left alone
  * A request with start < 0, len outside [0, max_len] or start + len past the
  * page table gets NaN in all max_len rows, a token in a bad page NaN in its
- * row.  Sizes: R, max_len >= 0.
+ * row.  Sizes: 0 <= R <= 65535, 0 <= max_len < 2^26 - 3.
  */
 int spec_kv_read(const void *k_cache, const void *v_cache, int cache_dtype, const float *k_scale,
                  const float *v_scale, int num_pages, int page_size, const int32_t *page_table,
@@ -546,7 +547,7 @@ int spec_kv_read(const void *k_cache, const void *v_cache, int cache_dtype, cons
  * [1, M), tokens past the page table or a bad page are data faults: nothing
  * of the request moves and out_ctx_len is -1.  A chain's accepted prefix lies
  * where it belongs already (path[i] = i + 1): no call is needed.
- * Sizes: R >= 0, 1 <= M <= SPEC_TREE_MAX_NODES.
+ * Sizes: 0 <= R < 2^24, 1 <= M <= SPEC_TREE_MAX_NODES.
  */
 int spec_kv_commit(void *k_cache, void *v_cache, int cache_dtype, float *k_scale, float *v_scale,
                    int num_pages, int page_size, const int32_t *page_table, int max_pages,
@@ -585,7 +586,9 @@ size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D)
  * (spec_qkv_write).  A call repeated gives the same bits; the order of a
  * row's sums depends on R, M and the lengths in the batch, and on nothing
  * else that the row does not see.
- * Sizes: R >= 0, 1 <= M <= SPEC_TREE_MAX_NODES, Hq / Hkv <= 64, window >= 0.
+ * Sizes: 0 <= R <= 65535, 1 <= M <= SPEC_TREE_MAX_NODES, Hq / Hkv <= 64,
+ * window >= 0; R * Hkv * (tiles of 16 or more of a key head's M * Hq / Hkv rows)
+ * * (128-token units of a page table's width) below 2^31.
  */
 int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const void *v_cache,
                         int cache_dtype, const float *k_scale, const float *v_scale,

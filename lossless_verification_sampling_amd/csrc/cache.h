@@ -52,6 +52,9 @@ __device__ __forceinline__ bool in_table(int first, int count, int max_pages, in
            (int64_t)first + count <= min((int64_t)max_pages << shift, (int64_t)0x7ffff000);
 }
 
+// Workgroups of kBlock threads along one axis of a launch: threads count in 32 bits.
+constexpr int64_t kMaxBlocks = (1ll << 32) / kBlock - 1;
+
 // Host checks of a cache's arguments that every entry point shares; 0 or a
 // negative spec_status.  (A missing page table is looked for once it is known
 // that the call has anything to do.)

@@ -474,7 +474,7 @@ int spec_qkv_write(const void *q, const void *k, const void *v, int dtype, int64
     if (rot_dim > D || rot_dim % 16) return SPEC_EUNSUPPORTED;
     if (rot_dim > 0 && max_pos < 1) return SPEC_EINVAL;
     const int64_t tokens = (int64_t)R * M;
-    if (tokens > 0x7fffffff) return SPEC_EUNSUPPORTED;
+    if (tokens > kMaxBlocks) return SPEC_EUNSUPPORTED;
     if (Hq % Hkv) return SPEC_EINVAL;
     if (tokens == 0) return SPEC_OK;  // (an empty q may well be null)
     if ((q != nullptr) != (Hq > 0)) return SPEC_EINVAL;
@@ -535,7 +535,7 @@ int spec_kv_read(const void *k_cache, const void *v_cache, int cache_dtype, cons
                                 page_size, max_pages, Hkv, D);
     if (bad) return bad;
     if (out_dtype != SPEC_BF16 && out_dtype != SPEC_F32) return SPEC_EDTYPE;
-    if (R > 65535) return SPEC_EUNSUPPORTED;
+    if (R > 65535 || max_len > kReadTokens * kMaxBlocks) return SPEC_EUNSUPPORTED;
     if (R == 0 || max_len == 0) return SPEC_OK;
     if (!start || !len || !out_k || !out_v || (max_pages > 0 && !page_table)) return SPEC_EINVAL;
     if (((uintptr_t)out_k | (uintptr_t)out_v) & 15u) return SPEC_EINVAL;
@@ -571,7 +571,7 @@ int spec_kv_commit(void *k_cache, void *v_cache, int cache_dtype, float *k_scale
     const int bad = check_pages(k_cache, v_cache, cache_dtype, k_scale, v_scale, num_pages,
                                 page_size, max_pages, Hkv, D);
     if (bad) return bad;
-    if (M > SPEC_TREE_MAX_NODES) return SPEC_EUNSUPPORTED;
+    if (M > SPEC_TREE_MAX_NODES || R > kMaxBlocks) return SPEC_EUNSUPPORTED;
     if (R == 0) return SPEC_OK;
     if (!ctx_len || !accepted || !path || out_ctx_len == ctx_len || (max_pages > 0 && !page_table))
         return SPEC_EINVAL;

@@ -178,3 +178,12 @@ def test_a_window_over_a_tree_needs_positions(attn):
     # with them, or without a window, or for a chain, the next check is reached
     assert attn(window=5, ws=None) == EWORKSPACE and attn(pos=None, ws=None) == EWORKSPACE
     assert attn(window=5, mask=None, pos=None, ws=None) == EWORKSPACE
+
+
+def test_more_workgroups_than_a_launch_holds(write, read, commit):
+    """2^24 - 1 workgroups of 256 threads are a launch's most."""
+    most = (1 << 24) - 1
+    assert write(R=1, M=most, ws=None) == EWORKSPACE and write(R=1, M=most + 1) == EUNSUPPORTED
+    assert write(R=1 << 12, M=1 << 12, ws=None) == EUNSUPPORTED
+    assert read(R=1, max_len=4 * most, ws=None) == EWORKSPACE and read(R=1, max_len=4 * most + 1) == EUNSUPPORTED
+    assert commit(R=most, ws=None) == EWORKSPACE and commit(R=most + 1) == EUNSUPPORTED

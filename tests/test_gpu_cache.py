@@ -356,3 +356,22 @@ def test_kv_commit_faults(sv, dev, fault):
     assert new.tolist() == [5, -1]
     for now, old in zip(c.dev, before):
         assert torch.equal(now.view(torch.uint8)[keep], old[keep])
+
+
+def test_the_largest_launches(sv, dev):
+    """One token of 2^24 - 1 (and the same beyond: refused before the launch)."""
+    most = (1 << 24) - 1
+    x = torch.empty(1, most + 1, 1, 64, dtype=torch.bfloat16, device=dev)
+    x[0, :1] = 2.0
+    k, v = (torch.zeros(1, 1, 16, 64, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    one = torch.ones(1, dtype=torch.int32, device=dev)
+    table, zero = torch.zeros(1, 1, dtype=torch.int32, device=dev), torch.zeros_like(one)
+    sv.spec_qkv_write(x[:, :most], x[:, :most], k, v, table, zero, one)
+    assert (k[0, 0, 0] == 2).all() and (v[0, 0, 0] == 2).all() and not k[0, 0, 1:].any()
+    with pytest.raises(sv.SpecError) as e:
+        sv.spec_qkv_write(x, x, k, v, table, zero, one)
+    assert e.value.status == -5
+    del x
+    x = torch.full((1, 4 * most, 1, 64), 7.0, dtype=torch.bfloat16, device=dev)
+    sv.spec_kv_read(k, v, table, zero, one, 4 * most, out_k=x, out_v=x)
+    assert (x[0, 0] == 2).all() and (x[0, 1:1000] == 7).all() and (x[0, -1000:] == 7).all()
