@@ -372,6 +372,108 @@ def test_the_largest_launches(sv, dev):
         sv.spec_qkv_write(x, x, k, v, table, zero, one)
     assert e.value.status == -5
     del x
-    x = torch.full((1, 4 * most, 1, 64), 7.0, dtype=torch.bfloat16, device=dev)
-    sv.spec_kv_read(k, v, table, zero, one, 4 * most, out_k=x, out_v=x)
-    assert (x[0, 0] == 2).all() and (x[0, 1:1000] == 7).all() and (x[0, -1000:] == 7).all()
+    got = [torch.full((1, 4 * most, 1, 64), 7.0, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    sv.spec_kv_read(k, v, table, zero, one, 4 * most, out_k=got[0], out_v=got[1])
+    for x in got:
+        assert (x[0, 0] == 2).all() and (x[0, 1:1000] == 7).all() and (x[0, -1000:] == 7).all()
+
+
+PROMPTS = [  # R, M, Hq, Hkv, D, page, norm, rot, interleaved
+    (7, 73, 5, 1, 64, 16, True, 64, False),        # 511 tokens: a head row a thread
+    (4, 128, 5, 1, 64, 16, True, 64, False),       # 512: a workgroup a token
+    (3, 171, 32, 8, 128, 64, True, 128, False),
+    (4, 131, 7, 7, 128, 32, True, 48, True),
+    (5, 110, 60, 4, 128, 16, True, 64, False),     # more rows than one pass holds
+    (4, 129, 128, 8, 64, 32, False, 16, False),
+    (3, 200, 2, 1, 256, 16, True, 256, True),
+    (4, 140, 16, 8, 256, 128, True, 64, False),
+    (4, 128, 33, 3, 256, 16, True, 0, False),
+    (2, 300, 0, 5, 128, 64, True, 128, False),     # no queries
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("case", PROMPTS)
+def test_qkv_write_prompts(sv, dev, case, dt, kind):
+    R, M, Hq, Hkv, Dh, page, norm, rot, inter = case
+    print(f"[write] {case} {dt} {kind}", flush=True)
+    g = np.random.default_rng([R, M])
+    ctx = g.integers(0, 60, R).astype(np.int32)
+    n = np.array([M, 0] + [int(x) for x in g.integers(1, M + 1, R - 2)], np.int32)
+    c = Cache(g, R, int(ctx.max()) + M, Hkv, Dh, page, kind).to(dev)
+    H = Hq + 2 * Hkv
+    x = bf16(g.standard_normal((R, M, H, Dh), np.float32) * 2)
+    if dt == "f32":
+        x = x.float() + torch.from_numpy(g.standard_normal((R, M, H, Dh), np.float32) * 1e-3)
+    w = [None, None]
+    if norm:
+        w = [bf16(1 + 0.3 * g.standard_normal(Dh)).to(x.dtype) for _ in range(2)]
+    rope, max_pos = None, int(ctx.max()) + M
+    if rot:
+        a = np.arange(max_pos)[:, None] * 100.0 ** -(np.arange(rot // 2) * 2 / rot)[None, :]
+        rope = np.stack([np.cos(a), np.sin(a)], -1).astype(np.float32)
+    before = [t.clone() for t in c.dev] + [None if t is None else t.clone() for t in c.scales]
+    out = torch.full((R, M, Hq, Dh), 7.0, dtype=torch.bfloat16, device=dev) if Hq else None
+    ws = sv.Workspace(dev, 256)
+    xd = x.to(dev)
+    sv.spec_qkv_write(xd[:, :, Hq:Hq + Hkv], xd[:, :, Hq + Hkv:], *c.args(), D(ctx, dev), D(n, dev),
+                      q=xd[:, :, :Hq] if Hq else None, q_weight=w[0].to(dev) if norm and Hq else None,
+                      k_weight=w[1].to(dev) if norm else None, eps=1e-5,
+                      rope=None if rope is None else D(rope, dev), interleaved=inter, out_q=out,
+                      workspace=ws, **c.kw())
+    torch.cuda.synchronize()
+    assert sv.spec_get_device_status(ws) == 0
+    live = np.arange(M)[None, :] < n[:, None]
+    r, i = np.nonzero(live)
+    t = ctx[r] + i
+    pg, off = c.table[r, t // page], t % page
+    rows = x.double().numpy()[live]                # [tokens, H, Dh]
+
+    def rotated(part, wt):
+        """(rows, those before the rotation), fp64"""
+        p = part
+        if wt is not None:
+            p = p / np.sqrt((p * p).mean(-1, keepdims=True) + 1e-5) * wt.double().numpy()
+        if not rot:
+            return p, p
+        z, y = rope[t].astype(np.float64)[:, None], p.copy()
+        h = rot // 2
+        a, b = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, h), slice(h, rot))
+        y[..., a] = p[..., a] * z[..., 0] - p[..., b] * z[..., 1]
+        y[..., b] = p[..., b] * z[..., 0] + p[..., a] * z[..., 1]
+        return y, p
+
+    def held(which):
+        """values of the cache rows that were written, fp64 [tokens, Hkv, Dh]"""
+        v = c.dev[which][torch.from_numpy(pg).long().to(dev), :, torch.from_numpy(off).long().to(dev)]
+        v = v.float().cpu().numpy().astype(np.float64)
+        if c.scales[which] is not None:
+            v = v * c.scales[which].cpu().numpy().astype(np.float64)[pg, :, off][..., None]
+        return v
+    # fp32: 13 roundings in the mean's sum (halved by the root), three to the
+    # factor, two products, three in the rotation of two terms: below 32 half
+    # steps of the row's largest value before it
+    if Hq:
+        y, p = rotated(rows[:, :Hq], w[0])
+        slack = 2.0 ** -19 * np.abs(p).max(-1, keepdims=True)
+        got = out.double().cpu().numpy()
+        assert (got[~live] == 7.0).all()
+        assert (np.abs(got[live] - y) <= np.abs(y) * BF16_U + slack).all()
+    y, p = rotated(rows[:, Hq:Hq + Hkv], w[1])
+    check_write(c, None, None, None, None, held(0), y, 2.0 ** -19 * np.abs(p).max(-1, keepdims=True))
+    val = rows[:, Hq + Hkv:].astype(np.float32)
+    if kind == "bf16":
+        want = bf16(val).double().numpy()
+    else:
+        codes, s = oc.quantise(val)
+        want = codes * s.astype(np.float64)[..., None]
+    np.testing.assert_array_equal(held(1), want)
+    touched = np.zeros((c.P, page), bool)
+    touched[pg, off] = True
+    keep = torch.from_numpy(~touched).to(dev)
+    for now, old in zip(c.dev + c.scales, before):
+        if now is None:
+            continue
+        b = torch.uint8 if now.element_size() == 1 else torch.int16 if now.element_size() == 2 else torch.int32
+        assert torch.equal(now.view(b).transpose(1, 2)[keep], old.view(b).transpose(1, 2)[keep])

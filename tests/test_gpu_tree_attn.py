@@ -355,3 +355,59 @@ def test_pages_before_the_window_are_not_looked_at(sv, dev, kind, tree, M, G, ct
     got = c.run(sv, dev, workspace=ws)
     assert sv.spec_get_device_status(ws) == 0
     c.check(got)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("M,G,Dh", [(6, 2, 128), (1, 1, 64), (40, 2, 64), (30, 4, 256)])
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 1.5])
+def test_scales_of_any_sign(sv, dev, kind, M, G, Dh, scale):
+    c = Case(26, 2, M, 2 * G, 2, Dh, 32, kind, [90, 5], M > 1)
+    c.scale = float(np.float32(scale))
+    c.check(c.run(sv, dev))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("M,G,ctx", [(1, 4, 2003), (8, 2, 2003), (30, 4, 1990)])
+def test_every_row_of_v_counts(sv, dev, kind, M, G, ctx):
+    """Token t's V row has one positive value, in dimension t mod 64: a value of
+    the output is the sum of some 31 weights, and nothing cancels, so a bound
+    relative to the value itself (two bf16 roundings) shows one wrong row."""
+    c = Case(27, 1, M, G, 1, 64, 16, kind, [ctx], False, qs=0.02)
+    t = np.arange(ctx + M)
+    v = np.zeros((ctx + M, 64), np.float32)
+    v[t, t % 64] = 1 + (t * 37 % 101) / 101
+    pg, off = c.c.table[0, t // 16], t % 16
+    if kind == "bf16":
+        c.c.dev[1][pg, 0, off] = bf16(v)
+    else:
+        codes, s = oc.quantise(v)
+        c.c.dev[1].view(torch.uint8)[pg, 0, off] = torch.from_numpy(codes.astype(np.float32)).to(
+            torch.float8_e4m3fn).view(torch.uint8)
+        c.c.scales[1][pg, 0, off] = torch.from_numpy(s)
+    c.check(c.run(sv, dev))                   # whose bound is |o| (2^-7 + less than 2^-9) here
+    s = (c.c.rows(0, 0, 0, ctx + M)[:, 0] @ c.q[0, -1, 0].double().numpy()) * c.scale
+    w = np.exp(s) * v.sum(-1)                 # the last node sees every token
+    whole = np.array([w[t % 64 == d].sum() for d in range(64)])
+    assert (w / whole[t % 64]).min() > 2.0 ** -7 + 2.0 ** -9
+
+
+@pytest.mark.parametrize("M", [2, 20])
+def test_many_idle_requests(sv, dev, M):
+    """A padded batch: a few live requests among 30000."""
+    R, live = 30000, [0, 1, 77, 15000, 29998]
+    c = Case(28, len(live), M, 4, 2, 64, 16, "bf16", [100, 3, 0, 250, 40], False)
+    c.c.to(dev)
+    q = torch.zeros(R, M, 4, 64, dtype=torch.bfloat16, device=dev)
+    table = torch.full((R, c.c.wide), -1, dtype=torch.int32, device=dev)
+    n, ctx = torch.zeros(R, dtype=torch.int32, device=dev), torch.zeros(R, dtype=torch.int32, device=dev)
+    at = torch.tensor(live, device=dev)
+    q[at], table[at], n[at], ctx[at] = c.q.to(dev), c.c.t, M, D(c.ctx, dev)
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((R, M, 4), 7.0, device=dev)
+    ws = sv.Workspace(dev, sv.spec_tree_attention_workspace_bytes(R, M, 4, 2, 64))
+    sv.spec_tree_attention(q, c.c.dev[0], c.c.dev[1], table, ctx, n, out=out, out_lse=lse, workspace=ws)
+    assert sv.spec_get_device_status(ws) == 0
+    c.check((out[at].double().cpu().numpy(), lse[at].double().cpu().numpy()))
+    idle = torch.ones(R, dtype=torch.bool, device=dev)
+    idle[at] = False
+    assert (out[idle] == 7).all() and (lse[idle] == 7).all()
