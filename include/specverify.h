@@ -458,6 +458,8 @@ int spec_tree_verify(const void *logits, int dtype, const int32_t *parent, const
  *    ctx_len - window + 1 on, so pages before may have been given back.
  *  - Two requests may share pages that only hold context (a common prefix);
  *    a page that one call writes must belong to one request.
+ *  - What a call writes overlaps nothing that it reads, but for the cache
+ *    itself in spec_kv_commit.
  */
 
 /* Workspace bytes of spec_tree_mask, spec_qkv_write, spec_kv_read and
@@ -541,7 +543,8 @@ int spec_kv_read(const void *k_cache, const void *v_cache, int cache_dtype, cons
  *   accepted  [R]     int32 as spec_tree_verify's out_accepted
  *   path      [R][M]  int32 as its out_path: accepted nodes, increasing
  *   out_ctx_len [R]   int32, nullable: ctx_len + 1 + accepted (may not be
- *                     ctx_len itself: other layers still read that)
+ *                     ctx_len itself, which other layers still read, nor
+ *                     accepted or path)
  * accepted[r] = -1 (an invalid tree) moves nothing and keeps ctx_len.  An
  * accepted outside [-1, M - 1], a path that is not increasing inside
  * [1, M), tokens past the page table or a bad page are data faults: nothing

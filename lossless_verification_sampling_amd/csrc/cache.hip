@@ -573,8 +573,8 @@ int spec_kv_commit(void *k_cache, void *v_cache, int cache_dtype, float *k_scale
     if (bad) return bad;
     if (M > SPEC_TREE_MAX_NODES || R > kMaxBlocks) return SPEC_EUNSUPPORTED;
     if (R == 0) return SPEC_OK;
-    if (!ctx_len || !accepted || !path || out_ctx_len == ctx_len || (max_pages > 0 && !page_table))
-        return SPEC_EINVAL;
+    if (!ctx_len || !accepted || !path || (max_pages > 0 && !page_table)) return SPEC_EINVAL;
+    if (out_ctx_len == ctx_len || out_ctx_len == accepted || out_ctx_len == path) return SPEC_EINVAL;
     if (bad_workspace(workspace, workspace_bytes, sizeof(Control))) return SPEC_EWORKSPACE;
     CommitArgs a{};
     a.c = make_pages(k_cache, v_cache, cache_dtype == SPEC_E4M3 ? k_scale : nullptr,

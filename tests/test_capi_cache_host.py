@@ -187,3 +187,12 @@ def test_more_workgroups_than_a_launch_holds(write, read, commit):
     assert write(R=1 << 12, M=1 << 12, ws=None) == EUNSUPPORTED
     assert read(R=1, max_len=4 * most, ws=None) == EWORKSPACE and read(R=1, max_len=4 * most + 1) == EUNSUPPORTED
     assert commit(R=most, ws=None) == EWORKSPACE and commit(R=most + 1) == EUNSUPPORTED
+
+
+def test_commit_outputs_are_no_input(commit):
+    """A workgroup stores its request's length while its other waves may not have
+    read their accepted count yet."""
+    assert commit(acc=A + 512, out_ctx=A + 512) == EINVAL
+    assert commit(path=A + 512, out_ctx=A + 512) == EINVAL
+    assert commit(acc=A + 512, out_ctx=A + 256, ws=None) == EWORKSPACE
+    assert commit(acc=A + 512, out_ctx=None, ws=None) == EWORKSPACE
