@@ -523,8 +523,9 @@ int spec_qkv_write(const void *q, const void *k, const void *v, int dtype, int64
 
 /*
  * Reads tokens start[r] .. start[r] + len[r] - 1 of every request back.
- *   out_k, out_v  [R][max_len][Hkv][D]  out_dtype (SPEC_BF16 or SPEC_F32;
- *                 code * scale rounded once); rows past len[r] are left alone
+ *   out_k, out_v  [R][max_len][Hkv][D]  out_dtype (SPEC_BF16 or SPEC_F32): the
+ *                 fp32 product code * scale, for bf16 output rounded again;
+ *                 rows past len[r] are left alone
  * A request with start < 0, len outside [0, max_len] or start + len past the
  * page table gets NaN in all max_len rows, a token in a bad page NaN in its
  * row.  Sizes: 0 <= R <= 65535, 0 <= max_len < 2^26 - 3.
@@ -575,7 +576,9 @@ size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D)
  * A token that a node does not see has no part in its row, whatever its
  * cache rows hold.  A row that sees nothing (or whose scores are all -inf) gets
  * 0 and log-sum-exp -inf.
- * Scores, softmax sums and products are held in fp32.
+ * Scores, maxima, softmax sums (of unrounded weights) and accumulators are held
+ * in fp32; a weight e^(s_j - m), times V's scale for SPEC_E4M3, is rounded to bf16
+ * for its product with V (up to 2^-8 of it, as much as out's own rounding).
  *   q         [R][M][Hq][D]  SPEC_BF16
  *   mask      [R][M][W]      uint32 as spec_tree_mask writes it, nullable
  *   positions [R][M]         int32 as spec_tree_mask writes it, at least ctx_len

@@ -110,7 +110,7 @@ __device__ __forceinline__ float value(const Raw4<T> &r, int i) {
 // rows in flight was slower (150 us against 125 for 16 k tokens of 48 rows:
 // the registers cost more waves than the waits).
 // Bound by HBM: the projections read, q and the cache written; 16 k tokens of
-// 48 rows to e4m3 pages take 73 us, 5.0 TB/s of 365 MB (a large copy: 4.74).
+// 48 rows to e4m3 pages take 74 us, 5.0 TB/s of 365 MB (a large copy: 4.74).
 template <typename T, bool FP8, int D, int ROWS>
 __global__ void __launch_bounds__(kBlock) qkv_write_kernel(WriteArgs a) {
     constexpr int LPR = D / 8, RPB = kBlock / LPR;
@@ -274,7 +274,7 @@ constexpr int kReadTokens = 4;
 // One workgroup per kReadTokens tokens of a request (y); a thread takes 8
 // values of a head row of each, all loads before the first store.
 // Bound by HBM: pages read, rows written; 32 users of 4 k tokens from e4m3
-// pages take 119 us, 5.1 TB/s of 614 MB (one token a workgroup: 147 us).
+// pages take 121 us, 5.1 TB/s of 614 MB (one token a workgroup: 147 us).
 template <typename T, bool FP8, int D>
 __global__ void __launch_bounds__(kBlock) kv_read_kernel(ReadArgs a) {
     const int r = blockIdx.y, i0 = blockIdx.x * kReadTokens;
@@ -356,7 +356,7 @@ struct CommitArgs {
 // in ascending order, reading the eight before it writes them: the path rises
 // from path[i] >= i + 1 on, so a later row's source path[j] >= j + 1 lies
 // behind every slot i + 1 <= j written for earlier ones.  Bound by four
-// dependent memory round trips: 256 users, 5.0 us.
+// dependent memory round trips: 256 users, 5.3 us.
 __global__ void __launch_bounds__(kBlock) kv_commit_kernel(CommitArgs a) {
     __shared__ int64_t from_s[SPEC_TREE_MAX_NODES], to_s[SPEC_TREE_MAX_NODES];
     const int r = blockIdx.x, tid = threadIdx.x;
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kBlock) kv_commit_kernel(CommitArgs a) {
 // Few tokens: one head row a thread, so that latency is a row's (64 tokens of
 // 48 rows: 4.0 us against 4.8); from two workgroups to a compute unit on, a
 // workgroup per token and four rows a thread (512 tokens 5.9 us against 6.2,
-// 16 k tokens 77 against 121).
+// 16 k tokens 77 against 121; all of 48 rows of 128).
 template <typename T, bool FP8, int D>
 static void launch_write(const WriteArgs &a, int64_t tokens, int rows, hipStream_t st) {
     constexpr int RPB = kBlock / (D / 8);

@@ -114,8 +114,8 @@ __device__ __forceinline__ int head_units(const AttnArgs &a, const Req &q) {
 // ranges as compute units, or two for each (fewer parts to join, against waits
 // that hide each other): one user's 30 k tokens, 1880 units, take 29.2 us with
 // 256 ranges and 32.6 with 512, 8 users of 4 k 22.7 and 24.7, 16 users (2300
-// units) 35.3 and 34.6, 32 users 78 (288 ranges) and 65.0.  Numbers between
-// leave some compute units twice the work of others.
+// units) 35.3 and 34.6, 32 users 78 (288 ranges) and 65.0 (all bf16, D = 128).
+// Numbers between leave some compute units twice the work of others.
 struct Place {
     int r;                       // the request of the range's first unit
     int off;                     // units into it
@@ -604,7 +604,7 @@ __device__ __forceinline__ Plain plain_of(const AttnArgs &a, const Req &rq, int 
 // ---------------------------------------------------------------------------
 
 // Bound by HBM: a workgroup's waves keep one step of K and V each in flight.
-// One token behind 30011 (bf16): 27.2 us, 4.5 TB/s; 64 chains of 8 behind up to
+// One token behind 30011 (bf16): 27.8 us, 4.4 TB/s; 64 chains of 8 behind up to
 // 4 k (e4m3): 83 us, 3.8 TB/s (two waves a SIMD, for the registers).
 template <int D, int RT> constexpr int waves_per_simd() {
     return D <= 128 && D * RT <= 256 ? 2 : 1;
@@ -867,10 +867,10 @@ constexpr int kTile = 64;              // tokens staged at a time
 // instead of the tokens: 64 tokens of K and V go to shared memory once per
 // workgroup, already in operand layout (converted and transposed on the way),
 // while the previous 64 are multiplied, and every wave reads them from there.
-// Bound by HBM for trees (64 of 48 nodes behind up to 4 k tokens, bf16: 177 us,
+// Bound by HBM for trees (64 of 48 nodes behind up to 4 k tokens, bf16: 176 us,
 // 3.6 TB/s; with the arithmetic left out 150), by the issue of matrix and
 // vector instructions for prompt chunks (4 of 1000 behind 12 k, five heads a
-// key head, e4m3: 803 us, 798 TFLOP/s, the matrix pipes 32% busy).
+// key head, e4m3: 771 us, 831 TFLOP/s, the matrix pipes 33% busy).
 template <bool FP8, int D> struct Stage {
     typedef Tile<FP8, D> TT;
     u32x4_t k[TT::KV];
@@ -1385,8 +1385,8 @@ __global__ void __launch_bounds__(kBlock) attn_wide_join_kernel(AttnArgs a) {
 // against 80.3).  A small batch, up to 48 rows to a compute unit, takes one:
 // more workgroups with less to store for the join, for pages read again from
 // L2 (one tree of 48 nodes behind 200 tokens 14.0 us against 20.1, behind 4 k
-// 27.7 and 31.4, behind 30 k 72 and 68; 8 trees 50.3 and 53.6, 16 trees 93 and
-// 81).
+// 27.7 and 31.4, but behind 30 k 72 and 68; 8 trees, the rule's last, 50.3 and
+// 53.6, 16 trees 93 and 81; between them it is not measured).
 struct Shape {
     bool wide;
     int RT, TR, groups;
