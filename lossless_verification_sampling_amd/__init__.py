@@ -220,11 +220,12 @@ def spec_tree_attention_workspace_bytes(R: int, M: int, Hq: int, Hkv: int, D: in
 # marshalling helpers
 # ---------------------------------------------------------------------------
 
-def _stream_ptr(stream: Optional[torch.cuda.Stream], device) -> int:
+def _stream_of(stream: Optional[torch.cuda.Stream], dev: int) -> int:
+    """Handle of the stream that a call for device `dev` runs on."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    if device.index is not None and stream.device.index != device.index:
-        raise ValueError(f"stream is on {stream.device}, expected {device}")
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, expected cuda:{dev}")
     return stream.cuda_stream
 
 
@@ -297,8 +298,9 @@ def _capturing(stream) -> bool:
 
 
 def _init(buf: torch.Tensor, stream):
-    _raise(_run(buf.get_device(), _lib.spec_workspace_init, _ptr(buf), buf.numel(),
-                _stream_ptr(stream, buf.device)), "spec_workspace_init")
+    dev = buf.get_device()
+    _raise(_run(dev, _lib.spec_workspace_init, _ptr(buf), buf.numel(), _stream_of(stream, dev)),
+           "spec_workspace_init")
 
 
 class Workspace:
@@ -330,8 +332,8 @@ class Workspace:
                 self._outgrown.append(self.buf)
             self.buf = buf
             self._recorded = inside
-            self._streams = {_stream_ptr(stream, buf.device)}
-        handle = _stream_ptr(stream, self.buf.device)
+            self._streams = {_stream_of(stream, buf.get_device())}
+        handle = _stream_of(stream, self.buf.get_device())
         if handle not in self._streams:  # its memory stays until that stream is done, too
             self.buf.record_stream(stream if stream is not None else
                                    torch.cuda.current_stream(self.buf.device))
@@ -347,6 +349,8 @@ _default_ws = {}
 
 
 def default_workspace(device) -> Workspace:
+    """The device's workspace for calls that give none.  There is one: calls on
+    several streams at a time need workspaces of their own."""
     device = torch.device(device)
     key = (device.type, device.index if device.index is not None else torch.cuda.current_device())
     ws = _default_ws.get(key)
@@ -368,10 +372,9 @@ def spec_get_device_status(workspace: Workspace, clear: bool = True, stream=None
     found = 0
     for buf in workspace._outgrown + [workspace.buf]:
         if buf is not None:
-            bits = ctypes.c_uint32(0)
-            _raise(_run(buf.get_device(), _lib.spec_get_device_status, _ptr(buf),
-                        ctypes.byref(bits), int(clear), _stream_ptr(stream, buf.device)),
-                   "spec_get_device_status")
+            bits, dev = ctypes.c_uint32(0), buf.get_device()
+            _raise(_run(dev, _lib.spec_get_device_status, _ptr(buf), ctypes.byref(bits),
+                        int(clear), _stream_of(stream, dev)), "spec_get_device_status")
             # (unknown bits: taken inside a capture and not replayed yet, the word
             # is what its memory held before)
             if not bits.value & ~(SPEC_DEV_BAD_REQUEST | SPEC_DEV_SPIN_TIMEOUT):
@@ -448,7 +451,7 @@ def spec_verify_batch(target_logits: torch.Tensor, draft_logits: Optional[torch.
               _ptr(draft_logits), d_dtype, _ptr(draft_tokens), _ptr(verify_len), _ptr(temperature),
               _ptr(u_accept), _ptr(u_sample), R, gamma, V, _ptr(o["tokens"]),
               _ptr(o["num_accepted"]), _ptr(o["cstar"]), _ptr(o["resid_mass"]), _ptr(o["logq"]),
-              _ptr(buf), buf.numel(), _stream_ptr(stream, dev))
+              _ptr(buf), buf.numel(), _stream_of(stream, dev.index))
     _raise(st, "spec_verify_batch")
     return o
 
@@ -474,7 +477,7 @@ def spec_verify_batch_noalloc(target_logits: torch.Tensor, draft_logits: Optiona
               _ptr(draft_logits), d_dtype, _ptr(draft_tokens), _ptr(verify_len), _ptr(temperature),
               _ptr(u_accept), _ptr(u_sample), R, gamma, V, _ptr(o["tokens"]),
               _ptr(o["num_accepted"]), _ptr(o["cstar"]), _ptr(o["resid_mass"]), _ptr(o["logq"]),
-              _stream_ptr(stream, dev))
+              _stream_of(stream, dev.index))
     _raise(st, "spec_verify_batch_noalloc")
     return o
 
@@ -515,7 +518,7 @@ def spec_tv_accept_rate(draft_logits: torch.Tensor, target_logits: torch.Tensor,
     buf = ws.ensure(need, stream)
     st = _run(dev.index, _lib.spec_tv_accept_rate, _ptr(draft_logits), _ptr(target_logits),
               _dtype(target_logits), _ptr(temperature), N, V, _ptr(cs), _ptr(rs), _ptr(buf),
-              buf.numel(), _stream_ptr(stream, dev))
+              buf.numel(), _stream_of(stream, dev.index))
     _raise(st, "spec_tv_accept_rate")
     return cs, rs
 
@@ -542,7 +545,7 @@ def spec_schedule_verify_len(confidence: torch.Tensor, sps: torch.Tensor, *, top
     buf = ws.ensure(spec_schedule_workspace_bytes(), stream)
     st = _run(dev.index, _lib.spec_schedule_verify_len, _ptr(confidence), _ptr(sps), R, gamma,
               sps.numel() - 1, _c_int(topk, "topk"), _ptr(ln), _ptr(th), _ptr(buf), buf.numel(),
-              _stream_ptr(stream, dev))
+              _stream_of(stream, dev.index))
     _raise(st, "spec_schedule_verify_len")
     return ln, th
 
@@ -572,7 +575,7 @@ def spec_sts_calibrate(conf_logits: torch.Tensor, accepted_len: torch.Tensor, gr
     st = _run(dev.index, _lib.spec_sts_calibrate, _ptr(conf_logits), _ptr(accepted_len), _ptr(grid),
               N, gamma, G, _c_int(bins, "bins"), _ptr(temps), _ptr(ece),
               _ptr(curve) if curve is not None else None, _ptr(buf), buf.numel(),
-              _stream_ptr(stream, dev))
+              _stream_of(stream, dev.index))
     _raise(st, "spec_sts_calibrate")
     return temps, ece, curve
 
@@ -601,7 +604,7 @@ def spec_tree_verify(logits: torch.Tensor, parent: torch.Tensor, tokens: torch.T
     buf = ws.ensure(need, stream)
     st = _run(dev.index, _lib.spec_tree_verify, _ptr(logits), _dtype(logits), _ptr(parent),
               _ptr(tokens), _ptr(n_nodes), R, M, V, _c_int(max_depth, "max_depth"), _ptr(acc),
-              _ptr(path), _ptr(tok), _ptr(buf), buf.numel(), _stream_ptr(stream, dev))
+              _ptr(path), _ptr(tok), _ptr(buf), buf.numel(), _stream_of(stream, dev.index))
     _raise(st, "spec_tree_verify")
     return acc, path, tok
 
@@ -642,7 +645,7 @@ def spec_rnn_draft_sample(U: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor,
     st = _run(dev.index, _lib.spec_rnn_draft_sample, _ptr(U), _dtype(U), _ptr(W1), _ptr(W2),
               SPEC_BF16, _ptr(hidden_states), hidden, _ptr(Wg), _ptr(bg), _ptr(anchor),
               _ptr(temperature), _ptr(u_draft), R, gamma, V, rank, _ptr(tok), _ptr(lg), _ptr(stt),
-              _ptr(buf), buf.numel(), _stream_ptr(stream, dev))
+              _ptr(buf), buf.numel(), _stream_of(stream, dev.index))
     _raise(st, "spec_rnn_draft_sample")
     return tok, lg, stt
 
@@ -676,7 +679,7 @@ def spec_markov_draft_sample(U: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor
     buf = ws.ensure(need, stream)
     st = _run(dev.index, _lib.spec_markov_draft_sample, _ptr(U), _dtype(U), _ptr(W1), _ptr(W2),
               SPEC_BF16, _ptr(anchor), _ptr(temperature), _ptr(u_draft), R, gamma, V, rank,
-              _ptr(tok), _ptr(lg), _ptr(buf), buf.numel(), _stream_ptr(stream, dev))
+              _ptr(tok), _ptr(lg), _ptr(buf), buf.numel(), _stream_of(stream, dev.index))
     _raise(st, "spec_markov_draft_sample")
     return tok, lg
 
@@ -697,12 +700,6 @@ def _all(dev: int, *specs):
         if t is not None and (t.dtype is not dtype or t.shape != shape or
                               t.get_device() != dev or not t.is_contiguous()):
             _check(t, name, dtype, shape, torch.device("cuda", dev))
-
-
-def _stream_of(stream: Optional[torch.cuda.Stream], dev: int) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return _stream_ptr(stream, torch.device("cuda", dev))
 
 
 _CACHE_CODES = {torch.bfloat16: SPEC_BF16, torch.float8_e4m3fn: SPEC_E4M3}
