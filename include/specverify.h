@@ -604,6 +604,98 @@ int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const v
                         int Hkv, int D, void *out, float *out_lse, void *workspace,
                         size_t workspace_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Drafting with the target's own cache, over a budget of its pages
+ *
+ * A drafting step may attend to the best `budget` full pages of the context
+ * instead of all of them; verification (full attention) keeps what is
+ * committed lossless.  Beside the cache of a layer stand the bounds of its keys,
+ *   k_min, k_max  [num_pages][Hkv][D]  SPEC_BF16: least and largest value of
+ *                                      each key dimension in the page
+ * and a step runs, in every layer,
+ *   spec_qkv_write      (as above)
+ *   spec_page_bounds    for the tokens written (after spec_kv_commit: for those
+ *                       moved)
+ *   spec_page_select    page lists, one per key head
+ *   spec_page_attention over the lists
+ * The common rules of the cache hold here too.
+ */
+
+/*
+ * Bounds of every page that holds one of tokens start[r] .. start[r] + len[r] - 1,
+ * over the page's tokens from its first to start + len - 1 (a page's tokens
+ * before start are read again; the values that codes stand for are fp32
+ * products code * scale, and a bound is rounded once, to nearest).
+ *   k_cache, k_scale, page_table   a layer's keys, as above
+ *   start, len    [R]  int32
+ *   k_min, k_max  as above, 16-byte aligned; pages that hold none of the tokens
+ *                 keep theirs
+ * A NaN among the values makes that dimension's bounds NaN.  A request with
+ * start < 0, len outside [0, max_len] or start + len past the page table is a
+ * data fault and writes nothing; a token in a bad page is one, and its page is
+ * passed over.  Two requests may name the same page where both fill it alike.
+ * Workspace: spec_cache_workspace_bytes.  Sizes: 0 <= R <= 65535,
+ * max_len >= 0, Hkv * (pages of max_len tokens) < 2^24 - 1.
+ */
+int spec_page_bounds(const void *k_cache, int cache_dtype, const float *k_scale, int num_pages,
+                     int page_size, const int32_t *page_table, int max_pages, const int32_t *start,
+                     const int32_t *len, int R, int max_len, int Hkv, int D, void *k_min,
+                     void *k_max, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of spec_page_select (0 for sizes it does not accept). */
+size_t spec_page_select_workspace_bytes(int R, int Hkv, int D, int max_pages);
+
+/*
+ * Page lists.  Of request r's F = ctx_len[r] / page_size full context pages, key
+ * head g lists T = min(budget, F): the first `first`, the last `last`, and of
+ * the others those with the largest
+ *   score = sum_d U_d k_max_d + N_d k_min_d,
+ *   U_d = sum of max(q_d, 0), N_d = sum of min(q_d, 0), over the rows of nodes
+ *         v < n_nodes[r] and the group's Hq / Hkv query heads,
+ * an upper bound of the sum of q . k over these rows for any key k of the page
+ * (sums in 64 bits; a NaN score stands with +infinity; equal scores: the lower
+ * page first).  The list holds page numbers (page_table entries) in the order
+ * of the context, then the pages of tokens F * page_size .. ctx_len + n_nodes - 1.
+ *   q          [R][M][Hq][D]  SPEC_BF16
+ *   k_min, k_max  as above (of full pages)
+ *   ctx_len, n_nodes  [R]     int32
+ *   out_lists  [R][Hkv][list_pages]  int32 page numbers, -1 padded
+ *   out_len    [R]            int32 context tokens listed: T * page_size + ctx_len %
+ *                             page_size, node v being token out_len + v of the list;
+ *                             0 and empty lists for an idle slot (n_nodes 0)
+ * A faulty request, or one with a bad page among its tokens' pages, gets
+ * lists of -1 and out_len -1 (which spec_page_attention marks in turn).
+ * Sizes: 0 <= R <= 65535, 1 <= M <= SPEC_TREE_MAX_NODES, Hq / Hkv <= 64,
+ * Hkv <= 65535; first + last <= budget, and
+ * list_pages >= min(budget, max_pages) + (M + page_size - 2) / page_size + 1
+ * (SPEC_EINVAL otherwise).
+ */
+int spec_page_select(const void *q, int q_dtype, const void *k_min, const void *k_max,
+                     int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                     const int32_t *ctx_len, const int32_t *n_nodes, int budget, int first,
+                     int last, int R, int M, int Hq, int Hkv, int D, int32_t *out_lists,
+                     int list_pages, int32_t *out_len, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/*
+ * spec_tree_attention where every key head has pages of its own: for query
+ * head h of request r, token t lies in page
+ * page_lists[r][h / (Hq / Hkv)][t / page_size]; tokens t < list_len[r] are
+ * seen by every node, and node u's token is list_len[r] + u.  Without a window;
+ * everything else (masks, scale, rounding, empty rows, faults, outputs, sizes
+ * with list_pages for max_pages) is as there, the workspace that of
+ * spec_tree_attention_workspace_bytes.
+ *   page_lists  [R][Hkv][list_pages]  int32 as spec_page_select writes them
+ *   list_len    [R]                   int32 as its out_len
+ */
+int spec_page_attention(const void *q, int q_dtype, const void *k_cache, const void *v_cache,
+                        int cache_dtype, const float *k_scale, const float *v_scale,
+                        int num_pages, int page_size, const int32_t *page_lists, int list_pages,
+                        const int32_t *list_len, const int32_t *n_nodes, const uint32_t *mask,
+                        float scale, int R, int M, int Hq, int Hkv, int D, void *out,
+                        float *out_lse, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, copies the workspace's device status word (the OR
  * of SPEC_DEV_* bits raised since the last clear) to *host_bits, and clears
  * it when `clear` is nonzero. */

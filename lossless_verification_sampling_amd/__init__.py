@@ -70,6 +70,10 @@ EXPORTED = (
     "spec_kv_commit",
     "spec_tree_attention_workspace_bytes",
     "spec_tree_attention",
+    "spec_page_bounds",
+    "spec_page_select_workspace_bytes",
+    "spec_page_select",
+    "spec_page_attention",
     "spec_get_device_status",
     "spec_time_stats_launch",
 )
@@ -146,6 +150,16 @@ def _load() -> ctypes.CDLL:
     lib.spec_tree_attention.restype = i
     lib.spec_tree_attention.argtypes = [p, i, p, p, i, p, p, i, i, p, i, p, p, p, p, f, i, i, i, i,
                                         i, i, p, p, p, sz, p]
+    lib.spec_page_bounds.restype = i
+    lib.spec_page_bounds.argtypes = [p, i, p, i, i, p, i, p, p, i, i, i, i, p, p, p, sz, p]
+    lib.spec_page_select_workspace_bytes.restype = sz
+    lib.spec_page_select_workspace_bytes.argtypes = [i, i, i, i]
+    lib.spec_page_select.restype = i
+    lib.spec_page_select.argtypes = [p, i, p, p, i, i, p, i, p, p, i, i, i, i, i, i, i, i, p, i, p,
+                                     p, sz, p]
+    lib.spec_page_attention.restype = i
+    lib.spec_page_attention.argtypes = [p, i, p, p, i, p, p, i, i, p, i, p, p, p, f, i, i, i, i, i,
+                                        p, p, p, sz, p]
     lib.spec_get_device_status.restype = i
     lib.spec_get_device_status.argtypes = [p, ctypes.POINTER(ctypes.c_uint32), i, p]
     return lib
@@ -214,6 +228,10 @@ def spec_cache_workspace_bytes() -> int:
 
 def spec_tree_attention_workspace_bytes(R: int, M: int, Hq: int, Hkv: int, D: int) -> int:
     return int(_lib.spec_tree_attention_workspace_bytes(R, M, Hq, Hkv, D))
+
+
+def spec_page_select_workspace_bytes(R: int, Hkv: int, D: int, max_pages: int) -> int:
+    return int(_lib.spec_page_select_workspace_bytes(R, Hkv, D, max_pages))
 
 
 # ---------------------------------------------------------------------------
@@ -705,17 +723,22 @@ def _all(dev: int, *specs):
 _CACHE_CODES = {torch.bfloat16: SPEC_BF16, torch.float8_e4m3fn: SPEC_E4M3}
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev):
+def _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev, lists=False):
     """Checks a layer's pages on device `dev` and returns (dtype code, P, Hkv,
-    page size, D, page table width)."""
+    page size, D, page table width).  lists: the table has a row per key head."""
     dtype = k_cache.dtype
     code = _CACHE_CODES.get(dtype)
     if code is None:
         raise TypeError(f"cache pages must be bfloat16 or float8_e4m3fn, got {dtype}")
     shape = k_cache.shape
     _need(len(shape) == 4, "k_cache must be [pages, heads, page size, D]")
-    _need(page_table.dim() == 2, "page_table must be [R, max_pages]")
-    wide = page_table.shape[1]
+    if lists:
+        _need(page_table.dim() == 3, "page_lists must be [R, heads, list_pages]")
+        name, rows = "page_lists", (R, shape[1])
+    else:
+        _need(page_table.dim() == 2, "page_table must be [R, max_pages]")
+        name, rows = "page_table", (R,)
+    wide = page_table.shape[-1]
     if code == SPEC_E4M3:
         _need(k_scale is not None and v_scale is not None, "e4m3 pages need k_scale and v_scale")
     else:
@@ -723,7 +746,7 @@ def _cache(k_cache, v_cache, k_scale, v_scale, page_table, R, dev):
     _all(dev, (k_cache, "k_cache", dtype, shape), (v_cache, "v_cache", dtype, shape),
          (k_scale, "k_scale", torch.float32, shape[:3]),
          (v_scale, "v_scale", torch.float32, shape[:3]),
-         (page_table, "page_table", torch.int32, (R, wide)))
+         (page_table, name, torch.int32, rows + (wide,)))
     P, Hkv, size, D = shape
     return code, P, Hkv, size, D, wide
 
@@ -953,4 +976,118 @@ def spec_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
               M, Hq, Hkv, D, out.data_ptr(), _raw(out_lse), buf, room, queue)
     if st:
         _raise(st, "spec_tree_attention")
+    return out, out_lse
+
+
+# ---------------------------------------------------------------------------
+# drafting over a budget of the cache's pages
+# ---------------------------------------------------------------------------
+
+def spec_page_bounds(k_cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
+                     length: torch.Tensor, max_len: int, k_min: torch.Tensor,
+                     k_max: torch.Tensor, *, k_scale: Optional[torch.Tensor] = None,
+                     workspace: Optional[Workspace] = None, stream=None) -> None:
+    """Least and largest key values, k_min and k_max [pages, Hkv, D] bfloat16,
+    of the pages that hold tokens start[r] .. start[r] + length[r] - 1
+    (length[r] <= max_len), over each page's tokens up to the last of them."""
+    R, dev = page_table.shape[0], _device(k_cache, "k_cache")
+    code, P, Hkv, size, D, wide = _cache(k_cache, k_cache, k_scale, k_scale, page_table, R, dev)
+    bounds = (P, Hkv, D)
+    _all(dev, (start, "start", torch.int32, (R,)), (length, "length", torch.int32, (R,)),
+         (k_min, "k_min", torch.bfloat16, bounds), (k_max, "k_max", torch.bfloat16, bounds))
+    buf, room, queue = _cache_buf(workspace, dev, 256, stream)
+    st = _run(dev, _lib.spec_page_bounds, k_cache.data_ptr(), code, _raw(k_scale), P, size,
+              page_table.data_ptr(), wide, start.data_ptr(), length.data_ptr(), R,
+              _c_int(max_len, "max_len"), Hkv, D, k_min.data_ptr(), k_max.data_ptr(), buf, room,
+              queue)
+    if st:
+        _raise(st, "spec_page_bounds")
+
+
+def spec_page_select(q: torch.Tensor, k_min: torch.Tensor, k_max: torch.Tensor,
+                     page_table: torch.Tensor, ctx_len: torch.Tensor, n_nodes: torch.Tensor,
+                     budget: int, page_size: int, *, first: int = 0, last: int = 0,
+                     out_lists: Optional[torch.Tensor] = None,
+                     out_len: Optional[torch.Tensor] = None,
+                     workspace: Optional[Workspace] = None, stream=None):
+    """Page lists of a step's queries q [R, M, Hq, D] bfloat16: for every key
+    head the `budget` full context pages (the first `first` and the last `last`
+    among them) with the best bounds, then the pages of the context's end and
+    of the nodes.  Returns (lists [R, Hkv, list_pages] int32, listed context
+    tokens [R] int32) for spec_page_attention."""
+    shape = q.shape
+    _need(len(shape) == 4, "q must be [R, M, Hq, D]")
+    R, M, Hq, D = shape
+    dev = _device(q, "q")
+    _need(k_min.dim() == 3 and k_min.shape[2] == D, "k_min must be [pages, heads, D] with q's D")
+    bounds = k_min.shape
+    P, Hkv = bounds[0], bounds[1]
+    _need(page_table.dim() == 2, "page_table must be [R, max_pages]")
+    wide, i32 = page_table.shape[1], torch.int32
+    budget, page_size = _c_int(budget, "budget"), _c_int(page_size, "page_size")
+    _need(budget >= 0 and page_size > 0, "budget must not be negative, page_size positive")
+    if out_lists is None:
+        out_lists = _empty((R, Hkv, min(budget, wide) + (M + page_size - 2) // page_size + 1), i32,
+                           q.device, stream)
+    if out_len is None:
+        out_len = _empty((R,), i32, q.device, stream)
+    _need(out_lists.dim() == 3, "out_lists must be [R, heads, list_pages]")
+    width = out_lists.shape[2]
+    _all(dev, (q, "q", torch.bfloat16, shape), (k_min, "k_min", torch.bfloat16, bounds),
+         (k_max, "k_max", torch.bfloat16, bounds), (page_table, "page_table", i32, (R, wide)),
+         (ctx_len, "ctx_len", i32, (R,)), (n_nodes, "n_nodes", i32, (R,)),
+         (out_lists, "out_lists", i32, (R, Hkv, width)), (out_len, "out_len", i32, (R,)))
+    need = spec_page_select_workspace_bytes(R, Hkv, D, wide)
+    if need == 0:
+        raise SpecError(-5, "spec_page_select_workspace_bytes")
+    buf, room, queue = _cache_buf(workspace, dev, need, stream)
+    st = _run(dev, _lib.spec_page_select, q.data_ptr(), SPEC_BF16, k_min.data_ptr(),
+              k_max.data_ptr(), P, page_size, page_table.data_ptr(), wide, ctx_len.data_ptr(),
+              n_nodes.data_ptr(), budget, _c_int(first, "first"), _c_int(last, "last"), R, M, Hq,
+              Hkv, D, out_lists.data_ptr(), width, out_len.data_ptr(), buf, room, queue)
+    if st:
+        _raise(st, "spec_page_select")
+    return out_lists, out_len
+
+
+def spec_page_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        page_lists: torch.Tensor, list_len: torch.Tensor, n_nodes: torch.Tensor, *,
+                        mask: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                        k_scale: Optional[torch.Tensor] = None,
+                        v_scale: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None, want_lse: bool = False,
+                        out_lse: Optional[torch.Tensor] = None,
+                        workspace: Optional[Workspace] = None, stream=None):
+    """spec_tree_attention over page lists of each key head's own (page_lists
+    [R, Hkv, list_pages], list_len [R] int32, as spec_page_select writes them):
+    q [R, M, Hq, D] bfloat16 sees the list_len[r] listed context tokens and, by
+    `mask` (spec_tree_mask; without one the tokens are a chain), its
+    ancestors.  Returns (out [R, M, Hq, D] bfloat16, log-sum-exp [R, M, Hq]
+    float32 or None)."""
+    shape = q.shape
+    _need(len(shape) == 4, "q must be [R, M, Hq, D]")
+    R, M, Hq, D = shape
+    dev = _device(q, "q")
+    code, P, Hkv, size, Dc, wide = _cache(k_cache, v_cache, k_scale, v_scale, page_lists, R, dev,
+                                          lists=True)
+    _need(Dc == D, "q and the cache differ in D")
+    if out is None:
+        out = _empty(shape, torch.bfloat16, q.device, stream)
+    if out_lse is None and want_lse:
+        out_lse = _empty(shape[:3], torch.float32, q.device, stream)
+    i32 = torch.int32
+    _all(dev, (q, "q", torch.bfloat16, shape), (list_len, "list_len", i32, (R,)),
+         (n_nodes, "n_nodes", i32, (R,)), (mask, "mask", i32, (R, M, (M + 31) // 32)),
+         (out, "out", torch.bfloat16, shape), (out_lse, "out_lse", torch.float32, shape[:3]))
+    need = _attention_bytes(R, M, Hq, Hkv, D)
+    if need == 0:
+        raise SpecError(-5, "spec_tree_attention_workspace_bytes")
+    buf, room, queue = _cache_buf(workspace, dev, need, stream)
+    st = _run(dev, _lib.spec_page_attention, q.data_ptr(), SPEC_BF16, k_cache.data_ptr(),
+              v_cache.data_ptr(), code, _raw(k_scale), _raw(v_scale), P, size,
+              page_lists.data_ptr(), wide, list_len.data_ptr(), n_nodes.data_ptr(), _raw(mask),
+              D ** -0.5 if scale is None else scale, R, M, Hq, Hkv, D, out.data_ptr(),
+              _raw(out_lse), buf, room, queue)
+    if st:
+        _raise(st, "spec_page_attention")
     return out, out_lse

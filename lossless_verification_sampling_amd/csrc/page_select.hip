@@ -1,0 +1,606 @@
+// page_select.hip -- key bounds of cache pages and the choice of pages that a
+// drafting step attends to, on gfx950.
+//
+// lo_d and hi_d are the least and the largest value of key dimension d in a
+// page of one key head.  For any query q and key k of the page q . k is at
+// most sum_d max(q_d lo_d, q_d hi_d), and summed over the query rows that share
+// the key head (nodes, and heads of the group) that is
+//   score = sum_d U_d hi_d + N_d lo_d,  U = sum of max(q, 0), N of min(q, 0):
+// two products a dimension whatever the number of rows.  Sums are in 64 bits:
+// the products of bf16 values with U and N are close to exact there, so that
+// which pages are chosen does not hang on the order of the sums.
+#include "cache.h"
+
+namespace sv {
+
+// ---------------------------------------------------------------------------
+// bounds
+// ---------------------------------------------------------------------------
+
+struct BoundsArgs {
+    Pages c;                     // (k only)
+    const int32_t *start, *len;  // [R]
+    int max_len;
+    uint16_t *lo, *hi;           // [num_pages][heads][D] bf16
+    Control *ctl;
+};
+
+// Least and largest of three, NaN if one is (v_minimum3, v_maximum3).
+__device__ __forceinline__ float least(float a, float b) { return __builtin_elementwise_minimum(a, b); }
+__device__ __forceinline__ float most(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+template <bool FP8> struct KeyVec;  // 16 bytes of one token's key
+template <> struct KeyVec<false> {
+    static constexpr int N = 8;
+    __device__ __forceinline__ static void run(u32x4_t w, float, float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = bf16_lo(w[i]);
+            x[2 * i + 1] = bf16_hi(w[i]);
+        }
+    }
+};
+template <> struct KeyVec<true> {
+    static constexpr int N = 16;
+    __device__ __forceinline__ static void run(u32x4_t w, float scale, float (&x)[16]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
+            const auto b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+            x[4 * i] = a[0] * scale;
+            x[4 * i + 1] = a[1] * scale;
+            x[4 * i + 2] = b[0] * scale;
+            x[4 * i + 3] = b[1] * scale;
+        }
+    }
+};
+
+// One wave per page and head (SPLIT: the four waves of a workgroup divide the
+// page's tokens).  A token's row is D EB / 16 lanes of 16 bytes; a lane keeps the
+// bounds of its dimensions over the tokens it meets, four loads at a time, and the lanes
+// that hold the same dimensions are joined at the end.  Tokens behind the
+// last one stand for it.  Bound by HBM.
+constexpr int kBoundLoads = 4;
+
+template <bool FP8, int D, bool SPLIT>
+__global__ void __launch_bounds__(kBlock) bounds_kernel(BoundsArgs a) {
+    typedef KeyVec<FP8> V;
+    constexpr int N = V::N, LPR = D / N, TPL = 64 / LPR;  // lanes a row, tokens a load
+    __shared__ float join_s[SPLIT ? kWaves : 1][2][SPLIT ? D : 1];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = blockIdx.y;
+    const int start = a.start[r], len = a.len[r];
+    const int64_t unit = SPLIT ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kWaves + wave;
+    if (len < 0 || len > a.max_len || !in_table(start, len, a.c.max_pages, a.c.shift)) {
+        if (tid == 0 && blockIdx.x == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+        return;
+    }
+    if (len == 0) return;
+    const int index = (start >> a.c.shift) + (int)(unit / a.c.heads), h = (int)(unit % a.c.heads);
+    if (index > (start + len - 1) >> a.c.shift) return;
+    const int page = a.c.table[(int64_t)r * a.c.max_pages + index];
+    if ((unsigned)page >= (unsigned)a.c.num_pages) {
+        if (lane == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+        return;
+    }
+    const int last = min(start + len - 1 - (index << a.c.shift), a.c.size - 1);  // in the page
+    const int64_t row = ((int64_t)page * a.c.heads + h) * a.c.size;
+    const int sub = lane % LPR, grp = lane / LPR;
+    const char *k = (const char *)a.c.k + (row * D) * (FP8 ? 1 : 2) + sub * 16;
+    float lo[N], hi[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        lo[i] = INFINITY;
+        hi[i] = -INFINITY;
+    }
+    for (int t = (SPLIT ? wave * TPL * kBoundLoads : 0); t <= last; t += (SPLIT ? kWaves : 1) * TPL * kBoundLoads) {
+        u32x4_t w[kBoundLoads];
+        float sc[kBoundLoads];
+#pragma unroll
+        for (int i = 0; i < kBoundLoads; ++i) {
+            const int tok = min(t + i * TPL + grp, last);
+            w[i] = *(const u32x4_t *)(k + tok * (D * (FP8 ? 1 : 2)));
+            sc[i] = FP8 ? a.c.k_scale[row + tok] : 1.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kBoundLoads; ++i) {
+            float x[N];
+            V::run(w[i], sc[i], x);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                lo[j] = least(lo[j], x[j]);
+                hi[j] = most(hi[j], x[j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int o = LPR; o < 64; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            lo[j] = least(lo[j], __shfl_xor(lo[j], o, 64));
+            hi[j] = most(hi[j], __shfl_xor(hi[j], o, 64));
+        }
+    if constexpr (SPLIT) {
+        if (grp == 0) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                join_s[wave][0][sub * N + j] = lo[j];
+                join_s[wave][1][sub * N + j] = hi[j];
+            }
+        }
+        __syncthreads();
+        if (wave) return;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) {
+                lo[j] = least(lo[j], join_s[w][0][sub * N + j]);
+                hi[j] = most(hi[j], join_s[w][1][sub * N + j]);
+            }
+    }
+    // group 0 stores the least values, group 1 the largest
+    if (grp > 1) return;
+    uint16_t *out = (grp ? a.hi : a.lo) + ((int64_t)page * a.c.heads + h) * D + sub * N;
+#pragma unroll
+    for (int j = 0; j < N; j += 8) {
+        u32x4_t w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = grp ? pack_bf16(hi[j + 2 * i], hi[j + 2 * i + 1]) : pack_bf16(lo[j + 2 * i], lo[j + 2 * i + 1]);
+        *(u32x4_t *)(out + j) = w;
+    }
+}
+
+// A workgroup's waves divide a page where it holds more than two rounds of one
+// wave's loads.
+template <bool FP8, int D>
+static void launch_bounds(const BoundsArgs &a, int64_t units, int R, hipStream_t st) {
+    constexpr int round = 64 / (D / KeyVec<FP8>::N) * kBoundLoads;
+    if (a.c.size > 2 * round)
+        hipLaunchKernelGGL((bounds_kernel<FP8, D, true>), dim3((unsigned)units, (unsigned)R), dim3(kBlock), 0, st, a);
+    else
+        hipLaunchKernelGGL((bounds_kernel<FP8, D, false>), dim3((unsigned)((units + kWaves - 1) / kWaves), (unsigned)R),
+                           dim3(kBlock), 0, st, a);
+}
+template <bool FP8>
+static void launch_bounds(const BoundsArgs &a, int D, int64_t units, int R, hipStream_t st) {
+    if (D == 64) launch_bounds<FP8, 64>(a, units, R, st);
+    else if (D == 128) launch_bounds<FP8, 128>(a, units, R, st);
+    else launch_bounds<FP8, 256>(a, units, R, st);
+}
+
+// ---------------------------------------------------------------------------
+// selection
+// ---------------------------------------------------------------------------
+
+struct SelectArgs {
+    const uint16_t *q;           // [R][M][Hq][D] bf16
+    const uint16_t *lo, *hi;     // [num_pages][heads][D] bf16
+    const int32_t *table;        // [R][max_pages]
+    const int32_t *ctx_len, *n_nodes;
+    int num_pages, max_pages, heads, shift;
+    int M, Hq, G, D;
+    int budget, first, last;
+    int32_t *lists, *list_len;   // [R][heads][width], [R]
+    int width;
+    double *sums;                // [R][heads][2][D] U and N, null: made where they are used
+    uint64_t *keys;              // [R][heads][max_pages] ordered scores
+    Control *ctl;
+};
+
+struct Context {
+    int n, ctx, full, take;      // full pages of context, of which `take` are listed
+    bool ok;
+};
+__device__ __forceinline__ Context context_of(const SelectArgs &a, int r) {
+    Context c;
+    c.n = a.n_nodes[r];
+    c.ctx = a.ctx_len[r];
+    c.ok = c.n >= 0 && c.n <= a.M && in_table(c.ctx, c.n, a.max_pages, a.shift);
+    c.full = c.ok && c.n ? c.ctx >> a.shift : 0;
+    c.take = min(c.full, a.budget);
+    return c;
+}
+
+// Adds a row's 8 values to its sums of positive and of negative parts (a NaN
+// goes to both).
+__device__ __forceinline__ void add_row(const uint16_t *row, double (&up)[8], double (&dn)[8]) {
+    const u32x4_t w = *(const u32x4_t *)row;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+        up[i] += (double)most(x, 0.f);
+        dn[i] += (double)least(x, 0.f);
+    }
+}
+__device__ __forceinline__ const uint16_t *query_row(const SelectArgs &a, int r, int h, int i) {
+    const int node = i / a.G;
+    return a.q + (((int64_t)r * a.M + node) * a.Hq + h * a.G + (i - node * a.G)) * a.D;
+}
+
+// U and N of one request and key head, where their rows are too many for every
+// workgroup of the score launch to read them.
+template <int D>
+__global__ void __launch_bounds__(kBlock) query_sums_kernel(SelectArgs a) {
+    constexpr int LPR = D / 8, GRP = kBlock / LPR;
+    __shared__ double part[GRP][2][D];
+    const int tid = threadIdx.x, sub = tid % LPR, grp = tid / LPR, h = blockIdx.x, r = blockIdx.y;
+    const Context c = context_of(a, r);
+    if (c.full <= a.budget) return;
+    double up[8], dn[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) up[i] = dn[i] = 0.0;
+    for (int i = grp; i < c.n * a.G; i += GRP) add_row(query_row(a, r, h, i) + sub * 8, up, dn);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        part[grp][0][sub * 8 + i] = up[i];
+        part[grp][1][sub * 8 + i] = dn[i];
+    }
+    __syncthreads();
+    for (int d = tid; d < 2 * D; d += kBlock) {
+        double s = 0.0;
+        for (int g = 0; g < GRP; ++g) s += part[g][d / D][d % D];
+        a.sums[((int64_t)r * a.heads + h) * 2 * D + d] = s;
+    }
+}
+
+// Sum over the LPR lanes of a row, the same in each of them.
+template <int LPR>
+__device__ __forceinline__ double row_sum(double v) {
+    v += dpp_d<kDppSwap1>(v);
+    v += dpp_d<kDppSwap2>(v);
+    v += dpp_d<kDppHalfMirror>(v);
+    if constexpr (LPR >= 16) v += dpp_d<kDppMirror>(v);
+    if constexpr (LPR >= 32) {
+        const long long b = __double_as_longlong(v);
+        uint32_t l0, l1, h0, h1;
+        lane_pair<16>((uint32_t)(b & 0xffffffffLL), l0, l1);
+        lane_pair<16>((uint32_t)(b >> 32), h0, h1);
+        v = __longlong_as_double((long long)((uint64_t)h0 << 32 | l0)) +
+            __longlong_as_double((long long)((uint64_t)h1 << 32 | l1));
+    }
+    return v;
+}
+
+// A score as a whole number in the same order; NaN stands with +infinity, for
+// a page that could hold anything.
+__device__ __forceinline__ uint64_t key_of(double s) {
+    s = s != s ? (double)INFINITY : s + 0.0;  // (-0 becomes 0)
+    const uint64_t b = (uint64_t)__double_as_longlong(s);
+    return b >> 63 ? ~b : b | 1ull << 63;
+}
+
+// Scores of 64 of a request's full pages for one key head, 16 a wave: D / 8
+// lanes of 8 dimensions a page, 64-bit products and sums.  Bound by HBM, as
+// half the time goes to 64-bit arithmetic beside it.
+constexpr int kScorePages = 16;     // pages a wave
+constexpr int kDirectRows = 16;     // query rows that every wave sums up by itself
+
+template <int D>
+__global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
+    constexpr int LPR = D / 8, PPL = 64 / LPR, IT = kScorePages / PPL;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int sub = lane % LPR, grp = lane / LPR, h = blockIdx.y, r = blockIdx.z;
+    const Context c = context_of(a, r);
+    const int p0 = (blockIdx.x * kWaves + wave) * kScorePages;
+    if (c.full <= a.budget || p0 >= c.full) return;
+    u32x4_t lo[IT], hi[IT];
+    bool ok[IT];
+#pragma unroll
+    for (int t = 0; t < IT; ++t) {
+        const int p = p0 + t * PPL + grp;
+        int page = p < c.full ? a.table[(int64_t)r * a.max_pages + p] : -1;
+        ok[t] = (unsigned)page < (unsigned)a.num_pages;
+        if (!ok[t]) page = 0;
+        const int64_t at = ((int64_t)page * a.heads + h) * D + sub * 8;
+        lo[t] = *(const u32x4_t *)(a.lo + at);
+        hi[t] = *(const u32x4_t *)(a.hi + at);
+    }
+    double up[8], dn[8];
+    if (a.sums) {
+        const double *s = a.sums + ((int64_t)r * a.heads + h) * 2 * D + sub * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            up[i] = s[i];
+            dn[i] = s[D + i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) up[i] = dn[i] = 0.0;
+        for (int i = 0; i < c.n * a.G; ++i) add_row(query_row(a, r, h, i) + sub * 8, up, dn);
+    }
+    uint64_t *keys = a.keys + ((int64_t)r * a.heads + h) * a.max_pages;
+#pragma unroll
+    for (int t = 0; t < IT; ++t) {
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = i & 1 ? bf16_hi(hi[t][i >> 1]) : bf16_lo(hi[t][i >> 1]);
+            const float y = i & 1 ? bf16_hi(lo[t][i >> 1]) : bf16_lo(lo[t][i >> 1]);
+            s = fma(up[i], (double)x, s);
+            s = fma(dn[i], (double)y, s);
+        }
+        s = row_sum<LPR>(s);
+        const int p = p0 + t * PPL + grp;
+        if (sub == 0 && p < c.full) keys[p] = ok[t] ? key_of(s) : 0ull;
+    }
+}
+
+// Sum over the workgroup and prefix before this thread, of two counts in one
+// word's halves (each total below 2^32).
+__device__ __forceinline__ uint64_t block_prefix(uint64_t v, uint64_t (&wave_s)[kWaves], uint64_t &total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t lo = wave_incl_scan_dpp((uint32_t)v), hi = wave_incl_scan_dpp((uint32_t)(v >> 32));
+    const uint64_t inc = (uint64_t)hi << 32 | lo;
+    __syncthreads();
+    if (lane == 63) wave_s[wave] = inc;
+    __syncthreads();
+    uint64_t before = inc - v;
+    total = 0;
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) before += wave_s[w];
+        total += wave_s[w];
+    }
+    return before;
+}
+
+// The best pages of one request and key head, and its list.  The cut is found
+// by counts over 2048 equal parts of the keys' range, the part that holds it
+// being cut again until it is taken whole or is one key (then the lowest
+// pages that have it are taken).  Keys of up to kHeldKeys pages stay in
+// shared memory.  Bound by latency: a handful of dependent passes over a few
+// keys a thread.
+constexpr int kHeldKeys = 4096;
+constexpr int kParts = 2048;
+
+__global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
+    __shared__ uint64_t held[kHeldKeys];
+    __shared__ uint32_t count_s[kParts];
+    __shared__ uint64_t wave_s[kWaves], cut_s[2], ends_s[2][kWaves];
+    const int tid = threadIdx.x, h = blockIdx.x, r = blockIdx.y;
+    const Context c = context_of(a, r);
+    const int32_t *table = a.table + (int64_t)r * a.max_pages;
+    int32_t *list = a.lists + ((int64_t)r * a.heads + h) * a.width;
+    // pages of the request's tokens, the nodes' among them
+    const int pages = c.ok && c.n ? (int)(((int64_t)c.ctx + c.n - 1) >> a.shift) + 1 : 0;
+    bool ok = c.ok;
+    for (int p = tid; p < pages; p += kBlock) ok = ok && (unsigned)table[p] < (unsigned)a.num_pages;
+    ok = __syncthreads_and(ok);
+    if (!ok) {
+        for (int i = tid; i < a.width; i += kBlock) list[i] = -1;
+        if (tid == 0 && h == 0) {
+            a.list_len[r] = -1;
+            atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
+        }
+        return;
+    }
+    // ---- the cut: keys above `cut` are taken, and the first `ties` that equal it
+    const int from = a.first, to = c.full - a.last;  // pages that compete
+    uint64_t cut = 0;
+    uint32_t ties = 0xffffffffu;
+    const uint64_t *keys = a.keys + ((int64_t)r * a.heads + h) * a.max_pages;
+    const bool choose = c.full > a.budget;
+    const bool in_lds = c.full <= kHeldKeys;
+    auto key = [&](int p) -> uint64_t { return in_lds ? held[p] : keys[p]; };
+    if (choose) {
+        uint64_t lo = ~0ull, hi = 0ull;
+        for (int p = from + tid; p < to; p += kBlock) {
+            const uint64_t k = keys[p];
+            if (in_lds) held[p] = k;
+            lo = min(lo, k);
+            hi = max(hi, k);
+        }
+        for (int o = 32; o; o >>= 1) {
+            lo = min(lo, (uint64_t)__shfl_xor((unsigned long long)lo, o, 64));
+            hi = max(hi, (uint64_t)__shfl_xor((unsigned long long)hi, o, 64));
+        }
+        if ((tid & 63) == 0) {
+            ends_s[0][tid >> 6] = lo;
+            ends_s[1][tid >> 6] = hi;
+        }
+        __syncthreads();
+        for (int w = 0; w < kWaves; ++w) {
+            lo = min(lo, ends_s[0][w]);
+            hi = max(hi, ends_s[1][w]);
+        }
+        uint32_t want = (uint32_t)(a.budget - a.first - a.last);
+        if (want == 0) {
+            cut = ~0ull;  // above every key: +infinity's is below
+        } else {
+            while (true) {
+                const int shift = hi == lo ? 0 : max(0, 53 - __clzll((long long)(hi - lo)));
+                for (int i = tid; i < kParts; i += kBlock) count_s[i] = 0u;
+                __syncthreads();
+                for (int p = from + tid; p < to; p += kBlock) {
+                    const uint64_t k = key(p);
+                    if (k >= lo && k <= hi) atomicAdd(&count_s[(k - lo) >> shift], 1u);
+                }
+                __syncthreads();
+                // thread tid sums its parts, the highest first
+                constexpr int EACH = kParts / kBlock;
+                uint32_t mine[EACH], sum = 0;
+#pragma unroll
+                for (int i = 0; i < EACH; ++i) {
+                    mine[i] = count_s[kParts - 1 - (tid * EACH + i)];
+                    sum += mine[i];
+                }
+                uint64_t total;
+                uint32_t before = (uint32_t)block_prefix(sum, wave_s, total);
+                if (before < want && before + sum >= want) {
+#pragma unroll
+                    for (int i = 0; i < EACH; ++i) {
+                        if (before < want && before + mine[i] >= want) {
+                            cut_s[0] = (uint64_t)(kParts - 1 - (tid * EACH + i));
+                            cut_s[1] = (uint64_t)mine[i] << 32 | (want - before);
+                        }
+                        before += mine[i];
+                    }
+                }
+                __syncthreads();
+                const uint64_t part = cut_s[0];
+                const uint32_t there = (uint32_t)(cut_s[1] >> 32);
+                want = (uint32_t)cut_s[1];
+                __syncthreads();
+                lo += part << shift;
+                hi = min(hi, lo + ((1ull << shift) - 1));
+                if (there == want) {  // every key of the part
+                    cut = lo - 1;     // (lo is above 0: no score's key is)
+                    ties = 0;
+                    break;
+                }
+                if (shift == 0) {
+                    cut = lo;
+                    ties = want;
+                    break;
+                }
+            }
+        }
+    }
+    // ---- the list, in the order of the context: a thread takes neighbouring pages
+    const int each = (c.full + kBlock - 1) / kBlock;
+    const int b = min(tid * each, c.full), e = min(b + each, c.full);
+    uint32_t above = 0, equal = 0;
+    for (int p = b; p < e; ++p) {
+        if (!choose || p < from || p >= to) {
+            ++above;
+        } else {
+            const uint64_t k = key(p);
+            above += k > cut;
+            equal += k == cut;
+        }
+    }
+    uint64_t total;
+    const uint64_t before = block_prefix((uint64_t)equal << 32 | above, wave_s, total);
+    uint32_t tie = (uint32_t)(before >> 32);
+    int at = (int)((uint32_t)before + min(tie, ties));
+    for (int p = b; p < e; ++p) {
+        bool in = true;
+        if (choose && p >= from && p < to) {
+            const uint64_t k = key(p);
+            in = k > cut || (k == cut && tie < ties);
+            tie += k == cut;
+        }
+        if (in && at < c.take) list[at++] = table[p];
+    }
+    const int tail = pages - c.full;
+    for (int i = c.take + tid; i < a.width; i += kBlock)
+        list[i] = i - c.take < tail ? table[c.full + i - c.take] : -1;
+    if (tid == 0 && h == 0) a.list_len[r] = c.n ? (c.take << a.shift) + (c.ctx & ((1 << a.shift) - 1)) : 0;
+}
+
+template <int D>
+static void launch_select(const SelectArgs &a, int R, hipStream_t st) {
+    if (a.sums)
+        hipLaunchKernelGGL((query_sums_kernel<D>), dim3((unsigned)a.heads, (unsigned)R), dim3(kBlock), 0, st, a);
+    if (a.max_pages > a.budget) {
+        const int per = kScorePages * kWaves;
+        hipLaunchKernelGGL((score_kernel<D>), dim3((unsigned)((a.max_pages + per - 1) / per), (unsigned)a.heads, (unsigned)R),
+                           dim3(kBlock), 0, st, a);
+    }
+    hipLaunchKernelGGL(select_kernel, dim3((unsigned)a.heads, (unsigned)R), dim3(kBlock), 0, st, a);
+}
+
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+int spec_page_bounds(const void *k_cache, int cache_dtype, const float *k_scale, int num_pages,
+                     int page_size, const int32_t *page_table, int max_pages, const int32_t *start,
+                     const int32_t *len, int R, int max_len, int Hkv, int D, void *k_min,
+                     void *k_max, void *workspace, size_t workspace_bytes, void *stream) {
+    if (R < 0 || max_len < 0) return SPEC_EINVAL;
+    const int bad = check_pages(k_cache, k_cache, cache_dtype, k_scale, k_scale, num_pages,
+                                page_size, max_pages, Hkv, D);
+    if (bad) return bad;
+    if (R > 65535) return SPEC_EUNSUPPORTED;
+    // pages that max_len tokens can lie in, whatever the first one's place is
+    int64_t units = max_len ? ((int64_t)max_len + page_size - 2) / page_size + 1 : 0;
+    if (units > max_pages) units = max_pages;
+    if (units > (int64_t)0x7fffffff / Hkv) return SPEC_EUNSUPPORTED;
+    units *= Hkv;
+    if (units >= kMaxBlocks) return SPEC_EUNSUPPORTED;
+    if (R == 0 || max_len == 0) return SPEC_OK;
+    if (!start || !len || !k_min || !k_max || (max_pages > 0 && !page_table)) return SPEC_EINVAL;
+    if (((uintptr_t)k_min | (uintptr_t)k_max) & 15u) return SPEC_EINVAL;
+    if (bad_workspace(workspace, workspace_bytes, sizeof(Control))) return SPEC_EWORKSPACE;
+    BoundsArgs a{};
+    a.c = make_pages(k_cache, nullptr, k_scale, nullptr, num_pages, page_size, page_table,
+                     max_pages, Hkv);
+    a.start = start;
+    a.len = len;
+    a.max_len = max_len;
+    a.lo = (uint16_t *)k_min;
+    a.hi = (uint16_t *)k_max;
+    a.ctl = (Control *)workspace;
+    if (units == 0) units = 1;  // (no table: every request with tokens is a faulty one)
+    if (cache_dtype == SPEC_E4M3) launch_bounds<true>(a, D, units, R, (hipStream_t)stream);
+    else launch_bounds<false>(a, D, units, R, (hipStream_t)stream);
+    return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
+}
+
+size_t spec_page_select_workspace_bytes(int R, int Hkv, int D, int max_pages) {
+    if (R < 0 || R > 65535 || Hkv < 1 || Hkv > 65535 || (D != 64 && D != 128 && D != 256) ||
+        max_pages < 0)
+        return 0;
+    return sizeof(Control) + (size_t)R * Hkv * ((size_t)max_pages + 2 * (size_t)D) * sizeof(double);
+}
+
+int spec_page_select(const void *q, int q_dtype, const void *k_min, const void *k_max,
+                     int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                     const int32_t *ctx_len, const int32_t *n_nodes, int budget, int first,
+                     int last, int R, int M, int Hq, int Hkv, int D, int32_t *out_lists,
+                     int list_pages, int32_t *out_len, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+    if (R < 0 || M < 1 || Hq < 1 || budget < 0 || first < 0 || last < 0 ||
+        (int64_t)first + last > budget)
+        return SPEC_EINVAL;
+    if (q_dtype != SPEC_BF16) return SPEC_EDTYPE;
+    const int bad = check_pages(k_min, k_max, SPEC_BF16, nullptr, nullptr, num_pages, page_size,
+                                max_pages, Hkv, D);
+    if (bad) return bad;
+    if (Hq % Hkv) return SPEC_EINVAL;
+    const size_t need = spec_page_select_workspace_bytes(R, Hkv, D, max_pages);
+    if (!need || M > SPEC_TREE_MAX_NODES || Hq / Hkv > 64) return SPEC_EUNSUPPORTED;
+    // the chosen pages, and those that hold the context's end and the nodes
+    if ((int64_t)list_pages < (int64_t)(budget < max_pages ? budget : max_pages) +
+                                  ((int64_t)M + page_size - 2) / page_size + 1)
+        return SPEC_EINVAL;
+    if (R == 0) return SPEC_OK;
+    if (!q || !ctx_len || !n_nodes || !out_lists || !out_len || (max_pages > 0 && !page_table))
+        return SPEC_EINVAL;
+    if ((uintptr_t)q & 15u) return SPEC_EINVAL;
+    if (bad_workspace(workspace, workspace_bytes, need)) return SPEC_EWORKSPACE;
+    SelectArgs a{};
+    a.q = (const uint16_t *)q;
+    a.lo = (const uint16_t *)k_min;
+    a.hi = (const uint16_t *)k_max;
+    a.table = page_table;
+    a.ctx_len = ctx_len;
+    a.n_nodes = n_nodes;
+    a.num_pages = num_pages;
+    a.max_pages = max_pages;
+    a.heads = Hkv;
+    a.shift = __builtin_ctz((unsigned)page_size);
+    a.M = M;
+    a.Hq = Hq;
+    a.G = Hq / Hkv;
+    a.D = D;
+    a.budget = budget;
+    a.first = first;
+    a.last = last;
+    a.lists = out_lists;
+    a.list_len = out_len;
+    a.width = list_pages;
+    a.ctl = (Control *)workspace;
+    a.keys = (uint64_t *)((char *)workspace + sizeof(Control));
+    if ((int64_t)M * a.G > kDirectRows && max_pages > budget)
+        a.sums = (double *)(a.keys + (size_t)R * Hkv * max_pages);
+    if (D == 64) launch_select<64>(a, R, (hipStream_t)stream);
+    else if (D == 128) launch_select<128>(a, R, (hipStream_t)stream);
+    else launch_select<256>(a, R, (hipStream_t)stream);
+    return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
+}
+
+}  // extern "C"

@@ -270,11 +270,18 @@ struct Half {
     int bad;                     // bit h: half h lies in a bad page
 };
 
+// The row of the page table that request r's key head h reads by: the
+// request's, or (LISTS) a page list of its own.  A template argument, so that
+// the launches over tables hold nothing of it: their scalar registers are short.
+template <bool LISTS>
+__device__ __forceinline__ int table_row(const AttnArgs &a, int r, int h) {
+    return LISTS ? r * a.c.heads + h : r;
+}
 // A page number, by a scalar load (the index is the wave's, and nothing in a
 // launch writes the table).
-__device__ __forceinline__ int page_number(const AttnArgs &a, int r, int index) {
+__device__ __forceinline__ int page_number(const AttnArgs &a, int row, int index) {
     typedef const __attribute__((address_space(4))) int32_t *table_t;
-    return ((table_t)(uintptr_t)(a.c.table + (int64_t)r * a.c.max_pages))[index];
+    return ((table_t)(uintptr_t)(a.c.table + (int64_t)row * a.c.max_pages))[index];
 }
 
 // The page numbers of a step's halves, one load ahead of their use: a wave
@@ -283,11 +290,11 @@ __device__ __forceinline__ int page_number(const AttnArgs &a, int r, int index) 
 struct Numbers {
     int page[2];
 };
-__device__ __forceinline__ Numbers numbers_of(const AttnArgs &a, int r, int t, int L) {
+__device__ __forceinline__ Numbers numbers_of(const AttnArgs &a, int row, int t, int L) {
     Numbers x;
     t = min(t, L - 1);                                  // a step behind the end is not used
-    x.page[0] = page_number(a, r, t >> a.c.shift);
-    x.page[1] = page_number(a, r, min(t + 16, L - 1) >> a.c.shift);
+    x.page[0] = page_number(a, row, t >> a.c.shift);
+    x.page[1] = page_number(a, row, min(t + 16, L - 1) >> a.c.shift);
     return x;
 }
 __device__ __forceinline__ Half halves_of(const AttnArgs &a, const Numbers &num, int h, int t, int L) {
@@ -546,7 +553,7 @@ __device__ __forceinline__ bool take_rare(float &sc, bool live) {
 }
 // Tokens [from, to) of the request, for the row whose sums acc holds.
 template <bool FP8, int D>
-__device__ __forceinline__ void add_rare(const AttnArgs &a, const Req &rq, int r, int h, int row,
+__device__ __forceinline__ void add_rare(const AttnArgs &a, const Req &rq, int r, int h, int trow, int row,
                                          int from, int to, int lane, f32x4_t (&acc)[D / 16]) {
     constexpr int DV = D / 16;
     const int g = here(lane) >> 4;
@@ -554,7 +561,7 @@ __device__ __forceinline__ void add_rare(const AttnArgs &a, const Req &rq, int r
     const uint32_t *mrow = a.mask ? a.mask + ((size_t)r * a.M + q.node) * a.W : nullptr;
 #pragma unroll 1
     for (int t = from; t < to; ++t) {
-        const int page = page_number(a, r, t >> a.c.shift), u = t - rq.ctx;
+        const int page = page_number(a, trow, t >> a.c.shift), u = t - rq.ctx;
         if ((unsigned)page >= (unsigned)a.c.num_pages) continue;
         const uint64_t tree = mrow && u >= 0 && u < rq.n ? mrow[u >> 5] >> (u & 31) & 1u : 0u;
         const bool see = sees(a, rq, t, q.node, q.pos, tree) & 1u;
@@ -610,7 +617,7 @@ template <int D, int RT> constexpr int waves_per_simd() {
     return D <= 128 && D * RT <= 256 ? 2 : 1;
 }
 
-template <bool FP8, int D, int RT>
+template <bool FP8, int D, int RT, bool LISTS>
 __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel(AttnArgs a) {
     typedef Tile<FP8, D> TT;
     constexpr int KS = TT::KS, DV = TT::DV, TR = 16 * RT;
@@ -637,6 +644,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
         const int units = tile_units<TR>(a, rq, t);
         const int u1 = min(units, u0 + left);
         const int t0 = rq.lo + u0 * kUnit, t1 = min(end, rq.lo + u1 * kUnit);
+        const int trow = table_row<LISTS>(a, r, h);
         const bool whole = u0 == 0 && u1 == units;
         // ---- the rows of this lane's column
         bf16x8_t qf[RT][KS];
@@ -668,8 +676,8 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
         // where the branch joins.)
         if (rq.ok && tok < t1) {
             TT kv;
-            Half cur = halves_of(a, numbers_of(a, r, tok, end), h, tok, end);
-            Numbers num = numbers_of(a, r, tok + kUnit, end);
+            Half cur = halves_of(a, numbers_of(a, trow, tok, end), h, tok, end);
+            Numbers num = numbers_of(a, trow, tok + kUnit, end);
             load_k<FP8, D>(a, cur, lane, kv);
             if constexpr (FP8) kv.sc = load_scale(a, cur, lane);
             load_v<FP8, D>(a, cur, lane, kv);
@@ -678,7 +686,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                 const bool more = nxt < t1;
                 Half nh = cur;
                 if (more) nh = halves_of(a, num, h, nxt, end);
-                num = numbers_of(a, r, nxt + kUnit, end);
+                num = numbers_of(a, trow, nxt + kUnit, end);
                 // ---- scores
                 f32x4_t s[RT][2];
 #pragma unroll
@@ -767,7 +775,7 @@ __global__ void __launch_bounds__(kBlock, (waves_per_simd<D, RT>())) attn_kernel
                 if (s >= plain.lo && s + kStep <= plain.hi) continue;
 #pragma unroll
                 for (int x = 0; x < RT; ++x)
-                    add_rare<FP8, D>(a, rq, r, h, t * TR + x * 16 + c, s, min(s + kStep, t1), lane, acc[x]);
+                    add_rare<FP8, D>(a, rq, r, h, trow, t * TR + x * 16 + c, s, min(s + kStep, t1), lane, acc[x]);
             }
         }
         if (bad && lane == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
@@ -889,8 +897,8 @@ template <bool FP8, int D, int TR> struct Shared {
 
 // The page number of this wave's 16 tokens of the tile at token t0; those
 // behind the end take the last token's page, and are not used.
-__device__ __forceinline__ int stage_page(const AttnArgs &a, int r, int t0, int end, int wave) {
-    return page_number(a, r, min(t0 + 16 * wave, end - 1) >> a.c.shift);
+__device__ __forceinline__ int stage_page(const AttnArgs &a, int row, int t0, int end, int wave) {
+    return page_number(a, row, min(t0 + 16 * wave, end - 1) >> a.c.shift);
 }
 
 // Loads this wave's 16 tokens of the tile at token t0 (rows [t0, end) exist).
@@ -996,7 +1004,7 @@ __device__ __forceinline__ void stage_store(const AttnArgs &a, SH &sh, int b, in
     if (lane == 0) sh.flags[b][wave] = flags;
 }
 
-template <bool FP8, int D, int RT>
+template <bool FP8, int D, int RT, bool LISTS>
 __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(AttnArgs a) {
     typedef Tile<FP8, D> TT;
     constexpr int KS = TT::KS, DV = TT::DV, TR = 64 * RT;
@@ -1020,6 +1028,7 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
         const int units = tile_units<TR>(a, rq, t);
         const int u1 = min(units, u0 + left);
         const int t0 = rq.lo + u0 * kUnit, t1 = min(end, rq.lo + u1 * kUnit);
+        const int trow = table_row<LISTS>(a, r, h);
         const bool whole = u0 == 0 && u1 == units;
         const int row0 = t * TR + wave * 16 * RT;  // the wave's rows
         bf16x8_t qf[RT][KS];
@@ -1060,8 +1069,8 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                 if (part && tid < TR)
                     sh.sight[buf][tid] = stage_sight<FP8, D>(a, rq, t_at, query_of(a, rq, r, t * TR + here(tid)), st);
             };
-            ask(stage_page(a, r, t0, end, wave), t0);
-            int page = stage_page(a, r, t0 + kTile, end, wave);
+            ask(stage_page(a, trow, t0, end, wave), t0);
+            int page = stage_page(a, trow, t0 + kTile, end, wave);
             __syncthreads();  // the last item's reads are done
             keep(0, t0);
             __syncthreads();
@@ -1070,7 +1079,7 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                 const bool more = tile + kTile < t1;
                 const bool part = tile < mid0 || tile >= mid1;
                 if (more) ask(page, tile + kTile);
-                page = stage_page(a, r, tile + 2 * kTile, end, wave);  // in time for the next load
+                page = stage_page(a, trow, tile + 2 * kTile, end, wave);  // in time for the next load
                 int flags[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) flags[i] = __builtin_amdgcn_readfirstlane(sh.flags[b][i]);
@@ -1155,7 +1164,7 @@ __global__ void __launch_bounds__(kBlock, D <= 128 ? 2 : 1) attn_wide_kernel(Att
                 if (s >= mid0 && s < mid1) continue;
 #pragma unroll
                 for (int x = 0; x < RT; ++x)
-                    add_rare<FP8, D>(a, rq, r, h, row0 + x * 16 + c, s, min(s + kTile, wend), lane, acc[x]);
+                    add_rare<FP8, D>(a, rq, r, h, trow, row0 + x * 16 + c, s, min(s + kTile, wend), lane, acc[x]);
             }
         }
         if (bad && lane == 0) atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
@@ -1407,14 +1416,14 @@ inline Shape shape_of(int64_t rows, int64_t heads, int D, bool fp8) {
     return s;
 }
 
-template <bool FP8, int D, int RT, bool WIDE>
+template <bool LISTS, bool FP8, int D, int RT, bool WIDE>
 static void launch_attn(const AttnArgs &a, hipStream_t st) {
     constexpr int TR = 16 * RT * (WIDE ? kWaves : 1);
     if constexpr (WIDE) {
-        hipLaunchKernelGGL((attn_wide_kernel<FP8, D, RT>), dim3(a.groups), dim3(kBlock), 0, st, a);
+        hipLaunchKernelGGL((attn_wide_kernel<FP8, D, RT, LISTS>), dim3(a.groups), dim3(kBlock), 0, st, a);
         hipLaunchKernelGGL((attn_wide_join_kernel<D, TR>), dim3(a.groups - 1, TR * D / 256 / kWaves), dim3(kBlock), 0, st, a);
     } else {
-        hipLaunchKernelGGL((attn_kernel<FP8, D, RT>), dim3(a.groups), dim3(kBlock), 0, st, a);
+        hipLaunchKernelGGL((attn_kernel<FP8, D, RT, LISTS>), dim3(a.groups), dim3(kBlock), 0, st, a);
         // items enough for every eighth range: eight parts an item at most, on
         // the average; fewer items: more parts than one wave reads at a time
         // (one user's 30 k tokens: 32.6 us with the parts divided, 36.0
@@ -1426,50 +1435,36 @@ static void launch_attn(const AttnArgs &a, hipStream_t st) {
             hipLaunchKernelGGL((attn_join_kernel<D, TR, true>), dim3(a.groups - 1, TR), dim3(kBlock), 0, st, a);
     }
 }
-template <bool FP8, int D>
+template <bool LISTS, bool FP8, int D>
 static void launch_attn(const AttnArgs &a, const Shape &s, hipStream_t st) {
     if (s.wide) {
-        if (s.RT == 1) launch_attn<FP8, D, 1, true>(a, st);
+        if (s.RT == 1) launch_attn<LISTS, FP8, D, 1, true>(a, st);
         else if constexpr (D <= 128) {
-            if (s.RT == 2) launch_attn<FP8, D, 2, true>(a, st);
-            else launch_attn<FP8, D, 3, true>(a, st);
+            if (s.RT == 2) launch_attn<LISTS, FP8, D, 2, true>(a, st);
+            else launch_attn<LISTS, FP8, D, 3, true>(a, st);
         }
     } else {
-        if (s.RT == 1) launch_attn<FP8, D, 1, false>(a, st);
-        else if constexpr (FP8 && D <= 128) launch_attn<FP8, D, 2, false>(a, st);
+        if (s.RT == 1) launch_attn<LISTS, FP8, D, 1, false>(a, st);
+        else if constexpr (FP8 && D <= 128) launch_attn<LISTS, FP8, D, 2, false>(a, st);
     }
 }
-template <bool FP8>
+template <bool LISTS, bool FP8>
 static void launch_attn(const AttnArgs &a, int D, const Shape &s, hipStream_t st) {
-    if (D == 64) launch_attn<FP8, 64>(a, s, st);
-    else if (D == 128) launch_attn<FP8, 128>(a, s, st);
-    else launch_attn<FP8, 256>(a, s, st);
+    if (D == 64) launch_attn<LISTS, FP8, 64>(a, s, st);
+    else if (D == 128) launch_attn<LISTS, FP8, 128>(a, s, st);
+    else launch_attn<LISTS, FP8, 256>(a, s, st);
 }
 
-}  // namespace sv
-
-using namespace sv;
-
-extern "C" {
-
-size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D) {
-    if (R < 0 || M < 1 || M > SPEC_TREE_MAX_NODES || Hkv < 1 || Hq < 1 || Hq % Hkv ||
-        Hq / Hkv > 64 || (D != 64 && D != 128 && D != 256))
-        return 0;
-    // the largest tiles that these sizes or smaller ones take
-    const int rows = M * (Hq / Hkv);
-    const size_t TR = rows <= 16 ? 16 : D == 256 || rows <= 64 ? 64 : 192;
-    const size_t groups = D <= 128 ? kMaxGroups : kMaxGroups / 2;
-    return sizeof(Control) + sizeof(Cut) * (kMaxGroups + 1) + 2 * groups * TR * (D + 2) * sizeof(float);
-}
-
-int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const void *v_cache,
-                        int cache_dtype, const float *k_scale, const float *v_scale,
-                        int num_pages, int page_size, const int32_t *page_table, int max_pages,
-                        const int32_t *ctx_len, const int32_t *n_nodes, const uint32_t *mask,
-                        const int32_t *positions, float scale, int window, int R, int M, int Hq,
-                        int Hkv, int D, void *out, float *out_lse, void *workspace,
-                        size_t workspace_bytes, void *stream) {
+// Both entry points: pages by the requests' tables, or (LISTS) by the lists of
+// every request's key heads.
+template <bool LISTS>
+static int attend(const void *q, int q_dtype, const void *k_cache, const void *v_cache,
+                  int cache_dtype, const float *k_scale, const float *v_scale,
+                  int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                  const int32_t *ctx_len, const int32_t *n_nodes, const uint32_t *mask,
+                  const int32_t *positions, float scale, int window, int R, int M, int Hq,
+                  int Hkv, int D, void *out, float *out_lse, void *workspace,
+                  size_t workspace_bytes, void *stream) {
     if (R < 0 || M < 1 || Hq < 1 || window < 0 || !isfinite(scale)) return SPEC_EINVAL;
     if (q_dtype != SPEC_BF16) return SPEC_EDTYPE;
     const int bad = check_pages(k_cache, v_cache, cache_dtype, k_scale, v_scale, num_pages,
@@ -1478,6 +1473,7 @@ int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const v
     if (Hq % Hkv) return SPEC_EINVAL;
     const size_t need = spec_tree_attention_workspace_bytes(R, M, Hq, Hkv, D);
     if (!need || R > 65535) return SPEC_EUNSUPPORTED;
+    if (LISTS && (int64_t)R * Hkv > 0x7fffffff) return SPEC_EUNSUPPORTED;  // rows of the lists
     if (R == 0) return SPEC_OK;
     if (!q || !ctx_len || !n_nodes || !out || (max_pages > 0 && !page_table)) return SPEC_EINVAL;
     if (mask && window > 0 && !positions) return SPEC_EINVAL;  // a node's index is not its level
@@ -1514,9 +1510,49 @@ int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const v
     const int64_t tiles = ((int64_t)M * a.G + s.TR - 1) / s.TR;
     const int64_t units = (((int64_t)max_pages << a.c.shift) + kUnit - 1) / kUnit + 1;
     if ((double)R * Hkv * (double)tiles * (double)units >= 2147483647.0) return SPEC_EUNSUPPORTED;
-    if (cache_dtype == SPEC_E4M3) launch_attn<true>(a, D, s, (hipStream_t)stream);
-    else launch_attn<false>(a, D, s, (hipStream_t)stream);
+    if (cache_dtype == SPEC_E4M3) launch_attn<LISTS, true>(a, D, s, (hipStream_t)stream);
+    else launch_attn<LISTS, false>(a, D, s, (hipStream_t)stream);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
+}
+
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+size_t spec_tree_attention_workspace_bytes(int R, int M, int Hq, int Hkv, int D) {
+    if (R < 0 || M < 1 || M > SPEC_TREE_MAX_NODES || Hkv < 1 || Hq < 1 || Hq % Hkv ||
+        Hq / Hkv > 64 || (D != 64 && D != 128 && D != 256))
+        return 0;
+    // the largest tiles that these sizes or smaller ones take
+    const int rows = M * (Hq / Hkv);
+    const size_t TR = rows <= 16 ? 16 : D == 256 || rows <= 64 ? 64 : 192;
+    const size_t groups = D <= 128 ? kMaxGroups : kMaxGroups / 2;
+    return sizeof(Control) + sizeof(Cut) * (kMaxGroups + 1) + 2 * groups * TR * (D + 2) * sizeof(float);
+}
+
+int spec_tree_attention(const void *q, int q_dtype, const void *k_cache, const void *v_cache,
+                        int cache_dtype, const float *k_scale, const float *v_scale,
+                        int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                        const int32_t *ctx_len, const int32_t *n_nodes, const uint32_t *mask,
+                        const int32_t *positions, float scale, int window, int R, int M, int Hq,
+                        int Hkv, int D, void *out, float *out_lse, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    return attend<false>(q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, num_pages,
+                         page_size, page_table, max_pages, ctx_len, n_nodes, mask, positions, scale,
+                         window, R, M, Hq, Hkv, D, out, out_lse, workspace, workspace_bytes, stream);
+}
+
+int spec_page_attention(const void *q, int q_dtype, const void *k_cache, const void *v_cache,
+                        int cache_dtype, const float *k_scale, const float *v_scale,
+                        int num_pages, int page_size, const int32_t *page_lists, int list_pages,
+                        const int32_t *list_len, const int32_t *n_nodes, const uint32_t *mask,
+                        float scale, int R, int M, int Hq, int Hkv, int D, void *out,
+                        float *out_lse, void *workspace, size_t workspace_bytes, void *stream) {
+    return attend<true>(q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, num_pages,
+                        page_size, page_lists, list_pages, list_len, n_nodes, mask, nullptr, scale,
+                        0, R, M, Hq, Hkv, D, out, out_lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
