@@ -696,6 +696,71 @@ int spec_page_attention(const void *q, int q_dtype, const void *k_cache, const v
                         float scale, int R, int M, int Hq, int Hkv, int D, void *out,
                         float *out_lse, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Truncated distributions
+ *
+ * Serving draws from a row's softmax cut off by top-k, top-p and min-p, and
+ * lossless verification holds for whatever two distributions it is given:
+ * with the target's and the draft's rows truncated alike (spec_truncate_logits,
+ * masked ids at -inf) spec_verify_batch commits tokens of the truncated target.
+ *
+ * For a row x of V logits with largest m, at temperature T > 0, ids stand in
+ * the order of falling logits, equal ones in that of their ids, and weigh
+ *   w_v = rint(2^44 e^((x_v - m) / T)),
+ * whole numbers whose sums are exact (so a result hangs on no order of
+ * summation).  Kept is the shortest of the prefixes that these leave:
+ *   top_k  the first top_k ids (0 or less: every one);
+ *   top_p  the fewest ids whose weights sum to at least ceil(top_p * W), W that
+ *          of the ids top_k leaves (1 or more: every one);
+ *   min_p  the ids with e^((x_v - m) / T) >= min_p (0: every one).
+ * Ids at -inf are never kept.  T = 0 keeps the lowest id of the largest logit.
+ *   logits       [R][J] rows of V, row (r, j) at element (r * J + j) * ld
+ *                (SPEC_F32 or SPEC_BF16, aligned to an element)
+ *   temperature  [R]  fp32, 0 or in [1e-30, 1e30]
+ *   top_k        [R]  int32, nullable (every id)
+ *   top_p, min_p [R]  fp32, nullable (every id); top_p > 0, 0 <= min_p <= 1
+ *   rows         [R]  int32 in [0, J], nullable (J): rows j >= rows[r] are
+ *                neither read nor written, in inputs and outputs
+ * Data faults (each sets SPEC_DEV_BAD_REQUEST): a setting outside its range
+ * marks the request's rows (rows[r] itself: all J), a NaN or +inf logit, a row
+ * that is entirely -inf or a uniform outside [0, 1) the row.
+ * Workspace: spec_sample_workspace_bytes.  Sizes: R, J >= 0, R * J < 2^22,
+ * 1 <= V <= SPEC_MAX_VERIFY_VOCAB, ld >= V.
+ */
+
+/* Workspace bytes of spec_sample and spec_truncate_logits (0 for sizes they do
+ * not accept). */
+size_t spec_sample_workspace_bytes(int R, int J, int V);
+
+/*
+ * Draws one token of every row: with W the kept weights' sum, the first kept id
+ * (ascending) whose running sum exceeds floor(u * W).  At T = 0 u is not read.
+ *   u            [R][J]  fp32 in [0, 1)
+ *   out_tokens   [R][J]  int32 (-1 in a faulty row)
+ *   out_logq     [R][J]  fp32, nullable: natural log of the token's share of W,
+ *                        (x - m) / T - log(W / 2^44) (0 at T = 0; NaN if faulty)
+ *   out_kept     [R][J]  int32, nullable: number of kept ids (-1 if faulty)
+ */
+int spec_sample(const void *logits, int dtype, int64_t ld, const float *temperature,
+                const int32_t *top_k, const float *top_p, const float *min_p, const int32_t *rows,
+                const float *u, int R, int J, int V, int32_t *out_tokens, float *out_logq,
+                int32_t *out_kept, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The rows with every id that is not kept at -inf, for spec_verify_batch at the
+ * same temperature (T = 0: its argmax rule sees the one id).
+ *   out_logits   [R][J] rows of V in the logits' type, row (r, j) at element
+ *                (r * J + j) * out_ld; `logits` itself (then out_ld == ld), or
+ *                memory apart from it.  A faulty row becomes NaN.
+ *   out_kept     [R][J]  int32, nullable, as spec_sample's
+ */
+int spec_truncate_logits(const void *logits, int dtype, int64_t ld, const float *temperature,
+                         const int32_t *top_k, const float *top_p, const float *min_p,
+                         const int32_t *rows, int R, int J, int V, void *out_logits,
+                         int64_t out_ld, int32_t *out_kept, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, copies the workspace's device status word (the OR
  * of SPEC_DEV_* bits raised since the last clear) to *host_bits, and clears
  * it when `clear` is nonzero. */

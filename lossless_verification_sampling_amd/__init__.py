@@ -74,6 +74,9 @@ EXPORTED = (
     "spec_page_select_workspace_bytes",
     "spec_page_select",
     "spec_page_attention",
+    "spec_sample_workspace_bytes",
+    "spec_sample",
+    "spec_truncate_logits",
     "spec_get_device_status",
     "spec_time_stats_launch",
 )
@@ -160,6 +163,12 @@ def _load() -> ctypes.CDLL:
     lib.spec_page_attention.restype = i
     lib.spec_page_attention.argtypes = [p, i, p, p, i, p, p, i, i, p, i, p, p, p, f, i, i, i, i, i,
                                         p, p, p, sz, p]
+    lib.spec_sample_workspace_bytes.restype = sz
+    lib.spec_sample_workspace_bytes.argtypes = [i, i, i]
+    lib.spec_sample.restype = i
+    lib.spec_sample.argtypes = [p, i, l, p, p, p, p, p, p, i, i, i, p, p, p, p, sz, p]
+    lib.spec_truncate_logits.restype = i
+    lib.spec_truncate_logits.argtypes = [p, i, l, p, p, p, p, p, i, i, i, p, l, p, p, sz, p]
     lib.spec_get_device_status.restype = i
     lib.spec_get_device_status.argtypes = [p, ctypes.POINTER(ctypes.c_uint32), i, p]
     return lib
@@ -232,6 +241,10 @@ def spec_tree_attention_workspace_bytes(R: int, M: int, Hq: int, Hkv: int, D: in
 
 def spec_page_select_workspace_bytes(R: int, Hkv: int, D: int, max_pages: int) -> int:
     return int(_lib.spec_page_select_workspace_bytes(R, Hkv, D, max_pages))
+
+
+def spec_sample_workspace_bytes(R: int, J: int, V: int) -> int:
+    return int(_lib.spec_sample_workspace_bytes(R, J, V))
 
 
 # ---------------------------------------------------------------------------
@@ -1091,3 +1104,108 @@ def spec_page_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if st:
         _raise(st, "spec_page_attention")
     return out, out_lse
+
+
+# ---------------------------------------------------------------------------
+# truncated distributions
+# ---------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=256)
+def _sample_bytes(*sizes) -> int:
+    return _lib.spec_sample_workspace_bytes(*sizes)
+
+
+def _spaced_rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
+    """Elements from one row to the next of [R, J, V] whose rows are evenly
+    spaced and dense."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    R, J, V = shape
+    s0, s1, s2 = t.stride()
+    ld = s1 if J > 1 else s0 if R > 1 else V
+    if ((s2 != 1 and V > 1) or ld < V or (s0 != J * ld and R > 1 and J > 1)) and t.numel():
+        raise ValueError(f"{name} must hold dense rows, evenly spaced")
+    return ld if ld > V else V
+
+
+def _settings(logits, temperature, top_k, top_p, min_p, rows):
+    """Checks what spec_sample and spec_truncate_logits share; returns (device,
+    logits' type code and spacing)."""
+    shape = logits.shape
+    _need(len(shape) == 3, "logits must be [R, J, V]")
+    _need(shape[2] > 0, "logits must have ids")
+    dev = _device(logits, "logits")
+    dt = _dtype(logits)
+    per = (shape[0],)
+    _need(temperature is not None, "temperature is needed")
+    _all(dev, (temperature, "temperature", torch.float32, per), (top_k, "top_k", torch.int32, per),
+         (top_p, "top_p", torch.float32, per), (min_p, "min_p", torch.float32, per),
+         (rows, "rows", torch.int32, per))
+    return dev, dt, _spaced_rows(logits, "logits", shape, dev)
+
+
+def spec_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: torch.Tensor,
+                top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                min_p: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None,
+                out: Optional[dict] = None, want_logq: bool = True, want_kept: bool = True,
+                workspace: Optional[Workspace] = None, stream=None) -> dict:
+    """One token of every row of logits [R, J, V] (float32 or bfloat16; rows
+    dense and evenly spaced) under temperature, top-k, top-p and min-p ([R]
+    each, top_k int32, the others float32) with uniforms u [R, J] float32;
+    rows [R] int32 limits how many of a request's rows are in use.  Returns
+    dict(tokens, logq, kept) [R, J]; `out` may supply them."""
+    dev, dt, ld = _settings(logits, temperature, top_k, top_p, min_p, rows)
+    R, J, V = logits.shape
+    out = {} if out is None else out
+    tokens, logq, kept = out.get("tokens"), out.get("logq"), out.get("kept")
+    shape, i32, f32 = (R, J), torch.int32, torch.float32
+    if tokens is None:
+        tokens = _empty(shape, i32, logits.device, stream)
+    if logq is None and want_logq:
+        logq = _empty(shape, f32, logits.device, stream)
+    if kept is None and want_kept:
+        kept = _empty(shape, i32, logits.device, stream)
+    _all(dev, (u, "u", f32, shape), (tokens, "out tokens", i32, shape),
+         (logq, "out logq", f32, shape), (kept, "out kept", i32, shape))
+    need = _sample_bytes(R, J, V)
+    if need == 0:
+        raise SpecError(-5, "spec_sample_workspace_bytes")
+    buf, room, queue = _cache_buf(workspace, dev, need, stream)
+    st = _run(dev, _lib.spec_sample, logits.data_ptr(), dt, ld, temperature.data_ptr(),
+              _raw(top_k), _raw(top_p), _raw(min_p), _raw(rows), u.data_ptr(), R, J, V,
+              tokens.data_ptr(), _raw(logq), _raw(kept), buf, room, queue)
+    if st:
+        _raise(st, "spec_sample")
+    return {"tokens": tokens, "logq": logq, "kept": kept}
+
+
+def spec_truncate_logits(logits: torch.Tensor, *, temperature: torch.Tensor,
+                         top_k: Optional[torch.Tensor] = None,
+                         top_p: Optional[torch.Tensor] = None,
+                         min_p: Optional[torch.Tensor] = None,
+                         rows: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                         out_kept: Optional[torch.Tensor] = None, want_kept: bool = True,
+                         workspace: Optional[Workspace] = None, stream=None):
+    """The rows of logits [R, J, V] with the ids that temperature, top-k, top-p
+    and min-p leave out at -inf (arguments as spec_sample's), for
+    spec_verify_batch.  `out` may be `logits` itself; rows not in use are left
+    as they were.  Returns (out [R, J, V], kept ids [R, J] int32 or None)."""
+    dev, dt, ld = _settings(logits, temperature, top_k, top_p, min_p, rows)
+    R, J, V = shape = logits.shape
+    if out is None:
+        out = _empty(shape, logits.dtype, logits.device, stream)
+    if out_kept is None and want_kept:
+        out_kept = _empty((R, J), torch.int32, logits.device, stream)
+    _need(out.dtype is logits.dtype and out.shape == shape, "out must be like logits")
+    out_ld = _spaced_rows(out, "out", shape, dev)
+    _all(dev, (out_kept, "out_kept", torch.int32, (R, J)))
+    need = _sample_bytes(R, J, V)
+    if need == 0:
+        raise SpecError(-5, "spec_sample_workspace_bytes")
+    buf, room, queue = _cache_buf(workspace, dev, need, stream)
+    st = _run(dev, _lib.spec_truncate_logits, logits.data_ptr(), dt, ld, temperature.data_ptr(),
+              _raw(top_k), _raw(top_p), _raw(min_p), _raw(rows), R, J, V, out.data_ptr(), out_ld,
+              _raw(out_kept), buf, room, queue)
+    if st:
+        _raise(st, "spec_truncate_logits")
+    return out, out_kept
