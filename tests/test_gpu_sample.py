@@ -189,6 +189,29 @@ def test_min_p_at_its_edge(sv, dev):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_of_many_kinds(sv, dev, dtype):
+    """Peaked rows, whose cuts lie among few candidates, and flat ones, whose
+    cuts lie deep; several chunks a row, equal logits and masked ids among
+    them; settings alone and together."""
+    g = np.random.default_rng(6)
+    V = 40007
+    x = np.empty((8, 1, V))
+    x[0] = g.standard_normal(V) * 2
+    x[0, 0, g.integers(0, V, 40)] = 12 + 2.5 * g.standard_normal(40)
+    x[1] = g.standard_normal(V) * 0.3                               # flat
+    x[2] = np.where(g.random(V) < 0.001, 9.0, g.standard_normal(V))  # equal likely ids
+    x[3] = np.where(g.random(V) < 0.995, -np.inf, 2 * g.standard_normal(V))
+    x[4] = -np.arange(V) / 50.0                                     # all in the first chunk
+    x[5] = np.arange(V) / 500.0 - 3                                 # in the last
+    x[6] = np.where(np.arange(V) // 8192 == 2, 3.0 * g.standard_normal(V), -np.inf)
+    x[7] = np.round(g.standard_normal(V) * 4) / 2
+    for k in (0, 1, 2, 40, 256, 257, 5000):
+        for p in (1.0, 0.9, 0.9999, 0.05):
+            for mp in (0.0, 0.05, 0.9, 1e-6):
+                Rows(x, dtype, t=0.9, k=k, p=p, mp=mp, u=uniforms(g, 8, 1)).check(sv, dev)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_data_faults(sv, dev, dtype):
     V = 700
     x = torch.zeros(12, 2, V, dtype=dtype)
@@ -279,6 +302,24 @@ def test_verification_of_truncated_rows(sv, dev, dtype):
     for r in range(R):
         for i in range(int(n[r]) + 1):
             assert q[r, i, int(out[r, i])] > -float("inf")
+
+
+def test_more_rows_than_one_slice(sv, dev):
+    """A call takes 16384 chunks at a time."""
+    g = np.random.default_rng(10)
+    x = D(g.standard_normal((4100, 2, 9000)), dev, BF16)            # two chunks a row
+    u, t = D(uniforms(g, 4100, 2), dev), torch.full((4100,), 0.8, device=dev)
+    how = dict(temperature=t, top_k=torch.full((4100,), 30, dtype=torch.int32, device=dev))
+    got = sv.spec_sample(x, u, **how)
+    out, kept = sv.spec_truncate_logits(x, **how)
+    assert (kept == 30).all() and torch.equal(got["kept"], kept) and ((out > -float("inf")).sum(-1) == 30).all()
+    for r in (0, 4094, 4095, 4096, 4099):
+        for j in range(2):
+            want = osm.draw(x[r, j].double().cpu().numpy(), float(t[0]), float(u[r, j]), 30)
+            assert int(got["tokens"][r, j]) == want[0]
+    parts = sv.spec_sample(x[4000:].contiguous(), u[4000:].contiguous(), temperature=t[4000:],
+                           top_k=how["top_k"][4000:])
+    assert all(torch.equal(parts[n], got[n][4000:]) for n in parts)
 
 
 def test_captured_calls_replay(sv, dev):
