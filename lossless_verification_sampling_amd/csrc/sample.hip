@@ -8,35 +8,36 @@
 // launch takes them in, and so are the comparisons that a token hangs on.  (A
 // row of 2^18 ids sums to 2^62 at most.)
 //
-// Three launches.  The first reads every row once, in chunks: largest logit,
-// the few ids that a cut can lie among (candidates, listed in the order of
-// ids), and for top-p an estimate of what the others weigh.  The second takes
-// one workgroup a row and finds the cut in the candidates.  The estimate has
-// proven bounds: where both ends of them give the same cut, that is the exact
-// one.  Rows that this does not settle (flat ones, whose cut lies deep, top_k
-// above kMostTopK, a cut between the bounds) are done whole by one workgroup
-// in the third launch; rows that nothing cuts off are summed in the second and
-// drawn from in the third, which also writes truncated rows.
-#include <math.h>
-
-#include "common.h"
+// Launches, over slices of rows:
+//   chunks   reads every row once: largest logit, the few ids that a cut can
+//            lie among (candidates, listed in the order of ids) and, for top-p, an
+//            estimate of what the others weigh
+//   finish   one workgroup a row: the cut among the candidates.  The estimate
+//            has proven bounds; where both of their ends give the same cut, that
+//            is the exact one.  Rows that this settles are done but for
+//            their writing.
+//   second   chunks of the other rows, from a work list: exact sums where
+//            nothing is cut off, else a histogram of weights (or of ids)
+//   third    the same rows where a cut is still to be found: the ids in the
+//            histogram's bin that holds it are listed, what lies above is summed
+//   draw     one workgroup a row that is not done: its cut and its token
+//   settle, write (truncation): its cut; the rows
+// A row that none of this fits (top_k above kMostTopK together with top_p, more
+// equal logits than a list holds) is done whole by one workgroup at the end.
+#include "sample.h"
 
 namespace sv {
 
-typedef unsigned long long u64;
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-
-constexpr int kRowThreads = 1024;             // threads of a row's workgroup in the third launch
-constexpr int kBins = 2048;                   // of a histogram
+constexpr int kRowThreads = 1024;             // threads of a row's workgroup in the last launches
 constexpr int kListKeys = 2048;               // keys that are looked at one by one
-constexpr int kChunk = 8192;                  // ids of the first launch's workgroup
+constexpr int kChunk = 8192;                  // ids of a chunk
 constexpr int kListed = 8192;                 // candidates of a row at most
+constexpr int kSorted = 1024;                 // candidates that are sorted at most
 constexpr int kMostTopK = kBlock;             // largest top_k that candidates are listed for
+constexpr int kDeepBins = kBlock;             // of a chunk's histogram
 constexpr int kSliceChunks = 16384;           // chunks that a launch takes at a time
+constexpr int kListGroups = 1024;             // workgroups of a launch over the work list
 constexpr int kWriteIds = 32768;              // ids that a writing workgroup takes
-constexpr double kOne = 17592186044416.0;     // 2^44, the weight of the largest logit
-// Weights below half a unit are 0: from 45 log 2 = 31.2 temperatures below m on.
-constexpr double kDeepest = 31.25;
 // Candidates of top-p: ids within this many temperatures of the chunk's largest
 // logit (a share of e^-10 = 4.5e-5 of its).
 constexpr float kHot = 10.0f;
@@ -44,17 +45,38 @@ constexpr float kHot = 10.0f;
 struct ChunkRec {
     uint32_t top;                // key of the largest logit
     uint32_t n;                  // candidates
-    uint32_t finite;             // ids that are not masked out
+    uint32_t finite;             // ids that are not masked out (after `second`: ids above the cut)
     uint32_t odd;                // a NaN or +inf is among them
     double tail;                 // estimate of sum e^((x - top) / T) over the others
     double pad;
 };
-enum : uint32_t { kDone, kWhole, kMany, kFault };  // a row's state after the second launch
+enum : uint32_t {                // a row's state
+    kDone,                       // token drawn, or kept ids listed
+    kFault,
+    kWhole,                      // its cut is every id at or above `key`
+    kDeep,                       // its cut is looked for by histograms
+    kMany,                       // by one workgroup
+    kCut,                        // (truncation) its cut is `key` and ids up to `last` that equal it
+    kWritten                     // (truncation) nothing is left to do
+};
 struct RowRec {
     uint32_t state;
-    uint32_t n;                  // kept ids, listed (kDone)
     float m;                     // largest logit
-    uint32_t finite;
+    uint32_t finite;             // ids that are not masked out
+    uint32_t n;                  // kept ids, listed (kDone)
+    uint32_t key;                // kWhole, kCut
+    uint32_t last;               // kCut
+    uint32_t by_weight;          // kDeep: top_p's cut, or top_k's
+    uint32_t pad;
+};
+struct DeepRec {                 // a kDeep row's bin (written by `third`)
+    Pair above;
+    Want want;
+    int bin;
+};
+struct Work {                    // rows of the later launches, in any order
+    uint32_t second, third;      // how many
+    uint32_t pad[62];
 };
 
 struct SampleArgs {
@@ -76,20 +98,14 @@ struct SampleArgs {
     int chunks, room;            // chunks of a row, candidates that each may list
     ChunkRec *chunk;             // [rows_here][chunks]
     RowRec *row;                 // [rows_here]
+    DeepRec *deep;               // [rows_here]
+    Work *work;
+    uint32_t *second, *third;    // [rows_here] rows of the slice
+    u64 *hist;                   // [rows_here][chunks][kDeepBins]
     u64 *subs;                   // [rows_here][chunks][kChunk / 256] weights of a wave's loads (draws)
     uint32_t *ids;               // [rows_here][chunks][room] candidates, then the row's kept ids
     float *vals;                 // their logits
 };
-
-// Whole numbers in the order of the floats (-0 and 0 alike).
-__device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    return b >> 31 ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float of_key(uint32_t k) {
-    return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);
-}
-constexpr uint32_t kNoKey = 0x007fffffu;      // of -inf: ids that are masked out
 
 // ---------------------------------------------------------------------------
 // a row's settings
@@ -99,7 +115,7 @@ struct Setting {
     bool live, ok;               // the row is in use; its settings are in their ranges
     float t, p, mp, u;
     int k;                       // 0: every id
-    bool greedy, whole, many;    // one id; nothing is cut off; not by candidates
+    bool greedy, whole, many;    // one id; nothing is cut off; top_k is not by candidates
 };
 template <bool DRAW>
 __device__ __forceinline__ Setting setting_of(const SampleArgs &a, int i) {
@@ -122,329 +138,128 @@ __device__ __forceinline__ Setting setting_of(const SampleArgs &a, int i) {
     return s;
 }
 
-// The least logit x with e^((x - m) / T) >= min_p, and one that is not above it.
-__device__ __forceinline__ uint32_t min_p_key(float m, float t, float mp) {
-    const double low = (double)m + (double)t * log((double)mp);
+// Key of the least logit x with e^((x - m) / T) >= min_p.  (It falls with m, so
+// a chunk's own largest logit gives a bound.)
+__device__ __forceinline__ uint32_t min_p_key(float m, const Setting &g) {
+    if (g.mp == 0.f) return kNoKey + 1;
+    const double low = (double)m + (double)g.t * log((double)g.mp);
     const float x = (float)low;
-    return key_of(x) + ((double)x < low);
+    return max(key_of(x) + ((double)x < low), kNoKey + 1);
+}
+
+// Where candidates of top-p begin.  (One operation: it must not round
+// differently in two places.)
+__device__ __forceinline__ float hot_edge(float top, const Setting &g) { return fmaf(-kHot, g.t, top); }
+
+__device__ __forceinline__ Weights weights_of(float m, float t, const double *table) {
+    return Weights{(double)m, t == 0.f ? 0.0 : 64.0 * kLog2e / (double)t, table};
+}
+__device__ __forceinline__ float log_share(const Weights &wt, float x, float t, u64 total) {
+    return t == 0.f ? 0.f : (float)(((double)x - wt.m) / (double)t - log((double)total / kOne));
 }
 
 // ---------------------------------------------------------------------------
-// weights
+// a chunk in registers
 // ---------------------------------------------------------------------------
 
-// w(x) = 2^(44 + (x - m) log2(e) / T): the exponent is cut into 64ths, whose
-// powers of two stand in a table, and the rest, at most ln 2 / 128 = 0.0055, goes through the
-// exponential's series to the fifth power (the next term is 4e-17).
-struct Weights {
-    double m, c;                 // the largest logit, 64 log2(e) / T
-    const double *table;         // 2^(i / 64), i < 64 (shared memory)
-};
-__device__ __forceinline__ u64 weight(const Weights &w, float x) {
-    constexpr double kRound = 6755399441055744.0;  // 1.5 2^52: adding it rounds to whole numbers
-    constexpr double z = kLn2 / 64;
-    const double y = fmax(((double)x - w.m) * w.c, -64.0 * 60.0);
-    const double s = y + kRound;
-    const int n = (int)(uint32_t)__double_as_longlong(s);
-    const double r = y - (s - kRound);
-    double p = fma(r, z * z * z * z * z / 120, z * z * z * z / 24);
-    p = fma(p, r, z * z * z / 6);
-    p = fma(p, r, z * z / 2);
-    p = fma(p, r, z);
-    p = fma(p, r, 1.0);
-    p = ldexp(p * w.table[n & 63], (n >> 6) + 44);
-    return (u64)(__double_as_longlong(p + kRound) - __double_as_longlong(kRound));
-}
-
-// ---------------------------------------------------------------------------
-// a row's ids
-// ---------------------------------------------------------------------------
-
-template <typename T> struct Row {
-    static constexpr int N = 16 / sizeof(T);  // ids of a 16-byte block
-    const T *p;                  // the block that holds id 0
-    int skip, V, blocks;         // elements before id 0 in it; ids; blocks
+// A workgroup of kBlock threads holds 32 ids a thread; a wave's ids lie side
+// by side, N of them a lane and load.
+template <typename T> struct Chunk {
+    static constexpr int N = Row<T>::N, NB = kChunk / (kBlock * N);
+    u32x4_t w[NB];
+    int b0;                      // this lane's first block
+    __device__ __forceinline__ float x(int j, int i) const { return Unpack<T>::get(w[j], i); }
 };
 template <typename T>
-__device__ __forceinline__ Row<T> row_of(const void *base, int64_t at, int V) {
-    Row<T> r;
-    const T *p = (const T *)base + at;
-    r.skip = (int)(((uintptr_t)p & 15u) / sizeof(T));
-    r.p = p - r.skip;
-    r.V = V;
-    r.blocks = (r.skip + V + Row<T>::N - 1) / Row<T>::N;
-    return r;
+__device__ __forceinline__ void load_chunk(const Row<T> &row, int c, Chunk<T> &k) {
+    constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
+    k.b0 = c * (kChunk / N) + (threadIdx.x >> 6) * 64 * NB + (threadIdx.x & 63);
+    load_blocks<NB>(row, k.b0, 64, k.w);
 }
-template <typename T> struct Unpack;
-template <> struct Unpack<float> {
-    static constexpr uint32_t kMasked = 0xff800000u;
-    __device__ __forceinline__ static float get(const u32x4_t &w, int i) { return __uint_as_float(w[i]); }
-};
-template <> struct Unpack<uint16_t> {
-    static constexpr uint32_t kMasked = 0xff80ff80u;
-    __device__ __forceinline__ static float get(const u32x4_t &w, int i) {
-        return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-    }
-};
-// Blocks b, b + stride, ..; what is not the row's becomes -inf and is not read.
-// Blocks that are the row's alone come in one load each, all of them under
-// way together; a row's first and last may not be (or not exist): those are
-// passed by, and read one by one.
-template <int NB, typename T>
-__device__ __forceinline__ void load_blocks(const Row<T> &r, int b, int stride, u32x4_t (&w)[NB]) {
-    constexpr int N = Row<T>::N;
-    const int full0 = r.skip ? 1 : 0, full1 = (r.skip + r.V) / N;  // blocks [full0, full1) are whole
-#pragma unroll
-    for (int j = 0; j < NB; ++j) w[j] = u32x4_t{} + Unpack<T>::kMasked;
-    if (full0 < full1) {
-        const u32x4_t *p = (const u32x4_t *)r.p;
-#pragma unroll
-        for (int j = 0; j < NB; ++j) w[j] = p[min(max(b + j * stride, full0), full1 - 1)];
-    }
+
+// Lists the chunk's ids whose bits are set in `hits` (bit j N + i), in their
+// order; returns their number (room for fewer: the others are left out).
+template <typename T>
+__device__ __forceinline__ uint32_t list_hits(const SampleArgs &a, int ri, int c, const Row<T> &row, const Chunk<T> &k,
+                                              uint32_t hits, uint32_t (&count_s)[kWaves]) {
+    constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    uint32_t count = 0, before[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-        const int at = b + j * stride;
-        if (at >= full0 && at < full1) continue;
-        w[j] = u32x4_t{} + Unpack<T>::kMasked;
-        if (at >= r.blocks) continue;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int id = at * N + i - r.skip;
-            if (id < 0 || id >= r.V) continue;
-            if constexpr (sizeof(T) == 4) w[j][i] = __float_as_uint(r.p[(int64_t)at * N + i]);
-            else {
-                const uint32_t e = r.p[(int64_t)at * N + i];
-                w[j][i >> 1] = i & 1 ? (w[j][i >> 1] & 0xffffu) | e << 16 : (w[j][i >> 1] & 0xffff0000u) | e;
-            }
+        const uint32_t n = __popc(hits >> (j * N) & ((1u << N) - 1u));
+        before[j] = count;
+        if (__any(n != 0)) {
+            const uint32_t inc = wave_incl_scan_dpp(n);
+            before[j] += inc - n;
+            count += (uint32_t)__builtin_amdgcn_readlane((int)inc, 63);
         }
     }
-}
-
-// ---------------------------------------------------------------------------
-// sums over the workgroup
-// ---------------------------------------------------------------------------
-
-struct Pair {                    // ids and their weight
-    uint32_t n;
-    u64 w;
-};
-__device__ __forceinline__ Pair operator+(Pair a, Pair b) { return {a.n + b.n, a.w + b.w}; }
-
-// A scan's step: two 32-bit moves, the source lanes out of range reading 0.
-template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ u64 dpp0_u64(u64 v) {
-    const uint32_t lo = (uint32_t)dpp0_i<CTRL, ROW_MASK>((int)(uint32_t)v);
-    const uint32_t hi = (uint32_t)dpp0_i<CTRL, ROW_MASK>((int)(uint32_t)(v >> 32));
-    return (u64)hi << 32 | lo;
-}
-__device__ __forceinline__ u64 wave_scan_u64(u64 v) {
-    v += dpp0_u64<kDppRowShr1, 0xf>(v);
-    v += dpp0_u64<kDppRowShr2, 0xf>(v);
-    v += dpp0_u64<kDppRowShr4, 0xf>(v);
-    v += dpp0_u64<kDppRowShr8, 0xf>(v);
-    v += dpp0_u64<kDppRowBcast15, 0xa>(v);
-    v += dpp0_u64<kDppRowBcast31, 0xc>(v);
-    return v;
-}
-__device__ __forceinline__ u64 lane_u64(u64 v, int l) {
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, l);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), l);
-    return (u64)hi << 32 | lo;
-}
-__device__ __forceinline__ u64 wave_sum_u64(u64 v) { return lane_u64(wave_scan_u64(v), 63); }
-__device__ __forceinline__ uint32_t wave_sum_u32(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_readlane((int)wave_incl_scan_dpp(v), 63);
-}
-
-// Shared memory of a workgroup of B threads.
-template <int B> struct Scratch {
-    u64 mass[kBins];             // a histogram: weights,
-    uint32_t count[kBins];       // and ids
-    double table[64];
-    Pair waves[2][B / 64];
-    uint32_t ends[2][B / 64];
-    uint32_t listed;
-    uint32_t found;              // the bin of a cut,
-    Pair before, there;          // what lies above it, and in it
-};
-
-// What lies in the threads before this one (in thread order), and in all.
-template <int B>
-__device__ __forceinline__ Pair block_before(Scratch<B> &s, Pair v, Pair &all) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Pair inc{wave_incl_scan_dpp(v.n), wave_scan_u64(v.w)};
+    if ((threadIdx.x & 63) == 0) count_s[wave] = count;
     __syncthreads();
-    if (lane == 63) s.waves[0][wave] = inc;
-    __syncthreads();
-    Pair b{inc.n - v.n, inc.w - v.w};
-    all = Pair{0, 0};
-    for (int w = 0; w < B / 64; ++w) {
-        if (w < wave) b = b + s.waves[0][w];
-        all = all + s.waves[0][w];
+    uint32_t base = 0, all = 0;
+    for (int v = 0; v < kWaves; ++v) {
+        if (v < wave) base += count_s[v];
+        all += count_s[v];
     }
-    return b;
-}
-// Least and largest over the workgroup.
-template <int B>
-__device__ __forceinline__ void block_ends(Scratch<B> &s, uint32_t &lo, uint32_t &hi) {
-    for (int o = 32; o; o >>= 1) {
-        lo = min(lo, (uint32_t)__shfl_xor((int)lo, o, 64));
-        hi = max(hi, (uint32_t)__shfl_xor((int)hi, o, 64));
-    }
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) {
-        s.ends[0][threadIdx.x >> 6] = lo;
-        s.ends[1][threadIdx.x >> 6] = hi;
-    }
-    __syncthreads();
-    for (int w = 0; w < B / 64; ++w) {
-        lo = min(lo, s.ends[0][w]);
-        hi = max(hi, s.ends[1][w]);
-    }
-}
-
-// ---------------------------------------------------------------------------
-// cuts
-// ---------------------------------------------------------------------------
-
-// The ids above `key` are in, and the first `ties` that equal it.
-struct Cut {
-    uint32_t key, ties;
-};
-// The shorter of two prefixes.
-__device__ __forceinline__ Cut shorter(Cut a, Cut b) {
-    return a.key > b.key || (a.key == b.key && a.ties < b.ties) ? a : b;
-}
-
-// A cut is asked for by its ids or by its weight: the shortest prefix with at
-// least that much.
-struct Want {
-    bool by_weight;
-    uint32_t n;
-    u64 w;
-    __device__ __forceinline__ bool reached(Pair p) const { return by_weight ? p.w >= w : p.n >= n; }
-};
-__device__ __forceinline__ Want top_p_want(float p, u64 total) {
-    return Want{true, 0, (u64)ceil((double)p * (double)total)};
-}
-
-// The histogram's bin (the highest first) in which `want` is reached, counted
-// from `above` on; into s.found, s.before and s.there.
-template <int B>
-__device__ __forceinline__ void find_bin(Scratch<B> &s, Pair above, const Want &want) {
-    constexpr int EACH = kBins / B;
-    Pair mine[EACH], sum{0, 0}, all;
-    __syncthreads();
+    if (count) {
+        const int64_t at = ((int64_t)ri * a.chunks + c) * a.room;
 #pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-        const int b = kBins - 1 - ((int)threadIdx.x * EACH + i);
-        mine[i] = Pair{s.count[b], s.mass[b]};
-        sum = sum + mine[i];
-    }
-    Pair at = above + block_before(s, sum, all);
+        for (int j = 0; j < NB; ++j) {
+            uint32_t pos = base + before[j];
 #pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-        if (!want.reached(at) && want.reached(at + mine[i])) {
-            s.found = (uint32_t)(kBins - 1 - ((int)threadIdx.x * EACH + i));
-            s.before = at;
-            s.there = mine[i];
-        }
-        at = at + mine[i];
-    }
-    __syncthreads();
-}
-
-template <int B>
-__device__ __forceinline__ void clear_bins(Scratch<B> &s) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += B) {
-        s.mass[i] = 0;
-        s.count[i] = 0;
-    }
-    __syncthreads();
-}
-
-// The cut among keys lo .. hi, with `above` before them and `want` reached in
-// them: counts over 2048 equal parts of the range, and again over the part
-// that holds the cut, until it is one key.  each(f) calls f for the keys
-// (others among them are passed over); masses: weights matter, be it for the
-// sum up to the cut alone, which goes to weight_to_cut.
-template <int B, typename F>
-__device__ __forceinline__ Cut cut_among(Scratch<B> &s, const Weights &wt, uint32_t lo, uint32_t hi, Pair above,
-                                         const Want &want, bool masses, u64 &weight_to_cut, F each) {
-    for (int level = 0; level < 3 && hi != lo; ++level) {  // (3 times 11 bits are 32)
-        const int shift = max(0, 21 - __clz((int)(hi - lo)));  // parts of 2^shift keys
-        clear_bins(s);
-        each([&](uint32_t k) {
-            if (k < lo || k > hi) return;
-            const uint32_t b = (k - lo) >> shift;
-            atomicAdd(&s.count[b], 1u);
-            if (masses) atomicAdd(&s.mass[b], weight(wt, of_key(k)));
-        });
-        find_bin(s, above, want);
-        above = s.before;
-        lo += s.found << shift;
-        hi = min(hi, lo + ((1u << shift) - 1u));
-        if (shift && s.there.n == 1) {  // (one id: its key is the part's only one)
-            uint32_t l = 0xffffffffu, h = 0;
-            each([&](uint32_t k) {
-                if (k >= lo && k <= hi) l = h = k;
-            });
-            block_ends(s, l, h);
-            lo = hi = h;
+            for (int i = 0; i < N; ++i)
+                if (hits >> (j * N + i) & 1u) {
+                    if (pos < (uint32_t)a.room) {
+                        a.ids[at + pos] = (uint32_t)((k.b0 + 64 * j) * N + i - row.skip);
+                        a.vals[at + pos] = k.x(j, i);
+                    }
+                    ++pos;
+                }
         }
     }
-    const u64 one = weight(wt, of_key(lo));
-    Cut c{lo, 0};
-    if (want.by_weight) c.ties = (uint32_t)((want.w - above.w + one - 1) / one);
-    else c.ties = want.n - above.n;
-    weight_to_cut = above.w + one * c.ties;
-    return c;
+    return all;
 }
 
 // ---------------------------------------------------------------------------
-// first launch: chunks
+// chunks
 // ---------------------------------------------------------------------------
 
-// A workgroup holds its chunk in registers, 32 ids a thread; a wave's ids lie
-// side by side, so that candidates come out in the order of ids.  One pass of
-// HBM: 64 clocks a wave's 64 ids where a tail is estimated, about what they
-// take to come.
 template <typename T>
 __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
-    constexpr int N = Row<T>::N, NB = kChunk / (kBlock * N);
-    __shared__ float top_s[kWaves], low_s[kWaves];
+    constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
+    __shared__ float top_s[kWaves];
     __shared__ uint32_t group_s[kBlock], count_s[kWaves], finite_s[kWaves];
     __shared__ double tail_s[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ri = blockIdx.x / a.chunks, c = blockIdx.x - ri * a.chunks;
+    if (blockIdx.x == 0 && tid == 0) a.work->second = a.work->third = 0;
     const Setting g = setting_of<false>(a, a.row0 + ri);
     if (!g.live || !g.ok) return;
     const Row<T> row = row_of<T>(a.logits, (int64_t)(a.row0 + ri) * a.ld, a.V);
-    const int b0 = c * (kChunk / N) + wave * 64 * NB + lane;
-    u32x4_t w[NB];
-    load_blocks<NB>(row, b0, 64, w);
+    Chunk<T> k;
+    load_chunk(row, c, k);
     ChunkRec rec{kNoKey, 0, 0, 0, 0.0, 0.0};
     // ---- largest and least logit
-    float top = -INFINITY, low = INFINITY;
+    float tops[NB], own = -INFINITY, low = INFINITY;
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
+    for (int j = 0; j < NB; ++j) {
+        tops[j] = -INFINITY;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float x = Unpack<T>::get(w[j], i);
-            top = __builtin_elementwise_maximum(top, x);
-            low = fminf(low, x);
+            tops[j] = __builtin_elementwise_maximum(tops[j], k.x(j, i));
+            low = fminf(low, k.x(j, i));
         }
-    const float own = top;
-    top = wave_max(top);
-    low = -wave_max(-low);
+        own = __builtin_elementwise_maximum(own, tops[j]);
+    }
+    float top = wave_max(own);
     uint32_t finite = 32;
-    if (low == -INFINITY) {
+    if (__any(low == -INFINITY)) {
         finite = 0;
 #pragma unroll
         for (int j = 0; j < NB; ++j)
 #pragma unroll
-            for (int i = 0; i < N; ++i) finite += Unpack<T>::get(w[j], i) > -INFINITY;
+            for (int i = 0; i < N; ++i) finite += k.x(j, i) > -INFINITY;
     }
     finite = wave_sum_u32(finite);
     if (lane == 0) {
@@ -453,7 +268,6 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     }
     group_s[tid] = key_of(own);
     __syncthreads();
-    rec.finite = 0;
     for (int v = 0; v < kWaves; ++v) {
         top = __builtin_elementwise_maximum(top, top_s[v]);
         rec.finite += finite_s[v];
@@ -467,7 +281,9 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     }
     // ---- where candidates begin
     float edge = top;
+    const bool estimate = !g.greedy && g.k == 0 && g.p < 1.f;
     if (!g.greedy) {
+        edge = estimate ? hot_edge(top, g) : -INFINITY;
         if (g.k > 0) {
             // At least k of the threads' largest logits lie at or above the
             // edge, so the row's first k ids do where they lie in this chunk.
@@ -480,96 +296,87 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
                 for (int v = 0; v < kBlock / 64; ++v) n += __popcll(__ballot(mine[v] >= next));
                 if (n >= g.k) at = next;
             }
-            edge = at > kNoKey ? of_key(at) : -INFINITY;
+            if (at > kNoKey) edge = of_key(at);
         }
-        if (g.k == 0 && g.p < 1.f) edge = top - kHot * g.t;
-        if (g.mp > 0.f && (g.k == 0 || g.p >= 1.f)) {
-            // (top_p's sum is over what top_k leaves)
-            const float x = of_key(min_p_key(top, g.t, g.mp));
-            edge = g.k == 0 && g.p >= 1.f ? x : fmaxf(edge, x);
-        }
+        // (top_p's sum is over what top_k leaves)
+        if (g.k == 0 || g.p >= 1.f) edge = fmaxf(edge, of_key(min_p_key(top, g)));
+        edge = fmaxf(edge, -3.402823466e38f);   // ids that are masked out are none
     }
     // ---- candidates, and the rest's weight
     uint32_t hits = 0;
     double tail = 0.0;
-    const bool estimate = !g.greedy && g.k == 0 && g.p < 1.f;
+    // 2^a with a = (x - top) log2(e) / T in fp32: see kTailError
+    const float ch = estimate ? (float)(kLog2e / (double)g.t) : 0.f;
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
+    for (int j = 0; j < NB; ++j) {
+        const bool some = __any(tops[j] >= edge);
+        if (some) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float x = Unpack<T>::get(w[j], i);
-            hits |= (x >= edge && x > -INFINITY ? 1u : 0u) << (j * N + i);
+            for (int i = 0; i < N; ++i) hits |= (k.x(j, i) >= edge ? 1u : 0u) << (j * N + i);
         }
-    if (estimate) {
-        // 2^a with a = d c: d = x - top, rounded, is off by 2^-24 |d|; a's whole
-        // part leaves, and the rest is taken from an exact product.  (Where a
-        // is far below, the rest need not be a number.)
-        const double cd = kLog2e / (double)g.t;
-        const float ch = (float)cd, cl = (float)(cd - (double)ch);
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
+        if (estimate) {
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float d = Unpack<T>::get(w[j], i) - top;
-                const float a = d * ch, n = rintf(a);
-                const float f = fmaf(d, cl, fmaf(d, ch, -n));
-                const float e = ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
-                sum += a > -120.f && !(hits >> (j * N + i) & 1u) ? e : 0.f;
+                const float e = __builtin_amdgcn_exp2f(fmaxf((k.x(j, i) - top) * ch, -126.f));
+                sum += some && k.x(j, i) >= edge ? 0.f : e;
             }
             tail += (double)sum;
         }
+    }
+    if (estimate) {
         tail = wave_sum(tail);
+        if (lane == 0) tail_s[wave] = tail;
     }
-    uint32_t count = 0, before[NB];
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        const uint32_t n = __popc(hits >> (j * N) & ((1u << N) - 1u));
-        before[j] = count;
-        if (__any(n != 0)) {
-            const uint32_t inc = wave_incl_scan_dpp(n);
-            before[j] += inc - n;
-            count += (uint32_t)__builtin_amdgcn_readlane((int)inc, 63);
-        }
-    }
-    if (lane == 0) {
-        count_s[wave] = count;
-        tail_s[wave] = tail;
-    }
-    __syncthreads();
-    uint32_t base = 0;
-    for (int v = 0; v < kWaves; ++v) {
-        if (v < wave) base += count_s[v];
-        rec.n += count_s[v];
-        rec.tail += tail_s[v];
-    }
+    rec.n = list_hits(a, ri, c, row, k, hits, count_s);
+    if (estimate)
+        for (int v = 0; v < kWaves; ++v) rec.tail += tail_s[v];
     if (tid == 0) *out = rec;
-    if (count == 0) return;
-    const int64_t at = ((int64_t)ri * a.chunks + c) * a.room;
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        uint32_t pos = base + before[j];
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (hits >> (j * N + i) & 1u) {
-                if (pos < (uint32_t)a.room) {
-                    a.ids[at + pos] = (uint32_t)((b0 + 64 * j) * N + i - row.skip);
-                    a.vals[at + pos] = Unpack<T>::get(w[j], i);
-                }
-                ++pos;
-            }
-    }
 }
 
 // ---------------------------------------------------------------------------
-// second launch: rows
+// finish
 // ---------------------------------------------------------------------------
 
-// The bounds of an estimated tail: an estimate's terms are off by 2^-19 at most
-// (the difference's rounding at 30 temperatures, and few of fp32 more; deeper
-// ids weigh two units at most), their sums of eight by 2^-21.
-constexpr double kTailError = 3.814697265625e-06;  // 2^-18
-constexpr double kTailUnits = 1048576.0;           // 2^20: four units an id
+// The bounds of an estimated tail.  A term's exponent is off by 3 2^-24 of
+// itself (the difference's, the factor's and the product's rounding), of
+// 30 log2(e) = 43.3 at most: 5.4e-6 of the term; the exponential by 2.4e-7 and a
+// sum of eight by 4.2e-7.  Ids that lie deeper weigh two units at most, and
+// each weight is rounded to a unit: four units an id.
+constexpr double kTailError = 7.62939453125e-06;   // 2^-17
+constexpr double kTailUnits = 1048576.0;           // 2^20
+
+// What every wave of a workgroup sees of a row's chunks: lane i chunk i's record.
+struct Records {
+    ChunkRec rec;
+    float m;                     // largest logit
+    bool ok;
+    uint32_t n, off;             // candidates of the row; before this lane's chunk
+    bool full;                   // more than a chunk or the row may list
+};
+__device__ __forceinline__ Records records_of(const SampleArgs &a, int ri) {
+    Records r;
+    const int lane = threadIdx.x & 63;
+    r.rec = ChunkRec{kNoKey, 0, 0, 0, 0.0, 0.0};
+    if (lane < a.chunks) r.rec = a.chunk[(int64_t)ri * a.chunks + lane];
+    r.m = wave_max(of_key(r.rec.top));
+    r.ok = !__any(r.rec.odd) && r.m > -INFINITY;
+    const uint32_t inc = wave_incl_scan_dpp(r.rec.n);
+    r.n = (uint32_t)__builtin_amdgcn_readlane((int)inc, 63);
+    r.off = inc - r.rec.n;
+    r.full = __any(r.rec.n > (uint32_t)a.room) || r.n > (uint32_t)kListed;
+    return r;
+}
+// Where candidate i of a row lies, off_s[c] of them before chunk c's.
+__device__ __forceinline__ int64_t place_of(const SampleArgs &a, int ri, const uint32_t (&off_s)[64], uint32_t i) {
+    int lo = 0, hi = a.chunks;                  // the last chunk that begins at or before it
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off_s[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    return ((int64_t)ri * a.chunks + lo) * a.room + (i - off_s[lo]);
+}
 
 template <bool DRAW>
 __device__ __forceinline__ void mark_fault(const SampleArgs &a, int ri) {
@@ -579,69 +386,73 @@ __device__ __forceinline__ void mark_fault(const SampleArgs &a, int ri) {
         if (a.out_logq) a.out_logq[i] = NAN;
     }
     if (a.out_kept) a.out_kept[i] = -1;
-    a.row[ri] = RowRec{kFault, 0, 0.f, 0};
+    RowRec r{};
+    r.state = kFault;
+    a.row[ri] = r;
     atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
 }
 
-__device__ __forceinline__ Weights weights_of(float m, float t, const double *table) {
-    return Weights{(double)m, t == 0.f ? 0.0 : 64.0 * kLog2e / (double)t, table};
-}
-__device__ __forceinline__ float log_share(const Weights &wt, float x, float t, u64 total) {
-    return t == 0.f ? 0.f : (float)(((double)x - wt.m) / (double)t - log((double)total / kOne));
+// Sorts n <= kSorted numbers in shared memory, ascending, over the next power
+// of two (what lies behind n becomes the largest number).  Pairs of a wave's
+// own 128 numbers need no barrier: a wave's accesses to shared memory are in order.
+__device__ __forceinline__ void sort_shared(u64 *x, int n) {
+    const int tid = threadIdx.x;
+    int size = 64;
+    while (size < n) size *= 2;
+    for (int i = n + tid; i < size; i += kBlock) x[i] = ~0ull;
+    __syncthreads();
+    for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j; j /= 2) {
+            for (int t = tid; t < size / 2; t += kBlock) {
+                const int i = 2 * t - (t & (j - 1));
+                const u64 p = x[i], q = x[i + j];
+                if ((p > q) == !(i & k)) {
+                    x[i] = q;
+                    x[i + j] = p;
+                }
+            }
+            if (j > 64 || (j == 1 && 2 * k > 128)) __syncthreads();
+            else {
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            }
+        }
+    __syncthreads();
 }
 
 template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
-    constexpr int N = Row<T>::N, NB = kChunk / (kBlock * N);
     __shared__ Scratch<kBlock> s;
     __shared__ float val_s[kListed];
     __shared__ uint32_t id_s[DRAW ? 1 : kListed];
-    __shared__ uint32_t off_s[64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int ri = DRAW ? blockIdx.x / a.chunks : blockIdx.x, c = DRAW ? blockIdx.x - ri * a.chunks : 0;
+    __shared__ uint32_t off_s[64], few_s[kMostTopK];
+    __shared__ u64 total_s;
+    __shared__ uint32_t ends_s[2];
+    const int tid = threadIdx.x, lane = tid & 63, ri = blockIdx.x;
     const Setting g = setting_of<DRAW>(a, a.row0 + ri);
-    if (!g.live || (c && !g.whole)) return;
-    if (!g.ok) {
-        if (tid == 0 && c == 0) mark_fault<DRAW>(a, ri);
+    if (!g.live) return;
+    const Records r = records_of(a, ri);
+    if (!g.ok || !r.ok) {
+        if (tid == 0) mark_fault<DRAW>(a, ri);
         return;
     }
-    // ---- the row, by every wave: lane i takes chunk i's record
-    ChunkRec rec{kNoKey, 0, 0, 0, 0.0, 0.0};
-    if (lane < a.chunks) rec = a.chunk[(int64_t)ri * a.chunks + lane];
-    const float m = wave_max(of_key(rec.top));
-    if (__any(rec.odd) || !(m > -INFINITY)) {
-        if (tid == 0 && c == 0) mark_fault<DRAW>(a, ri);
-        return;
-    }
-    const uint32_t finite = wave_sum_u32(rec.finite);
-    const Weights wt = weights_of(m, g.t, s.table);
-    if (tid < 64) s.table[tid] = exp2((double)tid / 64);
+    const float m = r.m;
+    const uint32_t finite = wave_sum_u32(r.rec.finite), n = r.n;
     const int64_t out = a.row0 + ri, list = (int64_t)ri * a.chunks * a.room;
-    if (g.whole) {
-        if (tid == 0 && c == 0) {
-            if (a.out_kept) a.out_kept[out] = (int32_t)finite;
-            a.row[ri] = RowRec{kWhole, 0, m, finite};
-        }
-        if constexpr (DRAW) {
-            const Row<T> row = row_of<T>(a.logits, out * a.ld, a.V);
-            u32x4_t w[NB];
-            load_blocks<NB>(row, c * (kChunk / N) + wave * 64 * NB + lane, 64, w);
-            __syncthreads();
-            u64 *subs = a.subs + ((int64_t)ri * a.chunks + c) * (kChunk / 256) + wave * NB;
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                u64 sum = 0;
-#pragma unroll
-                for (int i = 0; i < N; ++i) sum += weight(wt, Unpack<T>::get(w[j], i));
-                sum = wave_sum_u64(sum);
-                if (lane == 0) subs[j] = sum;
-            }
-        }
-        return;
-    }
+    RowRec rec{};
+    rec.m = m;
+    rec.finite = finite;
+    auto leave = [&](uint32_t state, bool second, bool third) {
+        if (tid) return;
+        rec.state = state;
+        a.row[ri] = rec;
+        if (second) a.second[atomicAdd(&a.work->second, 1u)] = (uint32_t)ri;
+        if (third) a.third[atomicAdd(&a.work->third, 1u)] = (uint32_t)ri;
+    };
     if (g.greedy) {
         // the first chunk that has it lists the lowest id first
-        const int at = __ffsll((unsigned long long)__ballot(of_key(rec.top) == m)) - 1;
+        const int at = __ffsll((unsigned long long)__ballot(of_key(r.rec.top) == m)) - 1;
         if (tid == 0) {
             const uint32_t id = a.ids[list + (int64_t)at * a.room];
             if constexpr (DRAW) {
@@ -652,104 +463,204 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
                 a.ids[list] = id;
             }
             if (a.out_kept) a.out_kept[out] = 1;
-            a.row[ri] = RowRec{kDone, 1, m, finite};
         }
-        return;
+        rec.n = 1;
+        return leave(kDone, false, false);
     }
-    const uint32_t inc = wave_incl_scan_dpp(rec.n);
-    const uint32_t n = (uint32_t)__builtin_amdgcn_readlane((int)inc, 63);
-    if (wave == 0) off_s[lane] = inc - rec.n;
-    if (g.many || __any(rec.n > (uint32_t)a.room) || n > (uint32_t)kListed) {
-        if (tid == 0) a.row[ri] = RowRec{kMany, 0, m, finite};
-        return;
+    const bool cuts = g.k > 0 && (uint32_t)g.k < finite;  // top_k leaves some out
+    const uint32_t low = min_p_key(m, g);
+    if (!cuts && g.p >= 1.f && (g.mp == 0.f || g.many || r.full)) {
+        rec.key = low;
+        if (tid == 0 && g.mp == 0.f && a.out_kept) a.out_kept[out] = (int32_t)finite;
+        return leave(kWhole, DRAW || g.mp > 0.f, false);
+    }
+    rec.by_weight = !cuts;
+    if (g.many || r.full) {
+        const bool many = cuts && g.p < 1.f;
+        return leave(many ? kMany : kDeep, !many, !many);
+    }
+    // ---- candidates, in the order of ids
+    const Weights wt = weights_of(m, g.t, s.table);
+    if (tid < 64) {
+        s.table[tid] = exp2((double)tid / 64);
+        off_s[tid] = r.off;
     }
     __syncthreads();
-    // ---- candidates, in the order of ids
-    auto place = [&](uint32_t i) -> int64_t {   // of the row's candidate i
-        int lo = 0, hi = a.chunks;              // the last chunk that begins at or before it
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (off_s[mid] <= i) lo = mid;
-            else hi = mid;
-        }
-        return list + (int64_t)lo * a.room + (i - off_s[lo]);
-    };
-    uint32_t lo = 0xffffffffu, hi = 0;
-    u64 sum = 0;
     for (uint32_t i = tid; i < n; i += kBlock) {
-        const int64_t at = place(i);
-        const float x = a.vals[at];
-        val_s[i] = x;
+        const int64_t at = place_of(a, ri, off_s, i);
+        val_s[i] = a.vals[at];
         if (!DRAW) id_s[i] = a.ids[at];
-        lo = min(lo, key_of(x));
-        hi = max(hi, key_of(x));
-        if (g.p < 1.f) sum += weight(wt, x);
     }
-    block_ends(s, lo, hi);
-    Pair all;
-    block_before(s, Pair{0, sum}, all);
-    u64 total = all.w;                          // of the candidates
-    auto each = [&](auto f) {
-        for (uint32_t i = tid; i < n; i += kBlock) f(key_of(val_s[i]));
-    };
-    // ---- the cut
-    Cut cut{kNoKey, 0};
-    // (fewer candidates than k: only ids below min_p's edge are missing, and
-    // the edge comes before the k-th id)
-    const bool few = g.k > 0 && (uint32_t)g.k < finite && (uint32_t)g.k <= n;
-    bool many = false;
-    if (few) cut = cut_among(s, wt, lo, hi, Pair{0, 0}, Want{false, (uint32_t)g.k, 0}, g.p < 1.f, total, each);
-    if (g.p < 1.f) {
-        u64 slack = 0;
-        Want want = top_p_want(g.p, total);
+    __syncthreads();
+    // What top_p wants of candidates that weigh `total`: at least `want`, at
+    // most `slack` more.  (Where top_k is set, they are all that counts.)
+    u64 slack = 0;
+    auto top_p_of = [&](u64 total) -> u64 {
+        u64 least = total, most = total;
         if (g.k == 0) {
-            const double share = exp(((double)of_key(rec.top) - wt.m) / (double)g.t);
-            const double rest = wave_sum(lane < a.chunks ? rec.tail * share : 0.0) * kOne;
-            const u64 least = (u64)fmax(0.0, rest * (1.0 - kTailError) - kTailUnits);
-            want = top_p_want(g.p, total + least);
-            slack = top_p_want(g.p, total + (u64)(rest * (1.0 + kTailError) + kTailUnits)).w - want.w;
+            const double share = exp(((double)of_key(r.rec.top) - (double)m) / (double)g.t);
+            const double rest = wave_sum(lane < a.chunks ? r.rec.tail * share : 0.0) * kOne;
+            least += (u64)fmax(0.0, rest * (1.0 - kTailError) - kTailUnits);
+            most += (u64)(rest * (1.0 + kTailError) + kTailUnits);
         }
-        // Every id at or above the largest chunk's edge is a candidate, ids
-        // below need not be: a cut there is not to be trusted (unless min_p's is
-        // above that edge, and so the shorter one).
-        const float edge = m - kHot * g.t;
-        const float low = g.mp > 0.f ? of_key(min_p_key(m, g.t, g.mp)) : -INFINITY;
-        Cut q{kNoKey, 0};
-        u64 reached = 0;
-        if (want.w + slack <= total) q = cut_among(s, wt, lo, hi, Pair{0, 0}, want, true, reached, each);
-        if (g.k == 0 && of_key(q.key) < fmaxf(edge, low)) {
-            many = low < edge;
-        } else {
-            many = reached < want.w + slack;    // the bounds' ends differ in their cuts
-            cut = few ? shorter(cut, q) : q;
-        }
-    }
-    if (many) {
-        if (tid == 0) a.row[ri] = RowRec{kMany, 0, m, finite};
-        return;
-    }
-    if (g.mp > 0.f) cut = shorter(cut, Cut{min_p_key(m, g.t, g.mp), 0xffffffffu});
-    // ---- what it leaves: neighbouring candidates to a thread
-    const uint32_t per = (n + kBlock - 1) / kBlock, from = min(tid * per, n), to = min(from + per, n);
-    uint32_t eq = 0;
-    for (uint32_t i = from; i < to; ++i) eq += key_of(val_s[i]) == cut.key;
-    const uint32_t tie0 = block_before(s, Pair{eq, 0}, all).n;
-    uint32_t tie = tie0;
-    Pair mine{0, 0};
-    auto kept = [&](uint32_t i) {
-        const uint32_t k = key_of(val_s[i]);
-        const bool equal = k == cut.key, in = k > cut.key || (equal && tie < cut.ties);
-        tie += equal;
-        return in;
+        const u64 want = top_p_want(g.p, least).w;
+        slack = top_p_want(g.p, most).w - want;
+        return want;
     };
+    // Every id at or above the largest chunk's edge is a candidate, ids below
+    // need not be: top_p's cut there is not to be trusted, unless min_p's is above
+    // that edge, and so the shorter one.
+    const float edge = hot_edge(m, g);
+    const bool by_low = of_key(low) >= edge;
+    auto trusted = [&](uint32_t key) { return g.k > 0 || of_key(key) >= fmaxf(edge, of_key(low)); };
+    // Candidates that are kept have their bit in s.count.
+    auto flag = [&](uint32_t i) { atomicOr(&s.count[i >> 5], 1u << (i & 31)); };
+    auto clear_flags = [&]() {
+        __syncthreads();
+        for (int i = tid; i < kListed / 32; i += kBlock) s.count[i] = 0u;
+        __syncthreads();
+    };
+    bool deep = false;
+    const bool few = cuts && n >= (uint32_t)g.k;  // (fewer: min_p's cut comes before the k-th id)
+    if (n <= kSorted || few) {
+        // ---- sorted: the k best first where they are more than that
+        uint32_t na = n;
+        if (n > kSorted) {
+            uint32_t lo = 0xffffffffu, hi = 0;
+            for (uint32_t i = tid; i < n; i += kBlock) {
+                lo = min(lo, key_of(val_s[i]));
+                hi = max(hi, key_of(val_s[i]));
+            }
+            block_ends(s, lo, hi);
+            u64 none;
+            const Cut cut = cut_among(s, wt, lo, hi, Pair{0, 0}, Want{false, (uint32_t)g.k, 0}, false, none, [&](auto f) {
+                for (uint32_t i = tid; i < n; i += kBlock) f(key_of(val_s[i]));
+            });
+            const uint32_t per = (n + kBlock - 1) / kBlock, from = min(tid * per, n), to = min(from + per, n);
+            Pair all, mine{0, 0};
+            for (uint32_t i = from; i < to; ++i) {
+                mine.n += key_of(val_s[i]) == cut.key;
+                mine.w += key_of(val_s[i]) > cut.key;
+            }
+            const Pair before = block_before(s, mine, all);
+            uint32_t tie = before.n, at = (uint32_t)before.w + min(before.n, cut.ties);
+            for (uint32_t i = from; i < to; ++i) {
+                const uint32_t key = key_of(val_s[i]);
+                if (key > cut.key || (key == cut.key && tie < cut.ties)) few_s[at++] = i;
+                tie += key == cut.key;
+            }
+            na = (uint32_t)g.k;
+            __syncthreads();
+        }
+        auto nth = [&](uint32_t i) { return n > kSorted ? few_s[i] : i; };
+        for (uint32_t i = tid; i < na; i += kBlock) s.mass[i] = (u64)~key_of(val_s[nth(i)]) << 32 | i;
+        sort_shared(s.mass, (int)na);
+        // ---- a thread's neighbours in that order
+        constexpr int E = kSorted / kBlock;
+        const uint32_t e = (na + kBlock - 1) / kBlock;
+        uint32_t key[E];
+        u64 w[E];
+        Pair sum{0, 0}, all;
+#pragma unroll
+        for (uint32_t i = 0; i < E; ++i) {
+            const uint32_t at = tid * e + i;
+            const bool in = i < e && at < na;
+            key[i] = in ? ~(uint32_t)(s.mass[at] >> 32) : 0u;
+            w[i] = in && g.p < 1.f ? weight(wt, of_key(key[i])) : 0;
+            sum = sum + Pair{in && key[i] >= low, w[i]};
+        }
+        const Pair before = block_before(s, sum, all);
+        uint32_t keep = min(all.n, na);         // what min_p leaves
+        const uint32_t nk = few ? (uint32_t)g.k : na;
+        keep = min(keep, nk);
+        if (g.p < 1.f) {
+            if (tid == 0) {
+                total_s = all.w;
+                ends_s[0] = ends_s[1] = 0;
+            }
+            __syncthreads();
+            u64 run = before.w;
+#pragma unroll
+            for (uint32_t i = 0; i < E; ++i) {
+                run += w[i];
+                if (i < e && tid * e + i + 1 == nk) total_s = run;
+            }
+            __syncthreads();
+            const u64 want = top_p_of(total_s);
+            run = before.w;
+#pragma unroll
+            for (uint32_t i = 0; i < E; ++i) {
+                const uint32_t at = tid * e + i + 1;
+                if (i < e && run < want && run + w[i] >= want) ends_s[0] = at;
+                if (i < e && run < want + slack && run + w[i] >= want + slack) ends_s[1] = at;
+                run += w[i];
+            }
+            __syncthreads();
+            const uint32_t np = ends_s[0];
+            const bool sure = np && trusted(~(uint32_t)(s.mass[np - 1] >> 32));
+            if (sure) {
+                deep = np != ends_s[1];         // the bounds' ends differ in their cuts
+                keep = min(keep, np);
+            } else {
+                deep = !by_low;
+            }
+        }
+        if (!deep) {
+            clear_flags();
+            for (uint32_t i = tid; i < keep; i += kBlock) flag(nth((uint32_t)s.mass[i]));
+        }
+    } else {
+        // ---- by histograms
+        Cut cut{low, 0xffffffffu};
+        if (g.p < 1.f) {
+            uint32_t lo = 0xffffffffu, hi = 0;
+            Pair sum{0, 0}, all;
+            for (uint32_t i = tid; i < n; i += kBlock) {
+                lo = min(lo, key_of(val_s[i]));
+                hi = max(hi, key_of(val_s[i]));
+                sum.w += weight(wt, val_s[i]);
+            }
+            block_ends(s, lo, hi);
+            block_before(s, sum, all);
+            const u64 want = top_p_of(all.w);
+            Cut q{kNoKey, 0};
+            u64 reached = 0;
+            if (want + slack <= all.w)
+                q = cut_among(s, wt, lo, hi, Pair{0, 0}, Want{true, 0, want}, true, reached, [&](auto f) {
+                    for (uint32_t i = tid; i < n; i += kBlock) f(key_of(val_s[i]));
+                });
+            if (trusted(q.key)) {
+                deep = reached < want + slack;
+                cut = shorter(cut, q);
+            } else {
+                deep = !by_low;
+            }
+        }
+        if (!deep) {
+            clear_flags();
+            const uint32_t per = (n + kBlock - 1) / kBlock, from = min(tid * per, n), to = min(from + per, n);
+            Pair all, mine{0, 0};
+            for (uint32_t i = from; i < to; ++i) mine.n += key_of(val_s[i]) == cut.key;
+            uint32_t tie = block_before(s, mine, all).n;
+            for (uint32_t i = from; i < to; ++i) {
+                const uint32_t key = key_of(val_s[i]);
+                if (key > cut.key || (key == cut.key && tie < cut.ties)) flag(i);
+                tie += key == cut.key;
+            }
+        }
+    }
+    if (deep) return leave(kDeep, true, true);
+    // ---- what is kept, in the order of ids
+    __syncthreads();
+    const uint32_t per = (n + kBlock - 1) / kBlock, from = min(tid * per, n), to = min(from + per, n);
+    auto kept = [&](uint32_t i) { return s.count[i >> 5] >> (i & 31) & 1u; };
+    Pair mine{0, 0}, all;
     for (uint32_t i = from; i < to; ++i)
         if (kept(i)) mine = mine + Pair{1, DRAW ? weight(wt, val_s[i]) : 0};
     Pair at = block_before(s, mine, all);
-    tie = tie0;
-    if (tid == 0) {
-        if (a.out_kept) a.out_kept[out] = (int32_t)all.n;
-        a.row[ri] = RowRec{kDone, all.n, m, finite};
-    }
+    if (tid == 0 && a.out_kept) a.out_kept[out] = (int32_t)all.n;
+    rec.n = all.n;
+    leave(kDone, false, false);
     if constexpr (DRAW) {
         const u64 target = (u64)((double)g.u * (double)all.w);
         if (at.w > target || at.w + mine.w <= target) return;
@@ -757,7 +668,7 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
             if (!kept(i)) continue;
             at.w += weight(wt, val_s[i]);
             if (at.w > target) {
-                a.out_tokens[out] = (int32_t)a.ids[place(i)];
+                a.out_tokens[out] = (int32_t)a.ids[place_of(a, ri, off_s, i)];
                 if (a.out_logq) a.out_logq[out] = log_share(wt, val_s[i], g.t, all.w);
                 return;
             }
@@ -765,7 +676,7 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
     } else {
         for (uint32_t i = from; i < to; ++i) {
             if (!kept(i)) continue;
-            a.ids[list + at.n] = id_s[i];       // (read from shared memory alone since the barriers)
+            a.ids[list + at.n] = id_s[i];       // (candidates are read from shared memory alone by now)
             a.vals[list + at.n] = val_s[i];
             ++at.n;
         }
@@ -773,7 +684,150 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// third launch: rows that are not settled, and truncated rows
+// second, third
+// ---------------------------------------------------------------------------
+
+// Weights (DRAW) of the chunk's ids whose bits are set, per wave's load.
+template <typename T>
+__device__ __forceinline__ void sum_loads(const SampleArgs &a, int ri, int c, const Chunk<T> &k, uint32_t in, const Weights &wt) {
+    constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
+    u64 *subs = a.subs + ((int64_t)ri * a.chunks + c) * (kChunk / 256) + (threadIdx.x >> 6) * NB;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        u64 sum = 0;
+        if (__any(in >> (j * N) & ((1u << N) - 1u))) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) sum += in >> (j * N + i) & 1u ? weight(wt, k.x(j, i)) : 0;
+            sum = wave_sum_u64(sum);
+        }
+        if ((threadIdx.x & 63) == 0) subs[j] = sum;
+    }
+}
+
+template <typename T, bool DRAW>
+__global__ void __launch_bounds__(kBlock) second_kernel(SampleArgs a) {
+    constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
+    __shared__ u64 hist_s[kDeepBins];
+    __shared__ double table_s[64];
+    __shared__ uint32_t count_s[kWaves];
+    const int tid = threadIdx.x;
+    if (tid < 64) table_s[tid] = exp2((double)tid / 64);
+    const int items = (int)a.work->second * a.chunks;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int ri = (int)a.second[item / a.chunks], c = item % a.chunks;
+        const Setting g = setting_of<DRAW>(a, a.row0 + ri);
+        const RowRec rec = a.row[ri];
+        const Row<T> row = row_of<T>(a.logits, (int64_t)(a.row0 + ri) * a.ld, a.V);
+        const Weights wt = weights_of(rec.m, g.t, table_s);
+        Chunk<T> k;
+        load_chunk(row, c, k);
+        __syncthreads();                        // (the item before is done with shared memory)
+        if (rec.state == kWhole) {
+            uint32_t in = 0;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int i = 0; i < N; ++i) in |= (key_of(k.x(j, i)) >= rec.key ? 1u : 0u) << (j * N + i);
+            if (DRAW) sum_loads(a, ri, c, k, in, wt);
+            const uint32_t n = wave_sum_u32(__popc(in));
+            if ((tid & 63) == 0) count_s[tid >> 6] = n;
+            __syncthreads();
+            if (tid == 0) {
+                uint32_t all = 0;
+                for (int v = 0; v < kWaves; ++v) all += count_s[v];
+                a.chunk[(int64_t)ri * a.chunks + c].finite = all;
+            }
+        } else {
+            const Scale<kDeepBins> scale(rec.m, g.t);
+            hist_s[tid] = 0;
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float x = k.x(j, i);
+                    if (x > -INFINITY) atomicAdd(&hist_s[scale.bin(x)], rec.by_weight ? weight(wt, x) : 1ull);
+                }
+            __syncthreads();
+            a.hist[((int64_t)ri * a.chunks + c) * kDeepBins + tid] = hist_s[tid];
+        }
+    }
+}
+
+template <typename T, bool DRAW>
+__global__ void __launch_bounds__(kBlock) third_kernel(SampleArgs a) {
+    constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
+    __shared__ u64 wave_s[kWaves], above_s, there_s;
+    __shared__ int bin_s;
+    __shared__ double table_s[64];
+    __shared__ uint32_t count_s[kWaves], above_n_s[kWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (tid < 64) table_s[tid] = exp2((double)tid / 64);
+    const int items = (int)a.work->third * a.chunks;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int ri = (int)a.third[item / a.chunks], c = item % a.chunks;
+        const Setting g = setting_of<DRAW>(a, a.row0 + ri);
+        const RowRec rec = a.row[ri];
+        const Row<T> row = row_of<T>(a.logits, (int64_t)(a.row0 + ri) * a.ld, a.V);
+        const Weights wt = weights_of(rec.m, g.t, table_s);
+        Chunk<T> k;
+        load_chunk(row, c, k);
+        // ---- the row's histogram, the highest bin in thread 0
+        const u64 *h = a.hist + (int64_t)ri * a.chunks * kDeepBins + (kDeepBins - 1 - tid);
+        u64 mine = 0;
+        for (int i = 0; i < a.chunks; ++i) mine += h[i * kDeepBins];
+        const u64 inc = wave_scan_u64(mine);
+        __syncthreads();                        // (the item before is done with shared memory)
+        if (lane == 63) wave_s[wave] = inc;
+        __syncthreads();
+        u64 before = inc - mine, total = 0;
+        for (int v = 0; v < kWaves; ++v) {
+            if (v < wave) before += wave_s[v];
+            total += wave_s[v];
+        }
+        const u64 want = rec.by_weight ? top_p_want(g.p, total).w : (u64)g.k;
+        if (before < want && before + mine >= want) {
+            bin_s = kDeepBins - 1 - tid;
+            above_s = before;
+        }
+        __syncthreads();
+        const int bin = bin_s;
+        if (c == 0 && tid == 0) {
+            DeepRec d;
+            d.bin = bin;
+            d.above = rec.by_weight ? Pair{0, above_s} : Pair{(uint32_t)above_s, 0};
+            d.want = rec.by_weight ? Want{true, 0, want} : Want{false, (uint32_t)want, 0};
+            a.deep[ri] = d;
+        }
+        // ---- ids in it and above it, of those that min_p leaves
+        const Scale<kDeepBins> scale(rec.m, g.t);
+        const uint32_t low = min_p_key(rec.m, g);
+        uint32_t hits = 0, above = 0;
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float x = k.x(j, i);
+                const int b = scale.bin(x);
+                const bool in = key_of(x) >= low;
+                hits |= (in && b == bin ? 1u : 0u) << (j * N + i);
+                above |= (in && b > bin ? 1u : 0u) << (j * N + i);
+            }
+        if (DRAW) sum_loads(a, ri, c, k, above, wt);
+        const uint32_t n = wave_sum_u32(__popc(above));
+        if (lane == 0) above_n_s[wave] = n;
+        const uint32_t listed = list_hits(a, ri, c, row, k, hits, count_s);
+        if (tid == 0) {
+            ChunkRec &out = a.chunk[(int64_t)ri * a.chunks + c];
+            out.finite = 0;
+            for (int v = 0; v < kWaves; ++v) out.finite += above_n_s[v];
+            out.n = listed;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the last launches
 // ---------------------------------------------------------------------------
 
 template <typename T> __device__ __forceinline__ T masked();
@@ -784,31 +838,9 @@ template <typename T> __device__ __forceinline__ T element_of(float x) {
     else return x;
 }
 
-// First histogram of a whole row: bins of equal width down to the deepest
-// logit with a weight, and one for the rest; the highest bin holds the largest.
-// A function of the logit alone that does not rise where the logit falls.
-struct Scale {
-    float m, per;                // largest logit, bins per unit
-};
-__device__ __forceinline__ int bin_of(const Scale &s, float x) {
-    return kBins - 1 - (int)fminf((s.m - x) * s.per, (float)(kBins - 1));
-}
-
-// Calls f for each finite logit of a row, in no order.
-template <typename T, typename F>
-__device__ __forceinline__ void for_each_logit(const Row<T> &row, F f) {
-    constexpr int N = Row<T>::N, NB = 4;
-    for (int b = threadIdx.x; b < row.blocks; b += NB * kRowThreads) {
-        u32x4_t w[NB];
-        load_blocks<NB>(row, b, kRowThreads, w);
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float x = Unpack<T>::get(w[j], i);
-                if (x > -INFINITY) f(x);
-            }
-    }
+template <typename T> __device__ __forceinline__ void set_element(u32x4_t &w, int i, T e) {
+    if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(e);
+    else w[i >> 1] = i & 1 ? (w[i >> 1] & 0xffffu) | (uint32_t)e << 16 : (w[i >> 1] & 0xffff0000u) | e;
 }
 
 template <typename T> struct RowShared {
@@ -816,14 +848,66 @@ template <typename T> struct RowShared {
     static constexpr int SUBS = SPEC_MAX_VERIFY_VOCAB / SUB + 1;
     static constexpr int EACH = (SUBS + kRowThreads - 1) / kRowThreads;
     Scratch<kRowThreads> s;
-    uint32_t list[kListKeys];
-    u64 sub_w[SUBS];             // weight above the cut, per wave's load
-    uint32_t sub_n[SUBS];        // ids above it,
-    uint32_t sub_e[SUBS];        // and at it
+    float val[kListed];          // candidates: logits,
+    uint32_t id[kListed];        // and ids
+    u64 sub_w[SUBS];             // kept weight, per wave's load
+    uint32_t sub_e[SUBS];        // ids at the cut's key
+    uint32_t off[64];
     u64 at_w;                    // of the load that holds the drawn token: weight
     uint32_t at_e;               // and ties before it
     int at_sub;
 };
+
+// The exact cut of a kDeep row, from the ids listed in its bin; candidates
+// and their tie ranks stay with the threads, n / kRowThreads neighbours each.
+// False: more ids than a list holds.
+struct Deep {
+    Cut cut;
+    uint32_t n, from, to;        // candidates; this thread's
+    uint32_t tie;                // ties before its first
+    uint32_t above;              // kept ids of higher bins
+};
+template <typename T>
+__device__ __forceinline__ bool deep_cut(const SampleArgs &a, RowShared<T> &sh, int ri, const Setting &g,
+                                         const RowRec &rec, const Weights &wt, Deep &d) {
+    constexpr int B = kRowThreads;
+    const int tid = threadIdx.x;
+    const Records r = records_of(a, ri);
+    if (r.full) return false;
+    const DeepRec bin = a.deep[ri];
+    d.n = r.n;
+    d.above = wave_sum_u32((tid & 63) < a.chunks ? r.rec.finite : 0u);
+    if (tid < 64) sh.off[tid] = r.off;
+    __syncthreads();
+    uint32_t lo = 0xffffffffu, hi = 0;
+    Pair sum{0, 0}, all;
+    for (uint32_t i = tid; i < d.n; i += B) {
+        const int64_t at = place_of(a, ri, sh.off, i);
+        const float x = a.vals[at];
+        sh.val[i] = x;
+        sh.id[i] = a.ids[at];
+        lo = min(lo, key_of(x));
+        hi = max(hi, key_of(x));
+        sum = sum + Pair{1, bin.want.by_weight ? weight(wt, x) : 0};
+    }
+    block_ends(sh.s, lo, hi);
+    block_before(sh.s, sum, all);
+    // (not reached where min_p left ids of the bin, or all of them, out: its cut is the shorter)
+    d.cut = Cut{min_p_key(rec.m, g), 0xffffffffu};
+    if (bin.want.reached(bin.above + all)) {
+        u64 none;
+        d.cut = shorter(d.cut, cut_among(sh.s, wt, lo, hi, bin.above, bin.want, bin.want.by_weight, none, [&](auto f) {
+            for (uint32_t i = tid; i < d.n; i += B) f(key_of(sh.val[i]));
+        }));
+    }
+    const uint32_t per = (d.n + B - 1) / B;
+    d.from = min(tid * per, d.n);
+    d.to = min(d.from + per, d.n);
+    Pair mine{0, 0};
+    for (uint32_t i = d.from; i < d.to; ++i) mine.n += key_of(sh.val[i]) == d.cut.key;
+    d.tie = block_before(sh.s, mine, all).n;
+    return true;
+}
 
 // Wave 0: the token in load sh.at_sub whose weights, with sh.at_w before them,
 // pass the target.
@@ -863,23 +947,70 @@ __device__ __forceinline__ void draw_in_load(const SampleArgs &a, const RowShare
     }
 }
 
+// Draws from the kept weights of sh.sub_w, a thread's loads being EACH tid on;
+// the ties at the cut that each load holds stand in sh.sub_e.
+template <typename T>
+__device__ __forceinline__ void draw_row(const SampleArgs &a, RowShared<T> &sh, const Row<T> &row, const Weights &wt,
+                                         const Setting &g, Cut cut, int64_t out) {
+    constexpr int EACH = RowShared<T>::EACH;
+    const int tid = threadIdx.x, subs = (row.blocks + 63) / 64;
+    Pair mine[EACH], sum{0, 0}, all;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int sub = tid * EACH + i;
+        mine[i] = sub < subs ? Pair{sh.sub_e[sub], sh.sub_w[sub]} : Pair{0, 0};
+        sum = sum + mine[i];
+    }
+    Pair before = block_before(sh.s, sum, all);
+    const u64 target = (u64)((double)g.u * (double)all.w);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        if (before.w <= target && before.w + mine[i].w > target) {
+            sh.at_sub = tid * EACH + i;
+            sh.at_w = before.w;
+            sh.at_e = before.n;
+        }
+        before = before + mine[i];
+    }
+    __syncthreads();
+    if (tid < 64) draw_in_load(a, sh, row, wt, g, cut, all.w, target, out);
+}
+
+// Calls f for each finite logit of a row, in no order.
+template <typename T, typename F>
+__device__ __forceinline__ void for_each_logit(const Row<T> &row, F f) {
+    constexpr int N = Row<T>::N, NB = 4;
+    for (int b = threadIdx.x; b < row.blocks; b += NB * kRowThreads) {
+        u32x4_t w[NB];
+        load_blocks<NB>(row, b, kRowThreads, w);
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float x = Unpack<T>::get(w[j], i);
+                if (x > -INFINITY) f(x);
+            }
+    }
+}
+
 // A whole row by one workgroup.
 template <typename T, bool DRAW>
 __device__ __forceinline__ void whole_row(const SampleArgs &a, RowShared<T> &sh, const Row<T> &row, const Setting &g,
-                                          const RowRec &rec, int64_t out) {
-    constexpr int N = Row<T>::N, B = kRowThreads, SUBS = RowShared<T>::SUBS, EACH = RowShared<T>::EACH;
+                                          const RowRec &rec, const Weights &wt, int64_t out) {
+    constexpr int N = Row<T>::N, B = kRowThreads, EACH = RowShared<T>::EACH;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     Scratch<B> &s = sh.s;
-    const Weights wt = weights_of(rec.m, g.t, s.table);
-    if (tid < 64) s.table[tid] = exp2((double)tid / 64);
-    const Scale scale{rec.m, (float)((kBins - 1) / (kDeepest * (double)g.t))};
+    uint32_t *const keys = (uint32_t *)sh.val;
+    const Scale<kBins> scale(rec.m, g.t);
+    __syncthreads();                                  // (the weights' table)
     Cut cut{kNoKey, 0};                               // every id with a finite logit
     // ---- the cut
     const bool few = g.k > 0 && (uint32_t)g.k < rec.finite;
     if (few || g.p < 1.f) {
         clear_bins(s);
         for_each_logit(row, [&](float x) {
-            const int b = bin_of(scale, x);
+            const int b = scale.bin(x);
             atomicAdd(&s.count[b], 1u);
             if (g.p < 1.f) atomicAdd(&s.mass[b], weight(wt, x));
         });
@@ -902,20 +1033,20 @@ __device__ __forceinline__ void whole_row(const SampleArgs &a, RowShared<T> &sh,
             if (tid == 0) s.listed = 0;
             __syncthreads();
             for_each_logit(row, [&](float x) {
-                if (bin_of(scale, x) != bin) return;
+                if (scale.bin(x) != bin) return;
                 const uint32_t k = key_of(x);
                 lo = min(lo, k);
                 hi = max(hi, k);
-                if (listed) sh.list[atomicAdd(&s.listed, 1u)] = k;  // (counted and summed alone: any order)
+                if (listed) keys[atomicAdd(&s.listed, 1u)] = k;  // (counted and summed alone: any order)
             });
             block_ends(s, lo, hi);
             if (listed)
                 return cut_among(s, wt, lo, hi, above, want, g.p < 1.f, total, [&](auto f) {
-                    for (uint32_t i = tid; i < there.n; i += B) f(sh.list[i]);
+                    for (uint32_t i = tid; i < there.n; i += B) f(keys[i]);
                 });
             return cut_among(s, wt, lo, hi, above, want, g.p < 1.f, total, [&](auto f) {
                 for_each_logit(row, [&](float x) {
-                    if (bin_of(scale, x) == bin) f(key_of(x));
+                    if (scale.bin(x) == bin) f(key_of(x));
                 });
             });
         };
@@ -932,10 +1063,11 @@ __device__ __forceinline__ void whole_row(const SampleArgs &a, RowShared<T> &sh,
             cut = few ? shorter(cut, q) : q;
         }
     }
-    if (g.mp > 0.f) cut = shorter(cut, Cut{min_p_key(rec.m, g.t, g.mp), 0xffffffffu});
+    cut = shorter(cut, Cut{min_p_key(rec.m, g), 0xffffffffu});
     // ---- what the cut leaves, per wave's load in the order of ids
     __syncthreads();
     const int subs = (row.blocks + 63) / 64;
+    uint32_t *const sub_n = sh.id;
     constexpr int NB = 4;
     for (int s0 = wave; s0 < subs; s0 += NB * (B / 64)) {
         u32x4_t w[NB];
@@ -959,13 +1091,13 @@ __device__ __forceinline__ void whole_row(const SampleArgs &a, RowShared<T> &sh,
             const int sub = s0 + j * (B / 64);
             if (lane == 0 && sub < subs) {
                 sh.sub_w[sub] = sum;
-                sh.sub_n[sub] = n & 0xffffu;
+                sub_n[sub] = n & 0xffffu;
                 sh.sub_e[sub] = n >> 16;
             }
         }
     }
     __syncthreads();
-    // ---- thread i: its loads; ties before them, then weights
+    // ---- thread i: its loads; the ties that are kept of each
     const u64 each = cut.ties ? weight(wt, of_key(cut.key)) : 0;
     Pair all;
     uint32_t eq[EACH], eq_sum = 0;
@@ -975,34 +1107,24 @@ __device__ __forceinline__ void whole_row(const SampleArgs &a, RowShared<T> &sh,
         eq[i] = sub < subs ? sh.sub_e[sub] : 0u;
         eq_sum += eq[i];
     }
-    uint32_t eq_before = block_before(s, Pair{eq_sum, 0}, all).n;
-    cut.ties = min(cut.ties, all.n);
-    Pair mine[EACH], sum{0, 0};
+    uint32_t before = block_before(s, Pair{eq_sum, 0}, all).n;
+    Pair kept{0, 0};
     uint32_t tie_at[EACH];
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int sub = tid * EACH + i;
-        tie_at[i] = eq_before;
-        const uint32_t in = min(eq_before + eq[i], cut.ties) - min(eq_before, cut.ties);
-        mine[i] = sub < subs ? Pair{sh.sub_n[sub] + in, sh.sub_w[sub] + each * in} : Pair{0, 0};
-        sum = sum + mine[i];
-        eq_before += eq[i];
+        tie_at[i] = before;
+        const uint32_t in = min(before + eq[i], cut.ties) - min(before, cut.ties);
+        if (sub < subs) {
+            kept.n += sub_n[sub] + in;
+            sh.sub_w[sub] += each * in;
+        }
+        before += eq[i];
     }
-    Pair before = block_before(s, sum, all);
+    block_before(s, kept, all);
     if (tid == 0 && a.out_kept) a.out_kept[out] = (int32_t)all.n;
     if constexpr (DRAW) {
-        const u64 target = (u64)((double)g.u * (double)all.w);
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            if (before.w <= target && before.w + mine[i].w > target) {
-                sh.at_sub = tid * EACH + i;
-                sh.at_w = before.w;
-                sh.at_e = tie_at[i];
-            }
-            before = before + mine[i];
-        }
-        __syncthreads();
-        if (wave == 0) draw_in_load(a, sh, row, wt, g, cut, all.w, target, out);
+        draw_row(a, sh, row, wt, g, cut, out);
     } else {
         // the ties before each load
         __syncthreads();
@@ -1041,7 +1163,7 @@ __device__ __forceinline__ void whole_row(const SampleArgs &a, RowShared<T> &sh,
 
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) draw_kernel(SampleArgs a) {
-    constexpr int EACH = RowShared<T>::EACH, PER = kChunk / RowShared<T>::SUB;  // loads of a chunk
+    constexpr int PER = kChunk / RowShared<T>::SUB;    // loads of a chunk
     __shared__ RowShared<T> sh;
     const int tid = threadIdx.x, ri = blockIdx.x;
     const Setting g = setting_of<true>(a, a.row0 + ri);
@@ -1050,79 +1172,138 @@ __global__ void __launch_bounds__(kRowThreads) draw_kernel(SampleArgs a) {
     if (rec.state == kDone || rec.state == kFault) return;
     const int64_t out = a.row0 + ri;
     const Row<T> row = row_of<T>(a.logits, out * a.ld, a.V);
-    if (rec.state == kMany) {
-        whole_row<T, true>(a, sh, row, g, rec, out);
-        return;
-    }
     const Weights wt = weights_of(rec.m, g.t, sh.s.table);
     if (tid < 64) sh.s.table[tid] = exp2((double)tid / 64);
     const int subs = (row.blocks + 63) / 64;
     const u64 *in = a.subs + (int64_t)ri * a.chunks * (kChunk / 256);
-    u64 mine[EACH], sum = 0;
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-        const int sub = tid * EACH + i;
-        mine[i] = sub < subs ? in[sub / PER * (kChunk / 256) + sub % PER] : 0;
-        sum += mine[i];
-    }
-    Pair all;
-    u64 before = block_before(sh.s, Pair{0, sum}, all).w;
-    const u64 target = (u64)((double)g.u * (double)all.w);
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-        if (before <= target && before + mine[i] > target) {
-            sh.at_sub = tid * EACH + i;
-            sh.at_w = before;
-            sh.at_e = 0;
-        }
-        before += mine[i];
+    for (int i = tid; i < subs; i += kRowThreads) {
+        sh.sub_w[i] = rec.state == kMany ? 0 : in[i / PER * (kChunk / 256) + i % PER];
+        sh.sub_e[i] = 0;
     }
     __syncthreads();
-    if (tid < 64) draw_in_load(a, sh, row, wt, g, Cut{kNoKey, 0}, all.w, target, out);
+    if (rec.state == kWhole) {
+        if (g.mp > 0.f && a.out_kept && tid < 64) {
+            const uint32_t n = wave_sum_u32(tid < a.chunks ? a.chunk[(int64_t)ri * a.chunks + tid].finite : 0u);
+            if (tid == 0) a.out_kept[out] = (int32_t)n;
+        }
+        draw_row(a, sh, row, wt, g, Cut{rec.key, 0xffffffffu}, out);
+        return;
+    }
+    Deep d;
+    if (rec.state == kMany || !deep_cut(a, sh, ri, g, rec, wt, d)) {
+        __syncthreads();
+        whole_row<T, true>(a, sh, row, g, rec, wt, out);
+        return;
+    }
+    Pair mine{0, 0}, all;
+    for (uint32_t i = d.from; i < d.to; ++i) {
+        const uint32_t key = key_of(sh.val[i]);
+        const int sub = (int)(sh.id[i] + row.skip) / RowShared<T>::SUB;
+        if (key == d.cut.key) atomicAdd(&sh.sub_e[sub], 1u);
+        if (key > d.cut.key || (key == d.cut.key && d.tie < d.cut.ties)) {
+            atomicAdd(&sh.sub_w[sub], weight(wt, sh.val[i]));
+            ++mine.n;
+        }
+        d.tie += key == d.cut.key;
+    }
+    block_before(sh.s, mine, all);
+    if (tid == 0 && a.out_kept) a.out_kept[out] = (int32_t)(d.above + all.n);
+    draw_row(a, sh, row, wt, g, d.cut, out);
+}
+
+// Cuts of truncated rows that are still to be found, for write_kernel; rows
+// done whole.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) settle_kernel(SampleArgs a) {
+    __shared__ RowShared<T> sh;
+    const int tid = threadIdx.x, ri = blockIdx.x;
+    const Setting g = setting_of<false>(a, a.row0 + ri);
+    if (!g.live) return;
+    RowRec rec = a.row[ri];
+    const int64_t out = a.row0 + ri;
+    if (rec.state == kWhole && g.mp > 0.f) {
+        if (a.out_kept && tid < 64) {
+            const uint32_t n = wave_sum_u32(tid < a.chunks ? a.chunk[(int64_t)ri * a.chunks + tid].finite : 0u);
+            if (tid == 0) a.out_kept[out] = (int32_t)n;
+        }
+        return;
+    }
+    if (rec.state != kDeep && rec.state != kMany) return;
+    const Weights wt = weights_of(rec.m, g.t, sh.s.table);
+    if (tid < 64) sh.s.table[tid] = exp2((double)tid / 64);
+    __syncthreads();
+    Deep d;
+    if (rec.state == kMany || !deep_cut(a, sh, ri, g, rec, wt, d)) {
+        __syncthreads();
+        whole_row<T, false>(a, sh, row_of<T>(a.logits, out * a.ld, a.V), g, rec, wt, out);
+        if (tid == 0) a.row[ri].state = kWritten;
+        return;
+    }
+    Pair mine{0, 0}, all;
+    uint32_t lo = 0xffffffffu, last = 0;
+    for (uint32_t i = d.from; i < d.to; ++i) {
+        const uint32_t key = key_of(sh.val[i]);
+        if (key > d.cut.key || (key == d.cut.key && d.tie < d.cut.ties)) {
+            ++mine.n;
+            if (key == d.cut.key) last = sh.id[i];
+        }
+        d.tie += key == d.cut.key;
+    }
+    block_before(sh.s, mine, all);
+    block_ends(sh.s, lo, last);
+    if (tid) return;
+    rec.state = kCut;
+    rec.key = d.cut.key;
+    // (min_p's cut may lie above the bin, and has no end)
+    rec.last = d.cut.ties == 0xffffffffu ? 0xffffffffu : last;
+    if (a.out_kept) a.out_kept[out] = (int32_t)(d.above + all.n);
+    a.row[ri] = rec;
 }
 
 // Truncated rows: kWriteIds ids a workgroup.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) write_kernel(SampleArgs a, int parts) {
     constexpr int N = Row<T>::N;
-    __shared__ RowShared<T> sh;
     const int tid = threadIdx.x, ri = blockIdx.x / parts, part = blockIdx.x - ri * parts;
     const Setting g = setting_of<false>(a, a.row0 + ri);
     if (!g.live) return;
     const RowRec rec = a.row[ri];
+    if (rec.state == kWritten) return;
     const int64_t out = a.row0 + ri;
-    const Row<T> row = row_of<T>(a.logits, out * a.ld, a.V);
-    if (rec.state == kMany) {
-        if (part == 0) whole_row<T, false>(a, sh, row, g, rec, out);
-        return;
-    }
     // blocks of the output row; its first and last may be other rows' too
-    const Row<T> dst = row_of<T>(a.out_logits, out * a.out_ld, a.V);
+    const Row<T> row = row_of<T>(a.logits, out * a.ld, a.V), dst = row_of<T>(a.out_logits, out * a.out_ld, a.V);
     T *const to = (T *)dst.p;
     const int b0 = part * (kWriteIds / N), b1 = min(b0 + kWriteIds / N, dst.blocks);
-    const bool copy = rec.state == kWhole;
-    if (copy && row.p == dst.p && row.skip == dst.skip) return;  // in place
-    const T fill = rec.state == kFault ? element_of<T>(NAN) : masked<T>();
+    const bool copy = rec.state == kWhole || rec.state == kCut, alike = row.skip == dst.skip;
+    if (copy && g.whole && row.p == dst.p && alike) return;  // in place
     const uint32_t nan = sizeof(T) == 2 ? 0x7fc07fc0u : 0x7fc00000u;
     const uint32_t word = rec.state == kFault ? nan : Unpack<T>::kMasked;
-    const bool alike = row.skip == dst.skip;
+    const uint32_t last = rec.state == kCut ? rec.last : 0xffffffffu;
+    auto kept = [&](float x, int id) {
+        const uint32_t k = key_of(x);
+        return k > rec.key || (k == rec.key && (uint32_t)id <= last);
+    };
     for (int b = b0 + tid; b < b1; b += kRowThreads) {
         const int id = b * N - dst.skip;
-        if (id >= 0 && id + N <= a.V) {
-            u32x4_t w{word, word, word, word};
-            if (copy) {
-                if (alike) w = *(const u32x4_t *)(row.p + (int64_t)b * N);
-                else {
-                    T e[N];
+        const bool whole = id >= 0 && id + N <= a.V;
+        u32x4_t w{word, word, word, word};
+        if (copy) {
+            if (whole && alike) w = *(const u32x4_t *)(row.p + (int64_t)b * N);
+            else {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) e[i] = row.p[row.skip + id + i];
-                    w = __builtin_bit_cast(u32x4_t, e);
-                }
+                for (int i = 0; i < N; ++i)
+                    if (id + i >= 0 && id + i < a.V) set_element<T>(w, i, row.p[row.skip + id + i]);
             }
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (!kept(Unpack<T>::get(w, i), id + i)) set_element<T>(w, i, masked<T>());
+        }
+        if (whole) {
             *(u32x4_t *)(to + (int64_t)b * N) = w;
         } else {
-            for (int i = max(id, 0); i < min(id + N, a.V); ++i)
-                to[dst.skip + i] = copy ? row.p[row.skip + i] : fill;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (id + i >= 0 && id + i < a.V) to[dst.skip + id + i] = element_of<T>(Unpack<T>::get(w, i));
         }
     }
     if (rec.state != kDone) return;
@@ -1151,13 +1332,13 @@ static int check_rows(const void *logits, int dtype, int64_t ld, int R, int J, i
 // A slice's memory.
 struct Layout {
     int chunks, room, rows;      // of a row; candidates of a chunk; rows of a slice
-    size_t chunk, row, subs, ids, vals, bytes;
+    size_t chunk, row, deep, work, lists, hist, subs, ids, vals, bytes;
 };
 static Layout layout_of(int R, int J, int V) {
     Layout l;
     l.chunks = (V + 7 + kChunk - 1) / kChunk;   // (up to 7 elements before the row in its first block)
-    // a chunk lists 512 ids at least, and a row as many as the second launch
-    // takes: short rows whole
+    // a chunk lists 512 ids at least, and a row as many as are taken: short
+    // rows whole
     l.room = kListed / l.chunks;
     if (l.room < 512) l.room = 512;
     if (l.room > V) l.room = V;
@@ -1165,13 +1346,22 @@ static Layout layout_of(int R, int J, int V) {
     l.rows = kSliceChunks / l.chunks;
     if (l.rows > rows) l.rows = (int)rows;
     const size_t n = (size_t)l.rows * l.chunks;
-    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    l.chunk = sizeof(Control);
-    l.row = l.chunk + up(n * sizeof(ChunkRec));
-    l.subs = l.row + up((size_t)l.rows * sizeof(RowRec));
-    l.ids = l.subs + up(n * (kChunk / 256) * sizeof(u64));
-    l.vals = l.ids + up(n * l.room * sizeof(uint32_t));
-    l.bytes = l.vals + up(n * l.room * sizeof(float));
+    size_t at = sizeof(Control);
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    l.work = take(sizeof(Work));
+    l.chunk = take(n * sizeof(ChunkRec));
+    l.row = take((size_t)l.rows * sizeof(RowRec));
+    l.deep = take((size_t)l.rows * sizeof(DeepRec));
+    l.lists = take((size_t)l.rows * 2 * sizeof(uint32_t));
+    l.hist = take(n * kDeepBins * sizeof(u64));
+    l.subs = take(n * (kChunk / 256) * sizeof(u64));
+    l.ids = take(n * l.room * sizeof(uint32_t));
+    l.vals = take(n * l.room * sizeof(float));
+    l.bytes = at;
     return l;
 }
 
@@ -1180,11 +1370,18 @@ static void launch_rows(SampleArgs a, const Layout &l, hipStream_t st) {
     const int rows = a.R * a.J, parts = (a.V + 7 + kWriteIds - 1) / kWriteIds;
     for (a.row0 = 0; a.row0 < rows; a.row0 += l.rows) {
         a.rows_here = rows - a.row0 < l.rows ? rows - a.row0 : l.rows;
-        const unsigned n = (unsigned)a.rows_here, c = (unsigned)l.chunks;
-        hipLaunchKernelGGL((chunk_kernel<T>), dim3(n * c), dim3(kBlock), 0, st, a);
-        hipLaunchKernelGGL((finish_kernel<T, DRAW>), dim3(DRAW ? n * c : n), dim3(kBlock), 0, st, a);
-        if constexpr (DRAW) hipLaunchKernelGGL((draw_kernel<T>), dim3(n), dim3(kRowThreads), 0, st, a);
-        else hipLaunchKernelGGL((write_kernel<T>), dim3(n * (unsigned)parts), dim3(kRowThreads), 0, st, a, parts);
+        const unsigned n = (unsigned)a.rows_here, c = n * (unsigned)l.chunks;
+        const unsigned w = c < (unsigned)kListGroups ? c : (unsigned)kListGroups;
+        hipLaunchKernelGGL((chunk_kernel<T>), dim3(c), dim3(kBlock), 0, st, a);
+        hipLaunchKernelGGL((finish_kernel<T, DRAW>), dim3(n), dim3(kBlock), 0, st, a);
+        hipLaunchKernelGGL((second_kernel<T, DRAW>), dim3(w), dim3(kBlock), 0, st, a);
+        hipLaunchKernelGGL((third_kernel<T, DRAW>), dim3(w), dim3(kBlock), 0, st, a);
+        if constexpr (DRAW) {
+            hipLaunchKernelGGL((draw_kernel<T>), dim3(n), dim3(kRowThreads), 0, st, a);
+        } else {
+            hipLaunchKernelGGL((settle_kernel<T>), dim3(n), dim3(kRowThreads), 0, st, a);
+            hipLaunchKernelGGL((write_kernel<T>), dim3(n * (unsigned)parts), dim3(kRowThreads), 0, st, a, parts);
+        }
     }
 }
 template <bool DRAW>
@@ -1195,8 +1392,13 @@ static int launch_rows(SampleArgs &a, int dtype, void *workspace, size_t workspa
     a.ctl = (Control *)ws;
     a.chunks = l.chunks;
     a.room = l.room;
+    a.work = (Work *)(ws + l.work);
     a.chunk = (ChunkRec *)(ws + l.chunk);
     a.row = (RowRec *)(ws + l.row);
+    a.deep = (DeepRec *)(ws + l.deep);
+    a.second = (uint32_t *)(ws + l.lists);
+    a.third = a.second + l.rows;
+    a.hist = (u64 *)(ws + l.hist);
     a.subs = (u64 *)(ws + l.subs);
     a.ids = (uint32_t *)(ws + l.ids);
     a.vals = (float *)(ws + l.vals);
