@@ -31,12 +31,13 @@ namespace sv {
 constexpr int kRowThreads = 1024;             // threads of a row's workgroup in the last launches
 constexpr int kListKeys = 2048;               // keys that are looked at one by one
 constexpr int kChunk = 8192;                  // ids of a chunk
-constexpr int kListed = 8192;                 // candidates of a row at most
+constexpr int kListed = 4096;                 // candidates that `finish` takes of a row at most
+constexpr int kInBin = 8192;                  // ids of one bin that the last launches take
 constexpr int kSorted = 1024;                 // candidates that are sorted at most
 constexpr int kMostTopK = kBlock;             // largest top_k that candidates are listed for
 constexpr int kDeepBins = kBlock;             // of a chunk's histogram
 constexpr int kSliceChunks = 16384;           // chunks that a launch takes at a time
-constexpr int kListGroups = 1024;             // workgroups of a launch over the work list
+constexpr int kListGroups = 2048;             // workgroups of a launch over the work list
 constexpr int kWriteIds = 32768;              // ids that a writing workgroup takes
 // Candidates of top-p: ids within this many temperatures of the chunk's largest
 // logit (a share of e^-10 = 4.5e-5 of its).
@@ -48,7 +49,8 @@ struct ChunkRec {
     uint32_t finite;             // ids that are not masked out (after `second`: ids above the cut)
     uint32_t odd;                // a NaN or +inf is among them
     double tail;                 // estimate of sum e^((x - top) / T) over the others
-    double pad;
+    uint32_t share;              // key that the chunk's share of the row's first top_k ids reach
+    uint32_t pad;
 };
 enum : uint32_t {                // a row's state
     kDone,                       // token drawn, or kept ids listed
@@ -229,7 +231,7 @@ template <typename T>
 __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
     __shared__ float top_s[kWaves];
-    __shared__ uint32_t group_s[kBlock], count_s[kWaves], finite_s[kWaves];
+    __shared__ uint32_t group_s[kBlock], count_s[kWaves], finite_s[kWaves], edge_s[kWaves];
     __shared__ double tail_s[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ri = blockIdx.x / a.chunks, c = blockIdx.x - ri * a.chunks;
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     const Row<T> row = row_of<T>(a.logits, (int64_t)(a.row0 + ri) * a.ld, a.V);
     Chunk<T> k;
     load_chunk(row, c, k);
-    ChunkRec rec{kNoKey, 0, 0, 0, 0.0, 0.0};
+    ChunkRec rec{kNoKey, 0, 0, 0, 0.0, 0xffffffffu, 0};
     // ---- largest and least logit
     float tops[NB], own = -INFINITY, low = INFINITY;
 #pragma unroll
@@ -275,6 +277,8 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     ChunkRec *const out = a.chunk + (int64_t)ri * a.chunks + c;
     rec.odd = !(top < INFINITY);
     rec.top = key_of(top);
+    const int here = min(row.blocks - c * (kChunk / N), kChunk / N);  // blocks
+    rec.share = here > 0 ? 0u : 0xffffffffu;    // (where no id is in, the share is not reached)
     if (rec.odd || top == -INFINITY || g.whole || g.many) {
         if (tid == 0) *out = rec;
         return;
@@ -285,18 +289,48 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     if (!g.greedy) {
         edge = estimate ? hot_edge(top, g) : -INFINITY;
         if (g.k > 0) {
-            // At least k of the threads' largest logits lie at or above the
-            // edge, so the row's first k ids do where they lie in this chunk.
-            // (20 bits of it: a few candidates more)
-            uint32_t mine[kBlock / 64], at = 0;
-            for (int v = 0; v < kBlock / 64; ++v) mine[v] = group_s[lane + 64 * v];
-            for (int bit = 31; bit >= 12; --bit) {
-                const uint32_t next = at | 1u << bit;
-                int n = 0;
-                for (int v = 0; v < kBlock / 64; ++v) n += __popcll(__ballot(mine[v] >= next));
-                if (n >= g.k) at = next;
+            // Groups of 8 ids; each wave finds an edge that its share of k
+            // groups reach with their largest logits.  So k ids of the chunk
+            // reach the least of the edges, and the row's first k ids do where they lie in
+            // this chunk.  In the same way, with groups of 32 ids, a key that
+            // the chunk's share of k ids reach: k ids of the row reach the least of the
+            // chunks' keys.  (20 bits of each: a few candidates more)
+            constexpr int Q = 4, PER = NB / Q;  // groups of a lane, loads of a group
+            uint32_t mine[Q], threads[Q], at = 0, to = 0;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                float t = tops[q * PER];
+                if constexpr (PER == 2) t = fmaxf(t, tops[q * PER + 1]);
+                mine[q] = key_of(t);
+                threads[q] = group_s[lane + 64 * q];
             }
+            auto groups = [&](int v) {          // that exist in wave v
+                const int blocks = row.blocks - (c * (kChunk / N) + v * 64 * NB);
+                int n = 0;
+                for (int q = 0; q < Q; ++q) n += min(max(blocks - q * PER * 64, 0), 64);
+                return n;
+            };
+            int all = 0;
+            for (int v = 0; v < kWaves; ++v) all += groups(v);
+            const int share = (g.k * groups(wave) + all - 1) / all;
+            const int of_row = (int)(((int64_t)g.k * here + row.blocks - 1) / row.blocks);
+            for (int bit = 31; bit >= 12; --bit) {
+                const uint32_t next = at | 1u << bit, then = to | 1u << bit;
+                int n = 0, t = 0;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    n += __popcll(__ballot(mine[q] >= next));
+                    t += __popcll(__ballot(threads[q] >= then));
+                }
+                if (n >= share) at = next;
+                if (t >= of_row) to = then;
+            }
+            if (lane == 0) edge_s[wave] = share > 0 ? at : 0xffffffffu;
+            __syncthreads();
+            at = 0xffffffffu;
+            for (int v = 0; v < kWaves; ++v) at = min(at, edge_s[v]);
             if (at > kNoKey) edge = of_key(at);
+            rec.share = to;
         }
         // (top_p's sum is over what top_k leaves)
         if (g.k == 0 || g.p >= 1.f) edge = fmaxf(edge, of_key(min_p_key(top, g)));
@@ -352,19 +386,19 @@ struct Records {
     float m;                     // largest logit
     bool ok;
     uint32_t n, off;             // candidates of the row; before this lane's chunk
-    bool full;                   // more than a chunk or the row may list
+    bool full;                   // more than a chunk may list
 };
 __device__ __forceinline__ Records records_of(const SampleArgs &a, int ri) {
     Records r;
     const int lane = threadIdx.x & 63;
-    r.rec = ChunkRec{kNoKey, 0, 0, 0, 0.0, 0.0};
+    r.rec = ChunkRec{kNoKey, 0, 0, 0, 0.0, 0xffffffffu, 0};
     if (lane < a.chunks) r.rec = a.chunk[(int64_t)ri * a.chunks + lane];
     r.m = wave_max(of_key(r.rec.top));
     r.ok = !__any(r.rec.odd) && r.m > -INFINITY;
     const uint32_t inc = wave_incl_scan_dpp(r.rec.n);
     r.n = (uint32_t)__builtin_amdgcn_readlane((int)inc, 63);
     r.off = inc - r.rec.n;
-    r.full = __any(r.rec.n > (uint32_t)a.room) || r.n > (uint32_t)kListed;
+    r.full = __any(r.rec.n > (uint32_t)a.room);
     return r;
 }
 // Where candidate i of a row lies, off_s[c] of them before chunk c's.
@@ -425,8 +459,8 @@ template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
     __shared__ Scratch<kBlock> s;
     __shared__ float val_s[kListed];
-    __shared__ uint32_t id_s[DRAW ? 1 : kListed];
-    __shared__ uint32_t off_s[64], few_s[kMostTopK];
+    __shared__ uint32_t id_s[kListed];
+    __shared__ uint32_t off_s[64];
     __shared__ u64 total_s;
     __shared__ uint32_t ends_s[2];
     const int tid = threadIdx.x, lane = tid & 63, ri = blockIdx.x;
@@ -438,7 +472,7 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
         return;
     }
     const float m = r.m;
-    const uint32_t finite = wave_sum_u32(r.rec.finite), n = r.n;
+    const uint32_t finite = wave_sum_u32(r.rec.finite);
     const int64_t out = a.row0 + ri, list = (int64_t)ri * a.chunks * a.room;
     RowRec rec{};
     rec.m = m;
@@ -469,35 +503,87 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
     }
     const bool cuts = g.k > 0 && (uint32_t)g.k < finite;  // top_k leaves some out
     const uint32_t low = min_p_key(m, g);
-    if (!cuts && g.p >= 1.f && (g.mp == 0.f || g.many || r.full)) {
+    auto whole = [&]() {                        // at most min_p's cut
         rec.key = low;
         if (tid == 0 && g.mp == 0.f && a.out_kept) a.out_kept[out] = (int32_t)finite;
-        return leave(kWhole, DRAW || g.mp > 0.f, false);
-    }
-    rec.by_weight = !cuts;
-    if (g.many || r.full) {
+        leave(kWhole, DRAW || g.mp > 0.f, false);
+    };
+    auto deep = [&]() {
         const bool many = cuts && g.p < 1.f;
-        return leave(many ? kMany : kDeep, !many, !many);
-    }
-    // ---- candidates, in the order of ids
+        rec.by_weight = !cuts;
+        leave(many ? kMany : kDeep, !many, !many);
+    };
+    if (!cuts && g.p >= 1.f && (g.mp == 0.f || g.many || r.full)) return whole();
+    if (g.many || r.full) return deep();
+    // ---- candidates, in the order of ids: those at or above a key that the
+    // cut cannot lie below.  Of the others only the weight counts, for top_p's sum.
     const Weights wt = weights_of(m, g.t, s.table);
     if (tid < 64) {
         s.table[tid] = exp2((double)tid / 64);
         off_s[tid] = r.off;
     }
-    __syncthreads();
-    for (uint32_t i = tid; i < n; i += kBlock) {
-        const int64_t at = place_of(a, ri, off_s, i);
-        val_s[i] = a.vals[at];
-        if (!DRAW) id_s[i] = a.ids[at];
+    const bool estimate = g.k == 0 && g.p < 1.f;
+    const uint32_t hot = estimate ? key_of(hot_edge(m, g)) : 0u;
+    uint32_t edge = max(low, hot);
+    if (cuts) {
+        uint32_t share = r.rec.share;           // (no chunk: the largest number)
+        for (int o = 32; o; o >>= 1) share = min(share, (uint32_t)__shfl_xor((int)share, o, 64));
+        edge = g.p < 1.f ? share : max(share, low);
     }
     __syncthreads();
-    // What top_p wants of candidates that weigh `total`: at least `want`, at
-    // most `slack` more.  (Where top_k is set, they are all that counts.)
+    uint32_t n;
+    u64 dropped = 0;
+    {
+        constexpr int E = 8;                    // loads under way
+        const uint32_t per = (r.n + kBlock - 1) / kBlock, from = min(tid * per, r.n), to = min(from + per, r.n);
+        int c = 0, hi = a.chunks;               // the last chunk that begins at or before `from`
+        while (hi - c > 1) {
+            const int mid = (c + hi) >> 1;
+            if (off_s[mid] <= from) c = mid;
+            else hi = mid;
+        }
+        auto walk = [&](auto take) {
+            int at = c;
+            for (uint32_t i = from; i < to; i += E) {
+                float x[E];
+                uint32_t place[E];
+#pragma unroll
+                for (uint32_t e = 0; e < E; ++e) {
+                    const uint32_t j = min(i + e, to - 1);
+                    while (at + 1 < a.chunks && off_s[at + 1] <= j) ++at;
+                    place[e] = (uint32_t)(at * a.room) + (j - off_s[at]);
+                    x[e] = a.vals[list + place[e]];
+                }
+#pragma unroll
+                for (uint32_t e = 0; e < E; ++e)
+                    if (i + e < to) take(x[e], place[e]);
+            }
+        };
+        Pair mine{0, 0}, all;
+        walk([&](float x, uint32_t) {
+            if (key_of(x) >= edge) ++mine.n;
+            else if (g.p < 1.f && !cuts) mine.w += weight(wt, x);
+        });
+        uint32_t at = block_before(s, mine, all).n;
+        n = all.n;
+        dropped = all.w;
+        if (n > (uint32_t)kListed) {
+            if (!cuts && g.p >= 1.f) return whole();
+            return deep();
+        }
+        walk([&](float x, uint32_t place) {
+            if (key_of(x) < edge) return;
+            val_s[at] = x;
+            id_s[at++] = a.ids[list + place];
+        });
+    }
+    __syncthreads();
+    // What top_p wants of the candidates, which weigh `total`: at least `want`,
+    // at most `slack` more.
     u64 slack = 0;
     auto top_p_of = [&](u64 total) -> u64 {
-        u64 least = total, most = total;
-        if (g.k == 0) {
+        u64 least = total + dropped, most = least;
+        if (estimate) {
             const double share = exp(((double)of_key(r.rec.top) - (double)m) / (double)g.t);
             const double rest = wave_sum(lane < a.chunks ? r.rec.tail * share : 0.0) * kOne;
             least += (u64)fmax(0.0, rest * (1.0 - kTailError) - kTailUnits);
@@ -507,12 +593,6 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
         slack = top_p_want(g.p, most).w - want;
         return want;
     };
-    // Every id at or above the largest chunk's edge is a candidate, ids below
-    // need not be: top_p's cut there is not to be trusted, unless min_p's is above
-    // that edge, and so the shorter one.
-    const float edge = hot_edge(m, g);
-    const bool by_low = of_key(low) >= edge;
-    auto trusted = [&](uint32_t key) { return g.k > 0 || of_key(key) >= fmaxf(edge, of_key(low)); };
     // Candidates that are kept have their bit in s.count.
     auto flag = [&](uint32_t i) { atomicOr(&s.count[i >> 5], 1u << (i & 31)); };
     auto clear_flags = [&]() {
@@ -520,59 +600,41 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
         for (int i = tid; i < kListed / 32; i += kBlock) s.count[i] = 0u;
         __syncthreads();
     };
-    bool deep = false;
     const bool few = cuts && n >= (uint32_t)g.k;  // (fewer: min_p's cut comes before the k-th id)
-    if (n <= kSorted || few) {
-        // ---- sorted: the k best first where they are more than that
-        uint32_t na = n;
-        if (n > kSorted) {
-            uint32_t lo = 0xffffffffu, hi = 0;
-            for (uint32_t i = tid; i < n; i += kBlock) {
-                lo = min(lo, key_of(val_s[i]));
-                hi = max(hi, key_of(val_s[i]));
-            }
-            block_ends(s, lo, hi);
-            u64 none;
-            const Cut cut = cut_among(s, wt, lo, hi, Pair{0, 0}, Want{false, (uint32_t)g.k, 0}, false, none, [&](auto f) {
-                for (uint32_t i = tid; i < n; i += kBlock) f(key_of(val_s[i]));
-            });
-            const uint32_t per = (n + kBlock - 1) / kBlock, from = min(tid * per, n), to = min(from + per, n);
-            Pair all, mine{0, 0};
-            for (uint32_t i = from; i < to; ++i) {
-                mine.n += key_of(val_s[i]) == cut.key;
-                mine.w += key_of(val_s[i]) > cut.key;
-            }
-            const Pair before = block_before(s, mine, all);
-            uint32_t tie = before.n, at = (uint32_t)before.w + min(before.n, cut.ties);
-            for (uint32_t i = from; i < to; ++i) {
-                const uint32_t key = key_of(val_s[i]);
-                if (key > cut.key || (key == cut.key && tie < cut.ties)) few_s[at++] = i;
-                tie += key == cut.key;
-            }
-            na = (uint32_t)g.k;
+    if (n <= kSorted) {
+        // ---- sorted
+        if (n <= kBlock) {
+            // each thread's place is the number of those before it
+            u64 own = ~0ull;
+            if (tid < (int)n) own = (u64)~key_of(val_s[tid]) << 32 | (uint32_t)tid;
+            s.mass[kBlock + tid] = own;
             __syncthreads();
+            uint32_t place = 0;
+            for (uint32_t i = 0; i < n; i += 4)
+#pragma unroll
+                for (uint32_t q = 0; q < 4; ++q) place += s.mass[kBlock + i + q] < own;
+            if (tid < (int)n) s.mass[place] = own;
+            __syncthreads();
+        } else {
+            for (uint32_t i = tid; i < n; i += kBlock) s.mass[i] = (u64)~key_of(val_s[i]) << 32 | i;
+            sort_shared(s.mass, (int)n);
         }
-        auto nth = [&](uint32_t i) { return n > kSorted ? few_s[i] : i; };
-        for (uint32_t i = tid; i < na; i += kBlock) s.mass[i] = (u64)~key_of(val_s[nth(i)]) << 32 | i;
-        sort_shared(s.mass, (int)na);
         // ---- a thread's neighbours in that order
         constexpr int E = kSorted / kBlock;
-        const uint32_t e = (na + kBlock - 1) / kBlock;
-        uint32_t key[E];
+        const uint32_t e = (n + kBlock - 1) / kBlock;
         u64 w[E];
         Pair sum{0, 0}, all;
 #pragma unroll
         for (uint32_t i = 0; i < E; ++i) {
             const uint32_t at = tid * e + i;
-            const bool in = i < e && at < na;
-            key[i] = in ? ~(uint32_t)(s.mass[at] >> 32) : 0u;
-            w[i] = in && g.p < 1.f ? weight(wt, of_key(key[i])) : 0;
-            sum = sum + Pair{in && key[i] >= low, w[i]};
+            const bool in = i < e && at < n;
+            const uint32_t key = in ? ~(uint32_t)(s.mass[at] >> 32) : 0u;
+            w[i] = in && g.p < 1.f ? weight(wt, of_key(key)) : 0;
+            sum = sum + Pair{in && key >= low, w[i]};
         }
         const Pair before = block_before(s, sum, all);
-        uint32_t keep = min(all.n, na);         // what min_p leaves
-        const uint32_t nk = few ? (uint32_t)g.k : na;
-        keep = min(keep, nk);
+        const uint32_t nk = few ? (uint32_t)g.k : n;
+        uint32_t keep = min(all.n, nk);         // what min_p and top_k leave
         if (g.p < 1.f) {
             if (tid == 0) {
                 total_s = all.w;
@@ -596,60 +658,51 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
                 run += w[i];
             }
             __syncthreads();
-            const uint32_t np = ends_s[0];
-            const bool sure = np && trusted(~(uint32_t)(s.mass[np - 1] >> 32));
-            if (sure) {
-                deep = np != ends_s[1];         // the bounds' ends differ in their cuts
-                keep = min(keep, np);
-            } else {
-                deep = !by_low;
-            }
+            // Behind the candidates: then min_p's cut is the shorter one if that is
+            // what ends them.  Between the bounds' cuts: not known.
+            if (ends_s[0] != ends_s[1] || (ends_s[0] == 0 && low < hot)) return deep();
+            if (ends_s[0]) keep = min(keep, ends_s[0]);
         }
-        if (!deep) {
-            clear_flags();
-            for (uint32_t i = tid; i < keep; i += kBlock) flag(nth((uint32_t)s.mass[i]));
-        }
+        clear_flags();
+        for (uint32_t i = tid; i < keep; i += kBlock) flag((uint32_t)s.mass[i]);
     } else {
         // ---- by histograms
+        uint32_t lo = 0xffffffffu, hi = 0;
+        Pair sum{0, 0}, all;
+        for (uint32_t i = tid; i < n; i += kBlock) {
+            const uint32_t key = key_of(val_s[i]);
+            lo = min(lo, key);
+            hi = max(hi, key);
+            if (g.p < 1.f) sum.w += weight(wt, val_s[i]);
+        }
+        block_ends(s, lo, hi);
+        block_before(s, sum, all);
+        u64 total = all.w, reached = 0;
+        auto each = [&](auto f) {
+            for (uint32_t i = tid; i < n; i += kBlock) f(key_of(val_s[i]));
+        };
         Cut cut{low, 0xffffffffu};
+        if (few) cut = shorter(cut, cut_among(s, wt, lo, hi, Pair{0, 0}, Want{false, (uint32_t)g.k, 0}, g.p < 1.f, total, each));
         if (g.p < 1.f) {
-            uint32_t lo = 0xffffffffu, hi = 0;
-            Pair sum{0, 0}, all;
-            for (uint32_t i = tid; i < n; i += kBlock) {
-                lo = min(lo, key_of(val_s[i]));
-                hi = max(hi, key_of(val_s[i]));
-                sum.w += weight(wt, val_s[i]);
-            }
-            block_ends(s, lo, hi);
-            block_before(s, sum, all);
-            const u64 want = top_p_of(all.w);
-            Cut q{kNoKey, 0};
-            u64 reached = 0;
-            if (want + slack <= all.w)
-                q = cut_among(s, wt, lo, hi, Pair{0, 0}, Want{true, 0, want}, true, reached, [&](auto f) {
-                    for (uint32_t i = tid; i < n; i += kBlock) f(key_of(val_s[i]));
-                });
-            if (trusted(q.key)) {
-                deep = reached < want + slack;
-                cut = shorter(cut, q);
-            } else {
-                deep = !by_low;
+            const u64 want = top_p_of(total);
+            if (want + slack <= total) {
+                cut = shorter(cut, cut_among(s, wt, lo, hi, Pair{0, 0}, Want{true, 0, want}, true, reached, each));
+                if (reached < want + slack) return deep();
+            } else if (want <= total || low < hot) {
+                return deep();
             }
         }
-        if (!deep) {
-            clear_flags();
-            const uint32_t per = (n + kBlock - 1) / kBlock, from = min(tid * per, n), to = min(from + per, n);
-            Pair all, mine{0, 0};
-            for (uint32_t i = from; i < to; ++i) mine.n += key_of(val_s[i]) == cut.key;
-            uint32_t tie = block_before(s, mine, all).n;
-            for (uint32_t i = from; i < to; ++i) {
-                const uint32_t key = key_of(val_s[i]);
-                if (key > cut.key || (key == cut.key && tie < cut.ties)) flag(i);
-                tie += key == cut.key;
-            }
+        clear_flags();
+        const uint32_t per = (n + kBlock - 1) / kBlock, from = min(tid * per, n), to = min(from + per, n);
+        Pair mine{0, 0};
+        for (uint32_t i = from; i < to; ++i) mine.n += key_of(val_s[i]) == cut.key;
+        uint32_t tie = block_before(s, mine, all).n;
+        for (uint32_t i = from; i < to; ++i) {
+            const uint32_t key = key_of(val_s[i]);
+            if (key > cut.key || (key == cut.key && tie < cut.ties)) flag(i);
+            tie += key == cut.key;
         }
     }
-    if (deep) return leave(kDeep, true, true);
     // ---- what is kept, in the order of ids
     __syncthreads();
     const uint32_t per = (n + kBlock - 1) / kBlock, from = min(tid * per, n), to = min(from + per, n);
@@ -668,7 +721,7 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
             if (!kept(i)) continue;
             at.w += weight(wt, val_s[i]);
             if (at.w > target) {
-                a.out_tokens[out] = (int32_t)a.ids[place_of(a, ri, off_s, i)];
+                a.out_tokens[out] = (int32_t)id_s[i];
                 if (a.out_logq) a.out_logq[out] = log_share(wt, val_s[i], g.t, all.w);
                 return;
             }
@@ -755,7 +808,7 @@ __global__ void __launch_bounds__(kBlock) second_kernel(SampleArgs a) {
 }
 
 template <typename T, bool DRAW>
-__global__ void __launch_bounds__(kBlock) third_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(kBlock, 4) third_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
     __shared__ u64 wave_s[kWaves], above_s, there_s;
     __shared__ int bin_s;
@@ -848,8 +901,8 @@ template <typename T> struct RowShared {
     static constexpr int SUBS = SPEC_MAX_VERIFY_VOCAB / SUB + 1;
     static constexpr int EACH = (SUBS + kRowThreads - 1) / kRowThreads;
     Scratch<kRowThreads> s;
-    float val[kListed];          // candidates: logits,
-    uint32_t id[kListed];        // and ids
+    float val[kInBin];           // candidates: logits,
+    uint32_t id[kInBin];        // and ids
     u64 sub_w[SUBS];             // kept weight, per wave's load
     uint32_t sub_e[SUBS];        // ids at the cut's key
     uint32_t off[64];
@@ -873,7 +926,7 @@ __device__ __forceinline__ bool deep_cut(const SampleArgs &a, RowShared<T> &sh, 
     constexpr int B = kRowThreads;
     const int tid = threadIdx.x;
     const Records r = records_of(a, ri);
-    if (r.full) return false;
+    if (r.full || r.n > (uint32_t)kInBin) return false;
     const DeepRec bin = a.deep[ri];
     d.n = r.n;
     d.above = wave_sum_u32((tid & 63) < a.chunks ? r.rec.finite : 0u);
