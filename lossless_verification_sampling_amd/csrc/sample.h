@@ -30,27 +30,52 @@ constexpr uint32_t kNoKey = 0x007fffffu;      // of -inf: ids that are masked ou
 // weights
 // ---------------------------------------------------------------------------
 
-// w(x) = 2^(44 + (x - m) log2(e) / T): the exponent is cut into 64ths, whose
-// powers of two stand in a table, and the rest, at most ln 2 / 128 = 0.0055, goes through the
-// exponential's series to the fifth power (the next term is 4e-17).
+// w(x) = 2^(44 + (x - m) log2(e) / T): the exponent is rounded to a 128th, whose
+// power of two stands in a table, and the rest, at most ln 2 / 256 = 0.0027, goes through
+// the exponential's series to the fourth power (the next term is 1.2e-15, a
+// fiftieth of a unit).
+constexpr int kSteps = 128;
 struct Weights {
-    double m, c;                 // the largest logit, 64 log2(e) / T
-    const double *table;         // 2^(i / 64), i < 64 (shared memory)
+    double m, c, least;          // the largest logit, 128 log2(e) / T, x - m of 2^-60 of its weight
+    double k1, k2, k3, k4;       // (ln 2 / 128)^i / i!
+    const double *table;         // 2^(44 + i / 128), i < 128 (shared memory)
 };
-__device__ __forceinline__ u64 weight(const Weights &w, float x) {
-    constexpr double kRound = 6755399441055744.0;  // 1.5 2^52: adding it rounds to whole numbers
-    constexpr double z = kLn2 / 64;
-    const double y = fmax(((double)x - w.m) * w.c, -64.0 * 60.0);
-    const double s = y + kRound;
+// A constant in scalar registers, opaque to the compiler, which would write
+// its 64 bits into vector registers before every use.
+__device__ __forceinline__ double constant(double v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+__device__ __forceinline__ Weights weights_of(float m, float t, const double *table) {
+    constexpr double z = kLn2 / kSteps;
+    const double c = kSteps * kLog2e / (double)t;
+    return Weights{readlane_d((double)m, 0), readlane_d(c, 0), readlane_d(-60.0 * kSteps / c, 0), constant(z),
+                   constant(z * z / 2), constant(z * z * z / 6), constant(z * z * z * z / 24), table};
+}
+__device__ __forceinline__ void fill_table(double *table) {
+    for (int i = threadIdx.x; i < kSteps; i += blockDim.x) table[i] = kOne * exp2((double)i / kSteps);
+}
+// (x - m) log2(e) / T in 128ths, rounded: a whole number that does not rise where x falls.
+constexpr double kRound = 6755399441055744.0;  // 1.5 2^52: adding it rounds to whole numbers
+__device__ __forceinline__ double steps_of(const Weights &w, float x, double &d) {
+    d = fmax((double)x - w.m, w.least);
+    return fma(d, w.c, kRound);
+}
+__device__ __forceinline__ u64 weight_at(const Weights &w, double s, double d) {
     const int n = (int)(uint32_t)__double_as_longlong(s);
-    const double r = y - (s - kRound);
-    double p = fma(r, z * z * z * z * z / 120, z * z * z * z / 24);
-    p = fma(p, r, z * z * z / 6);
-    p = fma(p, r, z * z / 2);
-    p = fma(p, r, z);
+    const double r = fma(d, w.c, -(s - kRound));
+    double p = fma(r, w.k4, w.k3);
+    p = fma(p, r, w.k2);
+    p = fma(p, r, w.k1);
     p = fma(p, r, 1.0);
-    p = ldexp(p * w.table[n & 63], (n >> 6) + 44);
-    return (u64)(__double_as_longlong(p + kRound) - __double_as_longlong(kRound));
+    p = ldexp(p * w.table[n & (kSteps - 1)], n >> 7) + kRound;
+    const u64 bits = (u64)__double_as_longlong(p);
+    return (u64)((uint32_t)(bits >> 32) - 0x43380000u) << 32 | (uint32_t)bits;  // (less kRound's)
+}
+__device__ __forceinline__ u64 weight(const Weights &w, float x) {
+    double d;
+    const double s = steps_of(w, x, d);
+    return weight_at(w, s, d);
 }
 
 // ---------------------------------------------------------------------------
@@ -157,7 +182,7 @@ __device__ __forceinline__ uint32_t wave_sum_u32(uint32_t v) {
 template <int B> struct Scratch {
     u64 mass[kBins];             // a histogram: weights,
     uint32_t count[kBins];       // and ids
-    double table[64];
+    double table[kSteps];
     Pair waves[2][B / 64];
     uint32_t ends[2][B / 64];
     uint32_t listed;

@@ -35,7 +35,9 @@ constexpr int kListed = 4096;                 // candidates that `finish` takes 
 constexpr int kInBin = 8192;                  // ids of one bin that the last launches take
 constexpr int kSorted = 1024;                 // candidates that are sorted at most
 constexpr int kMostTopK = kBlock;             // largest top_k that candidates are listed for
-constexpr int kDeepBins = kBlock;             // of a chunk's histogram
+// A chunk's histogram: bins of 16 steps (an eighth of a power of two) from
+// the largest logit, bin kDeepBins - 1, to behind the last one with a weight.
+constexpr int kDeepBins = 384;
 constexpr int kSliceChunks = 16384;           // chunks that a launch takes at a time
 constexpr int kListGroups = 2048;             // workgroups of a launch over the work list
 constexpr int kWriteIds = 32768;              // ids that a writing workgroup takes
@@ -153,9 +155,6 @@ __device__ __forceinline__ uint32_t min_p_key(float m, const Setting &g) {
 // differently in two places.)
 __device__ __forceinline__ float hot_edge(float top, const Setting &g) { return fmaf(-kHot, g.t, top); }
 
-__device__ __forceinline__ Weights weights_of(float m, float t, const double *table) {
-    return Weights{(double)m, t == 0.f ? 0.0 : 64.0 * kLog2e / (double)t, table};
-}
 __device__ __forceinline__ float log_share(const Weights &wt, float x, float t, u64 total) {
     return t == 0.f ? 0.f : (float)(((double)x - wt.m) / (double)t - log((double)total / kOne));
 }
@@ -187,13 +186,11 @@ __device__ __forceinline__ uint32_t list_hits(const SampleArgs &a, int ri, int c
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t count = 0, before[NB];
+    if (__any(hits != 0)) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        const uint32_t n = __popc(hits >> (j * N) & ((1u << N) - 1u));
-        before[j] = count;
-        if (__any(n != 0)) {
-            const uint32_t inc = wave_incl_scan_dpp(n);
-            before[j] += inc - n;
+        for (int j = 0; j < NB; ++j) {
+            const uint32_t n = __popc(hits >> (j * N) & ((1u << N) - 1u)), inc = wave_incl_scan_dpp(n);
+            before[j] = count + inc - n;
             count += (uint32_t)__builtin_amdgcn_readlane((int)inc, 63);
         }
     }
@@ -208,6 +205,7 @@ __device__ __forceinline__ uint32_t list_hits(const SampleArgs &a, int ri, int c
         const int64_t at = ((int64_t)ri * a.chunks + c) * a.room;
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
+            if (!__any(hits >> (j * N) & ((1u << N) - 1u))) continue;
             uint32_t pos = base + before[j];
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -250,7 +248,7 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             tops[j] = __builtin_elementwise_maximum(tops[j], k.x(j, i));
-            low = fminf(low, k.x(j, i));
+            low = __builtin_elementwise_minimum(low, k.x(j, i));
         }
         own = __builtin_elementwise_maximum(own, tops[j]);
     }
@@ -343,18 +341,22 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     const float ch = estimate ? (float)(kLog2e / (double)g.t) : 0.f;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-        const bool some = __any(tops[j] >= edge);
-        if (some) {
+        uint32_t bits = 0;
+        if (__any(tops[j] >= edge)) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) hits |= (k.x(j, i) >= edge ? 1u : 0u) << (j * N + i);
+            for (int i = 0; i < N; ++i) bits |= (k.x(j, i) >= edge ? 1u : 0u) << i;
+            hits |= bits << (j * N);
         }
         if (estimate) {
-            float sum = 0.f;
+            float e[N], sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float e = __builtin_amdgcn_exp2f(fmaxf((k.x(j, i) - top) * ch, -126.f));
-                sum += some && k.x(j, i) >= edge ? 0.f : e;
+            for (int i = 0; i < N; ++i) e[i] = __builtin_amdgcn_exp2f((k.x(j, i) - top) * ch);
+            if (__any(bits != 0)) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) e[i] = bits >> i & 1u ? 0.f : e[i];
             }
+#pragma unroll
+            for (int i = 0; i < N; ++i) sum += e[i];
             tail += (double)sum;
         }
     }
@@ -518,10 +520,8 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
     // ---- candidates, in the order of ids: those at or above a key that the
     // cut cannot lie below.  Of the others only the weight counts, for top_p's sum.
     const Weights wt = weights_of(m, g.t, s.table);
-    if (tid < 64) {
-        s.table[tid] = exp2((double)tid / 64);
-        off_s[tid] = r.off;
-    }
+    fill_table(s.table);
+    if (tid < 64) off_s[tid] = r.off;
     const bool estimate = g.k == 0 && g.p < 1.f;
     const uint32_t hot = estimate ? key_of(hot_edge(m, g)) : 0u;
     uint32_t edge = max(low, hot);
@@ -533,6 +533,21 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
     __syncthreads();
     uint32_t n;
     u64 dropped = 0;
+    // What top_p wants of the candidates, which weigh `total`: at least `want`,
+    // at most `slack` more.
+    u64 slack = 0;
+    auto top_p_of = [&](u64 total) -> u64 {
+        u64 least = total + dropped, most = least;
+        if (estimate) {
+            const double share = exp(((double)of_key(r.rec.top) - (double)m) / (double)g.t);
+            const double rest = wave_sum(lane < a.chunks ? r.rec.tail * share : 0.0) * kOne;
+            least += (u64)fmax(0.0, rest * (1.0 - kTailError) - kTailUnits);
+            most += (u64)(rest * (1.0 + kTailError) + kTailUnits);
+        }
+        const u64 want = top_p_want(g.p, least).w;
+        slack = top_p_want(g.p, most).w - want;
+        return want;
+    };
     {
         constexpr int E = 8;                    // loads under way
         const uint32_t per = (r.n + kBlock - 1) / kBlock, from = min(tid * per, r.n), to = min(from + per, r.n);
@@ -560,9 +575,11 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
             }
         };
         Pair mine{0, 0}, all;
+        u64 inside = 0;
         walk([&](float x, uint32_t) {
-            if (key_of(x) >= edge) ++mine.n;
-            else if (g.p < 1.f && !cuts) mine.w += weight(wt, x);
+            const bool in = key_of(x) >= edge;
+            mine.n += in;
+            if (g.p < 1.f && !cuts) (in ? inside : mine.w) += weight(wt, x);
         });
         uint32_t at = block_before(s, mine, all).n;
         n = all.n;
@@ -571,6 +588,11 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
             if (!cuts && g.p >= 1.f) return whole();
             return deep();
         }
+        if (estimate && low < hot) {            // top_p's cut must lie among them
+            block_before(s, Pair{0, inside}, all);
+            const u64 want = top_p_of(all.w);
+            if (want + slack > all.w) return deep();
+        }
         walk([&](float x, uint32_t place) {
             if (key_of(x) < edge) return;
             val_s[at] = x;
@@ -578,21 +600,6 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
         });
     }
     __syncthreads();
-    // What top_p wants of the candidates, which weigh `total`: at least `want`,
-    // at most `slack` more.
-    u64 slack = 0;
-    auto top_p_of = [&](u64 total) -> u64 {
-        u64 least = total + dropped, most = least;
-        if (estimate) {
-            const double share = exp(((double)of_key(r.rec.top) - (double)m) / (double)g.t);
-            const double rest = wave_sum(lane < a.chunks ? r.rec.tail * share : 0.0) * kOne;
-            least += (u64)fmax(0.0, rest * (1.0 - kTailError) - kTailUnits);
-            most += (u64)(rest * (1.0 + kTailError) + kTailUnits);
-        }
-        const u64 want = top_p_want(g.p, least).w;
-        slack = top_p_want(g.p, most).w - want;
-        return want;
-    };
     // Candidates that are kept have their bit in s.count.
     auto flag = [&](uint32_t i) { atomicOr(&s.count[i >> 5], 1u << (i & 31)); };
     auto clear_flags = [&]() {
@@ -740,6 +747,10 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
 // second, third
 // ---------------------------------------------------------------------------
 
+__device__ __forceinline__ int deep_bin(double steps) {
+    return max((int)(uint32_t)__double_as_longlong(steps) >> 4, 1 - kDeepBins) + kDeepBins - 1;
+}
+
 // Weights (DRAW) of the chunk's ids whose bits are set, per wave's load.
 template <typename T>
 __device__ __forceinline__ void sum_loads(const SampleArgs &a, int ri, int c, const Chunk<T> &k, uint32_t in, const Weights &wt) {
@@ -761,10 +772,10 @@ template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kBlock) second_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
     __shared__ u64 hist_s[kDeepBins];
-    __shared__ double table_s[64];
+    __shared__ double table_s[kSteps];
     __shared__ uint32_t count_s[kWaves];
     const int tid = threadIdx.x;
-    if (tid < 64) table_s[tid] = exp2((double)tid / 64);
+    fill_table(table_s);
     const int items = (int)a.work->second * a.chunks;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int ri = (int)a.second[item / a.chunks], c = item % a.chunks;
@@ -776,11 +787,12 @@ __global__ void __launch_bounds__(kBlock) second_kernel(SampleArgs a) {
         load_chunk(row, c, k);
         __syncthreads();                        // (the item before is done with shared memory)
         if (rec.state == kWhole) {
+            const float edge = of_key(rec.key);
             uint32_t in = 0;
 #pragma unroll
             for (int j = 0; j < NB; ++j)
 #pragma unroll
-                for (int i = 0; i < N; ++i) in |= (key_of(k.x(j, i)) >= rec.key ? 1u : 0u) << (j * N + i);
+                for (int i = 0; i < N; ++i) in |= (k.x(j, i) >= edge ? 1u : 0u) << (j * N + i);
             if (DRAW) sum_loads(a, ri, c, k, in, wt);
             const uint32_t n = wave_sum_u32(__popc(in));
             if ((tid & 63) == 0) count_s[tid >> 6] = n;
@@ -791,20 +803,40 @@ __global__ void __launch_bounds__(kBlock) second_kernel(SampleArgs a) {
                 a.chunk[(int64_t)ri * a.chunks + c].finite = all;
             }
         } else {
-            const Scale<kDeepBins> scale(rec.m, g.t);
-            hist_s[tid] = 0;
+            for (int i = tid; i < kDeepBins; i += kBlock) hist_s[i] = 0;
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < NB; ++j)
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const float x = k.x(j, i);
-                    if (x > -INFINITY) atomicAdd(&hist_s[scale.bin(x)], rec.by_weight ? weight(wt, x) : 1ull);
+                    double d;
+                    const double steps = steps_of(wt, k.x(j, i), d);
+                    const u64 w = rec.by_weight ? weight_at(wt, steps, d) : (u64)(k.x(j, i) > -INFINITY);
+                    atomicAdd(&hist_s[deep_bin(steps)], w);
                 }
             __syncthreads();
-            a.hist[((int64_t)ri * a.chunks + c) * kDeepBins + tid] = hist_s[tid];
+            u64 *h = a.hist + ((int64_t)ri * a.chunks + c) * kDeepBins;
+            for (int i = tid; i < kDeepBins; i += kBlock) h[i] = hist_s[i];
         }
     }
+}
+
+// The least logit of bins `bin` and above (+infinity: none), by 64 keys at a time.
+__device__ __forceinline__ float least_of_bin(const Weights &wt, int bin) {
+    // keys lo - 1 and below lie lower, hi and above do not (hi: the largest logit's, or none)
+    const uint32_t lane = threadIdx.x & 63, top = key_of((float)wt.m);
+    if (bin >= kDeepBins) return INFINITY;
+    uint32_t lo = kNoKey + 1, hi = top;
+    while (hi > lo) {
+        const uint32_t gap = (hi - lo) / 65 + 1, at = min(lo + lane * gap, hi);
+        double d;
+        const uint64_t below = __ballot(deep_bin(steps_of(wt, of_key(at), d)) < bin);
+        const int n = __popcll(below);          // the first lanes: keys rise with them
+        hi = n < 64 ? min(lo + n * gap, hi) : hi;
+        lo = n ? min(lo + (n - 1) * gap, hi) + 1 : lo;
+        if (n == 0) hi = lo;
+    }
+    return of_key(hi);
 }
 
 template <typename T, bool DRAW>
@@ -812,10 +844,10 @@ __global__ void __launch_bounds__(kBlock, 4) third_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
     __shared__ u64 wave_s[kWaves], above_s, there_s;
     __shared__ int bin_s;
-    __shared__ double table_s[64];
+    __shared__ double table_s[kSteps];
     __shared__ uint32_t count_s[kWaves], above_n_s[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (tid < 64) table_s[tid] = exp2((double)tid / 64);
+    fill_table(table_s);
     const int items = (int)a.work->third * a.chunks;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int ri = (int)a.third[item / a.chunks], c = item % a.chunks;
@@ -825,23 +857,35 @@ __global__ void __launch_bounds__(kBlock, 4) third_kernel(SampleArgs a) {
         const Weights wt = weights_of(rec.m, g.t, table_s);
         Chunk<T> k;
         load_chunk(row, c, k);
-        // ---- the row's histogram, the highest bin in thread 0
-        const u64 *h = a.hist + (int64_t)ri * a.chunks * kDeepBins + (kDeepBins - 1 - tid);
-        u64 mine = 0;
-        for (int i = 0; i < a.chunks; ++i) mine += h[i * kDeepBins];
-        const u64 inc = wave_scan_u64(mine);
+        // ---- the row's histogram, the highest bins in thread 0
+        constexpr int E = (kDeepBins + kBlock - 1) / kBlock;
+        const u64 *h = a.hist + (int64_t)ri * a.chunks * kDeepBins;
+        u64 mine[E] = {}, sum = 0;
+        for (int i = 0; i < a.chunks; ++i)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int b = kDeepBins - 1 - (tid * E + e);
+                if (b >= 0) mine[e] += h[i * kDeepBins + b];
+            }
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum += mine[e];
+        const u64 inc = wave_scan_u64(sum);
         __syncthreads();                        // (the item before is done with shared memory)
         if (lane == 63) wave_s[wave] = inc;
         __syncthreads();
-        u64 before = inc - mine, total = 0;
+        u64 before = inc - sum, total = 0;
         for (int v = 0; v < kWaves; ++v) {
             if (v < wave) before += wave_s[v];
             total += wave_s[v];
         }
         const u64 want = rec.by_weight ? top_p_want(g.p, total).w : (u64)g.k;
-        if (before < want && before + mine >= want) {
-            bin_s = kDeepBins - 1 - tid;
-            above_s = before;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (before < want && before + mine[e] >= want) {
+                bin_s = kDeepBins - 1 - (tid * E + e);
+                above_s = before;
+            }
+            before += mine[e];
         }
         __syncthreads();
         const int bin = bin_s;
@@ -852,20 +896,20 @@ __global__ void __launch_bounds__(kBlock, 4) third_kernel(SampleArgs a) {
             d.want = rec.by_weight ? Want{true, 0, want} : Want{false, (uint32_t)want, 0};
             a.deep[ri] = d;
         }
-        // ---- ids in it and above it, of those that min_p leaves
-        const Scale<kDeepBins> scale(rec.m, g.t);
-        const uint32_t low = min_p_key(rec.m, g);
+        // ---- ids in it and above it, of those that min_p leaves: logits
+        // from `edge` on, and from `over` on
+        const float low = of_key(min_p_key(rec.m, g));
+        const float edge = fmaxf(low, least_of_bin(wt, bin)), over = fmaxf(low, least_of_bin(wt, bin + 1));
         uint32_t hits = 0, above = 0;
 #pragma unroll
         for (int j = 0; j < NB; ++j)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float x = k.x(j, i);
-                const int b = scale.bin(x);
-                const bool in = key_of(x) >= low;
-                hits |= (in && b == bin ? 1u : 0u) << (j * N + i);
-                above |= (in && b > bin ? 1u : 0u) << (j * N + i);
+                hits |= (x >= edge ? 1u : 0u) << (j * N + i);
+                above |= (x >= over ? 1u : 0u) << (j * N + i);
             }
+        hits &= ~above;
         if (DRAW) sum_loads(a, ri, c, k, above, wt);
         const uint32_t n = wave_sum_u32(__popc(above));
         if (lane == 0) above_n_s[wave] = n;
@@ -1226,7 +1270,7 @@ __global__ void __launch_bounds__(kRowThreads) draw_kernel(SampleArgs a) {
     const int64_t out = a.row0 + ri;
     const Row<T> row = row_of<T>(a.logits, out * a.ld, a.V);
     const Weights wt = weights_of(rec.m, g.t, sh.s.table);
-    if (tid < 64) sh.s.table[tid] = exp2((double)tid / 64);
+    fill_table(sh.s.table);
     const int subs = (row.blocks + 63) / 64;
     const u64 *in = a.subs + (int64_t)ri * a.chunks * (kChunk / 256);
     for (int i = tid; i < subs; i += kRowThreads) {
@@ -1283,7 +1327,7 @@ __global__ void __launch_bounds__(kRowThreads) settle_kernel(SampleArgs a) {
     }
     if (rec.state != kDeep && rec.state != kMany) return;
     const Weights wt = weights_of(rec.m, g.t, sh.s.table);
-    if (tid < 64) sh.s.table[tid] = exp2((double)tid / 64);
+    fill_table(sh.s.table);
     __syncthreads();
     Deep d;
     if (rec.state == kMany || !deep_cut(a, sh, ri, g, rec, wt, d)) {
