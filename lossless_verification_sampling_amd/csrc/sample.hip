@@ -41,9 +41,12 @@ constexpr int kDeepBins = 384;
 constexpr int kSliceChunks = 16384;           // chunks that a launch takes at a time
 constexpr int kListGroups = 2048;             // workgroups of a launch over the work list
 constexpr int kWriteIds = 32768;              // ids that a writing workgroup takes
-// Candidates of top-p: ids within this many temperatures of the chunk's largest
-// logit (a share of e^-10 = 4.5e-5 of its).
+// Candidates without top_k: ids within this many temperatures of the chunk's largest
+// logit (a share of e^-10 = 4.5e-5 of its), those that min_p leaves, and not many
+// more than so many of a chunk.  (A chunk without likely ids would list its
+// thousands of unlikely ones.)
 constexpr float kHot = 10.0f;
+constexpr int kHotGroups = 64;
 
 struct ChunkRec {
     uint32_t top;                // key of the largest logit
@@ -52,7 +55,7 @@ struct ChunkRec {
     uint32_t odd;                // a NaN or +inf is among them
     double tail;                 // estimate of sum e^((x - top) / T) over the others
     uint32_t share;              // key that the chunk's share of the row's first top_k ids reach
-    uint32_t pad;
+    uint32_t edge;               // key that candidates reach
 };
 enum : uint32_t {                // a row's state
     kDone,                       // token drawn, or kept ids listed
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     const Row<T> row = row_of<T>(a.logits, (int64_t)(a.row0 + ri) * a.ld, a.V);
     Chunk<T> k;
     load_chunk(row, c, k);
-    ChunkRec rec{kNoKey, 0, 0, 0, 0.0, 0xffffffffu, 0};
+    ChunkRec rec{kNoKey, 0, 0, 0, 0.0, 0xffffffffu, 0u};
     // ---- largest and least logit
     float tops[NB], own = -INFINITY, low = INFINITY;
 #pragma unroll
@@ -285,23 +288,33 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     float edge = top;
     const bool estimate = !g.greedy && g.k == 0 && g.p < 1.f;
     if (!g.greedy) {
-        edge = estimate ? hot_edge(top, g) : -INFINITY;
-        if (g.k > 0) {
-            // Groups of 8 ids; each wave finds an edge that its share of k
-            // groups reach with their largest logits.  So k ids of the chunk
-            // reach the least of the edges, and the row's first k ids do where they lie in
-            // this chunk.  In the same way, with groups of 32 ids, a key that
-            // the chunk's share of k ids reach: k ids of the row reach the least of the
-            // chunks' keys.  (20 bits of each: a few candidates more)
-            constexpr int Q = 4, PER = NB / Q;  // groups of a lane, loads of a group
-            uint32_t mine[Q], threads[Q], at = 0, to = 0;
+        // Groups of 8 ids; each wave finds a key that its share of k groups reach
+        // with their largest logits.  So k ids of the chunk reach the least of
+        // the keys, and the row's first k ids do where they lie in this chunk.  In the
+        // same way, with groups of 32 ids, a key that the chunk's share of k ids
+        // reach: k ids of the row reach the least of the chunks' keys.  Without
+        // top_k: a key that kHotGroups ids reach.  (20 bits of each)
+        constexpr int Q = 4, PER = NB / Q;      // groups of a lane, loads of a group
+        uint32_t mine[Q], threads[Q], at;
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                float t = tops[q * PER];
-                if constexpr (PER == 2) t = fmaxf(t, tops[q * PER + 1]);
-                mine[q] = key_of(t);
-                threads[q] = group_s[lane + 64 * q];
+        for (int q = 0; q < Q; ++q) {
+            float t = tops[q * PER];
+            if constexpr (PER == 2) t = fmaxf(t, tops[q * PER + 1]);
+            mine[q] = key_of(t);
+            threads[q] = group_s[lane + 64 * q];
+        }
+        auto search = [&](int n, const uint32_t (&keys)[Q]) {
+            uint32_t key = 0;
+            for (int bit = 31; bit >= 12; --bit) {
+                const uint32_t next = key | 1u << bit;
+                int c = 0;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) c += __popcll(__ballot(keys[q] >= next));
+                if (c >= n) key = next;
             }
+            return key;
+        };
+        if (g.k > 0) {
             auto groups = [&](int v) {          // that exist in wave v
                 const int blocks = row.blocks - (c * (kChunk / N) + v * 64 * NB);
                 int n = 0;
@@ -311,29 +324,20 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
             int all = 0;
             for (int v = 0; v < kWaves; ++v) all += groups(v);
             const int share = (g.k * groups(wave) + all - 1) / all;
-            const int of_row = (int)(((int64_t)g.k * here + row.blocks - 1) / row.blocks);
-            for (int bit = 31; bit >= 12; --bit) {
-                const uint32_t next = at | 1u << bit, then = to | 1u << bit;
-                int n = 0, t = 0;
-#pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    n += __popcll(__ballot(mine[q] >= next));
-                    t += __popcll(__ballot(threads[q] >= then));
-                }
-                if (n >= share) at = next;
-                if (t >= of_row) to = then;
-            }
-            if (lane == 0) edge_s[wave] = share > 0 ? at : 0xffffffffu;
+            at = share > 0 ? search(share, mine) : 0xffffffffu;
+            if (lane == 0) edge_s[wave] = at;
             __syncthreads();
-            at = 0xffffffffu;
             for (int v = 0; v < kWaves; ++v) at = min(at, edge_s[v]);
-            if (at > kNoKey) edge = of_key(at);
-            rec.share = to;
+            rec.share = search((int)(((int64_t)g.k * here + row.blocks - 1) / row.blocks), threads);
+        } else {
+            at = search(kHotGroups, threads);
         }
+        edge = at > kNoKey ? of_key(at) : -3.402823466e38f;  // (ids that are masked out are none)
+        if (estimate) edge = fmaxf(edge, hot_edge(top, g));
         // (top_p's sum is over what top_k leaves)
         if (g.k == 0 || g.p >= 1.f) edge = fmaxf(edge, of_key(min_p_key(top, g)));
-        edge = fmaxf(edge, -3.402823466e38f);   // ids that are masked out are none
     }
+    rec.edge = key_of(edge);
     // ---- candidates, and the rest's weight
     uint32_t hits = 0;
     double tail = 0.0;
@@ -393,7 +397,7 @@ struct Records {
 __device__ __forceinline__ Records records_of(const SampleArgs &a, int ri) {
     Records r;
     const int lane = threadIdx.x & 63;
-    r.rec = ChunkRec{kNoKey, 0, 0, 0, 0.0, 0xffffffffu, 0};
+    r.rec = ChunkRec{kNoKey, 0, 0, 0, 0.0, 0xffffffffu, 0u};
     if (lane < a.chunks) r.rec = a.chunk[(int64_t)ri * a.chunks + lane];
     r.m = wave_max(of_key(r.rec.top));
     r.ok = !__any(r.rec.odd) && r.m > -INFINITY;
@@ -518,18 +522,20 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
     if (!cuts && g.p >= 1.f && (g.mp == 0.f || g.many || r.full)) return whole();
     if (g.many || r.full) return deep();
     // ---- candidates, in the order of ids: those at or above a key that the
-    // cut cannot lie below.  Of the others only the weight counts, for top_p's sum.
+    // cut cannot lie below, or from which on every id is one.  Of the others only
+    // the weight counts, for top_p's sum.
     const Weights wt = weights_of(m, g.t, s.table);
     fill_table(s.table);
     if (tid < 64) off_s[tid] = r.off;
     const bool estimate = g.k == 0 && g.p < 1.f;
-    const uint32_t hot = estimate ? key_of(hot_edge(m, g)) : 0u;
-    uint32_t edge = max(low, hot);
-    if (cuts) {
-        uint32_t share = r.rec.share;           // (no chunk: the largest number)
-        for (int o = 32; o; o >>= 1) share = min(share, (uint32_t)__shfl_xor((int)share, o, 64));
-        edge = g.p < 1.f ? share : max(share, low);
+    uint32_t share = r.rec.share, hot = r.rec.edge;  // (no chunk: the largest number, and 0)
+    for (int o = 32; o; o >>= 1) {
+        share = min(share, (uint32_t)__shfl_xor((int)share, o, 64));
+        hot = max(hot, (uint32_t)__shfl_xor((int)hot, o, 64));
     }
+    if (g.k > 0) hot = 0;                       // every id that matters is a candidate
+    if (!cuts && g.p >= 1.f && low < hot) return whole();
+    const uint32_t edge = cuts ? (g.p < 1.f ? share : max(share, low)) : max(low, hot);
     __syncthreads();
     uint32_t n;
     u64 dropped = 0;
