@@ -11,7 +11,6 @@ namespace sv {
 typedef unsigned long long u64;
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kBins = 2048;                   // of a histogram
 constexpr double kOne = 17592186044416.0;     // 2^44, the weight of the largest logit
 // Weights below half a unit are 0: from 45 log 2 = 31.2 temperatures below m on.
 constexpr double kDeepest = 31.25;
@@ -180,6 +179,7 @@ __device__ __forceinline__ uint32_t wave_sum_u32(uint32_t v) {
 
 // Shared memory of a workgroup of B threads.
 template <int B> struct Scratch {
+    static constexpr int kLog = B > 256 ? 11 : 10, kBins = 1 << kLog;
     u64 mass[kBins];             // a histogram: weights,
     uint32_t count[kBins];       // and ids
     double table[kSteps];
@@ -254,7 +254,7 @@ __device__ __forceinline__ Want top_p_want(float p, u64 total) {
 // from `above` on; into s.found, s.before and s.there.
 template <int B>
 __device__ __forceinline__ void find_bin(Scratch<B> &s, Pair above, const Want &want) {
-    constexpr int EACH = kBins / B;
+    constexpr int kBins = Scratch<B>::kBins, EACH = kBins / B;
     Pair mine[EACH], sum{0, 0}, all;
     __syncthreads();
 #pragma unroll
@@ -279,7 +279,7 @@ __device__ __forceinline__ void find_bin(Scratch<B> &s, Pair above, const Want &
 template <int B>
 __device__ __forceinline__ void clear_bins(Scratch<B> &s) {
     __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += B) {
+    for (int i = threadIdx.x; i < Scratch<B>::kBins; i += B) {
         s.mass[i] = 0;
         s.count[i] = 0;
     }
@@ -287,15 +287,15 @@ __device__ __forceinline__ void clear_bins(Scratch<B> &s) {
 }
 
 // The cut among keys lo .. hi, with `above` before them and `want` reached in
-// them: counts over 2048 equal parts of the range, and again over the part
-// that holds the cut, until it is one key.  each(f) calls f for the keys
+// them: counts over equal parts of the range, and again over the part that
+// holds the cut, until it is one key.  each(f) calls f for the keys
 // (others among them are passed over); masses: weights matter, be it for the
 // sum up to the cut alone, which goes to weight_to_cut.
 template <int B, typename F>
 __device__ __forceinline__ Cut cut_among(Scratch<B> &s, const Weights &wt, uint32_t lo, uint32_t hi, Pair above,
                                          const Want &want, bool masses, u64 &weight_to_cut, F each) {
-    for (int level = 0; level < 3 && hi != lo; ++level) {  // (3 times 11 bits are 32)
-        const int shift = max(0, 21 - __clz((int)(hi - lo)));  // parts of 2^shift keys
+    for (int level = 0; level < 4 && hi != lo; ++level) {  // (4 times 10 bits are 32)
+        const int shift = max(0, 32 - Scratch<B>::kLog - __clz((int)(hi - lo)));  // parts of 2^shift keys
         clear_bins(s);
         each([&](uint32_t k) {
             if (k < lo || k > hi) return;

@@ -33,7 +33,6 @@ constexpr int kListKeys = 2048;               // keys that are looked at one by 
 constexpr int kChunk = 8192;                  // ids of a chunk
 constexpr int kListed = 4096;                 // candidates that `finish` takes of a row at most
 constexpr int kInBin = 8192;                  // ids of one bin that the last launches take
-constexpr int kSorted = 1024;                 // candidates that are sorted at most
 constexpr int kMostTopK = kBlock;             // largest top_k that candidates are listed for
 // A chunk's histogram: bins of 16 steps (an eighth of a power of two) from
 // the largest logit, bin kDeepBins - 1, to behind the last one with a weight.
@@ -432,35 +431,6 @@ __device__ __forceinline__ void mark_fault(const SampleArgs &a, int ri) {
     atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
 }
 
-// Sorts n <= kSorted numbers in shared memory, ascending, over the next power
-// of two (what lies behind n becomes the largest number).  Pairs of a wave's
-// own 128 numbers need no barrier: a wave's accesses to shared memory are in order.
-__device__ __forceinline__ void sort_shared(u64 *x, int n) {
-    const int tid = threadIdx.x;
-    int size = 64;
-    while (size < n) size *= 2;
-    for (int i = n + tid; i < size; i += kBlock) x[i] = ~0ull;
-    __syncthreads();
-    for (int k = 2; k <= size; k *= 2)
-        for (int j = k / 2; j; j /= 2) {
-            for (int t = tid; t < size / 2; t += kBlock) {
-                const int i = 2 * t - (t & (j - 1));
-                const u64 p = x[i], q = x[i + j];
-                if ((p > q) == !(i & k)) {
-                    x[i] = q;
-                    x[i + j] = p;
-                }
-            }
-            if (j > 64 || (j == 1 && 2 * k > 128)) __syncthreads();
-            else {
-                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-            }
-        }
-    __syncthreads();
-}
-
 template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
     __shared__ Scratch<kBlock> s;
@@ -563,26 +533,29 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
             if (off_s[mid] <= from) c = mid;
             else hi = mid;
         }
-        auto walk = [&](auto take) {
+        float x[E];
+        uint32_t id[E];
+        auto walk = [&](bool again, auto take) {
             int at = c;
             for (uint32_t i = from; i < to; i += E) {
-                float x[E];
-                uint32_t place[E];
+                if (!again || per > E) {
 #pragma unroll
-                for (uint32_t e = 0; e < E; ++e) {
-                    const uint32_t j = min(i + e, to - 1);
-                    while (at + 1 < a.chunks && off_s[at + 1] <= j) ++at;
-                    place[e] = (uint32_t)(at * a.room) + (j - off_s[at]);
-                    x[e] = a.vals[list + place[e]];
+                    for (uint32_t e = 0; e < E; ++e) {
+                        const uint32_t j = min(i + e, to - 1);
+                        while (at + 1 < a.chunks && off_s[at + 1] <= j) ++at;
+                        const int64_t place = list + (int64_t)at * a.room + (j - off_s[at]);
+                        x[e] = a.vals[place];
+                        id[e] = a.ids[place];
+                    }
                 }
 #pragma unroll
                 for (uint32_t e = 0; e < E; ++e)
-                    if (i + e < to) take(x[e], place[e]);
+                    if (i + e < to) take(x[e], id[e]);
             }
         };
         Pair mine{0, 0}, all;
         u64 inside = 0;
-        walk([&](float x, uint32_t) {
+        walk(false, [&](float x, uint32_t) {
             const bool in = key_of(x) >= edge;
             mine.n += in;
             if (g.p < 1.f && !cuts) (in ? inside : mine.w) += weight(wt, x);
@@ -599,10 +572,10 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
             const u64 want = top_p_of(all.w);
             if (want + slack > all.w) return deep();
         }
-        walk([&](float x, uint32_t place) {
+        walk(true, [&](float x, uint32_t id) {
             if (key_of(x) < edge) return;
             val_s[at] = x;
-            id_s[at++] = a.ids[list + place];
+            id_s[at++] = id;
         });
     }
     __syncthreads();
@@ -614,62 +587,32 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
         __syncthreads();
     };
     const bool few = cuts && n >= (uint32_t)g.k;  // (fewer: min_p's cut comes before the k-th id)
-    if (n <= kSorted) {
-        // ---- sorted
-        if (n <= kBlock) {
-            // each thread's place is the number of those before it
-            u64 own = ~0ull;
-            if (tid < (int)n) own = (u64)~key_of(val_s[tid]) << 32 | (uint32_t)tid;
-            s.mass[kBlock + tid] = own;
-            __syncthreads();
-            uint32_t place = 0;
-            for (uint32_t i = 0; i < n; i += 4)
+    if (n <= kBlock) {
+        // ---- sorted: a thread's place is the number of those before its own
+        u64 own = ~0ull;
+        if (tid < (int)n) own = (u64)~key_of(val_s[tid]) << 32 | (uint32_t)tid;
+        s.mass[kBlock + tid] = own;
+        __syncthreads();
+        uint32_t place = 0;
+        for (uint32_t i = 0; i < n; i += 4)
 #pragma unroll
-                for (uint32_t q = 0; q < 4; ++q) place += s.mass[kBlock + i + q] < own;
-            if (tid < (int)n) s.mass[place] = own;
-            __syncthreads();
-        } else {
-            for (uint32_t i = tid; i < n; i += kBlock) s.mass[i] = (u64)~key_of(val_s[i]) << 32 | i;
-            sort_shared(s.mass, (int)n);
-        }
-        // ---- a thread's neighbours in that order
-        constexpr int E = kSorted / kBlock;
-        const uint32_t e = (n + kBlock - 1) / kBlock;
-        u64 w[E];
-        Pair sum{0, 0}, all;
-#pragma unroll
-        for (uint32_t i = 0; i < E; ++i) {
-            const uint32_t at = tid * e + i;
-            const bool in = i < e && at < n;
-            const uint32_t key = in ? ~(uint32_t)(s.mass[at] >> 32) : 0u;
-            w[i] = in && g.p < 1.f ? weight(wt, of_key(key)) : 0;
-            sum = sum + Pair{in && key >= low, w[i]};
-        }
-        const Pair before = block_before(s, sum, all);
+            for (uint32_t q = 0; q < 4; ++q) place += s.mass[kBlock + i + q] < own;
+        if (tid < (int)n) s.mass[place] = own;
+        __syncthreads();
+        const bool in = tid < (int)n;
+        const uint32_t key = in ? ~(uint32_t)(s.mass[tid] >> 32) : 0u;
+        const u64 w = in && g.p < 1.f ? weight(wt, of_key(key)) : 0;
+        Pair all;
+        const u64 before = block_before(s, Pair{in && key >= low, w}, all).w;
         const uint32_t nk = few ? (uint32_t)g.k : n;
         uint32_t keep = min(all.n, nk);         // what min_p and top_k leave
         if (g.p < 1.f) {
-            if (tid == 0) {
-                total_s = all.w;
-                ends_s[0] = ends_s[1] = 0;
-            }
-            __syncthreads();
-            u64 run = before.w;
-#pragma unroll
-            for (uint32_t i = 0; i < E; ++i) {
-                run += w[i];
-                if (i < e && tid * e + i + 1 == nk) total_s = run;
-            }
+            if (tid + 1 == (int)nk) total_s = before + w;
+            if (tid == 0) ends_s[0] = ends_s[1] = 0;
             __syncthreads();
             const u64 want = top_p_of(total_s);
-            run = before.w;
-#pragma unroll
-            for (uint32_t i = 0; i < E; ++i) {
-                const uint32_t at = tid * e + i + 1;
-                if (i < e && run < want && run + w[i] >= want) ends_s[0] = at;
-                if (i < e && run < want + slack && run + w[i] >= want + slack) ends_s[1] = at;
-                run += w[i];
-            }
+            if (before < want && before + w >= want) ends_s[0] = tid + 1;
+            if (before < want + slack && before + w >= want + slack) ends_s[1] = tid + 1;
             __syncthreads();
             // Behind the candidates: then min_p's cut is the shorter one if that is
             // what ends them.  Between the bounds' cuts: not known.
@@ -677,7 +620,7 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
             if (ends_s[0]) keep = min(keep, ends_s[0]);
         }
         clear_flags();
-        for (uint32_t i = tid; i < keep; i += kBlock) flag((uint32_t)s.mass[i]);
+        if (tid < (int)keep) flag((uint32_t)s.mass[tid]);
     } else {
         // ---- by histograms
         uint32_t lo = 0xffffffffu, hi = 0;
@@ -1104,6 +1047,7 @@ __device__ __forceinline__ void whole_row(const SampleArgs &a, RowShared<T> &sh,
     constexpr int N = Row<T>::N, B = kRowThreads, EACH = RowShared<T>::EACH;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     Scratch<B> &s = sh.s;
+    constexpr int kBins = Scratch<B>::kBins;
     uint32_t *const keys = (uint32_t *)sh.val;
     const Scale<kBins> scale(rec.m, g.t);
     __syncthreads();                                  // (the weights' table)
