@@ -41,11 +41,10 @@ constexpr int kSliceChunks = 16384;           // chunks that a launch takes at a
 constexpr int kListGroups = 2048;             // workgroups of a launch over the work list
 constexpr int kWriteIds = 32768;              // ids that a writing workgroup takes
 // Candidates without top_k: ids within this many temperatures of the chunk's largest
-// logit (a share of e^-10 = 4.5e-5 of its), those that min_p leaves, and not many
-// more than so many of a chunk.  (A chunk without likely ids would list its
+// logit (a share of e^-10 = 4.5e-5 of its), those that min_p leaves, and none below a
+// logit that each sixteenth of the chunk reaches.  (A chunk without likely ids would list its
 // thousands of unlikely ones.)
 constexpr float kHot = 10.0f;
-constexpr int kHotGroups = 64;
 
 struct ChunkRec {
     uint32_t top;                // key of the largest logit
@@ -74,6 +73,10 @@ struct RowRec {
     uint32_t last;               // kCut
     uint32_t by_weight;          // kDeep: top_p's cut, or top_k's
     uint32_t pad;
+};
+struct Listed {
+    uint32_t id;
+    float x;
 };
 struct DeepRec {                 // a kDeep row's bin (written by `third`)
     Pair above;
@@ -109,8 +112,7 @@ struct SampleArgs {
     uint32_t *second, *third;    // [rows_here] rows of the slice
     u64 *hist;                   // [rows_here][chunks][kDeepBins]
     u64 *subs;                   // [rows_here][chunks][kChunk / 256] weights of a wave's loads (draws)
-    uint32_t *ids;               // [rows_here][chunks][room] candidates, then the row's kept ids
-    float *vals;                 // their logits
+    Listed *list;                // [rows_here][chunks][room] candidates, then the row's kept ids
 };
 
 // ---------------------------------------------------------------------------
@@ -212,10 +214,8 @@ __device__ __forceinline__ uint32_t list_hits(const SampleArgs &a, int ri, int c
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 if (hits >> (j * N + i) & 1u) {
-                    if (pos < (uint32_t)a.room) {
-                        a.ids[at + pos] = (uint32_t)((k.b0 + 64 * j) * N + i - row.skip);
-                        a.vals[at + pos] = k.x(j, i);
-                    }
+                    if (pos < (uint32_t)a.room)
+                        a.list[at + pos] = Listed{(uint32_t)((k.b0 + 64 * j) * N + i - row.skip), k.x(j, i)};
                     ++pos;
                 }
         }
@@ -227,10 +227,22 @@ __device__ __forceinline__ uint32_t list_hits(const SampleArgs &a, int ri, int c
 // chunks
 // ---------------------------------------------------------------------------
 
+// Largest value of each row of 16 lanes (NaN if one is), in every lane of it.
+__device__ __forceinline__ float row_max(float v) {
+    v = __builtin_elementwise_maximum(v, dpp_f<kDppSwap1>(v));
+    v = __builtin_elementwise_maximum(v, dpp_f<kDppSwap2>(v));
+    v = __builtin_elementwise_maximum(v, dpp_f<kDppHalfMirror>(v));
+    return __builtin_elementwise_maximum(v, dpp_f<kDppMirror>(v));
+}
+__device__ __forceinline__ float of_rows(float v) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(readlane_f(v, 0), readlane_f(v, 16)),
+                                         __builtin_elementwise_maximum(readlane_f(v, 32), readlane_f(v, 48)));
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
-    __shared__ float top_s[kWaves];
+    __shared__ float top_s[kWaves], part_s[kWaves];
     __shared__ uint32_t group_s[kBlock], count_s[kWaves], finite_s[kWaves], edge_s[kWaves];
     __shared__ double tail_s[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -254,7 +266,11 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
         }
         own = __builtin_elementwise_maximum(own, tops[j]);
     }
-    float top = wave_max(own);
+    // rows of 16 lanes first: their least is a logit that every one of them reaches
+    float top = row_max(own);
+    float part = k.b0 - (lane & 15) < row.blocks ? top : INFINITY;  // (lanes without ids)
+    part = fminf(fminf(readlane_f(part, 0), readlane_f(part, 16)), fminf(readlane_f(part, 32), readlane_f(part, 48)));
+    top = of_rows(top);
     uint32_t finite = 32;
     if (__any(low == -INFINITY)) {
         finite = 0;
@@ -266,11 +282,13 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     finite = wave_sum_u32(finite);
     if (lane == 0) {
         top_s[wave] = top;
+        part_s[wave] = part;
         finite_s[wave] = finite;
     }
-    group_s[tid] = key_of(own);
+    if (g.k > 0) group_s[tid] = key_of(own);
     __syncthreads();
     for (int v = 0; v < kWaves; ++v) {
+        part = fminf(part, part_s[v]);
         top = __builtin_elementwise_maximum(top, top_s[v]);
         rec.finite += finite_s[v];
     }
@@ -287,33 +305,26 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     float edge = top;
     const bool estimate = !g.greedy && g.k == 0 && g.p < 1.f;
     if (!g.greedy) {
-        // Groups of 8 ids; each wave finds a key that its share of k groups reach
-        // with their largest logits.  So k ids of the chunk reach the least of
-        // the keys, and the row's first k ids do where they lie in this chunk.  In the
-        // same way, with groups of 32 ids, a key that the chunk's share of k ids
-        // reach: k ids of the row reach the least of the chunks' keys.  Without
-        // top_k: a key that kHotGroups ids reach.  (20 bits of each)
-        constexpr int Q = 4, PER = NB / Q;      // groups of a lane, loads of a group
-        uint32_t mine[Q], threads[Q], at;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            float t = tops[q * PER];
-            if constexpr (PER == 2) t = fmaxf(t, tops[q * PER + 1]);
-            mine[q] = key_of(t);
-            threads[q] = group_s[lane + 64 * q];
-        }
-        auto search = [&](int n, const uint32_t (&keys)[Q]) {
-            uint32_t key = 0;
-            for (int bit = 31; bit >= 12; --bit) {
-                const uint32_t next = key | 1u << bit;
-                int c = 0;
-#pragma unroll
-                for (int q = 0; q < Q; ++q) c += __popcll(__ballot(keys[q] >= next));
-                if (c >= n) key = next;
-            }
-            return key;
-        };
+        uint32_t at;
         if (g.k > 0) {
+            // Groups of 8 ids; each wave finds a key that its share of k groups
+            // reach with their largest logits.  So k ids of the chunk reach the least of
+            // the keys, and the row's first k ids do where they lie in this chunk.  In
+            // the same way, with groups of 32 ids, a key that the chunk's share of k
+            // ids reach: k ids of the row reach the least of the chunks' keys.  (The keys'
+            // upper 14 bits: a few candidates more.)
+            constexpr int Q = 4, PER = NB / Q;  // groups of a lane, loads of a group
+            auto search = [&](int n, const uint32_t (&keys)[Q]) {
+                uint32_t key = 0;
+                for (int bit = 31; bit >= 18; --bit) {
+                    const uint32_t next = key | 1u << bit;
+                    int c = 0;
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) c += __popcll(__ballot(keys[q] >= next));
+                    if (c >= n) key = next;
+                }
+                return key;
+            };
             auto groups = [&](int v) {          // that exist in wave v
                 const int blocks = row.blocks - (c * (kChunk / N) + v * 64 * NB);
                 int n = 0;
@@ -323,13 +334,24 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
             int all = 0;
             for (int v = 0; v < kWaves; ++v) all += groups(v);
             const int share = (g.k * groups(wave) + all - 1) / all;
+            uint32_t mine[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                float t = tops[q * PER];
+                if constexpr (PER == 2) t = fmaxf(t, tops[q * PER + 1]);
+                mine[q] = key_of(t);
+            }
             at = share > 0 ? search(share, mine) : 0xffffffffu;
             if (lane == 0) edge_s[wave] = at;
             __syncthreads();
             for (int v = 0; v < kWaves; ++v) at = min(at, edge_s[v]);
-            rec.share = search((int)(((int64_t)g.k * here + row.blocks - 1) / row.blocks), threads);
+            if (wave == 0) {                    // (which writes the record)
+#pragma unroll
+                for (int q = 0; q < Q; ++q) mine[q] = group_s[lane + 64 * q];
+                rec.share = search((int)(((int64_t)g.k * here + row.blocks - 1) / row.blocks), mine);
+            }
         } else {
-            at = search(kHotGroups, threads);
+            at = key_of(part);
         }
         edge = at > kNoKey ? of_key(at) : -3.402823466e38f;  // (ids that are masked out are none)
         if (estimate) edge = fmaxf(edge, hot_edge(top, g));
@@ -464,13 +486,12 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
         // the first chunk that has it lists the lowest id first
         const int at = __ffsll((unsigned long long)__ballot(of_key(r.rec.top) == m)) - 1;
         if (tid == 0) {
-            const uint32_t id = a.ids[list + (int64_t)at * a.room];
+            const Listed first = a.list[list + (int64_t)at * a.room];
             if constexpr (DRAW) {
-                a.out_tokens[out] = (int32_t)id;
+                a.out_tokens[out] = (int32_t)first.id;
                 if (a.out_logq) a.out_logq[out] = 0.f;
             } else {
-                a.vals[list] = a.vals[list + (int64_t)at * a.room];
-                a.ids[list] = id;
+                a.list[list] = first;
             }
             if (a.out_kept) a.out_kept[out] = 1;
         }
@@ -533,8 +554,7 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
             if (off_s[mid] <= from) c = mid;
             else hi = mid;
         }
-        float x[E];
-        uint32_t id[E];
+        Listed held[E];
         auto walk = [&](bool again, auto take) {
             int at = c;
             for (uint32_t i = from; i < to; i += E) {
@@ -543,22 +563,20 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
                     for (uint32_t e = 0; e < E; ++e) {
                         const uint32_t j = min(i + e, to - 1);
                         while (at + 1 < a.chunks && off_s[at + 1] <= j) ++at;
-                        const int64_t place = list + (int64_t)at * a.room + (j - off_s[at]);
-                        x[e] = a.vals[place];
-                        id[e] = a.ids[place];
+                        held[e] = a.list[list + (int64_t)at * a.room + (j - off_s[at])];
                     }
                 }
 #pragma unroll
                 for (uint32_t e = 0; e < E; ++e)
-                    if (i + e < to) take(x[e], id[e]);
+                    if (i + e < to) take(held[e]);
             }
         };
         Pair mine{0, 0}, all;
         u64 inside = 0;
-        walk(false, [&](float x, uint32_t) {
-            const bool in = key_of(x) >= edge;
+        walk(false, [&](Listed l) {
+            const bool in = key_of(l.x) >= edge;
             mine.n += in;
-            if (g.p < 1.f && !cuts) (in ? inside : mine.w) += weight(wt, x);
+            if (g.p < 1.f && !cuts) (in ? inside : mine.w) += weight(wt, l.x);
         });
         uint32_t at = block_before(s, mine, all).n;
         n = all.n;
@@ -572,10 +590,10 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
             const u64 want = top_p_of(all.w);
             if (want + slack > all.w) return deep();
         }
-        walk(true, [&](float x, uint32_t id) {
-            if (key_of(x) < edge) return;
-            val_s[at] = x;
-            id_s[at++] = id;
+        walk(true, [&](Listed l) {
+            if (key_of(l.x) < edge) return;
+            val_s[at] = l.x;
+            id_s[at++] = l.id;
         });
     }
     __syncthreads();
@@ -685,9 +703,8 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
     } else {
         for (uint32_t i = from; i < to; ++i) {
             if (!kept(i)) continue;
-            a.ids[list + at.n] = id_s[i];       // (candidates are read from shared memory alone by now)
-            a.vals[list + at.n] = val_s[i];
-            ++at.n;
+            // (candidates are read from shared memory alone by now)
+            a.list[list + at.n++] = Listed{id_s[i], val_s[i]};
         }
     }
 }
@@ -789,7 +806,7 @@ __device__ __forceinline__ float least_of_bin(const Weights &wt, int bin) {
 }
 
 template <typename T, bool DRAW>
-__global__ void __launch_bounds__(kBlock, 4) third_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(kBlock, 3) third_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
     __shared__ u64 wave_s[kWaves], above_s, there_s;
     __shared__ int bin_s;
@@ -810,12 +827,14 @@ __global__ void __launch_bounds__(kBlock, 4) third_kernel(SampleArgs a) {
         constexpr int E = (kDeepBins + kBlock - 1) / kBlock;
         const u64 *h = a.hist + (int64_t)ri * a.chunks * kDeepBins;
         u64 mine[E] = {}, sum = 0;
-        for (int i = 0; i < a.chunks; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int b = kDeepBins - 1 - (tid * E + e);
-                if (b >= 0) mine[e] += h[i * kDeepBins + b];
-            }
+        const int b0 = max(kDeepBins - 1 - tid * E, 0), b1 = max(b0 - 1, 0);
+        static_assert(E == 2, "two bins a thread");
+#pragma unroll 8
+        for (int i = 0; i < a.chunks; ++i) {
+            mine[0] += h[i * kDeepBins + b0];
+            mine[1] += h[i * kDeepBins + b1];
+        }
+        if (tid * E >= kDeepBins) mine[0] = mine[1] = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) sum += mine[e];
         const u64 inc = wave_scan_u64(sum);
@@ -927,14 +946,20 @@ __device__ __forceinline__ bool deep_cut(const SampleArgs &a, RowShared<T> &sh, 
     __syncthreads();
     uint32_t lo = 0xffffffffu, hi = 0;
     Pair sum{0, 0}, all;
-    for (uint32_t i = tid; i < d.n; i += B) {
-        const int64_t at = place_of(a, ri, sh.off, i);
-        const float x = a.vals[at];
-        sh.val[i] = x;
-        sh.id[i] = a.ids[at];
-        lo = min(lo, key_of(x));
-        hi = max(hi, key_of(x));
-        sum = sum + Pair{1, bin.want.by_weight ? weight(wt, x) : 0};
+    constexpr uint32_t E = 4;                   // loads under way
+    for (uint32_t i0 = tid; i0 < d.n; i0 += E * B) {
+        Listed l[E];
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e) l[e] = a.list[place_of(a, ri, sh.off, min(i0 + e * B, d.n - 1))];
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e) {
+            if (i0 + e * B >= d.n) continue;
+            sh.val[i0 + e * B] = l[e].x;
+            sh.id[i0 + e * B] = l[e].id;
+            lo = min(lo, key_of(l[e].x));
+            hi = max(hi, key_of(l[e].x));
+            sum = sum + Pair{1, bin.want.by_weight ? weight(wt, l[e].x) : 0};
+        }
     }
     block_ends(sh.s, lo, hi);
     block_before(sh.s, sum, all);
@@ -1357,8 +1382,9 @@ __global__ void __launch_bounds__(kRowThreads) write_kernel(SampleArgs a, int pa
     __syncthreads();                            // kept ids go over what this workgroup has written
     const int64_t list = (int64_t)ri * a.chunks * a.room;
     for (uint32_t i = tid; i < rec.n; i += kRowThreads) {
-        const int id = (int)a.ids[list + i], b = (id + dst.skip) / N;
-        if (b >= b0 && b < b1) to[dst.skip + id] = element_of<T>(a.vals[list + i]);
+        const Listed l = a.list[list + i];
+        const int b = (int)(l.id + dst.skip) / N;
+        if (b >= b0 && b < b1) to[dst.skip + l.id] = element_of<T>(l.x);
     }
 }
 
@@ -1379,7 +1405,7 @@ static int check_rows(const void *logits, int dtype, int64_t ld, int R, int J, i
 // A slice's memory.
 struct Layout {
     int chunks, room, rows;      // of a row; candidates of a chunk; rows of a slice
-    size_t chunk, row, deep, work, lists, hist, subs, ids, vals, bytes;
+    size_t chunk, row, deep, work, lists, hist, subs, list, bytes;
 };
 static Layout layout_of(int R, int J, int V) {
     Layout l;
@@ -1406,8 +1432,7 @@ static Layout layout_of(int R, int J, int V) {
     l.lists = take((size_t)l.rows * 2 * sizeof(uint32_t));
     l.hist = take(n * kDeepBins * sizeof(u64));
     l.subs = take(n * (kChunk / 256) * sizeof(u64));
-    l.ids = take(n * l.room * sizeof(uint32_t));
-    l.vals = take(n * l.room * sizeof(float));
+    l.list = take(n * l.room * sizeof(Listed));
     l.bytes = at;
     return l;
 }
@@ -1447,8 +1472,7 @@ static int launch_rows(SampleArgs &a, int dtype, void *workspace, size_t workspa
     a.third = a.second + l.rows;
     a.hist = (u64 *)(ws + l.hist);
     a.subs = (u64 *)(ws + l.subs);
-    a.ids = (uint32_t *)(ws + l.ids);
-    a.vals = (float *)(ws + l.vals);
+    a.list = (Listed *)(ws + l.list);
     if (dtype == SPEC_F32) launch_rows<float, DRAW>(a, l, (hipStream_t)stream);
     else launch_rows<uint16_t, DRAW>(a, l, (hipStream_t)stream);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
