@@ -40,11 +40,13 @@ constexpr int kDeepBins = 384;
 constexpr int kSliceChunks = 16384;           // chunks that a launch takes at a time
 constexpr int kListGroups = 2048;             // workgroups of a launch over the work list
 constexpr int kWriteIds = 32768;              // ids that a writing workgroup takes
-// Candidates without top_k: ids within this many temperatures of the chunk's largest
-// logit (a share of e^-10 = 4.5e-5 of its), those that min_p leaves, and none below a
-// logit that each sixteenth of the chunk reaches.  (A chunk without likely ids would list its
-// thousands of unlikely ones.)
+// Candidates without top_k: ids within this many temperatures of the chunk's
+// largest logit (a share of e^-10 = 4.5e-5 of its) that min_p leaves.  Where a
+// wave's 2048 ids hold more than kManyHits of them (a chunk without likely ids
+// has thousands of unlikely ones), those below the least of the largest logits
+// of its four parts are left out.
 constexpr float kHot = 10.0f;
+constexpr int kManyHits = 64;
 
 struct ChunkRec {
     uint32_t top;                // key of the largest logit
@@ -174,6 +176,13 @@ template <typename T> struct Chunk {
     u32x4_t w[NB];
     int b0;                      // this lane's first block
     __device__ __forceinline__ float x(int j, int i) const { return Unpack<T>::get(w[j], i); }
+    // What was unpacked before is not held for what comes: registers are waves.
+    __device__ __forceinline__ void forget() {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) asm volatile("" : "+v"(w[j]));
+        }
+    }
 };
 template <typename T>
 __device__ __forceinline__ void load_chunk(const Row<T> &row, int c, Chunk<T> &k) {
@@ -206,18 +215,15 @@ __device__ __forceinline__ uint32_t list_hits(const SampleArgs &a, int ri, int c
         all += count_s[v];
     }
     if (count) {
-        const int64_t at = ((int64_t)ri * a.chunks + c) * a.room;
+        Listed *const out = a.list + ((int64_t)ri * a.chunks + c) * a.room;
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-            if (!__any(hits >> (j * N) & ((1u << N) - 1u))) continue;
             uint32_t pos = base + before[j];
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (hits >> (j * N + i) & 1u) {
-                    if (pos < (uint32_t)a.room)
-                        a.list[at + pos] = Listed{(uint32_t)((k.b0 + 64 * j) * N + i - row.skip), k.x(j, i)};
-                    ++pos;
-                }
+            // few of them: each is read again (its registers have no index)
+            for (uint32_t bits = hits >> (j * N) & ((1u << N) - 1u); bits; bits &= bits - 1, ++pos) {
+                const int id = (k.b0 + 64 * j) * N + __ffs((int)bits) - 1 - row.skip;
+                if (pos < (uint32_t)a.room) out[pos] = Listed{(uint32_t)id, load_one(row.p, (long)(id + row.skip))};
+            }
         }
     }
     return all;
@@ -242,7 +248,7 @@ __device__ __forceinline__ float of_rows(float v) {
 template <typename T>
 __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
-    __shared__ float top_s[kWaves], part_s[kWaves];
+    __shared__ float top_s[kWaves];
     __shared__ uint32_t group_s[kBlock], count_s[kWaves], finite_s[kWaves], edge_s[kWaves];
     __shared__ double tail_s[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -267,6 +273,7 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
         own = __builtin_elementwise_maximum(own, tops[j]);
     }
     // rows of 16 lanes first: their least is a logit that every one of them reaches
+    k.forget();
     float top = row_max(own);
     float part = k.b0 - (lane & 15) < row.blocks ? top : INFINITY;  // (lanes without ids)
     part = fminf(fminf(readlane_f(part, 0), readlane_f(part, 16)), fminf(readlane_f(part, 32), readlane_f(part, 48)));
@@ -282,13 +289,11 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     finite = wave_sum_u32(finite);
     if (lane == 0) {
         top_s[wave] = top;
-        part_s[wave] = part;
         finite_s[wave] = finite;
     }
     if (g.k > 0) group_s[tid] = key_of(own);
     __syncthreads();
     for (int v = 0; v < kWaves; ++v) {
-        part = fminf(part, part_s[v]);
         top = __builtin_elementwise_maximum(top, top_s[v]);
         rec.finite += finite_s[v];
     }
@@ -351,37 +356,49 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
                 rec.share = search((int)(((int64_t)g.k * here + row.blocks - 1) / row.blocks), mine);
             }
         } else {
-            at = key_of(part);
+            at = kNoKey;
         }
         edge = at > kNoKey ? of_key(at) : -3.402823466e38f;  // (ids that are masked out are none)
         if (estimate) edge = fmaxf(edge, hot_edge(top, g));
         // (top_p's sum is over what top_k leaves)
         if (g.k == 0 || g.p >= 1.f) edge = fmaxf(edge, of_key(min_p_key(top, g)));
     }
-    rec.edge = key_of(edge);
     // ---- candidates, and the rest's weight
+    k.forget();
     uint32_t hits = 0;
     double tail = 0.0;
+    if (!g.greedy && g.k == 0) {
+        // a wave that would list many leaves those below its least row's largest out
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            if (!__any(tops[j] >= edge)) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i) n += __popcll(__ballot(k.x(j, i) >= edge));
+        }
+        if (n > kManyHits) edge = fmaxf(edge, part);
+        k.forget();
+        if (lane == 0) edge_s[wave] = key_of(edge);
+    }
     // 2^a with a = (x - top) log2(e) / T in fp32: see kTailError
     const float ch = estimate ? (float)(kLog2e / (double)g.t) : 0.f;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-        uint32_t bits = 0;
+        float x[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = k.x(j, i);
         if (__any(tops[j] >= edge)) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) bits |= (k.x(j, i) >= edge ? 1u : 0u) << i;
-            hits |= bits << (j * N);
+            for (int i = 0; i < N; ++i) {
+                const bool in = x[i] >= edge;
+                hits |= (in ? 1u : 0u) << (j * N + i);
+                x[i] = in ? -INFINITY : x[i];
+            }
         }
         if (estimate) {
-            float e[N], sum = 0.f;
+            float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) e[i] = __builtin_amdgcn_exp2f((k.x(j, i) - top) * ch);
-            if (__any(bits != 0)) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) e[i] = bits >> i & 1u ? 0.f : e[i];
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i) sum += e[i];
+            for (int i = 0; i < N; ++i) sum += __builtin_amdgcn_exp2f((x[i] - top) * ch);
             tail += (double)sum;
         }
     }
@@ -389,9 +406,12 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
         tail = wave_sum(tail);
         if (lane == 0) tail_s[wave] = tail;
     }
+    k.forget();
     rec.n = list_hits(a, ri, c, row, k, hits, count_s);
     if (estimate)
         for (int v = 0; v < kWaves; ++v) rec.tail += tail_s[v];
+    if (!g.greedy && g.k == 0)
+        for (int v = 0; v < kWaves; ++v) rec.edge = max(rec.edge, edge_s[v]);
     if (tid == 0) *out = rec;
 }
 
