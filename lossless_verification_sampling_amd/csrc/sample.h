@@ -307,13 +307,16 @@ __device__ __forceinline__ Cut cut_among(Scratch<B> &s, const Weights &wt, uint3
         above = s.before;
         lo += s.found << shift;
         hi = min(hi, lo + ((1u << shift) - 1u));
-        if (shift && s.there.n == 1) {  // (one id: its key is the part's only one)
+        if (shift) {                            // (often one key's, or nearly)
             uint32_t l = 0xffffffffu, h = 0;
             each([&](uint32_t k) {
-                if (k >= lo && k <= hi) l = h = k;
+                if (k < lo || k > hi) return;
+                l = min(l, k);
+                h = max(h, k);
             });
             block_ends(s, l, h);
-            lo = hi = h;
+            lo = l;
+            hi = h;
         }
     }
     const u64 one = weight(wt, of_key(lo));

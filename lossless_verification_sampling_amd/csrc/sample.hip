@@ -41,11 +41,11 @@ constexpr int kSliceChunks = 16384;           // chunks that a launch takes at a
 constexpr int kListGroups = 2048;             // workgroups of a launch over the work list
 constexpr int kWriteIds = 32768;              // ids that a writing workgroup takes
 // Candidates without top_k: ids within this many temperatures of the chunk's
-// largest logit (a share of e^-10 = 4.5e-5 of its) that min_p leaves.  Where a
+// largest logit (a share of e^-8 = 3.4e-4 of its) that min_p leaves.  Where a
 // wave's 2048 ids hold more than kManyHits of them (a chunk without likely ids
 // has thousands of unlikely ones), those below the least of the largest logits
 // of its four parts are left out.
-constexpr float kHot = 10.0f;
+constexpr float kHot = 8.0f;
 constexpr int kManyHits = 64;
 
 struct ChunkRec {
