@@ -244,21 +244,23 @@ __global__ void __launch_bounds__(kBlock) query_sums_kernel(SelectArgs a) {
     }
 }
 
-// Sum over the LPR lanes of a row, the same in each of them.
-template <int LPR>
-__device__ __forceinline__ double row_sum(double v) {
+// Sum over LANES neighbours, the same in each of them.
+template <int LANES>
+__device__ __forceinline__ double lanes_sum(double v) {
+    auto swap = [](double v, auto pair) {
+        const long long b = __double_as_longlong(v);
+        uint32_t l0, l1, h0, h1;
+        pair((uint32_t)(b & 0xffffffffLL), l0, l1);
+        pair((uint32_t)(b >> 32), h0, h1);
+        return __longlong_as_double((long long)((uint64_t)h0 << 32 | l0)) +
+               __longlong_as_double((long long)((uint64_t)h1 << 32 | l1));
+    };
     v += dpp_d<kDppSwap1>(v);
     v += dpp_d<kDppSwap2>(v);
     v += dpp_d<kDppHalfMirror>(v);
-    if constexpr (LPR >= 16) v += dpp_d<kDppMirror>(v);
-    if constexpr (LPR >= 32) {
-        const long long b = __double_as_longlong(v);
-        uint32_t l0, l1, h0, h1;
-        lane_pair<16>((uint32_t)(b & 0xffffffffLL), l0, l1);
-        lane_pair<16>((uint32_t)(b >> 32), h0, h1);
-        v = __longlong_as_double((long long)((uint64_t)h0 << 32 | l0)) +
-            __longlong_as_double((long long)((uint64_t)h1 << 32 | l1));
-    }
+    v += dpp_d<kDppMirror>(v);
+    if constexpr (LANES >= 32) v = swap(v, [](uint32_t x, uint32_t &a, uint32_t &b) { lane_pair<16>(x, a, b); });
+    if constexpr (LANES >= 64) v = swap(v, [](uint32_t x, uint32_t &a, uint32_t &b) { lane_pair<32>(x, a, b); });
     return v;
 }
 
@@ -270,59 +272,66 @@ __device__ __forceinline__ uint64_t key_of(double s) {
     return b >> 63 ? ~b : b | 1ull << 63;
 }
 
-// Scores of 64 of a request's full pages for one key head, 16 a wave: D / 8
-// lanes of 8 dimensions a page, 64-bit products and sums.  Bound by HBM, as
-// half the time goes to 64-bit arithmetic beside it.
-constexpr int kScorePages = 16;     // pages a wave
+// Scores of a request's full pages for one key head.  D / 4 lanes take a page,
+// the lower half 8 dimensions each of its largest values with U, the upper
+// half of its least ones with N: a lane holds one of the two sums, so that
+// eight waves fit a SIMD.  Bound by HBM.
+constexpr int kScoreLoads = 8;      // of 16 bytes a lane, all under way
 constexpr int kDirectRows = 16;     // query rows that every wave sums up by itself
 
 template <int D>
 __global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
-    constexpr int LPR = D / 8, PPL = 64 / LPR, IT = kScorePages / PPL;
+    constexpr int LPP = D / 4, PPL = 64 / LPP;  // lanes a page, pages a load
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int sub = lane % LPR, grp = lane / LPR, h = blockIdx.y, r = blockIdx.z;
+    const int grp = lane / LPP, sub = lane % (LPP / 2), h = blockIdx.y, r = blockIdx.z;
+    const bool least_side = lane % LPP >= LPP / 2;
     const Context c = context_of(a, r);
-    const int p0 = (blockIdx.x * kWaves + wave) * kScorePages;
-    if (c.full <= a.budget || p0 >= c.full) return;
-    u32x4_t lo[IT], hi[IT];
-    bool ok[IT];
+    const int p0 = (blockIdx.x * kWaves + wave) * (kScoreLoads * PPL) + grp;
+    if (c.full <= a.budget || p0 - grp >= c.full) return;
+    int page[kScoreLoads];
 #pragma unroll
-    for (int t = 0; t < IT; ++t) {
-        const int p = p0 + t * PPL + grp;
-        int page = p < c.full ? a.table[(int64_t)r * a.max_pages + p] : -1;
-        ok[t] = (unsigned)page < (unsigned)a.num_pages;
-        if (!ok[t]) page = 0;
-        const int64_t at = ((int64_t)page * a.heads + h) * D + sub * 8;
-        lo[t] = *(const u32x4_t *)(a.lo + at);
-        hi[t] = *(const u32x4_t *)(a.hi + at);
-    }
-    double up[8], dn[8];
-    if (a.sums) {
-        const double *s = a.sums + ((int64_t)r * a.heads + h) * 2 * D + sub * 8;
+    for (int t = 0; t < kScoreLoads; ++t)
+        page[t] = a.table[(int64_t)r * a.max_pages + min(p0 + t * PPL, c.full - 1)];
+    const uint16_t *const side = (least_side ? a.lo : a.hi) + (int64_t)h * D + sub * 8;
+    u32x4_t x[kScoreLoads];
+    uint32_t bad = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            up[i] = s[i];
-            dn[i] = s[D + i];
+    for (int t = 0; t < kScoreLoads; ++t) {
+        if ((unsigned)page[t] >= (unsigned)a.num_pages) {
+            bad |= 1u << t;                     // (the request is a faulty one: see select_kernel)
+            page[t] = 0;
         }
+        x[t] = *(const u32x4_t *)(side + (int64_t)page[t] * a.heads * D);
+    }
+    double q[8];
+    if (a.sums) {
+        const double *s = a.sums + ((int64_t)r * a.heads + h) * 2 * D + (least_side ? D : 0) + sub * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = s[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) up[i] = dn[i] = 0.0;
-        for (int i = 0; i < c.n * a.G; ++i) add_row(query_row(a, r, h, i) + sub * 8, up, dn);
+        for (int i = 0; i < 8; ++i) q[i] = 0.0;
+        for (int i = 0; i < c.n * a.G; ++i) {
+            const u32x4_t w = *(const u32x4_t *)(query_row(a, r, h, i) + sub * 8);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float v = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+                q[j] += (double)(least_side ? least(v, 0.f) : most(v, 0.f));
+            }
+        }
     }
     uint64_t *keys = a.keys + ((int64_t)r * a.heads + h) * a.max_pages;
 #pragma unroll
-    for (int t = 0; t < IT; ++t) {
+    for (int t = 0; t < kScoreLoads; ++t) {
         double s = 0.0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float x = i & 1 ? bf16_hi(hi[t][i >> 1]) : bf16_lo(hi[t][i >> 1]);
-            const float y = i & 1 ? bf16_hi(lo[t][i >> 1]) : bf16_lo(lo[t][i >> 1]);
-            s = fma(up[i], (double)x, s);
-            s = fma(dn[i], (double)y, s);
+            const float v = i & 1 ? bf16_hi(x[t][i >> 1]) : bf16_lo(x[t][i >> 1]);
+            s = fma(q[i], (double)v, s);
         }
-        s = row_sum<LPR>(s);
-        const int p = p0 + t * PPL + grp;
-        if (sub == 0 && p < c.full) keys[p] = ok[t] ? key_of(s) : 0ull;
+        s = lanes_sum<LPP>(s);
+        const int p = p0 + t * PPL;
+        if (lane % LPP == 0 && p < c.full) keys[p] = bad >> t & 1u ? 0ull : key_of(s);
     }
 }
 
@@ -363,8 +372,32 @@ __global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
     int32_t *list = a.lists + ((int64_t)r * a.heads + h) * a.width;
     // pages of the request's tokens, the nodes' among them
     const int pages = c.ok && c.n ? (int)(((int64_t)c.ctx + c.n - 1) >> a.shift) + 1 : 0;
+    const int from = a.first, to = c.full - a.last;  // pages that compete
+    const uint64_t *keys = a.keys + ((int64_t)r * a.heads + h) * a.max_pages;
+    const bool choose = c.full > a.budget;
+    const bool in_lds = c.full <= kHeldKeys;
     bool ok = c.ok;
-    for (int p = tid; p < pages; p += kBlock) ok = ok && (unsigned)table[p] < (unsigned)a.num_pages;
+    uint64_t lo = ~0ull, hi = 0ull;
+    constexpr int E = 8;                             // loads under way
+    for (int p0 = tid; p0 < pages; p0 += E * kBlock) {
+        int page[E];
+        uint64_t k[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) page[e] = table[min(p0 + e * kBlock, pages - 1)];
+        if (choose) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) k[e] = keys[min(p0 + e * kBlock, c.full - 1)];
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int p = p0 + e * kBlock;
+            ok = ok && (unsigned)page[e] < (unsigned)a.num_pages;
+            if (!choose || p < from || p >= to) continue;
+            if (in_lds) held[p] = k[e];
+            lo = min(lo, k[e]);
+            hi = max(hi, k[e]);
+        }
+    }
     ok = __syncthreads_and(ok);
     if (!ok) {
         for (int i = tid; i < a.width; i += kBlock) list[i] = -1;
@@ -375,21 +408,10 @@ __global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
         return;
     }
     // ---- the cut: keys above `cut` are taken, and the first `ties` that equal it
-    const int from = a.first, to = c.full - a.last;  // pages that compete
     uint64_t cut = 0;
     uint32_t ties = 0xffffffffu;
-    const uint64_t *keys = a.keys + ((int64_t)r * a.heads + h) * a.max_pages;
-    const bool choose = c.full > a.budget;
-    const bool in_lds = c.full <= kHeldKeys;
     auto key = [&](int p) -> uint64_t { return in_lds ? held[p] : keys[p]; };
     if (choose) {
-        uint64_t lo = ~0ull, hi = 0ull;
-        for (int p = from + tid; p < to; p += kBlock) {
-            const uint64_t k = keys[p];
-            if (in_lds) held[p] = k;
-            lo = min(lo, k);
-            hi = max(hi, k);
-        }
         for (int o = 32; o; o >>= 1) {
             lo = min(lo, (uint64_t)__shfl_xor((unsigned long long)lo, o, 64));
             hi = max(hi, (uint64_t)__shfl_xor((unsigned long long)hi, o, 64));
@@ -493,7 +515,7 @@ static void launch_select(const SelectArgs &a, int R, hipStream_t st) {
     if (a.sums)
         hipLaunchKernelGGL((query_sums_kernel<D>), dim3((unsigned)a.heads, (unsigned)R), dim3(kBlock), 0, st, a);
     if (a.max_pages > a.budget) {
-        const int per = kScorePages * kWaves;
+        const int per = kScoreLoads * (256 / D) * kWaves;
         hipLaunchKernelGGL((score_kernel<D>), dim3((unsigned)((a.max_pages + per - 1) / per), (unsigned)a.heads, (unsigned)R),
                            dim3(kBlock), 0, st, a);
     }
