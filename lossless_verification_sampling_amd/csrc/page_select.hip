@@ -247,20 +247,18 @@ __global__ void __launch_bounds__(kBlock) query_sums_kernel(SelectArgs a) {
 // Sum over LANES neighbours, the same in each of them.
 template <int LANES>
 __device__ __forceinline__ double lanes_sum(double v) {
-    auto swap = [](double v, auto pair) {
-        const long long b = __double_as_longlong(v);
-        uint32_t l0, l1, h0, h1;
-        pair((uint32_t)(b & 0xffffffffLL), l0, l1);
-        pair((uint32_t)(b >> 32), h0, h1);
-        return __longlong_as_double((long long)((uint64_t)h0 << 32 | l0)) +
-               __longlong_as_double((long long)((uint64_t)h1 << 32 | l1));
-    };
     v += dpp_d<kDppSwap1>(v);
     v += dpp_d<kDppSwap2>(v);
     v += dpp_d<kDppHalfMirror>(v);
-    v += dpp_d<kDppMirror>(v);
-    if constexpr (LANES >= 32) v = swap(v, [](uint32_t x, uint32_t &a, uint32_t &b) { lane_pair<16>(x, a, b); });
-    if constexpr (LANES >= 64) v = swap(v, [](uint32_t x, uint32_t &a, uint32_t &b) { lane_pair<32>(x, a, b); });
+    if constexpr (LANES >= 16) v += dpp_d<kDppMirror>(v);
+    if constexpr (LANES >= 32) {
+        const long long b = __double_as_longlong(v);
+        uint32_t l0, l1, h0, h1;
+        lane_pair<16>((uint32_t)(b & 0xffffffffLL), l0, l1);
+        lane_pair<16>((uint32_t)(b >> 32), h0, h1);
+        v = __longlong_as_double((long long)((uint64_t)h0 << 32 | l0)) +
+            __longlong_as_double((long long)((uint64_t)h1 << 32 | l1));
+    }
     return v;
 }
 
@@ -272,28 +270,50 @@ __device__ __forceinline__ uint64_t key_of(double s) {
     return b >> 63 ? ~b : b | 1ull << 63;
 }
 
-// Scores of a request's full pages for one key head.  D / 4 lanes take a page,
-// the lower half 8 dimensions each of its largest values with U, the upper
-// half of its least ones with N: a lane holds one of the two sums, so that
-// eight waves fit a SIMD.  Bound by HBM.
-constexpr int kScoreLoads = 8;      // of 16 bytes a lane, all under way
+// Scores of a request's full pages.  A page's bounds, all key heads of them,
+// lie side by side: SPAN lanes take 8 values each of them (the launch's y axis goes
+// over rows of more than 64 lanes), so that a wave reads pieces of up to a
+// kilobyte; D / 8 lanes share a head.  The largest values go with U, then the
+// least with N: one of the two sums is in registers at a time.  Bound by HBM.
+constexpr int kScoreLoads = 4;      // of 16 bytes a lane and side, all under way
 constexpr int kDirectRows = 16;     // query rows that every wave sums up by itself
 
-template <int D>
+// U (or, LEAST, N) of this lane's 8 dimensions.
+template <int D, bool LEAST>
+__device__ __forceinline__ void query_sums(const SelectArgs &a, const Context &c, int r, int h, int sub, double (&q)[8]) {
+    if (a.sums) {
+        const double *s = a.sums + ((int64_t)r * a.heads + h) * 2 * D + (LEAST ? D : 0) + sub * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = s[i];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = 0.0;
+    for (int i = 0; i < c.n * a.G; ++i) {
+        const u32x4_t w = *(const u32x4_t *)(query_row(a, r, h, i) + sub * 8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float v = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+            q[j] += (double)(LEAST ? least(v, 0.f) : most(v, 0.f));
+        }
+    }
+}
+
+template <int D, int SPAN>
 __global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
-    constexpr int LPP = D / 4, PPL = 64 / LPP;  // lanes a page, pages a load
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int grp = lane / LPP, sub = lane % (LPP / 2), h = blockIdx.y, r = blockIdx.z;
-    const bool least_side = lane % LPP >= LPP / 2;
+    constexpr int PPL = 64 / SPAN;              // pages a load
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = blockIdx.z;
     const Context c = context_of(a, r);
-    const int p0 = (blockIdx.x * kWaves + wave) * (kScoreLoads * PPL) + grp;
-    if (c.full <= a.budget || p0 - grp >= c.full) return;
+    const int first = (blockIdx.x * kWaves + wave) * (kScoreLoads * PPL), p0 = first + lane / SPAN;
+    if (c.full <= a.budget || first >= c.full) return;
+    const int at = blockIdx.y * 512 + lane % SPAN * 8;      // value of a page's row
+    const bool in = at < a.heads * D;
+    const int h = in ? at / D : 0, sub = in ? at % D / 8 : 0;
     int page[kScoreLoads];
 #pragma unroll
     for (int t = 0; t < kScoreLoads; ++t)
         page[t] = a.table[(int64_t)r * a.max_pages + min(p0 + t * PPL, c.full - 1)];
-    const uint16_t *const side = (least_side ? a.lo : a.hi) + (int64_t)h * D + sub * 8;
-    u32x4_t x[kScoreLoads];
+    u32x4_t hi[kScoreLoads], lo[kScoreLoads];
     uint32_t bad = 0;
 #pragma unroll
     for (int t = 0; t < kScoreLoads; ++t) {
@@ -301,37 +321,30 @@ __global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
             bad |= 1u << t;                     // (the request is a faulty one: see select_kernel)
             page[t] = 0;
         }
-        x[t] = *(const u32x4_t *)(side + (int64_t)page[t] * a.heads * D);
+        const int64_t e = ((int64_t)page[t] * a.heads + h) * D + sub * 8;
+        hi[t] = *(const u32x4_t *)(a.hi + e);
+        lo[t] = *(const u32x4_t *)(a.lo + e);
     }
-    double q[8];
-    if (a.sums) {
-        const double *s = a.sums + ((int64_t)r * a.heads + h) * 2 * D + (least_side ? D : 0) + sub * 8;
+    double s[kScoreLoads], q[8];
+    auto add = [&](const u32x4_t (&x)[kScoreLoads]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = s[i];
-    } else {
+        for (int t = 0; t < kScoreLoads; ++t)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = 0.0;
-        for (int i = 0; i < c.n * a.G; ++i) {
-            const u32x4_t w = *(const u32x4_t *)(query_row(a, r, h, i) + sub * 8);
+            for (int i = 0; i < 8; ++i)
+                s[t] = fma(q[i], (double)(i & 1 ? bf16_hi(x[t][i >> 1]) : bf16_lo(x[t][i >> 1])), s[t]);
+    };
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float v = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-                q[j] += (double)(least_side ? least(v, 0.f) : most(v, 0.f));
-            }
-        }
-    }
+    for (int t = 0; t < kScoreLoads; ++t) s[t] = 0.0;
+    query_sums<D, false>(a, c, r, h, sub, q);
+    add(hi);
+    query_sums<D, true>(a, c, r, h, sub, q);
+    add(lo);
     uint64_t *keys = a.keys + ((int64_t)r * a.heads + h) * a.max_pages;
 #pragma unroll
     for (int t = 0; t < kScoreLoads; ++t) {
-        double s = 0.0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float v = i & 1 ? bf16_hi(x[t][i >> 1]) : bf16_lo(x[t][i >> 1]);
-            s = fma(q[i], (double)v, s);
-        }
-        s = lanes_sum<LPP>(s);
+        const double sum = lanes_sum<D / 8>(s[t]);
         const int p = p0 + t * PPL;
-        if (lane % LPP == 0 && p < c.full) keys[p] = bad >> t & 1u ? 0ull : key_of(s);
+        if (in && sub == 0 && p < c.full) keys[p] = bad >> t & 1u ? 0ull : key_of(sum);
     }
 }
 
@@ -515,9 +528,19 @@ static void launch_select(const SelectArgs &a, int R, hipStream_t st) {
     if (a.sums)
         hipLaunchKernelGGL((query_sums_kernel<D>), dim3((unsigned)a.heads, (unsigned)R), dim3(kBlock), 0, st, a);
     if (a.max_pages > a.budget) {
-        const int per = kScoreLoads * (256 / D) * kWaves;
-        hipLaunchKernelGGL((score_kernel<D>), dim3((unsigned)((a.max_pages + per - 1) / per), (unsigned)a.heads, (unsigned)R),
-                           dim3(kBlock), 0, st, a);
+        // lanes of a page's row, the next power of two
+        const int64_t row = (int64_t)a.heads * D / 8;
+        const int span = row <= D / 8 ? D / 8 : row <= 16 ? 16 : row <= 32 ? 32 : 64;
+        const int per = kScoreLoads * (64 / span) * kWaves;
+        const dim3 grid((unsigned)((a.max_pages + per - 1) / per), (unsigned)((row + 63) / 64), (unsigned)R);
+        if constexpr (D == 64) {
+            if (span == 8) hipLaunchKernelGGL((score_kernel<D, 8>), grid, dim3(kBlock), 0, st, a);
+        }
+        if constexpr (D <= 128) {
+            if (span == 16) hipLaunchKernelGGL((score_kernel<D, 16>), grid, dim3(kBlock), 0, st, a);
+        }
+        if (span == 32) hipLaunchKernelGGL((score_kernel<D, 32>), grid, dim3(kBlock), 0, st, a);
+        if (span == 64) hipLaunchKernelGGL((score_kernel<D, 64>), grid, dim3(kBlock), 0, st, a);
     }
     hipLaunchKernelGGL(select_kernel, dim3((unsigned)a.heads, (unsigned)R), dim3(kBlock), 0, st, a);
 }
