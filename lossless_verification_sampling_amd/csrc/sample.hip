@@ -319,26 +319,30 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
             // ids reach: k ids of the row reach the least of the chunks' keys.  (The keys'
             // upper 14 bits: a few candidates more.)
             constexpr int Q = 4, PER = NB / Q;  // groups of a lane, loads of a group
-            auto search = [&](int n, const uint32_t (&keys)[Q]) {
+            auto search = [&](int n, auto reach) {
                 uint32_t key = 0;
                 for (int bit = 31; bit >= 18; --bit) {
                     const uint32_t next = key | 1u << bit;
-                    int c = 0;
-#pragma unroll
-                    for (int q = 0; q < Q; ++q) c += __popcll(__ballot(keys[q] >= next));
-                    if (c >= n) key = next;
+                    if (reach(next) >= n) key = next;
                 }
                 return key;
             };
-            auto groups = [&](int v) {          // that exist in wave v
-                const int blocks = row.blocks - (c * (kChunk / N) + v * 64 * NB);
+            auto of_four = [&](const uint32_t (&keys)[Q], uint32_t key) {
                 int n = 0;
-                for (int q = 0; q < Q; ++q) n += min(max(blocks - q * PER * 64, 0), 64);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) n += __popcll(__ballot(keys[q] >= key));
                 return n;
             };
-            int all = 0;
-            for (int v = 0; v < kWaves; ++v) all += groups(v);
-            const int share = (g.k * groups(wave) + all - 1) / all;
+            // Of whole waves (or chunks) and a last one that is filled in part, that one
+            // takes no share where it is filled less than half: the key of a few
+            // groups strays, and the least of the keys counts.
+            auto share_of = [&](int i, int blocks, int each) {
+                const int all = blocks / each, rest = blocks - all * each;
+                const int in = all > 0 && 2 * rest < each ? blocks - rest : blocks;
+                const int mine = min(max(in - i * each, 0), each);
+                return (int)(((int64_t)g.k * mine + in - 1) / in);
+            };
+            const int share = share_of(wave, here, 64 * NB);
             uint32_t mine[Q];
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
@@ -346,14 +350,31 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
                 if constexpr (PER == 2) t = fmaxf(t, tops[q * PER + 1]);
                 mine[q] = key_of(t);
             }
-            at = share > 0 ? search(share, mine) : 0xffffffffu;
+            at = 0xffffffffu;
+            if (share > 0) {
+                if (2 * 8 * g.k <= here * N) {
+                    at = search(share, [&](uint32_t key) { return of_four(mine, key); });
+                } else {                        // (a short chunk: by its ids, groups would list most of it)
+                    at = search(share, [&](uint32_t key) {
+                        const float x = key > kNoKey ? of_key(key) : -INFINITY;
+                        int n = 0;
+                        k.forget();
+#pragma unroll
+                        for (int j = 0; j < NB; ++j)
+#pragma unroll
+                            for (int i = 0; i < N; ++i) n += __popcll(__ballot(k.x(j, i) >= x));
+                        return n;
+                    });
+                }
+            }
             if (lane == 0) edge_s[wave] = at;
             __syncthreads();
             for (int v = 0; v < kWaves; ++v) at = min(at, edge_s[v]);
             if (wave == 0) {                    // (which writes the record)
 #pragma unroll
                 for (int q = 0; q < Q; ++q) mine[q] = group_s[lane + 64 * q];
-                rec.share = search((int)(((int64_t)g.k * here + row.blocks - 1) / row.blocks), mine);
+                const int n = share_of(c, row.blocks, kChunk / N);
+                rec.share = n > 0 ? search(n, [&](uint32_t key) { return of_four(mine, key); }) : 0xffffffffu;
             }
         } else {
             at = kNoKey;

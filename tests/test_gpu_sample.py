@@ -164,6 +164,26 @@ def test_wide_logits(sv, dev, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V, shift", [(8186, 5), (8192, 0), (8192, 1), (8193, 0), (8240, 3), (16384 + 1100, 0), (24575, 2)])
+def test_rows_that_end_inside_a_part(sv, dev, V, shift, dtype):
+    """Lengths around a multiple of the 8192 ids that a workgroup reads; the
+    likely ids spread, or all at one end of the row, or the rest masked out."""
+    print(f"[sample] V={V} {dtype}", flush=True)
+    g = np.random.default_rng(V)
+    R = 6
+    x = g.standard_normal((R, 1, V)) * 2
+    ids = [np.arange(0, V, V // 60), np.arange(300), V - 1 - np.arange(300), g.choice(V, 900, False), np.arange(0), [V - 1]]
+    for r, at in enumerate(ids):
+        x[r, 0, at] += 6 + 3 * g.random(len(at))
+    x[3, 0, : V // 2] = -np.inf
+    x[4, 0, 7000:] = -np.inf
+    x[5, 0, : V - 500] = -np.inf
+    for k, p, mp in ((1, 0.5, 0.0), (20, 1.0, 0.0), (140, 0.9, 0.0), (200, 1.0, 1e-4), (256, 0.97, 0.0), (257, 0.97, 0.0),
+                     (0, 0.99, 1e-3), (0, 0.6, 0.0), (2000, 1.0, 0.0)):
+        Rows(x, dtype, t=1.1, k=k, p=p, mp=mp, u=uniforms(g, R, 1)).check(sv, dev, V + shift, shift)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("u", [0.0, float(1 - 2.0 ** -24), 0.5, 1e-45])
 def test_the_ends_of_the_uniforms(sv, dev, u, dtype):
     g = np.random.default_rng(5)
