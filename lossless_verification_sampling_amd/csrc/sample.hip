@@ -587,7 +587,8 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
         return want;
     };
     {
-        constexpr int E = 8;                    // loads under way
+        // A thread's neighbours, which stay in its registers up to kHeld of them.
+        constexpr uint32_t kHeld = 32, E = 8;
         const uint32_t per = (r.n + kBlock - 1) / kBlock, from = min(tid * per, r.n), to = min(from + per, r.n);
         int c = 0, hi = a.chunks;               // the last chunk that begins at or before `from`
         while (hi - c > 1) {
@@ -595,21 +596,29 @@ __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
             if (off_s[mid] <= from) c = mid;
             else hi = mid;
         }
-        Listed held[E];
+        Listed held[kHeld];
         auto walk = [&](bool again, auto take) {
             int at = c;
-            for (uint32_t i = from; i < to; i += E) {
-                if (!again || per > E) {
+            for (uint32_t i = 0; i < per; i += kHeld) {
+                if (!again || per > kHeld) {
 #pragma unroll
-                    for (uint32_t e = 0; e < E; ++e) {
-                        const uint32_t j = min(i + e, to - 1);
-                        while (at + 1 < a.chunks && off_s[at + 1] <= j) ++at;
-                        held[e] = a.list[list + (int64_t)at * a.room + (j - off_s[at])];
+                    for (uint32_t b = 0; b < kHeld; b += E) {
+                        if (i + b >= per || from >= to) continue;
+#pragma unroll
+                        for (uint32_t e = b; e < b + E; ++e) {
+                            const uint32_t j = min(from + i + e, to - 1);
+                            while (at + 1 < a.chunks && off_s[at + 1] <= j) ++at;
+                            held[e] = a.list[list + (int64_t)at * a.room + (j - off_s[at])];
+                        }
                     }
                 }
 #pragma unroll
-                for (uint32_t e = 0; e < E; ++e)
-                    if (i + e < to) take(held[e]);
+                for (uint32_t b = 0; b < kHeld; b += E) {
+                    if (i + b >= per) continue;
+#pragma unroll
+                    for (uint32_t e = b; e < b + E; ++e)
+                        if (from + i + e < to) take(held[e]);
+                }
             }
         };
         Pair mine{0, 0}, all;
