@@ -46,7 +46,7 @@ constexpr int kWriteIds = 32768;              // ids that a writing workgroup ta
 // has thousands of unlikely ones), those below the least of the largest logits
 // of its four parts are left out.
 constexpr float kHot = 8.0f;
-constexpr int kManyHits = 64;
+constexpr int kManyHits = 64, kManyLanes = 40;
 
 struct ChunkRec {
     uint32_t top;                // key of the largest logit
@@ -201,10 +201,14 @@ __device__ __forceinline__ uint32_t list_hits(const SampleArgs &a, int ri, int c
     uint32_t count = 0, before[NB];
     if (__any(hits != 0)) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            const uint32_t n = __popc(hits >> (j * N) & ((1u << N) - 1u)), inc = wave_incl_scan_dpp(n);
-            before[j] = count + inc - n;
-            count += (uint32_t)__builtin_amdgcn_readlane((int)inc, 63);
+        for (int j = 0; j < NB; j += 2) {       // (64 N at most: two loads' counts in one word)
+            const uint32_t n0 = __popc(hits >> (j * N) & ((1u << N) - 1u));
+            const uint32_t n1 = __popc(hits >> ((j + 1) * N) & ((1u << N) - 1u));
+            const uint32_t inc = wave_incl_scan_dpp(n0 | n1 << 16), all = (uint32_t)__builtin_amdgcn_readlane((int)inc, 63);
+            before[j] = count + (inc & 0xffffu) - n0;
+            count += all & 0xffffu;
+            before[j + 1] = count + (inc >> 16) - n1;
+            count += all >> 16;
         }
     }
     if ((threadIdx.x & 63) == 0) count_s[wave] = count;
@@ -216,14 +220,14 @@ __device__ __forceinline__ uint32_t list_hits(const SampleArgs &a, int ri, int c
     }
     if (count) {
         Listed *const out = a.list + ((int64_t)ri * a.chunks + c) * a.room;
+        // few of them: each is read again (its registers have no index)
+        for (uint32_t bits = hits; bits; bits &= bits - 1) {
+            const uint32_t bit = (uint32_t)__ffs((int)bits) - 1u, j = bit / N;
+            uint32_t pos = base + __popc((hits ^ bits) >> (j * N));
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            uint32_t pos = base + before[j];
-            // few of them: each is read again (its registers have no index)
-            for (uint32_t bits = hits >> (j * N) & ((1u << N) - 1u); bits; bits &= bits - 1, ++pos) {
-                const int id = (k.b0 + 64 * j) * N + __ffs((int)bits) - 1 - row.skip;
-                if (pos < (uint32_t)a.room) out[pos] = Listed{(uint32_t)id, load_one(row.p, (long)(id + row.skip))};
-            }
+            for (int q = 0; q < NB; ++q) pos += j == q ? before[q] : 0u;
+            const int at = (k.b0 + 64 * (int)j) * N + (int)(bit % N);
+            if (pos < (uint32_t)a.room) out[pos] = Listed{(uint32_t)(at - row.skip), load_one(row.p, (long)at)};
         }
     }
     return all;
@@ -260,7 +264,9 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     Chunk<T> k;
     load_chunk(row, c, k);
     ChunkRec rec{kNoKey, 0, 0, 0, 0.0, 0xffffffffu, 0u};
-    // ---- largest and least logit
+    // ---- largest and least logit (the least: is an id masked out?  That counts where
+    // top_k or nothing cuts)
+    const bool counts = g.k > 0 || (g.p >= 1.f && g.mp == 0.f);
     float tops[NB], own = -INFINITY, low = INFINITY;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             tops[j] = __builtin_elementwise_maximum(tops[j], k.x(j, i));
-            low = __builtin_elementwise_minimum(low, k.x(j, i));
+            if (counts) low = __builtin_elementwise_minimum(low, k.x(j, i));
         }
         own = __builtin_elementwise_maximum(own, tops[j]);
     }
@@ -390,45 +396,60 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     double tail = 0.0;
     if (!g.greedy && g.k == 0) {
         // a wave that would list many leaves those below its least row's largest out
-        int n = 0;
+        // (where most lanes have one there is no need to count)
+        int n = __popcll(__ballot(own >= edge)) > kManyLanes ? kManyHits + 1 : 0;
+        if (n == 0) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            if (!__any(tops[j] >= edge)) continue;
+            for (int j = 0; j < NB; ++j) {
+                if (!__any(tops[j] >= edge)) continue;
 #pragma unroll
-            for (int i = 0; i < N; ++i) n += __popcll(__ballot(k.x(j, i) >= edge));
+                for (int i = 0; i < N; ++i) n += __popcll(__ballot(k.x(j, i) >= edge));
+            }
         }
         if (n > kManyHits) edge = fmaxf(edge, part);
         k.forget();
         if (lane == 0) edge_s[wave] = key_of(edge);
     }
-    // 2^a with a = (x - top) log2(e) / T in fp32: see kTailError
-    const float ch = estimate ? (float)(kLog2e / (double)g.t) : 0.f;
+    // 2^a with a = (x - top) ch, ch = log2(e) / T, in fp32: see kTailError.  In one
+    // operation, x ch + b, where b = -top ch rounded is small; what that rounding took
+    // (less than 2^-4) comes back with the sum.
+    const float ch = estimate ? (float)(kLog2e / (double)g.t) : 0.f, b = -top * ch;
+    const bool fused = fabsf(b) < 1048576.f;
+    const double rounded = fused ? -(double)top * (double)ch - (double)b : 0.0;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
         float x[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] = k.x(j, i);
+        // (the first id's bit is the highest)
         if (__any(tops[j] >= edge)) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const bool in = x[i] >= edge;
-                hits |= (in ? 1u : 0u) << (j * N + i);
+                hits = hits + hits + in;
                 x[i] = in ? -INFINITY : x[i];
             }
+        } else {
+            hits <<= N;
         }
         if (estimate) {
             float sum = 0.f;
+            if (fused) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) sum += __builtin_amdgcn_exp2f((x[i] - top) * ch);
+                for (int i = 0; i < N; ++i) sum += __builtin_amdgcn_exp2f(fmaf(x[i], ch, b));
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) sum += __builtin_amdgcn_exp2f((x[i] - top) * ch);
+            }
             tail += (double)sum;
         }
     }
     if (estimate) {
-        tail = wave_sum(tail);
+        tail = wave_sum(tail) * (double)__builtin_amdgcn_exp2f((float)rounded);
         if (lane == 0) tail_s[wave] = tail;
     }
     k.forget();
-    rec.n = list_hits(a, ri, c, row, k, hits, count_s);
+    rec.n = list_hits(a, ri, c, row, k, __brev(hits), count_s);
     if (estimate)
         for (int v = 0; v < kWaves; ++v) rec.tail += tail_s[v];
     if (!g.greedy && g.k == 0)
