@@ -29,6 +29,20 @@ struct BoundsArgs {
 __device__ __forceinline__ float least(float a, float b) { return __builtin_elementwise_minimum(a, b); }
 __device__ __forceinline__ float most(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
+// Of a and the P-lane partner's a in lanes whose bit P is 0, of b in the others.
+template <int P>
+__device__ __forceinline__ float least_of_pair(float a, float b) {
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    if constexpr (P == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        return least(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    } else {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+        return least(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+}
+constexpr int kDppRowRor4 = 0x124, kDppRowRor8 = 0x128;  // from lane i + 4, i + 8 of a row of 16
+
 template <bool FP8> struct KeyVec;  // 16 bytes of one token's key
 template <> struct KeyVec<false> {
     static constexpr int N = 8;
@@ -56,10 +70,15 @@ template <> struct KeyVec<true> {
 };
 
 // One wave per page and head (SPLIT: the four waves of a workgroup divide the
-// page's tokens).  A token's row is D EB / 16 lanes of 16 bytes; a lane keeps the
-// bounds of its dimensions over the tokens it meets, four loads at a time, and the lanes
-// that hold the same dimensions are joined at the end.  Tokens behind the
-// last one stand for it.  Bound by HBM.
+// page's tokens).  A token's row is LPR lanes of 16 bytes; a lane keeps the
+// bounds of its N dimensions over the tokens it meets, up to four loads at a time.
+// Tokens behind the last one stand for it.  The lanes that hold the same dimensions are
+// joined at the end: as all bounds are least values (largest ones negated), an
+// exchange with the other half of the wave, then with the other row of 16, leaves each
+// lane half of its values, then a quarter.  (By shuffles of all of them through shared
+// memory the prompts below took 29.5 us, and e4m3 pages of 16 tokens 1.7 times as
+// long.)  Bound by HBM: 8 prompts of up to 12 k tokens, 110 MB of e4m3 keys, scales and
+// bounds, 22 us, 5 TB/s; a step's few pages by latency, 3.4 us.
 constexpr int kBoundLoads = 4;
 
 template <bool FP8, int D, bool SPLIT>
@@ -98,12 +117,14 @@ __global__ void __launch_bounds__(kBlock) bounds_kernel(BoundsArgs a) {
         float sc[kBoundLoads];
 #pragma unroll
         for (int i = 0; i < kBoundLoads; ++i) {
+            if (!SPLIT && t + i * TPL > last) continue;
             const int tok = min(t + i * TPL + grp, last);
             w[i] = *(const u32x4_t *)(k + tok * (D * (FP8 ? 1 : 2)));
             sc[i] = FP8 ? a.c.k_scale[row + tok] : 1.f;
         }
 #pragma unroll
         for (int i = 0; i < kBoundLoads; ++i) {
+            if (!SPLIT && t + i * TPL > last) continue;
             float x[N];
             V::run(w[i], sc[i], x);
 #pragma unroll
@@ -113,46 +134,45 @@ __global__ void __launch_bounds__(kBlock) bounds_kernel(BoundsArgs a) {
             }
         }
     }
+    // ---- lanes 0 .. 31 go on with the least values, the others with the largest
+    constexpr int C = LPR <= 16 ? N / 2 : N;    // of a row: its first or second half
 #pragma unroll
-    for (int o = LPR; o < 64; o <<= 1)
+    for (int j = 0; j < N; ++j) lo[j] = least_of_pair<32>(lo[j], -hi[j]);
+    if constexpr (LPR <= 16) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            lo[j] = least(lo[j], __shfl_xor(lo[j], o, 64));
-            hi[j] = most(hi[j], __shfl_xor(hi[j], o, 64));
-        }
+        for (int j = 0; j < C; ++j) lo[j] = least_of_pair<16>(lo[j], lo[j + C]);
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        if constexpr (LPR <= 8) lo[j] = least(lo[j], dpp_f<kDppRowRor8>(lo[j]));
+        if constexpr (LPR <= 4) lo[j] = least(lo[j], dpp_f<kDppRowRor4>(lo[j]));
+    }
+    const int largest = lane >> 5, at = sub * N + (LPR <= 16 ? (lane >> 4 & 1) * C : 0);
     if constexpr (SPLIT) {
-        if (grp == 0) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                join_s[wave][0][sub * N + j] = lo[j];
-                join_s[wave][1][sub * N + j] = hi[j];
-            }
-        }
+        for (int j = 0; j < C; ++j) join_s[wave][largest][at + j] = lo[j];  // (the same from every lane that has it)
         __syncthreads();
         if (wave) return;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
+        for (int j = 0; j < C; ++j)
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) {
-                lo[j] = least(lo[j], join_s[w][0][sub * N + j]);
-                hi[j] = most(hi[j], join_s[w][1][sub * N + j]);
-            }
+            for (int w = 1; w < kWaves; ++w) lo[j] = least(lo[j], join_s[w][largest][at + j]);
     }
-    // group 0 stores the least values, group 1 the largest
-    if (grp > 1) return;
-    uint16_t *out = (grp ? a.hi : a.lo) + ((int64_t)page * a.c.heads + h) * D + sub * N;
+    if (LPR < 16 && (lane & 15) >= LPR) return;
+    uint16_t *out = (largest ? a.hi : a.lo) + ((int64_t)page * a.c.heads + h) * D + at;
+    const float sign = largest ? -1.f : 1.f;
+    uint32_t w[C / 2];
 #pragma unroll
-    for (int j = 0; j < N; j += 8) {
-        u32x4_t w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = grp ? pack_bf16(hi[j + 2 * i], hi[j + 2 * i + 1]) : pack_bf16(lo[j + 2 * i], lo[j + 2 * i + 1]);
-        *(u32x4_t *)(out + j) = w;
-    }
+    for (int j = 0; j < C; j += 2) w[j / 2] = pack_bf16(lo[j] * sign, lo[j + 1] * sign);
+    if constexpr (C == 8) *(u32x4_t *)out = u32x4_t{w[0], w[1], w[2], w[3]};
+    else *(uint2 *)out = uint2{w[0], w[1]};
 }
 
 // A workgroup's waves divide a page where it holds more than two rounds of one
-// wave's loads.
+// wave's loads (8 prompts of 4096 tokens, 8 heads of 128, a wave a page against four:
+// e4m3 pages of 64 tokens, two rounds, 9.2 against 12.1 us, of 128 9.6 against 8.7, of
+// 1024 31.5 against 10.1; bf16 of 32 13.0 against 13.5, of 64 13.8 against 12.3, of 1024
+// 40.8 against 12.3).
 template <bool FP8, int D>
 static void launch_bounds(const BoundsArgs &a, int64_t units, int R, hipStream_t st) {
     constexpr int round = 64 / (D / KeyVec<FP8>::N) * kBoundLoads;
@@ -179,11 +199,11 @@ struct SelectArgs {
     const int32_t *table;        // [R][max_pages]
     const int32_t *ctx_len, *n_nodes;
     int num_pages, max_pages, heads, shift;
-    int M, Hq, G, D;
+    int M, Hq, G;
     int budget, first, last;
     int32_t *lists, *list_len;   // [R][heads][width], [R]
     int width;
-    double *sums;                // [R][heads][2][D] U and N, null: made where they are used
+    double *sums;                // [R][heads][2][D] U and N
     uint64_t *keys;              // [R][heads][max_pages] ordered scores
     Control *ctl;
 };
@@ -202,24 +222,10 @@ __device__ __forceinline__ Context context_of(const SelectArgs &a, int r) {
     return c;
 }
 
-// Adds a row's 8 values to its sums of positive and of negative parts (a NaN
-// goes to both).
-__device__ __forceinline__ void add_row(const uint16_t *row, double (&up)[8], double (&dn)[8]) {
-    const u32x4_t w = *(const u32x4_t *)row;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-        up[i] += (double)most(x, 0.f);
-        dn[i] += (double)least(x, 0.f);
-    }
-}
-__device__ __forceinline__ const uint16_t *query_row(const SelectArgs &a, int r, int h, int i) {
-    const int node = i / a.G;
-    return a.q + (((int64_t)r * a.M + node) * a.Hq + h * a.G + (i - node * a.G)) * a.D;
-}
-
-// U and N of one request and key head, where their rows are too many for every
-// workgroup of the score launch to read them.
+// U and N of one request and key head.  (A launch of its own: sums that every wave of
+// the score launch makes for itself took 41.8 against 33.5 us for 32 requests of 16 k
+// tokens and 4 query rows a head, 72 against 33.6 for 16 rows; 15.5 against 16.1 for
+// one request of 32 k tokens and 4 rows.)
 template <int D>
 __global__ void __launch_bounds__(kBlock) query_sums_kernel(SelectArgs a) {
     constexpr int LPR = D / 8, GRP = kBlock / LPR;
@@ -230,7 +236,17 @@ __global__ void __launch_bounds__(kBlock) query_sums_kernel(SelectArgs a) {
     double up[8], dn[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) up[i] = dn[i] = 0.0;
-    for (int i = grp; i < c.n * a.G; i += GRP) add_row(query_row(a, r, h, i) + sub * 8, up, dn);
+    for (int i = grp; i < c.n * a.G; i += GRP) {
+        const int node = i / a.G;
+        const uint16_t *row = a.q + (((int64_t)r * a.M + node) * a.Hq + h * a.G + (i - node * a.G)) * D;
+        const u32x4_t w = *(const u32x4_t *)(row + sub * 8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {           // (a NaN goes to both)
+            const float x = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+            up[j] += (double)most(x, 0.f);
+            dn[j] += (double)least(x, 0.f);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         part[grp][0][sub * 8 + i] = up[i];
@@ -274,29 +290,19 @@ __device__ __forceinline__ uint64_t key_of(double s) {
 // lie side by side: SPAN lanes take 8 values each of them (the launch's y axis goes
 // over rows of more than 64 lanes), so that a wave reads pieces of up to a
 // kilobyte; D / 8 lanes share a head.  The largest values go with U, then the
-// least with N: one of the two sums is in registers at a time.  Bound by HBM.
+// least with N: one of the two sums is in registers at a time.  Bound by HBM:
+// 171 MB of bounds (64 requests of up to 16 k tokens, 8 heads of 128, 16-token pages) in
+// 27.5 us.  Two pages of one head a lane pair and eight loads a side took longer (80 us
+// for the call against 58, and 44 us for this launch against 42, where each wave still
+// summed its queries).
 constexpr int kScoreLoads = 4;      // of 16 bytes a lane and side, all under way
-constexpr int kDirectRows = 16;     // query rows that every wave sums up by itself
 
 // U (or, LEAST, N) of this lane's 8 dimensions.
 template <int D, bool LEAST>
-__device__ __forceinline__ void query_sums(const SelectArgs &a, const Context &c, int r, int h, int sub, double (&q)[8]) {
-    if (a.sums) {
-        const double *s = a.sums + ((int64_t)r * a.heads + h) * 2 * D + (LEAST ? D : 0) + sub * 8;
+__device__ __forceinline__ void query_sums(const SelectArgs &a, int r, int h, int sub, double (&q)[8]) {
+    const double *s = a.sums + ((int64_t)r * a.heads + h) * 2 * D + (LEAST ? D : 0) + sub * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = s[i];
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = 0.0;
-    for (int i = 0; i < c.n * a.G; ++i) {
-        const u32x4_t w = *(const u32x4_t *)(query_row(a, r, h, i) + sub * 8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float v = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-            q[j] += (double)(LEAST ? least(v, 0.f) : most(v, 0.f));
-        }
-    }
+    for (int i = 0; i < 8; ++i) q[i] = s[i];
 }
 
 template <int D, int SPAN>
@@ -335,9 +341,9 @@ __global__ void __launch_bounds__(kBlock) score_kernel(SelectArgs a) {
     };
 #pragma unroll
     for (int t = 0; t < kScoreLoads; ++t) s[t] = 0.0;
-    query_sums<D, false>(a, c, r, h, sub, q);
+    query_sums<D, false>(a, r, h, sub, q);
     add(hi);
-    query_sums<D, true>(a, c, r, h, sub, q);
+    query_sums<D, true>(a, r, h, sub, q);
     add(lo);
     uint64_t *keys = a.keys + ((int64_t)r * a.heads + h) * a.max_pages;
 #pragma unroll
@@ -371,7 +377,7 @@ __device__ __forceinline__ uint64_t block_prefix(uint64_t v, uint64_t (&wave_s)[
 // being cut again until it is taken whole or is one key (then the lowest
 // pages that have it are taken).  Keys of up to kHeldKeys pages stay in
 // shared memory.  Bound by latency: a handful of dependent passes over a few
-// keys a thread.
+// keys a thread (10.6 us for eight lists of 1875 pages, 9.3 for 512 of up to 1000).
 constexpr int kHeldKeys = 4096;
 constexpr int kParts = 2048;
 
@@ -525,9 +531,8 @@ __global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
 
 template <int D>
 static void launch_select(const SelectArgs &a, int R, hipStream_t st) {
-    if (a.sums)
-        hipLaunchKernelGGL((query_sums_kernel<D>), dim3((unsigned)a.heads, (unsigned)R), dim3(kBlock), 0, st, a);
     if (a.max_pages > a.budget) {
+        hipLaunchKernelGGL((query_sums_kernel<D>), dim3((unsigned)a.heads, (unsigned)R), dim3(kBlock), 0, st, a);
         // lanes of a page's row, the next power of two
         const int64_t row = (int64_t)a.heads * D / 8;
         const int span = row <= D / 8 ? D / 8 : row <= 16 ? 16 : row <= 32 ? 32 : 64;
@@ -631,7 +636,6 @@ int spec_page_select(const void *q, int q_dtype, const void *k_min, const void *
     a.M = M;
     a.Hq = Hq;
     a.G = Hq / Hkv;
-    a.D = D;
     a.budget = budget;
     a.first = first;
     a.last = last;
@@ -640,8 +644,7 @@ int spec_page_select(const void *q, int q_dtype, const void *k_min, const void *
     a.width = list_pages;
     a.ctl = (Control *)workspace;
     a.keys = (uint64_t *)((char *)workspace + sizeof(Control));
-    if ((int64_t)M * a.G > kDirectRows && max_pages > budget)
-        a.sums = (double *)(a.keys + (size_t)R * Hkv * max_pages);
+    a.sums = (double *)(a.keys + (size_t)R * Hkv * max_pages);
     if (D == 64) launch_select<64>(a, R, (hipStream_t)stream);
     else if (D == 128) launch_select<128>(a, R, (hipStream_t)stream);
     else launch_select<256>(a, R, (hipStream_t)stream);
