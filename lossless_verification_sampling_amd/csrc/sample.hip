@@ -24,27 +24,40 @@
 //   settle, write (truncation): its cut; the rows
 // A row that none of this fits (top_k above kMostTopK together with top_p, more
 // equal logits than a list holds) is done whole by one workgroup at the end.
+//
+// Draws of bf16 rows of 151936 ids, 40 likely ones above a normal floor, T = 0.9,
+// in us for one row and for 256 (whose bytes alone take 15 at a copy's rate):
+//   nothing cut 28, 72      top_p 0.9 27, 42       top_p 0.999 48, 167
+//   min_p 0.05 26, 35       top_k 50 28, 48        top_k 200 28, 55
+//   top_k 1000 38, 128      top_k 50, top_p 0.9 27, 46
+//   top_k 1000, top_p 0.9 (whole rows) 101, 125
+// Truncation of the 256: 48, 55, 165, 47, 60, 68, 136, 59, 167 in the same order.
 #include "sample.h"
 
 namespace sv {
 
 constexpr int kRowThreads = 1024;             // threads of a row's workgroup in the last launches
 constexpr int kListKeys = 2048;               // keys that are looked at one by one
-constexpr int kChunk = 8192;                  // ids of a chunk
+// Ids of a chunk: 32 a lane, which stay in registers between the passes; a user's
+// single row still makes a workgroup for each of 19 compute units.
+constexpr int kChunk = 8192;
 constexpr int kListed = 4096;                 // candidates that `finish` takes of a row at most
 constexpr int kInBin = 8192;                  // ids of one bin that the last launches take
 constexpr int kMostTopK = kBlock;             // largest top_k that candidates are listed for
 // A chunk's histogram: bins of 16 steps (an eighth of a power of two) from
 // the largest logit, bin kDeepBins - 1, to behind the last one with a weight.
 constexpr int kDeepBins = 384;
-constexpr int kSliceChunks = 16384;           // chunks that a launch takes at a time
-constexpr int kListGroups = 2048;             // workgroups of a launch over the work list
+// Chunks, and room for candidates, that a launch takes at a time: the workspace stays
+// below 200 MB whatever the batch, and thousands of workgroups fill the card.
+constexpr int kSliceChunks = 16384, kSliceListed = 1 << 24;
+constexpr int kListGroups = 2048;             // workgroups of a launch over the work list: what the card holds
 constexpr int kWriteIds = 32768;              // ids that a writing workgroup takes
 // Candidates without top_k: ids within this many temperatures of the chunk's
 // largest logit (a share of e^-8 = 3.4e-4 of its) that min_p leaves.  Where a
 // wave's 2048 ids hold more than kManyHits of them (a chunk without likely ids
-// has thousands of unlikely ones), those below the least of the largest logits
-// of its four parts are left out.
+// has thousands of unlikely ones; more than kManyLanes lanes that hold one are taken for
+// that), those below the least of the largest logits of its four rows of lanes are left
+// out.  (All of them listed, 256 rows of 151936 ids took 200 us instead of 110.)
 constexpr float kHot = 8.0f;
 constexpr int kManyHits = 64, kManyLanes = 40;
 
@@ -249,6 +262,9 @@ __device__ __forceinline__ float of_rows(float v) {
                                          __builtin_elementwise_maximum(readlane_f(v, 32), readlane_f(v, 48)));
 }
 
+// The first launch.  Under top-p it is bound by vector instructions, 600 a wave (the
+// issue slots are 90% busy): 256 rows of 151936 bf16 ids, 78 MB, in 26.5 us against 15
+// for rows that nothing cuts, which are read alone.
 template <typename T>
 __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
@@ -515,6 +531,11 @@ __device__ __forceinline__ void mark_fault(const SampleArgs &a, int ri) {
     atomic_or_u32(&a.ctl->status, SPEC_DEV_BAD_REQUEST);
 }
 
+// One workgroup a row.  Up to 256 candidates are sorted, a thread's place being the number
+// of those before its own; more are cut by histograms (sorted so, 512 took 32 us where
+// the histograms take 23).  A thread keeps up to 32 candidates in registers from one pass
+// to the next (8: 23 us against 19.6).  Bound by latency, some ten dependent steps of
+// a microsecond: 13 us for 256 rows under top-p, 19.6 for 64 rows with top_k up to 200.
 template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
     __shared__ Scratch<kBlock> s;
@@ -805,6 +826,8 @@ __device__ __forceinline__ void sum_loads(const SampleArgs &a, int ri, int c, co
     }
 }
 
+// Chunks of the rows that `finish` left.  Bound by fp64 instructions, 20 a weight: 256 rows
+// with nothing cut, each id's weight, take 43 us; a few rows' histograms 9 us, by latency.
 template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kBlock) second_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
@@ -876,6 +899,9 @@ __device__ __forceinline__ float least_of_bin(const Weights &wt, int bin) {
     return of_key(hi);
 }
 
+// The same chunks again where a cut is looked for.  Every workgroup adds the row's
+// histograms up for itself (58 kB out of the caches), so that no launch for it comes
+// between.  Bound by latency: a dozen rows of 151936 ids 12 us.
 template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kBlock, 3) third_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
@@ -1304,6 +1330,8 @@ __device__ __forceinline__ void whole_row(const SampleArgs &a, RowShared<T> &sh,
     }
 }
 
+// Tokens of the rows that are not done.  Bound by latency: 18 us for a dozen cuts
+// with up to 2000 ids in the bin that holds them, 10 where nothing was cut.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) draw_kernel(SampleArgs a) {
     constexpr int PER = kChunk / RowShared<T>::SUB;    // loads of a chunk
@@ -1355,7 +1383,7 @@ __global__ void __launch_bounds__(kRowThreads) draw_kernel(SampleArgs a) {
 }
 
 // Cuts of truncated rows that are still to be found, for write_kernel; rows
-// done whole.
+// done whole.  14 us for a few rows, by latency.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) settle_kernel(SampleArgs a) {
     __shared__ RowShared<T> sh;
@@ -1403,7 +1431,10 @@ __global__ void __launch_bounds__(kRowThreads) settle_kernel(SampleArgs a) {
     a.row[ri] = rec;
 }
 
-// Truncated rows: kWriteIds ids a workgroup.
+// Truncated rows: kWriteIds ids a workgroup.  Bound by HBM: 512 rows of 151936 bf16 ids,
+// 156 MB written, 30.8 us, 5.1 TB/s.  (The rows that `finish` settled written beside
+// the two launches after it, which wait more than they work: 129 to 132 us for the
+// call against 128, those launches taking as much longer.)
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) write_kernel(SampleArgs a, int parts) {
     constexpr int N = Row<T>::N;
@@ -1487,7 +1518,9 @@ static Layout layout_of(int R, int J, int V) {
     if (l.room < 512) l.room = 512;
     if (l.room > V) l.room = V;
     const int64_t rows = (int64_t)R * J;
+    const int listed = kSliceListed / (l.chunks * l.room);
     l.rows = kSliceChunks / l.chunks;
+    if (l.rows > listed) l.rows = listed;
     if (l.rows > rows) l.rows = (int)rows;
     const size_t n = (size_t)l.rows * l.chunks;
     size_t at = sizeof(Control);
