@@ -751,8 +751,10 @@ int spec_sample(const void *logits, int dtype, int64_t ld, const float *temperat
  * The rows with every id that is not kept at -inf, for spec_verify_batch at the
  * same temperature (T = 0: its argmax rule sees the one id).
  *   out_logits   [R][J] rows of V in the logits' type, row (r, j) at element
- *                (r * J + j) * out_ld; `logits` itself (then out_ld == ld), or
- *                memory apart from it.  A faulty row becomes NaN.
+ *                (r * J + j) * out_ld; the rows of `logits` themselves, or rows
+ *                apart from all of them (SPEC_EINVAL otherwise: with another
+ *                ld, all of the memory between the first and the last).  A
+ *                faulty row becomes NaN.
  *   out_kept     [R][J]  int32, nullable, as spec_sample's
  */
 int spec_truncate_logits(const void *logits, int dtype, int64_t ld, const float *temperature,

@@ -1504,6 +1504,19 @@ static int check_rows(const void *logits, int dtype, int64_t ld, int R, int J, i
     return SPEC_OK;
 }
 
+// Rows that share memory and are not the same rows.  (Rows that lie between each other's
+// do not, as far as the same spacing shows it.)
+static bool rows_overlap(const void *a, int64_t ld_a, const void *b, int64_t ld_b, int64_t rows, int64_t V, int64_t size) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    const uint64_t span_a = (uint64_t)((rows - 1) * ld_a + V) * size, span_b = (uint64_t)((rows - 1) * ld_b + V) * size;
+    if (x + span_a <= y || y + span_b <= x) return false;
+    if (rows > 1 && ld_a != ld_b) return true;
+    if (x == y) return false;
+    if (rows == 1) return true;
+    const uint64_t step = (uint64_t)(ld_a * size), off = (x < y ? y - x : x - y) % step;
+    return off < (uint64_t)(V * size) || step - off < (uint64_t)(V * size);
+}
+
 // A slice's memory.
 struct Layout {
     int chunks, room, rows;      // of a row; candidates of a chunk; rows of a slice
@@ -1627,7 +1640,7 @@ int spec_truncate_logits(const void *logits, int dtype, int64_t ld, const float 
     if (out_ld < V) return SPEC_EINVAL;
     if (R == 0 || J == 0) return SPEC_OK;
     if (!out_logits || ((uintptr_t)out_logits & (dtype == SPEC_F32 ? 3u : 1u))) return SPEC_EINVAL;
-    if (out_logits == logits && out_ld != ld) return SPEC_EINVAL;  // in place, or apart
+    if (rows_overlap(logits, ld, out_logits, out_ld, (int64_t)R * J, V, dtype == SPEC_F32 ? 4 : 2)) return SPEC_EINVAL;
     SampleArgs a{};
     a.logits = logits;
     a.ld = ld;

@@ -36,6 +36,22 @@ def test_arguments(sample, truncate):
     assert truncate(out=A, out_ld=1001) == EINVAL                   # in place, but spaced otherwise
 
 
+def test_truncation_into_rows_that_overlap(truncate):
+    """2 x 3 bf16 rows of 1000: the rows themselves or others, between them or
+    apart (EWORKSPACE is what a call that passed the check is stopped by)."""
+    def f(off, ld=1000, out_ld=1000, **kw):
+        return truncate(out=A + 2 * off, ld=ld, out_ld=out_ld, ws_bytes=0, **kw)
+    assert f(0) == f(6000) == f(-6000) == EWORKSPACE
+    assert f(1) == f(1000) == f(5999) == f(-1) == f(-5999) == EINVAL
+    assert f(0, 2500, 2500) == f(1000, 2500, 2500) == f(1500, 2500, 2500) == f(-1000, 2500, 2500) == EWORKSPACE
+    assert f(999, 2500, 2500) == f(1501, 2500, 2500) == f(2500, 2500, 2500) == f(-1501, 2500, 2500) == EINVAL
+    assert f(13500, 2500, 2500) == EWORKSPACE and f(12500, 2500, 2500) == f(0, 2500, 2600) == EINVAL
+    assert f(13500, 2500, 1000) == f(-6000, 2500, 1000) == EWORKSPACE and f(13499, 2500, 1000) == EINVAL
+    # one row has no spacing
+    assert f(0, 1000, 1001, R=1, J=1) == f(1000, 1000, 1001, R=1, J=1) == EWORKSPACE
+    assert f(999, 1000, 1001, R=1, J=1) == EINVAL
+
+
 def test_workspace_query(lib, sample, truncate):  # noqa: F811
     size = lib.spec_sample_workspace_bytes
     size.restype = S

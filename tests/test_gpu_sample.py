@@ -164,6 +164,38 @@ def test_wide_logits(sv, dev, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("off", [300.0, -300.0, 4e4, -4e4, 3e5])
+def test_logits_far_from_zero(sv, dev, off, dtype):
+    """top_p's estimated tail where x / T is far larger than the differences."""
+    g = np.random.default_rng(11)
+    V = 20000
+    x = g.standard_normal((4, 1, V)) * 2 * max(1.0, abs(off) / 300)
+    x[:, :, ::500] += 9 * max(1.0, abs(off) / 300)
+    for t, p in ((1.0, 0.9), (0.3, 0.99), (1.0, 0.99), (0.02, 0.7)):
+        Rows(x + off, dtype, t=t * max(1.0, abs(off) / 300), p=p, u=uniforms(g, 4, 1)).check(sv, dev)
+    if dtype is F32:                                                # steps of 2^-5 at 3e5, x / T past 2^20
+        x = g.standard_normal((4, 1, V)) * 2 + off
+        for t, p in ((0.2, 0.9), (0.7, 0.95), (0.7, 0.6)):
+            Rows(x, dtype, t=t, p=p, u=uniforms(g, 4, 1)).check(sv, dev)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_truncation_into_rows_between(sv, dev, dtype):
+    """The output's rows lie between the logits' own."""
+    g = np.random.default_rng(12)
+    s = Rows(g.standard_normal((7, 2, 1001)) * 4, dtype, **SETTINGS)
+    both = torch.full((7, 2, 2100), 5.0, dtype=dtype, device=dev)
+    x, out = both[:, :, :1001], both[:, :, 1050:2051]
+    x.copy_(s.x)
+    want, _ = sv.spec_truncate_logits(x.contiguous(), **s.kw(dev))
+    sv.spec_truncate_logits(x, **s.kw(dev), out=out)
+    assert torch.equal(out, want) and torch.equal(x.cpu(), s.x)
+    assert (both[:, :, 1001:1050] == 5.0).all() and (both[:, :, 2051:] == 5.0).all()
+    with pytest.raises(sv.SpecError):
+        sv.spec_truncate_logits(x, **s.kw(dev), out=both[:, :, 1000:2001])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("V, shift", [(8186, 5), (8192, 0), (8192, 1), (8193, 0), (8240, 3), (16384 + 1100, 0), (24575, 2)])
 def test_rows_that_end_inside_a_part(sv, dev, V, shift, dtype):
     """Lengths around a multiple of the 8192 ids that a workgroup reads; the
