@@ -372,6 +372,10 @@ __device__ __forceinline__ uint64_t block_prefix(uint64_t v, uint64_t (&wave_s)[
     return before;
 }
 
+// (min and max of unlike 64-bit types are taken as doubles, which round.)
+__device__ __forceinline__ uint64_t lower(uint64_t a, uint64_t b) { return a < b ? a : b; }
+__device__ __forceinline__ uint64_t higher(uint64_t a, uint64_t b) { return a > b ? a : b; }
+
 // The best pages of one request and key head, and its list.  The cut is found
 // by counts over 2048 equal parts of the keys' range, the part that holds it
 // being cut again until it is taken whole or is one key (then the lowest
@@ -413,8 +417,8 @@ __global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
             ok = ok && (unsigned)page[e] < (unsigned)a.num_pages;
             if (!choose || p < from || p >= to) continue;
             if (in_lds) held[p] = k[e];
-            lo = min(lo, k[e]);
-            hi = max(hi, k[e]);
+            lo = lower(lo, k[e]);
+            hi = higher(hi, k[e]);
         }
     }
     ok = __syncthreads_and(ok);
@@ -432,8 +436,8 @@ __global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
     auto key = [&](int p) -> uint64_t { return in_lds ? held[p] : keys[p]; };
     if (choose) {
         for (int o = 32; o; o >>= 1) {
-            lo = min(lo, (uint64_t)__shfl_xor((unsigned long long)lo, o, 64));
-            hi = max(hi, (uint64_t)__shfl_xor((unsigned long long)hi, o, 64));
+            lo = lower(lo, __shfl_xor((unsigned long long)lo, o, 64));
+            hi = higher(hi, __shfl_xor((unsigned long long)hi, o, 64));
         }
         if ((tid & 63) == 0) {
             ends_s[0][tid >> 6] = lo;
@@ -441,8 +445,8 @@ __global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
         }
         __syncthreads();
         for (int w = 0; w < kWaves; ++w) {
-            lo = min(lo, ends_s[0][w]);
-            hi = max(hi, ends_s[1][w]);
+            lo = lower(lo, ends_s[0][w]);
+            hi = higher(hi, ends_s[1][w]);
         }
         uint32_t want = (uint32_t)(a.budget - a.first - a.last);
         if (want == 0) {
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
                 want = (uint32_t)cut_s[1];
                 __syncthreads();
                 lo += part << shift;
-                hi = min(hi, lo + ((1ull << shift) - 1));
+                hi = lower(hi, lo + ((1ull << shift) - 1));
                 if (there == want) {  // every key of the part
                     cut = lo - 1;     // (lo is above 0: no score's key is)
                     ties = 0;

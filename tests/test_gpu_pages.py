@@ -205,6 +205,22 @@ def test_equal_scores_take_the_lower_pages(sv, dev, budget):
     s.check(s.run(sv, dev))
 
 
+@pytest.mark.parametrize("budget, first, last", [(1, 0, 0), (4, 1, 2), (30, 0, 1), (149, 0, 0)])
+@pytest.mark.parametrize("F", [150, 4200])                          # keys in shared memory, and not
+def test_scores_that_differ_in_their_last_bits(sv, dev, F, budget, first, last):
+    """1 + i 2^-52, or far below: neighbours in fp64, whose keys differ in the lowest
+    bits, in a range that has to be narrowed several times."""
+    s = Lists(25, 1, 1, 1, 1, 64, 16, [16 * F], budget, first, last)
+    i = np.random.default_rng(F).permutation(F) % 256
+    s.q[:], s.lo[:], s.hi[:] = 0.0, 0.0, 0.0
+    s.q[..., 3], s.q[..., 40] = 1.0, 2.0 ** -52
+    at = torch.from_numpy(s.table[0, :F]).long()
+    s.hi[at, 0, 3], s.hi[at, 0, 40] = 1.0, torch.from_numpy(i.astype(np.float32)).to(torch.bfloat16)
+    s.check(s.run(sv, dev))
+    s.hi[at[i < 200], 0, 3] = 0.5
+    s.check(s.run(sv, dev))
+
+
 def test_scores_that_are_no_numbers(sv, dev):
     s = Lists(22, 1, 1, 2, 1, 64, 16, [16 * 30], 4)
     t = s.table[0]
