@@ -64,7 +64,7 @@ constexpr int kManyHits = 64, kManyLanes = 40;
 struct ChunkRec {
     uint32_t top;                // key of the largest logit
     uint32_t n;                  // candidates
-    uint32_t finite;             // ids that are not masked out (after `second`: ids above the cut)
+    uint32_t finite;             // ids that are not masked out, where it counts (after `second`: ids above the cut)
     uint32_t odd;                // a NaN or +inf is among them
     double tail;                 // estimate of sum e^((x - top) / T) over the others
     uint32_t share;              // key that the chunk's share of the row's first top_k ids reach
@@ -82,7 +82,7 @@ enum : uint32_t {                // a row's state
 struct RowRec {
     uint32_t state;
     float m;                     // largest logit
-    uint32_t finite;             // ids that are not masked out
+    uint32_t finite;             // ids that are not masked out, where it counts
     uint32_t n;                  // kept ids, listed (kDone)
     uint32_t key;                // kWhole, kCut
     uint32_t last;               // kCut
@@ -478,10 +478,11 @@ __global__ void __launch_bounds__(kBlock) chunk_kernel(SampleArgs a) {
 // ---------------------------------------------------------------------------
 
 // The bounds of an estimated tail.  A term's exponent is off by 3 2^-24 of
-// itself (the difference's, the factor's and the product's rounding), of
-// 30 log2(e) = 43.3 at most: 5.4e-6 of the term; the exponential by 2.4e-7 and a
-// sum of eight by 4.2e-7.  Ids that lie deeper weigh two units at most, and
-// each weight is rounded to a unit: four units an id.
+// itself (the difference's, the factor's and the product's rounding; in one operation
+// the factor's and the result's), of 30 log2(e) = 43.3 at most: 5.4e-6 of the term; the
+// exponential by 2.4e-7 (and again for b's rounding) and a sum of eight by 4.2e-7.  Ids
+// that lie deeper weigh two units at most, and each weight is rounded to a unit: four
+// units an id.
 constexpr double kTailError = 7.62939453125e-06;   // 2^-17
 constexpr double kTailUnits = 1048576.0;           // 2^20
 
@@ -905,7 +906,7 @@ __device__ __forceinline__ float least_of_bin(const Weights &wt, int bin) {
 template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kBlock, 3) third_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
-    __shared__ u64 wave_s[kWaves], above_s, there_s;
+    __shared__ u64 wave_s[kWaves], above_s;
     __shared__ int bin_s;
     __shared__ double table_s[kSteps];
     __shared__ uint32_t count_s[kWaves], above_n_s[kWaves];
@@ -917,7 +918,6 @@ __global__ void __launch_bounds__(kBlock, 3) third_kernel(SampleArgs a) {
         const Setting g = setting_of<DRAW>(a, a.row0 + ri);
         const RowRec rec = a.row[ri];
         const Row<T> row = row_of<T>(a.logits, (int64_t)(a.row0 + ri) * a.ld, a.V);
-        const Weights wt = weights_of(rec.m, g.t, table_s);
         Chunk<T> k;
         load_chunk(row, c, k);
         // ---- the row's histogram, the highest bins in thread 0
@@ -926,10 +926,21 @@ __global__ void __launch_bounds__(kBlock, 3) third_kernel(SampleArgs a) {
         u64 mine[E] = {}, sum = 0;
         const int b0 = max(kDeepBins - 1 - tid * E, 0), b1 = max(b0 - 1, 0);
         static_assert(E == 2, "two bins a thread");
-#pragma unroll 8
-        for (int i = 0; i < a.chunks; ++i) {
-            mine[0] += h[i * kDeepBins + b0];
-            mine[1] += h[i * kDeepBins + b1];
+        constexpr int LOADS = 10;               // chunks whose bins are under way
+        for (int i0 = 0; i0 < a.chunks; i0 += LOADS) {
+            u64 got[LOADS][E];
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const u64 *const of = h + min(i0 + i, a.chunks - 1) * kDeepBins;
+                got[i][0] = of[b0];
+                got[i][1] = of[b1];
+            }
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                if (i0 + i >= a.chunks) continue;
+                mine[0] += got[i][0];
+                mine[1] += got[i][1];
+            }
         }
         if (tid * E >= kDeepBins) mine[0] = mine[1] = 0;
 #pragma unroll
@@ -961,6 +972,7 @@ __global__ void __launch_bounds__(kBlock, 3) third_kernel(SampleArgs a) {
             d.want = rec.by_weight ? Want{true, 0, want} : Want{false, (uint32_t)want, 0};
             a.deep[ri] = d;
         }
+        const Weights wt = weights_of(rec.m, g.t, table_s);
         // ---- ids in it and above it, of those that min_p leaves: logits
         // from `edge` on, and from `over` on
         const float low = of_key(min_p_key(rec.m, g));
@@ -1031,12 +1043,11 @@ struct Deep {
 };
 template <typename T>
 __device__ __forceinline__ bool deep_cut(const SampleArgs &a, RowShared<T> &sh, int ri, const Setting &g,
-                                         const RowRec &rec, const Weights &wt, Deep &d) {
+                                         const RowRec &rec, const Records &r, const DeepRec &bin, const Weights &wt,
+                                         Deep &d) {
     constexpr int B = kRowThreads;
     const int tid = threadIdx.x;
-    const Records r = records_of(a, ri);
     if (r.full || r.n > (uint32_t)kInBin) return false;
-    const DeepRec bin = a.deep[ri];
     d.n = r.n;
     d.above = wave_sum_u32((tid & 63) < a.chunks ? r.rec.finite : 0u);
     if (tid < 64) sh.off[tid] = r.off;
@@ -1340,7 +1351,9 @@ __global__ void __launch_bounds__(kRowThreads) draw_kernel(SampleArgs a) {
     const Setting g = setting_of<true>(a, a.row0 + ri);
     if (!g.live) return;
     const RowRec rec = a.row[ri];
+    const Records r = records_of(a, ri);        // (both loaded before either is looked at)
     if (rec.state == kDone || rec.state == kFault) return;
+    const DeepRec bin = a.deep[ri];             // (of kDeep rows alone)
     const int64_t out = a.row0 + ri;
     const Row<T> row = row_of<T>(a.logits, out * a.ld, a.V);
     const Weights wt = weights_of(rec.m, g.t, sh.s.table);
@@ -1361,7 +1374,7 @@ __global__ void __launch_bounds__(kRowThreads) draw_kernel(SampleArgs a) {
         return;
     }
     Deep d;
-    if (rec.state == kMany || !deep_cut(a, sh, ri, g, rec, wt, d)) {
+    if (rec.state == kMany || !deep_cut(a, sh, ri, g, rec, r, bin, wt, d)) {
         __syncthreads();
         whole_row<T, true>(a, sh, row, g, rec, wt, out);
         return;
@@ -1391,6 +1404,7 @@ __global__ void __launch_bounds__(kRowThreads) settle_kernel(SampleArgs a) {
     const Setting g = setting_of<false>(a, a.row0 + ri);
     if (!g.live) return;
     RowRec rec = a.row[ri];
+    const Records r = records_of(a, ri);
     const int64_t out = a.row0 + ri;
     if (rec.state == kWhole && g.mp > 0.f) {
         if (a.out_kept && tid < 64) {
@@ -1400,11 +1414,12 @@ __global__ void __launch_bounds__(kRowThreads) settle_kernel(SampleArgs a) {
         return;
     }
     if (rec.state != kDeep && rec.state != kMany) return;
+    const DeepRec bin = a.deep[ri];
     const Weights wt = weights_of(rec.m, g.t, sh.s.table);
     fill_table(sh.s.table);
     __syncthreads();
     Deep d;
-    if (rec.state == kMany || !deep_cut(a, sh, ri, g, rec, wt, d)) {
+    if (rec.state == kMany || !deep_cut(a, sh, ri, g, rec, r, bin, wt, d)) {
         __syncthreads();
         whole_row<T, false>(a, sh, row_of<T>(a.logits, out * a.ld, a.V), g, rec, wt, out);
         if (tid == 0) a.row[ri].state = kWritten;
