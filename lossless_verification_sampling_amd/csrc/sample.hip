@@ -536,7 +536,7 @@ __device__ __forceinline__ void mark_fault(const SampleArgs &a, int ri) {
 // of those before its own; more are cut by histograms (sorted so, 512 took 32 us where
 // the histograms take 23).  A thread keeps up to 32 candidates in registers from one pass
 // to the next (8: 23 us against 19.6).  Bound by latency, some ten dependent steps of
-// a microsecond: 13 us for 256 rows under top-p, 19.6 for 64 rows with top_k up to 200.
+// a microsecond: 12.6 us for 256 rows under top-p, 19.6 for 64 rows with top_k up to 200.
 template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
     __shared__ Scratch<kBlock> s;
@@ -902,7 +902,8 @@ __device__ __forceinline__ float least_of_bin(const Weights &wt, int bin) {
 
 // The same chunks again where a cut is looked for.  Every workgroup adds the row's
 // histograms up for itself (58 kB out of the caches), so that no launch for it comes
-// between.  Bound by latency: a dozen rows of 151936 ids 12 us.
+// between.  Bound by latency: a dozen rows of 151936 ids 11 us (12 with the histograms
+// eight at a time and the rest one by one).
 template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kBlock, 3) third_kernel(SampleArgs a) {
     constexpr int N = Row<T>::N, NB = Chunk<T>::NB;
