@@ -225,10 +225,9 @@ def prepare(case, seed):
     if op in ("sample", "truncate"):
         J, V = case["J"], case["V"]
         g = torch.Generator(device=DEV).manual_seed(seed)
-        # a broad floor of logits and a few dozen likely ids a row (one in each
-        # fortieth of it: two of the same id would leave the logit to chance)
+        # a broad floor of logits and a few dozen likely ids a row
         x = 2.0 * torch.randn(R, J, V, generator=g, device=DEV)
-        at = torch.randint(V // 40, (R, J, 40), generator=g, device=DEV) + torch.arange(40, device=DEV) * (V // 40)
+        at = torch.randint(V, (R, J, 40), generator=g, device=DEV)
         x.scatter_(2, at, 12.0 + 2.5 * torch.randn(R, J, 40, generator=g, device=DEV))
         x = x.to(torch.bfloat16 if case["dtype"] == "bf16" else torch.float32)
         u = torch.floor(torch.rand(R, J, generator=g, device=DEV, dtype=torch.float64) * 2 ** 24) / 2 ** 24
