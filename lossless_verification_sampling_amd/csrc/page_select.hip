@@ -10,6 +10,7 @@
 // the products of bf16 values with U and N are close to exact there, so that
 // which pages are chosen does not hang on the order of the sums.
 #include "cache.h"
+#include "page_cut.h"
 
 namespace sv {
 
@@ -377,13 +378,11 @@ __device__ __forceinline__ uint64_t lower(uint64_t a, uint64_t b) { return a < b
 __device__ __forceinline__ uint64_t higher(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 // The best pages of one request and key head, and its list.  The cut is found
-// by counts over 2048 equal parts of the keys' range, the part that holds it
-// being cut again until it is taken whole or is one key (then the lowest
-// pages that have it are taken).  Keys of up to kHeldKeys pages stay in
-// shared memory.  Bound by latency: a handful of dependent passes over a few
-// keys a thread (10.6 us for eight lists of 1875 pages, 9.3 for 512 of up to 1000).
+// by counts over 2048 equal parts of the keys' range, and again over the part that
+// holds it (page_cut.h; of one key the lowest pages that have it are taken).  Keys of
+// up to kHeldKeys pages stay in shared memory.  Bound by latency: a handful of
+// dependent passes over a few keys a thread (10.6 us for eight lists of 1875 pages, 9.3 for 512 of up to 1000).
 constexpr int kHeldKeys = 4096;
-constexpr int kParts = 2048;
 
 __global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
     __shared__ uint64_t held[kHeldKeys];
@@ -448,12 +447,11 @@ __global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
             lo = lower(lo, ends_s[0][w]);
             hi = higher(hi, ends_s[1][w]);
         }
-        uint32_t want = (uint32_t)(a.budget - a.first - a.last);
+        const uint32_t want = (uint32_t)(a.budget - a.first - a.last);
         if (want == 0) {
             cut = ~0ull;  // above every key: +infinity's is below
         } else {
-            while (true) {
-                const int shift = hi == lo ? 0 : max(0, 53 - __clzll((long long)(hi - lo)));
+            const KeyCut found = key_cut(lo, hi, want, [&](uint64_t lo, uint64_t hi, int shift, uint32_t want) {
                 for (int i = tid; i < kParts; i += kBlock) count_s[i] = 0u;
                 __syncthreads();
                 for (int p = from + tid; p < to; p += kBlock) {
@@ -482,23 +480,12 @@ __global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {
                     }
                 }
                 __syncthreads();
-                const uint64_t part = cut_s[0];
-                const uint32_t there = (uint32_t)(cut_s[1] >> 32);
-                want = (uint32_t)cut_s[1];
+                const CutPart part{cut_s[0], (uint32_t)(cut_s[1] >> 32), (uint32_t)cut_s[1]};
                 __syncthreads();
-                lo += part << shift;
-                hi = lower(hi, lo + ((1ull << shift) - 1));
-                if (there == want) {  // every key of the part
-                    cut = lo - 1;     // (lo is above 0: no score's key is)
-                    ties = 0;
-                    break;
-                }
-                if (shift == 0) {
-                    cut = lo;
-                    ties = want;
-                    break;
-                }
-            }
+                return part;
+            });
+            cut = found.key;              // (above 0: no score's key is 0)
+            ties = found.ties;
         }
     }
     // ---- the list, in the order of the context: a thread takes neighbouring pages

@@ -237,6 +237,33 @@ def test_scores_that_are_no_numbers(sv, dev):
     s.check(got)
 
 
+@pytest.mark.parametrize("budget, first, last", [(1, 0, 0), (4, 0, 0), (4, 1, 1), (9, 2, 3), (12, 0, 0), (29, 0, 2)])
+@pytest.mark.parametrize("F", [30, 4200])                           # keys in shared memory, and not
+@pytest.mark.parametrize("kind", ["nan", "inf", "query"])
+def test_more_infinite_scores_than_places(sv, dev, kind, F, budget, first, last):
+    """Beside negative scores and -infinity the keys' range is wider than 2^63."""
+    s = Lists(26, 2, 2, 4, 2, 64, 16, [16 * F, 16 * F - 5], budget, first, last)
+    g = np.random.default_rng(F + budget)
+    t = torch.from_numpy(s.table[:, g.permutation(F)]).long()
+    many, some = t[:, :10 if F < 100 else 2000].flatten(), t[:, -7:].flatten()
+    print(f"[infinite] {kind} {F} {budget} {first} {last}", flush=True)
+    if kind != "query":                                             # scores by the largest values' sign
+        s.q = s.q.abs()
+        s.hi[::3] = -s.hi[::3].abs()
+    if kind == "nan":
+        s.lo[many, :, 9] = float("nan")
+    elif kind == "inf":
+        s.hi[many, :, 9] = float("inf")
+        s.hi[some, :, 9] = float("-inf")
+    else:                                                           # by the sign of the bound
+        s.q[:, 0, ::2, 11] = float("inf")
+        s.hi[..., 11] = -s.hi[..., 11].abs()
+        s.hi[many, :, 11] = s.hi[many, :, 11].abs()
+        s.lo[..., 11] = -2.0
+    s.check(s.run(sv, dev))
+    assert status(sv) == 0
+
+
 def test_list_data_faults(sv, dev):
     s = Lists(23, 7, 3, 4, 2, 64, 16, [200, 200, 200, 200, 200, 200, 200], 5)
     s.ctx[1], s.ctx[2] = -1, 210                                    # past the table with its nodes
