@@ -653,10 +653,13 @@ size_t spec_page_select_workspace_bytes(int R, int Hkv, int D, int max_pages);
  *   score = sum_d U_d k_max_d + N_d k_min_d,
  *   U_d = sum of max(q_d, 0), N_d = sum of min(q_d, 0), over the rows of nodes
  *         v < n_nodes[r] and the group's Hq / Hkv query heads,
- * an upper bound of the sum of q . k over these rows for any key k of the page
  * (sums in 64 bits; a NaN score stands with +infinity; equal scores: the lower
- * page first).  The list holds page numbers (page_table entries) in the order
- * of the context, then the pages of tokens F * page_size .. ctx_len + n_nodes - 1.
+ * page first).  For bounds of spec_page_bounds over bf16 pages that is an upper bound
+ * of the sum of q . k over these rows for any key k of the page; over SPEC_E4M3 pages,
+ * whose bounds are rounded, up to 2^-8 sum_d |U_d max_d| + |N_d min_d|, max and min
+ * being the page's values before the rounding.  The list holds page numbers (page_table
+ * entries) in the order of the context, then the pages of tokens
+ * F * page_size .. ctx_len + n_nodes - 1.
  *   q          [R][M][Hq][D]  SPEC_BF16
  *   k_min, k_max  as above (of full pages)
  *   ctx_len, n_nodes  [R]     int32

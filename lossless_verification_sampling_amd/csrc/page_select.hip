@@ -6,7 +6,10 @@
 // most sum_d max(q_d lo_d, q_d hi_d), and summed over the query rows that share
 // the key head (nodes, and heads of the group) that is
 //   score = sum_d U_d hi_d + N_d lo_d,  U = sum of max(q, 0), N of min(q, 0):
-// two products a dimension whatever the number of rows.  Sums are in 64 bits:
+// two products a dimension whatever the number of rows.  (lo and hi are kept in bf16.
+// Those of bf16 pages are values of theirs; those of e4m3 pages are rounded to nearest,
+// and the score may lie below what it bounds by 2^-8 of its terms: it chooses
+// pages, and outward rounding would double the bounds' error.)  Sums are in 64 bits:
 // the products of bf16 values with U and N are close to exact there, so that
 // which pages are chosen does not hang on the order of the sums.
 #include "cache.h"

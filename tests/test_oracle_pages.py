@@ -1,6 +1,8 @@
 """Pins of the page oracle (CPU): hand-made choices and the bound's meaning."""
 import numpy as np
 
+from cache_util import bf16
+from oracle import cache as oc
 from oracle import pages as op
 
 
@@ -13,6 +15,27 @@ def test_a_score_bounds_every_key_of_the_page():
         corner = np.where(q.T > 0, hi[p].T, lo[p].T)                # the box's best corner of every row
         assert np.isclose(s[p], (corner.T * q).sum())
         assert (keys[p, :, 0] @ q.T).sum(1).max() <= s[p] + 1e-12
+
+
+def test_a_score_of_rounded_bounds():
+    """e4m3 pages: values are fp32 products code * scale, their bounds rounded to bf16
+    (half a step: 2^-8 of each).  The score bounds q . k up to that of its terms, and no
+    better."""
+    g = np.random.default_rng(2)
+    codes, scale = oc.quantise(g.standard_normal((50, 16, 1, 64)).astype(np.float32) * 3)
+    keys = (codes.astype(np.float32) * scale[..., None]).astype(np.float64)
+    q = g.standard_normal((5, 64))
+    lo, hi = (np.array(b)[:, 0] for b in zip(*(op.bounds(k) for k in keys)))
+    kept = [bf16(b).double().numpy() for b in (lo, hi)]
+    up, down = np.maximum(q, 0).sum(0), np.minimum(q, 0).sum(0)
+    slack = 2.0 ** -8 * (np.abs(up * hi) + np.abs(down * lo)).sum(1)
+    s, exact = op.scores(q, *kept), op.scores(q, lo, hi)
+    assert (np.abs(s - exact) <= slack + 1e-12).all()
+    assert ((keys[:, :, 0] @ q.T).sum(2).max(1) <= s + slack + 1e-12).all()
+    one = np.zeros((1, 64))
+    one[0, 0] = 1.0                                                 # a single dimension: the largest value itself
+    below = op.scores(one, *kept) < hi[:, 0]
+    assert below.any() and not below.all()
 
 
 def test_choice_by_hand():
