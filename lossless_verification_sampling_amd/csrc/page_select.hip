@@ -296,7 +296,7 @@ __device__ __forceinline__ uint64_t key_of(double s) {
 // kilobyte; D / 8 lanes share a head.  The largest values go with U, then the
 // least with N: one of the two sums is in registers at a time.  Bound by HBM:
 // 171 MB of bounds (64 requests of up to 16 k tokens, 8 heads of 128, 16-token pages) in
-// 27.5 us.  Two pages of one head a lane pair and eight loads a side took longer (80 us
+// 26.7 us.  Two pages of one head a lane pair and eight loads a side took longer (80 us
 // for the call against 58, and 44 us for this launch against 42, where each wave still
 // summed its queries).
 constexpr int kScoreLoads = 4;      // of 16 bytes a lane and side, all under way
@@ -384,7 +384,7 @@ __device__ __forceinline__ uint64_t higher(uint64_t a, uint64_t b) { return a > 
 // by counts over 2048 equal parts of the keys' range, and again over the part that
 // holds it (page_cut.h; of one key the lowest pages that have it are taken).  Keys of
 // up to kHeldKeys pages stay in shared memory.  Bound by latency: a handful of
-// dependent passes over a few keys a thread (10.6 us for eight lists of 1875 pages, 9.3 for 512 of up to 1000).
+// dependent passes over a few keys a thread (10.4 us for eight lists of 1875 pages, 9.2 for 512 of up to 1000).
 constexpr int kHeldKeys = 4096;
 
 __global__ void __launch_bounds__(kBlock) select_kernel(SelectArgs a) {

@@ -25,13 +25,13 @@
 // A row that none of this fits (top_k above kMostTopK together with top_p, more
 // equal logits than a list holds) is done whole by one workgroup at the end.
 //
-// Draws of bf16 rows of 151936 ids, 40 likely ones above a normal floor, T = 0.9,
-// in us for one row and for 256 (whose bytes alone take 15 at a copy's rate):
-//   nothing cut 28, 72      top_p 0.9 27, 42       top_p 0.999 48, 167
-//   min_p 0.05 26, 35       top_k 50 28, 48        top_k 200 28, 55
-//   top_k 1000 38, 128      top_k 50, top_p 0.9 27, 46
+// Draws of bf16 rows of 151936 ids, 40 likely ones at random places above a normal floor,
+// T = 0.9, in us for one row and for 256 (whose bytes alone take 15 at a copy's rate):
+//   nothing cut 26, 71      top_p 0.9 27, 64       top_p 0.999 47, 166
+//   min_p 0.05 26, 36       top_k 50 27, 48        top_k 200 28, 55
+//   top_k 1000 37, 127      top_k 50, top_p 0.9 26, 48
 //   top_k 1000, top_p 0.9 (whole rows) 101, 125
-// Truncation of the 256: 48, 55, 165, 47, 60, 68, 136, 59, 167 in the same order.
+// Truncation of the 256: 49, 73, 162, 50, 61, 69, 133, 61, 168 in the same order.
 #include "sample.h"
 
 namespace sv {
@@ -536,7 +536,7 @@ __device__ __forceinline__ void mark_fault(const SampleArgs &a, int ri) {
 // of those before its own; more are cut by histograms (sorted so, 512 took 32 us where
 // the histograms take 23).  A thread keeps up to 32 candidates in registers from one pass
 // to the next (8: 23 us against 19.6).  Bound by latency, some ten dependent steps of
-// a microsecond: 12.6 us for 256 rows under top-p, 19.6 for 64 rows with top_k up to 200.
+// a microsecond: 12.8 us for 256 rows under top-p, 19.6 for 64 rows with top_k up to 200.
 template <typename T, bool DRAW>
 __global__ void __launch_bounds__(kBlock) finish_kernel(SampleArgs a) {
     __shared__ Scratch<kBlock> s;
